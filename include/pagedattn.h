@@ -72,6 +72,7 @@ typedef enum pa_kv_dtype {
 #define PA_DEVERR_BAD_BATCH 1u  /* cumulative_sequence_length / past_seqlens inconsistent: nothing was computed or written */
 #define PA_DEVERR_BAD_BLOCK 2u  /* a block_table entry of an active page is outside [0, num_blocks): that page read as zeros */
 #define PA_DEVERR_BAD_SLOT 4u   /* a slot (given or derived) is outside [0, num_blocks*block_size) and not -1: write skipped */
+#define PA_DEVERR_NO_BLOCKS 16u /* pa_build_block_tables: fewer free pages than the step needs: refused, nothing changed */
 #define PA_DEVERR_TIMEOUT 8u    /* a pipeline wait inside a kernel gave up (results of that work item are undefined) */
 
 /* Routing of sequences to kernels (pa_dims.route). */
@@ -311,6 +312,146 @@ pa_status pa_paged_attention_ex(const void* query, const void* key, const void* 
                                 int32_t kv_num_heads, float scale, void* output,
                                 const pa_extensions* ext, const pa_dims* dims, void* workspace,
                                 size_t workspace_bytes, void* stream);
+
+/* ======================= operators around the attention call =========================== */
+
+/*
+ * Conventions of the entry points below, beyond those above: no workspace; a batch is given
+ * as to pa_paged_attention, but cumulative_sequence_length may end before num_tokens: rows
+ * behind the last sequence (a padded batch) are left as they were. `error`, where it may be
+ * NULL, is a device word that the caller has cleared and that accumulates PA_DEVERR_* bits:
+ * PA_DEVERR_BAD_BATCH for a sequence whose lengths do not fit the batch or its table row,
+ * PA_DEVERR_BAD_BLOCK for a page outside the pool (or a selection entry that is not a page
+ * of the row's history in ascending order); what is bad is skipped, the rest is computed.
+ * Calls on the same tensors follow their stream's order; calls share no other state.
+ */
+
+/* Most requests of one pa_build_block_tables call. */
+#define PA_MAX_TABLE_REQUESTS 8192
+/* Most columns of a block_table whose pages pa_select_pages scores. */
+#define PA_MAX_SCORED_PAGES 32768
+/* Largest top_k. */
+#define PA_MAX_SELECTED_PAGES 4096
+
+/*
+ * The step's prefix sums, positions, slots and block tables from the requests' lengths, with
+ * pages taken from and returned to a ring of free pages, all on the GPU.
+ *
+ *   past_seqlens   int32 (B): cached length of each request before the step.
+ *   query_lens     int32 (B): its new rows; 0: none this step (it keeps its pages); -1: the
+ *                  request is finished and gives its pages back.
+ *   blocks_held    int32 (B): pages the request holds, the first columns of its table row.
+ *   block_table    int32 (B, max_blocks_per_sequence), in place: a request that needs
+ *                  ceil((past + q) / block_size) pages and holds fewer gets the next free
+ *                  ones, requests in order, in the columns from blocks_held on.
+ *   free_blocks    int32 (free_capacity), a ring, in place: its free pages are the entries
+ *                  (head + i) mod free_capacity, i < count, of free_state = {head, count}.
+ *                  Pages are taken at the head; finished requests' pages are appended behind
+ *                  the last free page, requests and columns in order, and none of them is
+ *                  given out by the same call.
+ *
+ * Written: cumulative_sequence_length (B + 1); slot_mapping and positions (num_tokens), -1
+ * for rows behind the last request (and slot -1 where the table holds no valid page);
+ * blocks_held_out (B), free_state_out (2): the state for the next step, in other memory than
+ * blocks_held and free_state; error (1), not accumulated: 0, or the reason why the step was
+ * refused: PA_DEVERR_NO_BLOCKS (fewer free pages than needed) or PA_DEVERR_BAD_BATCH
+ * (lengths that are negative, exceed the table row or num_tokens, or a free_state that does
+ * not fit the ring). A refused step changes neither table nor ring, repeats the state, and
+ * describes an empty batch. A call repeated on the same inputs gives the same results.
+ */
+pa_status pa_build_block_tables(const int32_t* past_seqlens, const int32_t* query_lens, const int32_t* blocks_held,
+                                int32_t* block_table, int32_t* free_blocks, const int32_t* free_state,
+                                int32_t batch_size, int32_t num_tokens, int32_t max_blocks_per_sequence,
+                                int32_t block_size, int32_t free_capacity, int32_t* cumulative_sequence_length,
+                                int32_t* slot_mapping, int32_t* positions, int32_t* blocks_held_out,
+                                int32_t* free_state_out, uint32_t* error, void* stream);
+
+/*
+ * The Q/K preparation of pa_qk_prep for rows that stay in tensors: RMSNorm of every query
+ * and key head (with a weight), then the rotary embedding at positions[i], rounded once to
+ * T. interleaved != 0 pairs component 2u with 2u + 1 instead of u with u + d/2. rotary_dim
+ * is a multiple of 16 up to head_size (else PA_ERR_UNSUPPORTED). Row i of query starts at
+ * query + i * query_stride elements (key, query_out and key_out likewise; strides are
+ * multiples of 8, so that packed [Q | K | V] rows can be given as they are). query_out and
+ * key_out may be query and key (in place) but may not overlap them otherwise. A row with a
+ * negative position is left as it was.
+ */
+pa_status pa_qk_norm_rope(const void* query, const void* key, const int32_t* positions, const pa_qk_prep* prep,
+                          int32_t interleaved, int32_t num_tokens, int32_t num_heads, int32_t kv_num_heads,
+                          int32_t head_size, int32_t dtype, int64_t query_stride, int64_t key_stride,
+                          void* query_out, void* key_out, int64_t query_out_stride, int64_t key_out_stride,
+                          void* stream);
+
+/* Host-side sizes of the sparse-attention entry points. */
+typedef struct pa_sparse_dims {
+  int32_t num_tokens;              /* rows of query, output and selected */
+  int32_t batch_size;
+  int32_t num_heads;
+  int32_t kv_num_heads;            /* divides num_heads */
+  int32_t head_size;               /* 64, 128 or 256 */
+  int32_t num_blocks;
+  int32_t block_size;              /* a positive multiple of 16 */
+  int32_t max_blocks_per_sequence;
+  int32_t dtype;                   /* pa_dtype of T, the type of query, caches and output */
+  int32_t top_k;                   /* pages per row and KV head: the last extent of `selected` */
+  int32_t query_block;             /* R: rows [jR, (j + 1)R) of a sequence share one selection;
+                                      R * num_heads / kv_num_heads is at most 1024 */
+  int32_t sink_pages;              /* first pages of a history that are always selected */
+  int32_t local_pages;             /* pages up to the block's first row, its own among them, that are (>= 1) */
+  int32_t reserved;                /* 0 */
+  int64_t query_stride;            /* elements between rows of query: a multiple of 8 */
+} pa_sparse_dims;
+
+/*
+ * Bounds of the keys that this step wrote. page_bounds is int8 (num_blocks, kv_num_heads, 2,
+ * head_size): per page, KV head and channel the least (0) and the largest (1) code
+ * min(max(rint(fl32(k) / s), -127), 127) of the page's keys, with s = bound_scale (fp32
+ * (kv_num_heads, head_size), positive: the K scales of an INT8 cache serve). Reads the keys at
+ * positions past .. past + q - 1 of every sequence from key_cache (call it after the cache
+ * write); a page that begins with one of them starts afresh, a page that held keys before
+ * keeps their bounds. To bound a cache that is there already, pass past_seqlens of 0 and the
+ * whole lengths. Sequences of one call must not write to the same page. NaN keys do not
+ * count. Uses num_heads, top_k, query_block and the query stride of `dims` for nothing.
+ */
+pa_status pa_update_page_bounds(const void* key_cache, int8_t* page_bounds, const float* bound_scale,
+                                const int32_t* cumulative_sequence_length, const int32_t* past_seqlens,
+                                const int32_t* block_table, const pa_sparse_dims* dims, uint32_t* error,
+                                void* stream);
+
+/*
+ * The pages that each query row attends. For a block of query rows and a KV head the products
+ * x = fl32(q_c * s_c) of all its rows and the group's heads (those that are not finite count
+ * as 0) become codes t = rint(fl32(x * fl32(4095 / max|x|))) (all 0 when max|x| <= 1e-30),
+ * P_c and M_c are the sums of max(t, 0) and max(-t, 0), a_c = floor((510 P_c + m) / 2m) and
+ * b_c = floor((510 M_c + m) / 2m) with m = max(P, M), and page j scores
+ *   sum_c a_c * bounds[j][g][1][c] - b_c * bounds[j][g][0][c],
+ * a whole number. Selected are the first sink_pages pages of the history, the last local_pages
+ * pages up to the one of the block's first row, the pages of the block's rows, and the best
+ * others (ties: the lower page) up to top_k, which must have room for the former
+ * (top_k >= sink_pages + local_pages + ceil((query_block - 1) / block_size)).
+ * selected is int32 (N, kv_num_heads, top_k): logical pages in ascending order, then -1; the
+ * rows of a block hold the same. Pages that are selected without a comparison are not looked
+ * up; a scored page outside the pool scores 0, with PA_DEVERR_BAD_BLOCK.
+ */
+pa_status pa_select_pages(const void* query, const int8_t* page_bounds, const float* bound_scale,
+                          const int32_t* cumulative_sequence_length, const int32_t* past_seqlens,
+                          const int32_t* block_table, const pa_sparse_dims* dims, int32_t* selected, uint32_t* error,
+                          void* stream);
+
+/*
+ * pa_paged_attention's read path over selected pages only: row j of sequence b attends, for
+ * the heads of KV head g, the keys at positions <= past_seqlens[b] + j that lie in the pages
+ * selected[cumulative_sequence_length[b] + j0][g], j0 = j - j mod query_block (the selection of
+ * the block's first row; the other rows' are not read). Entries are logical pages in strictly
+ * ascending order; -1 entries are passed over, anything else is skipped with
+ * PA_DEVERR_BAD_BLOCK. A row that attends no key gives zeros and an lse of -inf. scale, output
+ * and lse (fp32 (N, num_heads) or NULL) as in pa_paged_attention_lse; query rows may be strided.
+ * The caches hold T and already hold this step's rows.
+ */
+pa_status pa_sparse_paged_attention(const void* query, const void* key_cache, const void* value_cache,
+                                    const int32_t* cumulative_sequence_length, const int32_t* past_seqlens,
+                                    const int32_t* block_table, const int32_t* selected, float scale, void* output,
+                                    float* lse, const pa_sparse_dims* dims, uint32_t* error, void* stream);
 
 /* Static description of a status code. Never NULL. */
 const char* pa_status_string(pa_status status);

@@ -21,7 +21,7 @@ LIBRARY_PATH = os.path.join(_HERE, "libpagedattn.so")
 STAGE_PLAN, STAGE_CACHE_WRITE, STAGE_PREFILL, STAGE_DECODE = 1, 2, 4, 8
 STAGE_ALL = 15
 ROUTE_AUTO, ROUTE_ALL_PREFILL = 0, 1
-DEVERR_BAD_BATCH, DEVERR_BAD_BLOCK, DEVERR_BAD_SLOT, DEVERR_TIMEOUT = 1, 2, 4, 8
+DEVERR_BAD_BATCH, DEVERR_BAD_BLOCK, DEVERR_BAD_SLOT, DEVERR_TIMEOUT, DEVERR_NO_BLOCKS = 1, 2, 4, 8, 16
 
 _STATUS = {0: "PA_OK", 1: "PA_ERR_INVALID_ARGUMENT", 2: "PA_ERR_UNSUPPORTED",
            3: "PA_ERR_WORKSPACE_TOO_SMALL", 4: "PA_ERR_CUDA"}
@@ -251,5 +251,9 @@ def paged_attention(query: torch.Tensor, key: Optional[torch.Tensor], value: Opt
     return output
 
 
-__all__ = ["KV_SAME", "KV_INT8", "KV_INT4", "paged_attention", "workspace_size", "make_dims", "PaQkPrep", "PaExtensions", "read_device_error", "kernel_launch_count",
+from .step import (BlockTables, PaSparseDims, build_block_tables, qk_norm_rope, select_pages,  # noqa: E402
+                   sparse_paged_attention, update_page_bounds)
+
+__all__ = ["BlockTables", "PaSparseDims", "build_block_tables", "qk_norm_rope", "select_pages",
+           "sparse_paged_attention", "update_page_bounds", "KV_SAME", "KV_INT8", "KV_INT4", "paged_attention", "workspace_size", "make_dims", "PaQkPrep", "PaExtensions", "read_device_error", "kernel_launch_count",
            "load_library", "PagedAttentionError", "PaDims", "LIBRARY_PATH"]

@@ -6,7 +6,7 @@
 #include <atomic>
 #include <mutex>
 
-#include "common.cuh"
+#include "ops.cuh"
 
 
 namespace {
@@ -304,6 +304,25 @@ pa_status launch_all(pa::Args& args, const pa_dims* d, const void* query, void* 
 }
 
 }  // namespace
+
+// the helpers that the operators' entry points share (ops.cuh)
+namespace pa {
+pa_status cuda_fail(cudaError_t e, const char* what) { return ::cuda_fail(e, what); }
+pa_status cuda_fail_text(const char* text) {
+  g_last_error = text;
+  return PA_ERR_CUDA;
+}
+void count_launch() { ++g_launches; }
+bool device_sms(int* sms) {
+  DeviceInfo info;
+  if (!device_info(&info)) return false;
+  *sms = info.sms;
+  return true;
+}
+bool cache_map_16(CUtensorMap* m, const void* base, bool bf16, int hs, int kvh, int64_t slots, int rows) {
+  return cache_map(m, const_cast<void*>(base), bf16 ? PA_BFLOAT16 : PA_FLOAT16, hs, kvh, slots, rows);
+}
+}  // namespace pa
 
 extern "C" {
 

@@ -1,0 +1,111 @@
+// Shared declarations of the operators around paged attention: block tables, Q/K norm and
+// rotation, page bounds, page selection and attention over selected pages.
+#pragma once
+
+#include "common.cuh"
+
+namespace pa {
+
+// ---- host helpers defined with the paged-attention entry points (api.cu) -------------------
+pa_status cuda_fail(cudaError_t e, const char* what);  // records the message for pa_last_error
+pa_status cuda_fail_text(const char* text);
+void count_launch();
+bool device_sms(int* sms);  // SMs of the current device
+// 3-D map over a cache of 16-bit values viewed as (head_size, kv_heads, slots), box 64 x 1 x
+// rows, 128-byte swizzle
+bool cache_map_16(CUtensorMap* m, const void* base, bool bf16, int hs, int kvh, int64_t slots, int rows);
+
+// ---- batch lookup without a plan -----------------------------------------------------------
+// Work units are numbered so that sequence b's begin at cum[b] / div + mul * b: a CTA finds
+// its sequence from its own index by searching that increasing function, and no kernel has to
+// lay the units out first. (With mul = 1 there is room for ceil(q_b / div) units per
+// sequence, with mul = 2 for one more, as rows that start inside a page touch; unused numbers
+// in between belong to no unit.) The largest b with cum[b] / div + mul * b <= u, by a whole
+// warp, 32 candidates a step; -1 if there is none.
+__device__ __forceinline__ int find_seq(const int32_t* cum, int B, int div, int mul, int u, int lane) {
+  int lo = 0, n = B;
+  while (n > 0) {
+    const int step = (n + 31) / 32, i = lo + lane * step;
+    const bool ok = i < lo + n && cum[i] / div + mul * i <= u;
+    const unsigned m = __ballot_sync(0xffffffffu, ok);
+    if (m == 0) return -1;
+    const int k = 31 - __clz(m);
+    n = min(step, lo + n - (lo + k * step));
+    lo += k * step;
+    if (step == 1) break;
+  }
+  return lo;
+}
+
+// A sequence's rows and history; ok is false for lengths that do not belong to a batch
+// of N rows and tables of max_blocks pages (such a sequence is skipped).
+struct Seq {
+  int c0, q, past;
+  bool ok;
+};
+__device__ __forceinline__ Seq load_seq(const int32_t* cum, const int32_t* past, int b, int N, int max_blocks,
+                                        int bs) {
+  Seq s;
+  s.c0 = cum[b];
+  const int c1 = cum[b + 1];
+  s.past = past[b];
+  s.q = c1 - s.c0;
+  s.ok = s.c0 >= 0 && c1 >= s.c0 && c1 <= N && s.past >= 0 && (int64_t)s.past + s.q <= (int64_t)max_blocks * bs;
+  return s;
+}
+
+// the checks of the whole batch, by one CTA: sets PA_DEVERR_BAD_BATCH
+__device__ __forceinline__ void check_batch(const int32_t* cum, const int32_t* past, int B, int N, int max_blocks,
+                                            int bs, uint32_t* err) {
+  if (!err) return;
+  bool bad = threadIdx.x == 0 && cum[0] != 0;
+  for (int b = threadIdx.x; b < B; b += blockDim.x) bad |= !load_seq(cum, past, b, N, max_blocks, bs).ok;
+  if (bad) atomicOr(err, PA_DEVERR_BAD_BATCH);
+}
+
+// ---- argument records ----------------------------------------------------------------------
+struct TableArgs {
+  const int32_t *past, *query_lens, *held;
+  int32_t *table, *ring;
+  const int32_t* state;
+  int32_t *cum, *slots, *positions, *held_out, *state_out;
+  uint32_t* error;
+  int32_t B, N, max_blocks, bs, cap;
+};
+
+struct RotateArgs {
+  const uint16_t *query, *key, *q_weight, *k_weight;
+  uint16_t *query_out, *key_out;
+  const int32_t* positions;
+  int64_t q_stride, k_stride, qo_stride, ko_stride;  // elements between rows
+  int32_t N, nh, kvh, rotary_dim, interleaved;
+  int32_t split;  // warps that share a row's heads
+  float eps;
+  float inv_freq[128];
+};
+
+struct PageArgs {
+  const uint16_t *query, *key_cache, *value_cache;
+  int8_t* bounds;      // (num_blocks, kvh, 2, hs): minimum, then maximum codes
+  const float* scale;  // (kvh, hs)
+  const int32_t *cum, *past, *table;
+  int32_t* selected;   // (N, kvh, top_k)
+  void* output;
+  float* lse;
+  uint32_t* error;
+  int64_t q_stride;
+  int32_t N, B, nh, kvh, G, hs, num_blocks, bs, max_blocks;
+  int32_t top_k, R, sink, local;
+  float scale_log2;
+};
+
+cudaError_t launch_tables(const TableArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_rotate(const RotateArgs& a, bool bf16, int hs, int sms, cudaStream_t s);
+cudaError_t launch_bounds(const PageArgs& a, bool bf16, cudaStream_t s);
+cudaError_t launch_select(const PageArgs& a, bool bf16, int sms, cudaStream_t s);
+cudaError_t launch_sparse(const PageArgs& a, bool bf16, int sms, cudaStream_t s);
+
+// numbers of query blocks (units of div rows, with mul numbers to spare per sequence)
+inline int64_t query_blocks(const PageArgs& a) { return a.R == 1 ? a.N : (int64_t)a.N / a.R + a.B; }
+
+}  // namespace pa
