@@ -14,6 +14,10 @@ bool device_sms(int* sms);  // SMs of the current device
 // 3-D map over a cache of 16-bit values viewed as (head_size, kv_heads, slots), box 64 x 1 x
 // rows, 128-byte swizzle
 bool cache_map_16(CUtensorMap* m, const void* base, bool bf16, int hs, int kvh, int64_t slots, int rows);
+// 3-D map over query rows viewed as (head_size, heads, rows) with rows `stride` elements apart,
+// box 64 x heads x rows, 128-byte swizzle
+bool query_block_map(CUtensorMap* m, const void* base, bool bf16, int hs, int nh, int64_t n, int64_t stride, int heads,
+                     int rows);
 
 // ---- batch lookup without a plan -----------------------------------------------------------
 // Work units are numbered so that sequence b's begin at cum[b] / div + mul * b: a CTA finds
