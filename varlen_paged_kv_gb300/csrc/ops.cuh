@@ -67,6 +67,30 @@ __device__ __forceinline__ void check_batch(const int32_t* cum, const int32_t* p
   if (bad) atomicOr(err, PA_DEVERR_BAD_BATCH);
 }
 
+// ---- clusters ------------------------------------------------------------------------------
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the address in CTA `rank` of the cluster that `p` has in this one
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 // ---- argument records ----------------------------------------------------------------------
 struct TableArgs {
   const int32_t *past, *query_lens, *held;
@@ -108,6 +132,31 @@ cudaError_t launch_rotate(const RotateArgs& a, bool bf16, int hs, int sms, cudaS
 cudaError_t launch_bounds(const PageArgs& a, bool bf16, cudaStream_t s);
 cudaError_t launch_select(const PageArgs& a, bool bf16, int sms, cudaStream_t s);
 cudaError_t launch_sparse(const PageArgs& a, bool bf16, int sms, cudaStream_t s);
+
+// A launch whose CTAs along z form one cluster each.
+template <typename... KArgs, typename... Actual>
+inline cudaError_t launch_clusters(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                                   Actual&&... args) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  if (grid.z > 8) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = grid.z;
+  cfg.attrs = attr;
+  cfg.numAttrs = grid.z > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Actual&&>(args)...);
+}
 
 // numbers of query blocks (units of div rows, with mul numbers to spare per sequence)
 inline int64_t query_blocks(const PageArgs& a) { return a.R == 1 ? a.N : (int64_t)a.N / a.R + a.B; }

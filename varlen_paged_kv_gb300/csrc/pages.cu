@@ -133,6 +133,9 @@ cudaError_t launch_bounds(const PageArgs& a, bool bf16, cudaStream_t s) {
 // ---- selection -----------------------------------------------------------------------------
 
 constexpr int kSelThreads = 256;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelLoads = 8;     // 16-byte loads in flight per lane while scoring
+constexpr int kSelBins = 2048;   // of the histograms that find the threshold
 
 // unsigned bytes times signed bytes, added to c
 __device__ __forceinline__ int dot4_us(uint32_t u, uint32_t s, int c) {
@@ -141,16 +144,182 @@ __device__ __forceinline__ int dot4_us(uint32_t u, uint32_t s, int c) {
   return d;
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const PageArgs a) {
-  extern __shared__ int score[];  // [max_blocks]
-  __shared__ uint32_t qcode[2][64];  // codes of the summed negative (0) and positive (1) parts
-  __shared__ int red[kSelThreads / 32][2];
-  __shared__ float redf[kSelThreads / 32];
-  int* list = score + a.max_blocks;  // [top_k]
+// what a select CTA holds beside its scores and list
+struct SelShared {
+  int plus[256], minus[256];      // the block's summed 12-bit codes
+  __align__(16) uint8_t code[2][256];  // 8-bit codes: negative (0), positive (1) parts
+  int hist[kSelBins];
+  int warp_a[kSelWarps], warp_b[kSelWarps];
+  float warp_f[kSelWarps];
+  int found[2];
+};
+
+// The block's codes into sh.code: 12-bit codes of every row in units of the block's largest
+// product, summed by sign, rescaled to 8 bits. A thread holds up to eight 16-byte pieces of
+// the rows in registers between finding the largest value and rounding by it, so that up to
+// 8 * 256 / (HS / 8) rows are read from memory once (more are read twice).
+template <int HS, bool BF16>
+__device__ void query_codes(const PageArgs& a, int row0, int rows, int g, SelShared& sh) {
+  constexpr int CH = HS / 8, GROUPS = kSelThreads / CH, HOLD = 8;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = blockIdx.y;
-  if (blockIdx.x == 0 && g == 0) check_batch(a.cum, a.past, a.B, a.N, a.max_blocks, a.bs, a.error);
+  const int c = tid % CH * 8, group = tid / CH, total = rows * a.G;
+  const uint16_t* q = a.query + (int64_t)row0 * a.q_stride + (int64_t)g * a.G * HS + c;
+  float sc[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sc[e] = __ldg(a.scale + g * HS + c + e);
+  auto load = [&](int r) {
+    return __ldg(reinterpret_cast<const uint4*>(q + (int64_t)(r / a.G) * a.q_stride + (int64_t)(r % a.G) * HS));
+  };
+  auto products = [&](const uint4& v, float (&x)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[e] = __fmul_rn(half_of<BF16>(w[e / 2], e & 1), sc[e]);
+      if (!isfinite(x[e])) x[e] = 0.f;
+    }
+  };
+  uint4 held[HOLD];
+#pragma unroll
+  for (int k = 0; k < HOLD; ++k)
+    held[k] = group + k * GROUPS < total ? load(group + k * GROUPS) : make_uint4(0, 0, 0, 0);
+  float most = 0.f;
+  auto widest = [&](const uint4& v) {
+    float x[8];
+    products(v, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(x[e]));
+  };
+#pragma unroll
+  for (int k = 0; k < HOLD; ++k) widest(held[k]);
+  for (int r = group + HOLD * GROUPS; r < total; r += GROUPS) widest(load(r));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+  if (lane == 0) sh.warp_f[warp] = most;
+  for (int i = tid; i < HS; i += kSelThreads) sh.plus[i] = sh.minus[i] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kSelWarps; ++i) most = fmaxf(most, sh.warp_f[i]);
+  const float fine = most > 1e-30f ? __fdiv_rn(4095.f, most) : 0.f;
+  int plus[8] = {}, minus[8] = {};
+  auto add = [&](const uint4& v) {
+    float x[8];
+    products(v, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int t = __float2int_rn(__fmul_rn(x[e], fine));
+      plus[e] += max(t, 0);
+      minus[e] += max(-t, 0);
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < HOLD; ++k) add(held[k]);
+  for (int r = group + HOLD * GROUPS; r < total; r += GROUPS) add(load(r));
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    // (lanes CH apart hold the same channels)
+#pragma unroll
+    for (int o = CH; o < 32; o <<= 1) {
+      plus[e] += __shfl_xor_sync(0xffffffffu, plus[e], o);
+      minus[e] += __shfl_xor_sync(0xffffffffu, minus[e], o);
+    }
+    if (lane < CH && group < total) {
+      atomicAdd(&sh.plus[c + e], plus[e]);
+      atomicAdd(&sh.minus[c + e], minus[e]);
+    }
+  }
+  __syncthreads();
+  const int p = tid < HS ? sh.plus[tid] : 0, m = tid < HS ? sh.minus[tid] : 0;
+  int big = __reduce_max_sync(0xffffffffu, max(p, m));
+  if (lane == 0) sh.warp_a[warp] = big;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kSelWarps; ++i) big = max(big, sh.warp_a[i]);
+  big = max(big, 1);
+  if (tid < HS) {
+    // (510 p + big) / (2 big): 510 * 1024 rows * 4095 stays below 2^31
+    sh.code[1][tid] = (uint8_t)((uint32_t)(510 * p + big) / (uint32_t)(2 * big));
+    sh.code[0][tid] = (uint8_t)((uint32_t)(510 * m + big) / (uint32_t)(2 * big));
+  }
+  __syncthreads();
+}
+
+// Scores of pages [i0, i1) of a history into `put(page, score)`. A page's 2 * HS bytes are CH
+// 16-byte pieces: a lane keeps the query codes of its own piece in registers and takes it from
+// kSelLoads * 32 / CH pages at once; the pieces' sums meet by a transposing reduction, so that
+// every lane ends with one page's score (or shares one).
+template <int HS, typename Put>
+__device__ void score_pages(const PageArgs& a, const int* table, int g, int i0, int i1, const SelShared& sh, Put put) {
+  constexpr int CH = HS / 8;             // pieces of a page: half minimum, half maximum codes
+  constexpr int PER = 32 / CH;           // pages per load of the warp
+  constexpr int BATCH = kSelLoads * PER;  // pages per step
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int piece = lane % CH, sub = lane / CH;
+  const bool upper = piece >= CH / 2;
+  const uint4 q = *reinterpret_cast<const uint4*>(sh.code[upper ? 1 : 0] + piece % (CH / 2) * 16);
+  const int8_t* base = a.bounds + (int64_t)g * 2 * HS + piece * 16;
+  const int64_t page_bytes = (int64_t)a.kvh * 2 * HS;
+  bool bad = false;
+  for (int i = i0 + warp * BATCH; i < i1; i += kSelWarps * BATCH) {
+    int phys = i + lane < i1 && lane < BATCH ? table[i + lane] : -1;
+    if (phys >= a.num_blocks) phys = -1;
+    bad |= phys < 0 && lane < BATCH && i + lane < i1;
+    uint4 v[kSelLoads];
+#pragma unroll
+    for (int k = 0; k < kSelLoads; ++k) {
+      const int p = __shfl_sync(0xffffffffu, phys, k * PER + sub);
+      v[k] = p >= 0 ? __ldg(reinterpret_cast<const uint4*>(base + p * page_bytes)) : make_uint4(0, 0, 0, 0);
+    }
+    int d[kSelLoads];
+#pragma unroll
+    for (int k = 0; k < kSelLoads; ++k) {
+      const int x = dot4_us(q.x, v[k].x, dot4_us(q.y, v[k].y, dot4_us(q.z, v[k].z, dot4_us(q.w, v[k].w, 0))));
+      d[k] = upper ? x : -x;
+    }
+    // halve the values a lane holds while summing over the pieces: after the step of bit o
+    // the lanes with that bit set keep the upper half
+    int first = 0;
+#pragma unroll
+    for (int o = CH / 2, n = kSelLoads; o >= 1; o >>= 1) {
+      if (n > 1) {
+        n >>= 1;
+        const bool hi = lane & o;
+#pragma unroll
+        for (int k = 0; k < n; ++k) {
+          const int send = hi ? d[k] : d[k + n], keep = hi ? d[k + n] : d[k];
+          d[k] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+        first += hi ? n : 0;
+      } else {
+        d[0] += __shfl_xor_sync(0xffffffffu, d[0], o);
+      }
+    }
+    // lanes that differ in the bits left over hold the same
+    constexpr int SAME = CH > kSelLoads ? CH / kSelLoads : 1;
+    if (lane % SAME == 0) {
+#pragma unroll
+      for (int k = 0; k < (CH < kSelLoads ? kSelLoads / CH : 1); ++k) {
+        const int page = i + (first + k) * PER + sub;
+        if (page < i1) put(page, d[k]);
+      }
+    }
+  }
+  if (bad && a.error) atomicOr(a.error, PA_DEVERR_BAD_BLOCK);
+}
+
+// The CTAs of a cluster score a share of the pages each into the first one's shared memory,
+// which then finds the want-th best score and writes the list: the largest score first, a
+// histogram of the distances from it in 2048 bins, and histograms inside the bin that the
+// want-th falls in until bins are single scores (two or three passes over the scores, not one
+// per bit). Bytes bound the scoring of long histories (2 HS bytes a page and head); short ones
+// are a chain of latencies.
+template <int HS, bool BF16>
+__global__ void __launch_bounds__(kSelThreads) select_kernel(const PageArgs a) {
+  extern __shared__ int score[];  // [max_blocks], then the list [top_k]
+  __shared__ SelShared sh;
+  int* list = score + a.max_blocks;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = blockIdx.y, rank = blockIdx.z, C = gridDim.z;
+  if (blockIdx.x == 0 && g == 0 && rank == 0) check_batch(a.cum, a.past, a.B, a.N, a.max_blocks, a.bs, a.error);
   const int u = blockIdx.x;
   const int b = find_seq(a.cum, a.B, a.R, a.R == 1 ? 0 : 1, u, lane);
   if (b < 0) return;
@@ -166,108 +335,104 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const PageArgs a) {
   const int want = a.top_k - (n - (end - begin));            // of which this many are taken
   int* out = a.selected + ((int64_t)(s.c0 + j0) * a.kvh + g) * a.top_k;
   const int64_t row_step = (int64_t)a.kvh * a.top_k;
-  if (want >= end - begin) {  // every page
-    for (int r = 0; r < rows; ++r)
-      for (int i = tid; i < a.top_k; i += kSelThreads) out[r * row_step + i] = i < n ? i : -1;
+  if (want >= end - begin) {  // every page (all CTAs of a cluster agree)
+    if (rank == 0)
+      for (int r = 0; r < rows; ++r)
+        for (int i = tid; i < a.top_k; i += kSelThreads) out[r * row_step + i] = i < n ? i : -1;
     return;
   }
-  // ---- the block's codes: 12-bit codes of every row in units of the block's largest value,
-  // summed by sign, rescaled to 8 bits ----
-  const uint16_t* q = a.query + (int64_t)(s.c0 + j0) * a.q_stride + (int64_t)g * a.G * a.hs;
-  const int c = tid;  // (hs <= 256 = threads: thread c sums channel c)
-  const float sc = c < a.hs ? a.scale[g * a.hs + c] : 0.f;
-  auto value = [&](int r, int h) {
-    const uint16_t bits = q[(int64_t)r * a.q_stride + h * a.hs + c];
-    const float x = __fmul_rn(BF16 ? __uint_as_float((uint32_t)bits << 16) : __half2float(__ushort_as_half(bits)), sc);
-    return isfinite(x) ? x : 0.f;
-  };
-  float most = 0.f;
-  if (c < a.hs)
-    for (int r = 0; r < rows; ++r)
-      for (int h = 0; h < a.G; ++h) most = fmaxf(most, fabsf(value(r, h)));
-  for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-  if (lane == 0) redf[warp] = most;
-  __syncthreads();
-  for (int i = 0; i < kSelThreads / 32; ++i) most = fmaxf(most, redf[i]);
-  const float fine = most > 1e-30f ? __fdiv_rn(4095.f, most) : 0.f;
-  int plus = 0, minus = 0;
-  if (c < a.hs)
-    for (int r = 0; r < rows; ++r)
-      for (int h = 0; h < a.G; ++h) {
-        const int t = __float2int_rn(__fmul_rn(value(r, h), fine));
-        plus += max(t, 0);
-        minus += max(-t, 0);
-      }
-  int big = max(plus, minus);
-  big = __reduce_max_sync(0xffffffffu, big);
-  if (lane == 0) red[warp][0] = big;
-  __syncthreads();
-  for (int i = 0; i < kSelThreads / 32; ++i) big = max(big, red[i][0]);
-  big = max(big, 1);
-  if (c < a.hs) {
-    // (510 * plus + big) / (2 big): 510 * 1024 rows * 4095 stays below 2^31
-    reinterpret_cast<uint8_t*>(qcode[1])[c] = (uint8_t)((uint32_t)(510 * plus + big) / (uint32_t)(2 * big));
-    reinterpret_cast<uint8_t*>(qcode[0])[c] = (uint8_t)((uint32_t)(510 * minus + big) / (uint32_t)(2 * big));
+  query_codes<HS, BF16>(a, s.c0 + j0, rows, g, sh);
+  const int* table = a.table + (int64_t)b * a.max_blocks;
+  const int count = end - begin;
+  if (C == 1) {
+    score_pages<HS>(a, table, g, begin, end, sh, [&](int page, int d) { score[page - begin] = d; });
+    __syncthreads();
+  } else {
+    cluster_sync();  // (the first CTA runs before it is written to)
+    const uint32_t first = cluster_addr(score, 0);
+    score_pages<HS>(a, table, g, begin + (int)((int64_t)count * rank / C), begin + (int)((int64_t)count * (rank + 1) / C),
+                    sh, [&](int page, int d) {
+                      asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(first + (uint32_t)(page - begin) * 4), "r"(d)
+                                   : "memory");
+                    });
+    cluster_sync();
+    if (rank != 0) return;
   }
+  // ---- the threshold: scores above `cut` are taken, and the first `ties` of those at it ----
+  int top = INT32_MIN, low = INT32_MAX;
+  for (int i = tid; i < count; i += kSelThreads) top = max(top, score[i]), low = min(low, score[i]);
+  top = __reduce_max_sync(0xffffffffu, top);
+  low = __reduce_min_sync(0xffffffffu, low);
+  if (lane == 0) sh.warp_a[warp] = top, sh.warp_b[warp] = low;
   __syncthreads();
-  // ---- scores ----
-  const int words = a.hs / 4;
-  for (int i = begin + tid; i < end; i += kSelThreads) {
-    const int phys = a.table[(int64_t)b * a.max_blocks + i];
-    int d = 0;
-    if (phys >= 0 && phys < a.num_blocks) {
-      const uint32_t* p = reinterpret_cast<const uint32_t*>(a.bounds + ((int64_t)phys * a.kvh + g) * 2 * a.hs);
-      int neg = 0;
-      for (int k = 0; k < words; ++k) {
-        neg = dot4_us(qcode[0][k], p[k], neg);
-        d = dot4_us(qcode[1][k], p[words + k], d);
-      }
-      d -= neg;
-    } else if (a.error) {
-      atomicOr(a.error, PA_DEVERR_BAD_BLOCK);
+#pragma unroll
+  for (int w = 0; w < kSelWarps; ++w) top = max(top, sh.warp_a[w]), low = min(low, sh.warp_b[w]);
+  // distances top - score from `from` on, below `from + span`, in bins of 2^shift
+  uint32_t from = 0, span = (uint32_t)(top - low) + 1;
+  int ties = want;  // still to be taken among them
+  for (;;) {
+    const int bits = 32 - __clz(span - 1 | 1), shift = max(bits - 11, 0);
+    for (int i = tid; i < kSelBins; i += kSelThreads) sh.hist[i] = 0;
+    __syncthreads();
+    for (int i = tid; i < count; i += kSelThreads) {
+      const uint32_t x = (uint32_t)(top - score[i]) - from;
+      if (x < span) atomicAdd(&sh.hist[x >> shift], 1);
     }
-    score[i] = d;
-  }
-  __syncthreads();
-  // ---- the largest threshold that at least `want` scores reach, by bisection; each warp
-  // counts its own contiguous part ----
-  const int per = (int)align_up(ceil_div(end - begin, kSelThreads / 32), 32);
-  const int i0 = min(end, begin + warp * per), i1 = min(end, i0 + per);
-  int lo = -(1 << 24), hi = 1 << 24;  // count(score >= lo) >= want > count(score >= hi)
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    int cnt = 0;
-    for (int i = i0 + lane; i < i1; i += 32) cnt += score[i] >= mid;
-    cnt = __reduce_add_sync(0xffffffffu, cnt);
-    if (lane == 0) red[warp][0] = cnt;
     __syncthreads();
-    cnt = 0;
-    for (int w = 0; w < kSelThreads / 32; ++w) cnt += red[w][0];
+    constexpr int MINE = kSelBins / kSelThreads;
+    int h[MINE], sum = 0;
+#pragma unroll
+    for (int k = 0; k < MINE; ++k) h[k] = sh.hist[tid * MINE + k], sum += h[k];
+    int inc = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += y;
+    }
+    if (lane == 31) sh.warp_a[warp] = inc;
     __syncthreads();
-    if (cnt >= want) lo = mid;
-    else hi = mid;
+    int before = inc - sum;
+#pragma unroll
+    for (int w = 0; w < kSelWarps; ++w)
+      if (w < warp) before += sh.warp_a[w];
+    if (before < ties && ties <= before + sum) {  // the want-th falls in one of this thread's bins
+#pragma unroll
+      for (int k = 0; k < MINE; ++k) {
+        if (before < ties && ties <= before + h[k]) sh.found[0] = tid * MINE + k, sh.found[1] = ties - before;
+        before += h[k];
+      }
+    }
+    if (ties == 0 && tid == 0) sh.found[0] = 0, sh.found[1] = 0;  // (nothing to take: a threshold above all)
+    __syncthreads();
+    from += (uint32_t)sh.found[0] << shift;
+    ties = sh.found[1];
+    if (shift == 0) break;
+    span = min(span - ((uint32_t)sh.found[0] << shift), 1u << shift);
+    if (span == 1) break;
   }
-  // ---- the taken pages in order: those above the threshold, and of those at it the first ----
+  const int cut = top - (int)from;
+  // ---- the taken pages in order, each warp a contiguous part ----
+  const int per = (int)align_up(ceil_div(count, kSelWarps), 32);
+  const int i0 = min(count, warp * per), i1 = min(count, i0 + per);
   int above = 0, at = 0;
-  for (int i = i0 + lane; i < i1; i += 32) above += score[i] > lo, at += score[i] == lo;
+  for (int i = i0 + lane; i < i1; i += 32) above += score[i] > cut, at += score[i] == cut;
   above = __reduce_add_sync(0xffffffffu, above);
   at = __reduce_add_sync(0xffffffffu, at);
-  if (lane == 0) red[warp][0] = above, red[warp][1] = at;
   __syncthreads();
-  int all_above = 0, before_above = 0, before_at = 0;
-  for (int w = 0; w < kSelThreads / 32; ++w) {
-    if (w < warp) before_above += red[w][0], before_at += red[w][1];
-    all_above += red[w][0];
-  }
-  const int ties = want - all_above;
+  if (lane == 0) sh.warp_a[warp] = above, sh.warp_b[warp] = at;
+  __syncthreads();
+  int before_above = 0, before_at = 0;
+#pragma unroll
+  for (int w = 0; w < kSelWarps; ++w)
+    if (w < warp) before_above += sh.warp_a[w], before_at += sh.warp_b[w];
   for (int i = i0; i < i1; i += 32) {
-    const int x = i + lane < i1 ? score[i + lane] : INT32_MIN;
-    const unsigned up = __ballot_sync(0xffffffffu, i + lane < i1 && x > lo);
-    const unsigned eq = __ballot_sync(0xffffffffu, i + lane < i1 && x == lo);
+    const int x = i + lane < i1 ? score[i + lane] : 0;
+    const unsigned up = __ballot_sync(0xffffffffu, i + lane < i1 && x > cut);
+    const unsigned eq = __ballot_sync(0xffffffffu, i + lane < i1 && x == cut);
     const unsigned below = (1u << lane) - 1;
     const int eq_rank = before_at + __popc(eq & below);
     if ((up >> lane & 1) || ((eq >> lane & 1) && eq_rank < ties))
-      list[begin + before_above + __popc(up & below) + min(eq_rank, ties)] = i + lane;
+      list[begin + before_above + __popc(up & below) + min(eq_rank, ties)] = begin + i + lane;
     before_above += __popc(up);
     before_at += __popc(eq);
   }
@@ -278,13 +443,18 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const PageArgs a) {
     for (int i = tid; i < a.top_k; i += kSelThreads) out[r * row_step + i] = list[i];
 }
 
-cudaError_t launch_select(const PageArgs& a, bool bf16, int /*sms*/, cudaStream_t s) {
+cudaError_t launch_select(const PageArgs& a, bool bf16, int sms, cudaStream_t s) {
   const size_t smem = ((size_t)a.max_blocks + a.top_k) * 4;
-  const dim3 grid((unsigned)query_blocks(a), (unsigned)a.kvh);
-  auto kernel = bf16 ? select_kernel<true> : select_kernel<false>;
-  if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
-  kernel<<<grid, kSelThreads, smem, s>>>(a);
-  return cudaGetLastError();
+  // CTAs that share the pages of a block: to about four per SM, each with two steps of pages
+  const int64_t items = ceil_div(a.N, a.R) * a.kvh;
+  int c = 1;
+  while (c < 16 && items * 2 * c <= 4 * (int64_t)sms && a.max_blocks >= 2 * c * 128) c *= 2;
+  const dim3 grid((unsigned)query_blocks(a), (unsigned)a.kvh, (unsigned)c);
+#define PA_SELECT(HS)                                                          \
+  (bf16 ? launch_clusters(select_kernel<HS, true>, grid, kSelThreads, smem, s, a) \
+        : launch_clusters(select_kernel<HS, false>, grid, kSelThreads, smem, s, a))
+  return a.hs == 64 ? PA_SELECT(64) : a.hs == 128 ? PA_SELECT(128) : PA_SELECT(256);
+#undef PA_SELECT
 }
 
 }  // namespace pa
