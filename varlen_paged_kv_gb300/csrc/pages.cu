@@ -145,100 +145,150 @@ __device__ __forceinline__ int dot4_us(uint32_t u, uint32_t s, int c) {
 }
 
 // what a select CTA holds beside its scores and list
+template <int HS>
 struct SelShared {
-  int plus[256], minus[256];      // the block's summed 12-bit codes
+  static constexpr int kSums = kSelWarps * 2 * HS > kSelBins ? kSelWarps * 2 * HS : kSelBins;
   __align__(16) uint8_t code[2][256];  // 8-bit codes: negative (0), positive (1) parts
-  int hist[kSelBins];
+  union {
+    int hist[kSums];
+    __align__(16) float sums[kSelWarps][2][HS];  // a warp's sums of t and of |t| per channel
+  };
   int warp_a[kSelWarps], warp_b[kSelWarps];
   float warp_f[kSelWarps];
   int found[2];
 };
 
-// The block's codes into sh.code: 12-bit codes of every row in units of the block's largest
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+template <bool BF16>
+__device__ __forceinline__ uint64_t f2_unpack(uint32_t w) {
+  return f2_make(half_of<BF16>(w, 0), half_of<BF16>(w, 1));
+}
+
+// The block's codes into sh.code: 12-bit codes t of every row in units of the block's largest
 // product, summed by sign, rescaled to 8 bits. A thread holds up to eight 16-byte pieces of
 // the rows in registers between finding the largest value and rounding by it, so that up to
-// 8 * 256 / (HS / 8) rows are read from memory once (more are read twice).
+// 8 * 256 / (HS / 8) rows are read from memory once (more are read twice). Arithmetic bounds
+// it on prompts, so it runs on packed pairs: rounding to a whole number is adding and taking
+// off 1.5 * 2^23, and the sums by sign come from those of t and |t| (whole numbers below 2^23,
+// so exact in fp32). Products that are not finite are looked for by a sum of x * 0 and left
+// out in a second form of the same steps.
 template <int HS, bool BF16>
-__device__ void query_codes(const PageArgs& a, int row0, int rows, int g, SelShared& sh) {
+__device__ void query_codes(const PageArgs& a, int row0, int rows, int g, SelShared<HS>& sh) {
   constexpr int CH = HS / 8, GROUPS = kSelThreads / CH, HOLD = 8;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int c = tid % CH * 8, group = tid / CH, total = rows * a.G;
   const uint16_t* q = a.query + (int64_t)row0 * a.q_stride + (int64_t)g * a.G * HS + c;
-  float sc[8];
+  uint64_t sc[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) sc[e] = __ldg(a.scale + g * HS + c + e);
+  for (int e = 0; e < 4; ++e) sc[e] = f2_make(__ldg(a.scale + g * HS + c + 2 * e), __ldg(a.scale + g * HS + c + 2 * e + 1));
   auto load = [&](int r) {
     return __ldg(reinterpret_cast<const uint4*>(q + (int64_t)(r / a.G) * a.q_stride + (int64_t)(r % a.G) * HS));
-  };
-  auto products = [&](const uint4& v, float (&x)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x[e] = __fmul_rn(half_of<BF16>(w[e / 2], e & 1), sc[e]);
-      if (!isfinite(x[e])) x[e] = 0.f;
-    }
   };
   uint4 held[HOLD];
 #pragma unroll
   for (int k = 0; k < HOLD; ++k)
     held[k] = group + k * GROUPS < total ? load(group + k * GROUPS) : make_uint4(0, 0, 0, 0);
   float most = 0.f;
-  auto widest = [&](const uint4& v) {
-    float x[8];
-    products(v, x);
+  uint64_t odd = f2_make(0.f, 0.f);  // NaN once a product is not finite
+  auto widest = [&](const uint4& v, bool filter) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(x[e]));
+    for (int e = 0; e < 4; ++e) {
+      const uint64_t x2 = f2_mul(f2_unpack<BF16>(w[e]), sc[e]);
+      float x0, x1;
+      f2_split(x2, x0, x1);
+      if (filter) {
+        x0 = isfinite(x0) ? x0 : 0.f;
+        x1 = isfinite(x1) ? x1 : 0.f;
+      } else {
+        odd = f2_fma(x2, f2_make(0.f, 0.f), odd);
+      }
+      most = fmax3(most, fabsf(x0), fabsf(x1));
+    }
   };
+  auto every = [&](auto&& f) {  // the thread's pieces
 #pragma unroll
-  for (int k = 0; k < HOLD; ++k) widest(held[k]);
-  for (int r = group + HOLD * GROUPS; r < total; r += GROUPS) widest(load(r));
+    for (int k = 0; k < HOLD; ++k) f(held[k]);
+    for (int r = group + HOLD * GROUPS; r < total; r += GROUPS) f(load(r));
+  };
+  every([&](const uint4& v) { widest(v, false); });
+  float odd0, odd1;
+  f2_split(odd, odd0, odd1);
+  const bool filter = __syncthreads_or(odd0 != 0.f || odd1 != 0.f);  // (NaN compares unequal)
+  if (filter) {
+    most = 0.f;
+    every([&](const uint4& v) { widest(v, true); });
+  }
 #pragma unroll
   for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
   if (lane == 0) sh.warp_f[warp] = most;
-  for (int i = tid; i < HS; i += kSelThreads) sh.plus[i] = sh.minus[i] = 0;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kSelWarps; ++i) most = fmaxf(most, sh.warp_f[i]);
   const float fine = most > 1e-30f ? __fdiv_rn(4095.f, most) : 0.f;
-  int plus[8] = {}, minus[8] = {};
-  auto add = [&](const uint4& v) {
-    float x[8];
-    products(v, x);
+  const uint64_t fine2 = f2_make(fine, fine), magic = f2_make(12582912.f, 12582912.f),
+                 unmagic = f2_make(-12582912.f, -12582912.f);
+  uint64_t sum[4];
+  float mag[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int t = __float2int_rn(__fmul_rn(x[e], fine));
-      plus[e] += max(t, 0);
-      minus[e] += max(-t, 0);
+  for (int e = 0; e < 4; ++e) sum[e] = f2_make(0.f, 0.f), mag[2 * e] = mag[2 * e + 1] = 0.f;
+  auto add = [&](const uint4& v, bool filter) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint64_t x2 = f2_mul(f2_unpack<BF16>(w[e]), sc[e]);
+      float x0, x1;
+      if (filter) {
+        f2_split(x2, x0, x1);
+        x2 = f2_make(isfinite(x0) ? x0 : 0.f, isfinite(x1) ? x1 : 0.f);
+      }
+      const uint64_t t = f2_add(f2_add(f2_mul(x2, fine2), magic), unmagic);
+      f2_split(t, x0, x1);
+      sum[e] = f2_add(sum[e], t);
+      mag[2 * e] += fabsf(x0);
+      mag[2 * e + 1] += fabsf(x1);
     }
   };
+  if (!filter) every([&](const uint4& v) { add(v, false); });
+  else every([&](const uint4& v) { add(v, true); });
+  float tot[8];
 #pragma unroll
-  for (int k = 0; k < HOLD; ++k) add(held[k]);
-  for (int r = group + HOLD * GROUPS; r < total; r += GROUPS) add(load(r));
+  for (int e = 0; e < 4; ++e) f2_split(sum[e], tot[2 * e], tot[2 * e + 1]);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    // (lanes CH apart hold the same channels)
+  for (int o = CH; o < 32; o <<= 1)  // (lanes CH apart hold the same channels)
 #pragma unroll
-    for (int o = CH; o < 32; o <<= 1) {
-      plus[e] += __shfl_xor_sync(0xffffffffu, plus[e], o);
-      minus[e] += __shfl_xor_sync(0xffffffffu, minus[e], o);
+    for (int e = 0; e < 8; ++e) {
+      tot[e] += __shfl_xor_sync(0xffffffffu, tot[e], o);
+      mag[e] += __shfl_xor_sync(0xffffffffu, mag[e], o);
     }
-    if (lane < CH && group < total) {
-      atomicAdd(&sh.plus[c + e], plus[e]);
-      atomicAdd(&sh.minus[c + e], minus[e]);
+  if (lane < CH) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 4) {
+      *reinterpret_cast<float4*>(&sh.sums[warp][0][c + e]) = make_float4(tot[e], tot[e + 1], tot[e + 2], tot[e + 3]);
+      *reinterpret_cast<float4*>(&sh.sums[warp][1][c + e]) = make_float4(mag[e], mag[e + 1], mag[e + 2], mag[e + 3]);
     }
   }
   __syncthreads();
-  const int p = tid < HS ? sh.plus[tid] : 0, m = tid < HS ? sh.minus[tid] : 0;
-  int big = __reduce_max_sync(0xffffffffu, max(p, m));
+  float t = 0.f, m = 0.f;
+  if (tid < HS) {
+#pragma unroll
+    for (int w = 0; w < kSelWarps; ++w) t += sh.sums[w][0][tid], m += sh.sums[w][1][tid];
+  }
+  const int plus = (int)((m + t) * 0.5f), minus = (int)((m - t) * 0.5f);
+  int big = __reduce_max_sync(0xffffffffu, max(plus, minus));
   if (lane == 0) sh.warp_a[warp] = big;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kSelWarps; ++i) big = max(big, sh.warp_a[i]);
   big = max(big, 1);
   if (tid < HS) {
-    // (510 p + big) / (2 big): 510 * 1024 rows * 4095 stays below 2^31
-    sh.code[1][tid] = (uint8_t)((uint32_t)(510 * p + big) / (uint32_t)(2 * big));
-    sh.code[0][tid] = (uint8_t)((uint32_t)(510 * m + big) / (uint32_t)(2 * big));
+    // (510 plus + big) / (2 big): 510 * 1024 rows * 4095 stays below 2^31
+    sh.code[1][tid] = (uint8_t)((uint32_t)(510 * plus + big) / (uint32_t)(2 * big));
+    sh.code[0][tid] = (uint8_t)((uint32_t)(510 * minus + big) / (uint32_t)(2 * big));
   }
   __syncthreads();
 }
@@ -248,7 +298,7 @@ __device__ void query_codes(const PageArgs& a, int row0, int rows, int g, SelSha
 // kSelLoads * 32 / CH pages at once; the pieces' sums meet by a transposing reduction, so that
 // every lane ends with one page's score (or shares one).
 template <int HS, typename Put>
-__device__ void score_pages(const PageArgs& a, const int* table, int g, int i0, int i1, const SelShared& sh, Put put) {
+__device__ void score_pages(const PageArgs& a, const int* table, int g, int i0, int i1, const SelShared<HS>& sh, Put put) {
   constexpr int CH = HS / 8;             // pieces of a page: half minimum, half maximum codes
   constexpr int PER = 32 / CH;           // pages per load of the warp
   constexpr int BATCH = kSelLoads * PER;  // pages per step
@@ -259,9 +309,11 @@ __device__ void score_pages(const PageArgs& a, const int* table, int g, int i0, 
   const int8_t* base = a.bounds + (int64_t)g * 2 * HS + piece * 16;
   const int64_t page_bytes = (int64_t)a.kvh * 2 * HS;
   bool bad = false;
+  auto entry = [&](int i) { return lane < BATCH && i + lane < i1 ? __ldg(table + i + lane) : -1; };
+  int next = entry(i0 + warp * BATCH);
   for (int i = i0 + warp * BATCH; i < i1; i += kSelWarps * BATCH) {
-    int phys = i + lane < i1 && lane < BATCH ? table[i + lane] : -1;
-    if (phys >= a.num_blocks) phys = -1;
+    const int phys = next < a.num_blocks ? next : -1;
+    next = entry(i + kSelWarps * BATCH);  // a step ahead
     bad |= phys < 0 && lane < BATCH && i + lane < i1;
     uint4 v[kSelLoads];
 #pragma unroll
@@ -313,9 +365,9 @@ __device__ void score_pages(const PageArgs& a, const int* table, int g, int i0, 
 // per bit). Bytes bound the scoring of long histories (2 HS bytes a page and head); short ones
 // are a chain of latencies.
 template <int HS, bool BF16>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const PageArgs a) {
+__global__ void __launch_bounds__(kSelThreads, 3) select_kernel(const PageArgs a) {
   extern __shared__ int score[];  // [max_blocks], then the list [top_k]
-  __shared__ SelShared sh;
+  __shared__ SelShared<HS> sh;
   int* list = score + a.max_blocks;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = blockIdx.y, rank = blockIdx.z, C = gridDim.z;
