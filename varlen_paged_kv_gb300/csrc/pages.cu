@@ -132,8 +132,6 @@ cudaError_t launch_bounds(const PageArgs& a, bool bf16, cudaStream_t s) {
 
 // ---- selection -----------------------------------------------------------------------------
 
-constexpr int kSelThreads = 256;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelLoads = 8;     // 16-byte loads in flight per lane while scoring
 constexpr int kSelBins = 2048;   // of the histograms that find the threshold
 
@@ -145,16 +143,17 @@ __device__ __forceinline__ int dot4_us(uint32_t u, uint32_t s, int c) {
 }
 
 // what a select CTA holds beside its scores and list
-template <int HS>
+template <int HS, int T>
 struct SelShared {
-  static constexpr int kSums = kSelWarps * 2 * HS > kSelBins ? kSelWarps * 2 * HS : kSelBins;
+  static constexpr int kWarps = T / 32;
+  static constexpr int kSums = kWarps * 2 * HS > kSelBins ? kWarps * 2 * HS : kSelBins;
   __align__(16) uint8_t code[2][256];  // 8-bit codes: negative (0), positive (1) parts
   union {
     int hist[kSums];
-    __align__(16) float sums[kSelWarps][2][HS];  // a warp's sums of t and of |t| per channel
+    __align__(16) float sums[kWarps][2][HS];  // a warp's sums of t and of |t| per channel
   };
-  int warp_a[kSelWarps], warp_b[kSelWarps];
-  float warp_f[kSelWarps];
+  int warp_a[kWarps], warp_b[kWarps];
+  float warp_f[kWarps];
   int found[2];
 };
 
@@ -169,16 +168,16 @@ __device__ __forceinline__ uint64_t f2_unpack(uint32_t w) {
 }
 
 // The block's codes into sh.code: 12-bit codes t of every row in units of the block's largest
-// product, summed by sign, rescaled to 8 bits. A thread holds up to eight 16-byte pieces of
+// product, summed by sign, rescaled to 8 bits. A thread holds up to HOLD 16-byte pieces of
 // the rows in registers between finding the largest value and rounding by it, so that up to
-// 8 * 256 / (HS / 8) rows are read from memory once (more are read twice). Arithmetic bounds
+// HOLD * T / (HS / 8) rows are read from memory once (more are read twice). Arithmetic bounds
 // it on prompts, so it runs on packed pairs: rounding to a whole number is adding and taking
 // off 1.5 * 2^23, and the sums by sign come from those of t and |t| (whole numbers below 2^23,
 // so exact in fp32). Products that are not finite are looked for by a sum of x * 0 and left
 // out in a second form of the same steps.
-template <int HS, bool BF16>
-__device__ void query_codes(const PageArgs& a, int row0, int rows, int g, SelShared<HS>& sh) {
-  constexpr int CH = HS / 8, GROUPS = kSelThreads / CH, HOLD = 8;
+template <int HS, bool BF16, int T>
+__device__ void query_codes(const PageArgs& a, int row0, int rows, int g, SelShared<HS, T>& sh) {
+  constexpr int CH = HS / 8, GROUPS = T / CH, HOLD = T == 256 ? 8 : 4, WARPS = T / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int c = tid % CH * 8, group = tid / CH, total = rows * a.G;
   const uint16_t* q = a.query + (int64_t)row0 * a.q_stride + (int64_t)g * a.G * HS + c;
@@ -228,7 +227,7 @@ __device__ void query_codes(const PageArgs& a, int row0, int rows, int g, SelSha
   if (lane == 0) sh.warp_f[warp] = most;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kSelWarps; ++i) most = fmaxf(most, sh.warp_f[i]);
+  for (int i = 0; i < WARPS; ++i) most = fmaxf(most, sh.warp_f[i]);
   const float fine = most > 1e-30f ? __fdiv_rn(4095.f, most) : 0.f;
   const uint64_t fine2 = f2_make(fine, fine), magic = f2_make(12582912.f, 12582912.f),
                  unmagic = f2_make(-12582912.f, -12582912.f);
@@ -273,22 +272,30 @@ __device__ void query_codes(const PageArgs& a, int row0, int rows, int g, SelSha
     }
   }
   __syncthreads();
-  float t = 0.f, m = 0.f;
-  if (tid < HS) {
+  constexpr int MINE = (HS + T - 1) / T;  // channels of a thread
+  int plus[MINE], minus[MINE], big = 0;
 #pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) t += sh.sums[w][0][tid], m += sh.sums[w][1][tid];
+  for (int i = 0; i < MINE; ++i) {
+    float t = 0.f, m = 0.f;
+    if (tid + i * T < HS) {
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) t += sh.sums[w][0][tid + i * T], m += sh.sums[w][1][tid + i * T];
+    }
+    plus[i] = (int)((m + t) * 0.5f), minus[i] = (int)((m - t) * 0.5f);
+    big = max(big, max(plus[i], minus[i]));
   }
-  const int plus = (int)((m + t) * 0.5f), minus = (int)((m - t) * 0.5f);
-  int big = __reduce_max_sync(0xffffffffu, max(plus, minus));
+  big = __reduce_max_sync(0xffffffffu, big);
   if (lane == 0) sh.warp_a[warp] = big;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kSelWarps; ++i) big = max(big, sh.warp_a[i]);
+  for (int i = 0; i < WARPS; ++i) big = max(big, sh.warp_a[i]);
   big = max(big, 1);
-  if (tid < HS) {
+#pragma unroll
+  for (int i = 0; i < MINE; ++i) {
+    if (tid + i * T >= HS) break;
     // (510 plus + big) / (2 big): 510 * 1024 rows * 4095 stays below 2^31
-    sh.code[1][tid] = (uint8_t)((uint32_t)(510 * plus + big) / (uint32_t)(2 * big));
-    sh.code[0][tid] = (uint8_t)((uint32_t)(510 * minus + big) / (uint32_t)(2 * big));
+    sh.code[1][tid + i * T] = (uint8_t)((uint32_t)(510 * plus[i] + big) / (uint32_t)(2 * big));
+    sh.code[0][tid + i * T] = (uint8_t)((uint32_t)(510 * minus[i] + big) / (uint32_t)(2 * big));
   }
   __syncthreads();
 }
@@ -297,11 +304,12 @@ __device__ void query_codes(const PageArgs& a, int row0, int rows, int g, SelSha
 // 16-byte pieces: a lane keeps the query codes of its own piece in registers and takes it from
 // kSelLoads * 32 / CH pages at once; the pieces' sums meet by a transposing reduction, so that
 // every lane ends with one page's score (or shares one).
-template <int HS, typename Put>
-__device__ void score_pages(const PageArgs& a, const int* table, int g, int i0, int i1, const SelShared<HS>& sh, Put put) {
+template <int HS, int T, typename Put>
+__device__ void score_pages(const PageArgs& a, const int* table, int g, int i0, int i1, const SelShared<HS, T>& sh, Put put) {
   constexpr int CH = HS / 8;             // pieces of a page: half minimum, half maximum codes
   constexpr int PER = 32 / CH;           // pages per load of the warp
   constexpr int BATCH = kSelLoads * PER;  // pages per step
+  constexpr int WARPS = T / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int piece = lane % CH, sub = lane / CH;
   const bool upper = piece >= CH / 2;
@@ -311,9 +319,9 @@ __device__ void score_pages(const PageArgs& a, const int* table, int g, int i0, 
   bool bad = false;
   auto entry = [&](int i) { return lane < BATCH && i + lane < i1 ? __ldg(table + i + lane) : -1; };
   int next = entry(i0 + warp * BATCH);
-  for (int i = i0 + warp * BATCH; i < i1; i += kSelWarps * BATCH) {
+  for (int i = i0 + warp * BATCH; i < i1; i += WARPS * BATCH) {
     const int phys = next < a.num_blocks ? next : -1;
-    next = entry(i + kSelWarps * BATCH);  // a step ahead
+    next = entry(i + WARPS * BATCH);  // a step ahead
     bad |= phys < 0 && lane < BATCH && i + lane < i1;
     uint4 v[kSelLoads];
 #pragma unroll
@@ -364,10 +372,11 @@ __device__ void score_pages(const PageArgs& a, const int* table, int g, int i0, 
 // want-th falls in until bins are single scores (two or three passes over the scores, not one
 // per bit). Bytes bound the scoring of long histories (2 HS bytes a page and head); short ones
 // are a chain of latencies.
-template <int HS, bool BF16>
-__global__ void __launch_bounds__(kSelThreads, 3) select_kernel(const PageArgs a) {
+template <int HS, bool BF16, int T>
+__global__ void __launch_bounds__(T, T == 256 ? 3 : 1024 / T) select_kernel(const PageArgs a) {
+  constexpr int WARPS = T / 32;
   extern __shared__ int score[];  // [max_blocks], then the list [top_k]
-  __shared__ SelShared<HS> sh;
+  __shared__ SelShared<HS, T> sh;
   int* list = score + a.max_blocks;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = blockIdx.y, rank = blockIdx.z, C = gridDim.z;
@@ -389,20 +398,22 @@ __global__ void __launch_bounds__(kSelThreads, 3) select_kernel(const PageArgs a
   const int64_t row_step = (int64_t)a.kvh * a.top_k;
   if (want >= end - begin) {  // every page (all CTAs of a cluster agree)
     if (rank == 0)
-      for (int r = 0; r < rows; ++r)
-        for (int i = tid; i < a.top_k; i += kSelThreads) out[r * row_step + i] = i < n ? i : -1;
+      for (int i = tid; i < rows * a.top_k; i += T) {
+        const int k = i % a.top_k;
+        out[i / a.top_k * row_step + k] = k < n ? k : -1;
+      }
     return;
   }
-  query_codes<HS, BF16>(a, s.c0 + j0, rows, g, sh);
+  query_codes<HS, BF16, T>(a, s.c0 + j0, rows, g, sh);
   const int* table = a.table + (int64_t)b * a.max_blocks;
   const int count = end - begin;
   if (C == 1) {
-    score_pages<HS>(a, table, g, begin, end, sh, [&](int page, int d) { score[page - begin] = d; });
+    score_pages<HS, T>(a, table, g, begin, end, sh, [&](int page, int d) { score[page - begin] = d; });
     __syncthreads();
   } else {
     cluster_sync();  // (the first CTA runs before it is written to)
     const uint32_t first = cluster_addr(score, 0);
-    score_pages<HS>(a, table, g, begin + (int)((int64_t)count * rank / C), begin + (int)((int64_t)count * (rank + 1) / C),
+    score_pages<HS, T>(a, table, g, begin + (int)((int64_t)count * rank / C), begin + (int)((int64_t)count * (rank + 1) / C),
                     sh, [&](int page, int d) {
                       asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(first + (uint32_t)(page - begin) * 4), "r"(d)
                                    : "memory");
@@ -412,26 +423,26 @@ __global__ void __launch_bounds__(kSelThreads, 3) select_kernel(const PageArgs a
   }
   // ---- the threshold: scores above `cut` are taken, and the first `ties` of those at it ----
   int top = INT32_MIN, low = INT32_MAX;
-  for (int i = tid; i < count; i += kSelThreads) top = max(top, score[i]), low = min(low, score[i]);
+  for (int i = tid; i < count; i += T) top = max(top, score[i]), low = min(low, score[i]);
   top = __reduce_max_sync(0xffffffffu, top);
   low = __reduce_min_sync(0xffffffffu, low);
   if (lane == 0) sh.warp_a[warp] = top, sh.warp_b[warp] = low;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kSelWarps; ++w) top = max(top, sh.warp_a[w]), low = min(low, sh.warp_b[w]);
+  for (int w = 0; w < WARPS; ++w) top = max(top, sh.warp_a[w]), low = min(low, sh.warp_b[w]);
   // distances top - score from `from` on, below `from + span`, in bins of 2^shift
   uint32_t from = 0, span = (uint32_t)(top - low) + 1;
   int ties = want;  // still to be taken among them
   for (;;) {
     const int bits = 32 - __clz(span - 1 | 1), shift = max(bits - 11, 0);
-    for (int i = tid; i < kSelBins; i += kSelThreads) sh.hist[i] = 0;
+    for (int i = tid; i < kSelBins; i += T) sh.hist[i] = 0;
     __syncthreads();
-    for (int i = tid; i < count; i += kSelThreads) {
+    for (int i = tid; i < count; i += T) {
       const uint32_t x = (uint32_t)(top - score[i]) - from;
       if (x < span) atomicAdd(&sh.hist[x >> shift], 1);
     }
     __syncthreads();
-    constexpr int MINE = kSelBins / kSelThreads;
+    constexpr int MINE = kSelBins / T;
     int h[MINE], sum = 0;
 #pragma unroll
     for (int k = 0; k < MINE; ++k) h[k] = sh.hist[tid * MINE + k], sum += h[k];
@@ -445,7 +456,7 @@ __global__ void __launch_bounds__(kSelThreads, 3) select_kernel(const PageArgs a
     __syncthreads();
     int before = inc - sum;
 #pragma unroll
-    for (int w = 0; w < kSelWarps; ++w)
+    for (int w = 0; w < WARPS; ++w)
       if (w < warp) before += sh.warp_a[w];
     if (before < ties && ties <= before + sum) {  // the want-th falls in one of this thread's bins
 #pragma unroll
@@ -464,7 +475,7 @@ __global__ void __launch_bounds__(kSelThreads, 3) select_kernel(const PageArgs a
   }
   const int cut = top - (int)from;
   // ---- the taken pages in order, each warp a contiguous part ----
-  const int per = (int)align_up(ceil_div(count, kSelWarps), 32);
+  const int per = (int)align_up(ceil_div(count, WARPS), 32);
   const int i0 = min(count, warp * per), i1 = min(count, i0 + per);
   int above = 0, at = 0;
   for (int i = i0 + lane; i < i1; i += 32) above += score[i] > cut, at += score[i] == cut;
@@ -475,7 +486,7 @@ __global__ void __launch_bounds__(kSelThreads, 3) select_kernel(const PageArgs a
   __syncthreads();
   int before_above = 0, before_at = 0;
 #pragma unroll
-  for (int w = 0; w < kSelWarps; ++w)
+  for (int w = 0; w < WARPS; ++w)
     if (w < warp) before_above += sh.warp_a[w], before_at += sh.warp_b[w];
   for (int i = i0; i < i1; i += 32) {
     const int x = i + lane < i1 ? score[i + lane] : 0;
@@ -488,23 +499,32 @@ __global__ void __launch_bounds__(kSelThreads, 3) select_kernel(const PageArgs a
     before_above += __popc(up);
     before_at += __popc(eq);
   }
-  for (int i = tid; i < begin; i += kSelThreads) list[i] = i;
-  for (int i = end + tid; i < n; i += kSelThreads) list[begin + want + i - end] = i;
+  for (int i = tid; i < begin; i += T) list[i] = i;
+  for (int i = end + tid; i < n; i += T) list[begin + want + i - end] = i;
   __syncthreads();
-  for (int r = 0; r < rows; ++r)
-    for (int i = tid; i < a.top_k; i += kSelThreads) out[r * row_step + i] = list[i];
+  for (int i = tid; i < rows * a.top_k; i += T) out[i / a.top_k * row_step + i % a.top_k] = list[i % a.top_k];
+}
+
+template <int HS, bool BF16>
+static cudaError_t launch_select_t(const PageArgs& a, int sms, cudaStream_t s) {
+  const size_t smem = ((size_t)a.max_blocks + a.top_k) * 4;
+  const int64_t items = ceil_div(a.N, a.R) * a.kvh;
+  // CTAs that share the pages of a block: as many as run at once, each with a step of pages
+  int c = 1;
+  while (c < 16 && items * 2 * c <= 2 * (int64_t)sms && a.max_blocks >= 2 * c * 128) c *= 2;
+  const dim3 grid((unsigned)query_blocks(a), (unsigned)a.kvh, (unsigned)c);
+  // Threads by the longest history the table can hold. Short ones are chains of latencies that
+  // more CTAs per SM overlap (tables of 544 pages, 4 prompts of 2048 rows: 58 us with 128
+  // threads, 67 with 256, 86 with 512; 65 pages, 64 decode rows: 8.2, 11.0, 18.4 us), long ones
+  // a stream of bounds and a last CTA's passes over the scores (8193 pages, 8 decode rows: 63,
+  // 41, 33 us; 1025 pages, 32 drafts of 4: 18.4, 15.4, 16.1 us).
+  if (a.max_blocks <= 768) return launch_clusters(select_kernel<HS, BF16, 128>, grid, 128, smem, s, a);
+  if (a.max_blocks <= 4096) return launch_clusters(select_kernel<HS, BF16, 256>, grid, 256, smem, s, a);
+  return launch_clusters(select_kernel<HS, BF16, 512>, grid, 512, smem, s, a);
 }
 
 cudaError_t launch_select(const PageArgs& a, bool bf16, int sms, cudaStream_t s) {
-  const size_t smem = ((size_t)a.max_blocks + a.top_k) * 4;
-  // CTAs that share the pages of a block: to about four per SM, each with two steps of pages
-  const int64_t items = ceil_div(a.N, a.R) * a.kvh;
-  int c = 1;
-  while (c < 16 && items * 2 * c <= 4 * (int64_t)sms && a.max_blocks >= 2 * c * 128) c *= 2;
-  const dim3 grid((unsigned)query_blocks(a), (unsigned)a.kvh, (unsigned)c);
-#define PA_SELECT(HS)                                                          \
-  (bf16 ? launch_clusters(select_kernel<HS, true>, grid, kSelThreads, smem, s, a) \
-        : launch_clusters(select_kernel<HS, false>, grid, kSelThreads, smem, s, a))
+#define PA_SELECT(HS) (bf16 ? launch_select_t<HS, true>(a, sms, s) : launch_select_t<HS, false>(a, sms, s))
   return a.hs == 64 ? PA_SELECT(64) : a.hs == 128 ? PA_SELECT(128) : PA_SELECT(256);
 #undef PA_SELECT
 }

@@ -396,9 +396,10 @@ __global__ void __launch_bounds__(kRowsThreads, HS == 256 ? 1 : 2)
 // The up to 128 rows r = j * G + head of a block are one M = 128 tile (TMA lays them out so
 // from a (channel, head, row) view of the query; rows past the item are computed and not
 // stored). Warp 0 gathers K and V tiles (two stages), warp 1 issues S_t = Q K_t^T into one of
-// two S buffers in TMEM and O += P_t V_t, warps 2 .. 5 are the softmax: a thread owns a row,
-// reads its 64 scores, writes P over them (fp16, or bf16 hi and lo terms) and rescales O in
-// TMEM when its maximum grew by more than 2^8. S_{t+1} is issued before P_t is waited for, so
+// two S buffers in TMEM and O += P_t V_t, warps 2 .. 9 are the softmax: two threads share a
+// row (TMEM lets a warp at 32 of the 128 lanes), read 32 of its 64 scores each, exchange their
+// maxima through shared memory, write P over the scores (fp16, or bf16 hi and lo terms) and
+// rescale O in TMEM when the maximum grew by more than 2^8. S_{t+1} is issued before P_t is waited for, so
 // the tensor core works during the softmax; two CTAs share an SM (one with 256-wide heads)
 // and fill each other's gaps, the prologue included.
 template <int HS>
@@ -412,7 +413,8 @@ struct TileSmem {
   static constexpr int kAbort = kBars + kNumBars * 8;               // abort flag, error word, TMEM address
   static constexpr int kItem = (kAbort + 12 + 15) / 16 * 16;
   static constexpr int kMl = kItem + 32;                            // float [2][128]: m and l of the rows
-  static constexpr int kList = kMl + 2 * 128 * 4;
+  static constexpr int kX = kMl + 2 * 128 * 4;                      // float [2][128][2]: maxima and sums of half rows
+  static constexpr int kList = kX + 2 * 128 * 2 * 4;
   static constexpr uint32_t kTmem = HS == 256 ? 512 : 256;          // S, S, O at columns 0, 64, 128
   static_assert(128 * HS * 4 <= 2 * kStages * kTileBytes, "the cluster's partial result lies over the ring");
   // At least a third of an SM's shared memory, so that no more CTAs share an SM than find TMEM
@@ -422,7 +424,7 @@ struct TileSmem {
     return need < 80 * 1024 ? 80 * 1024 : need;
   }
 };
-constexpr int kTileThreads = 192;
+constexpr int kTileThreads = 320;
 
 template <int HS, bool BF16>
 __global__ void __launch_bounds__(kTileThreads, HS == 256 ? 1 : 2)
@@ -448,6 +450,7 @@ __global__ void __launch_bounds__(kTileThreads, HS == 256 ? 1 : 2)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kAbort + 8);
   SparseItem* item_s = reinterpret_cast<SparseItem*>(smem + L::kItem);
   float* ml = reinterpret_cast<float*>(smem + L::kMl);
+  float2* half = reinterpret_cast<float2*>(smem + L::kX);  // [2][128]
   int2* list = reinterpret_cast<int2*>(smem + L::kList);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = blockIdx.y, u = blockIdx.x / chunks, sub = blockIdx.x % chunks * sub_rows;
@@ -462,7 +465,7 @@ __global__ void __launch_bounds__(kTileThreads, HS == 256 ? 1 : 2)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
+      mbar_init(&p_full[i], 256);
     }
     mbar_init(o_done, 1);
     *abort = 0;
@@ -488,7 +491,8 @@ __global__ void __launch_bounds__(kTileThreads, HS == 256 ? 1 : 2)
   const int tiles = (it.v_end + kSpTile - 1) / kSpTile;
   const int t0 = (int)((int64_t)tiles * rank / C), n = (int)((int64_t)tiles * (rank + 1) / C) - t0;
 
-  const int row = (warp & 3) * 32 + lane;  // (softmax warps 2 .. 5) the thread's TMEM lane
+  const int row = (warp & 3) * 32 + lane;  // (softmax warps) the thread's TMEM lane
+  const int side = warp >= 6;              // and its half of the row's columns
   const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
   const int j = row / a.G;                  // its row in the item
   const bool live = warp >= 2 && j < it.rows && row < sub_rows * a.G;
@@ -595,25 +599,27 @@ __global__ void __launch_bounds__(kTileThreads, HS == 256 ? 1 : 2)
     }
   } else {
     // ---- softmax ----
+    constexpr int COLS = kSpTile / 2, OCOLS = HS / 2;
     const float c = a.scale_log2;
     const float none = c > 0.f ? -INFINITY : INFINITY;  // a score whose product with c is -inf
     const int lim = it.pos0 + min(j, it.rows - 1);
     const bool any_live = __any_sync(0xffffffffu, live);
+    const uint32_t o_tmem = tmem + lane_off + kO + side * OCOLS;
+    const int bar = 1 + (warp & 3);  // of the two warps of a lane quarter
     for (int t = 0; t < n; ++t) {
+      mbar_wait(&s_full[t & 1], (t >> 1) & 1, abort, err);
       if (!any_live) {  // rows past the item: whatever their P holds stays in their rows of O
-        mbar_wait(&s_full[t & 1], (t >> 1) & 1, abort, err);
         mbar_arrive(&p_full[t & 1]);
         continue;
       }
-      const uint32_t st = tmem + lane_off + (t & 1) * kSpTile;
-      mbar_wait(&s_full[t & 1], (t >> 1) & 1, abort, err);
       tc_fence_after();
-      uint32_t r[kSpTile];
-      tmem_ld_x64(st, r);
-      const int v0 = (t0 + t) * kSpTile;
-      if (v0 + kSpTile > it.v_mask) {
+      const uint32_t st = tmem + lane_off + (t & 1) * kSpTile;
+      uint32_t r[COLS];
+      tmem_ld_x32(st + side * COLS, r);
+      const int v0 = (t0 + t) * kSpTile + side * COLS;
+      if (v0 + COLS > it.v_mask) {
 #pragma unroll
-        for (int k = 0; k < kSpTile / 16; ++k) {  // (16 keys never straddle a page)
+        for (int k = 0; k < COLS / 16; ++k) {  // (16 keys never straddle a page)
           const int v = v0 + 16 * k, i = v / a.bs;
           const int base = i < it.n_list ? list[i].x * a.bs + (v - i * a.bs) : INT32_MAX - 16;
 #pragma unroll
@@ -624,19 +630,23 @@ __global__ void __launch_bounds__(kTileThreads, HS == 256 ? 1 : 2)
       float mc[4] = {none, none, none, none};
       if (c > 0.f) {
 #pragma unroll
-        for (int e = 0; e < kSpTile; e += 8)
+        for (int e = 0; e < COLS; e += 8)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             mc[k] = fmax3(mc[k], __uint_as_float(r[e + 2 * k]), __uint_as_float(r[e + 2 * k + 1]));
       } else {
 #pragma unroll
-        for (int e = 0; e < kSpTile; e += 8)
+        for (int e = 0; e < COLS; e += 8)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             mc[k] = fmin3(mc[k], __uint_as_float(r[e + 2 * k]), __uint_as_float(r[e + 2 * k + 1]));
       }
       const float best = c > 0.f ? fmax3(fmaxf(mc[0], mc[1]), mc[2], mc[3]) : fmin3(fminf(mc[0], mc[1]), mc[2], mc[3]);
-      const float m_new = fmaxf(m_used, best * c);
+      float2* hx = half + (t & 1) * 128 + row;
+      (side ? hx->y : hx->x) = best * c;
+      named_bar_sync(bar, 64);
+      const float2 both = *hx;
+      const float m_new = fmaxf(m_used, fmaxf(both.x, both.y));
       const bool grow = __any_sync(0xffffffffu, live && m_new > m_used + 8.f);
       float alpha = 1.f;
       if (grow) {
@@ -645,34 +655,37 @@ __global__ void __launch_bounds__(kTileThreads, HS == 256 ? 1 : 2)
         l *= alpha;
       }
       const float neg_m = m_used == -INFINITY ? 0.f : -m_used;  // (no key yet: every weight is 0)
-      float lc[2] = {0.f, 0.f};
+      const uint64_t c2 = f2_make(c, c), nm2 = f2_make(neg_m, neg_m);
+      uint64_t lsum = f2_make(0.f, 0.f);
 #pragma unroll
-      for (int k = 0; k < kSpTile / 16; ++k) {
+      for (int k = 0; k < COLS / 16; ++k) {
         uint32_t* q = r + k * 16;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float p0 = fast_exp2(fmaf(__uint_as_float(q[2 * e]), c, neg_m));
-          const float p1 = fast_exp2(fmaf(__uint_as_float(q[2 * e + 1]), c, neg_m));
-          lc[0] += p0;
-          lc[1] += p1;
+          float x0, x1;
+          f2_split(f2_fma(f2_make(__uint_as_float(q[2 * e]), __uint_as_float(q[2 * e + 1])), c2, nm2), x0, x1);
+          const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+          lsum = f2_add(lsum, f2_make(p0, p1));
           if constexpr (BF16) split_bf16x2(p0, p1, q[2 * e], q[2 * e + 1]);
           else q[2 * e] = pack2<false>(p0, p1);
         }
-        tmem_st_x8_nowait(st + p_col(k), q[0], q[2], q[4], q[6], q[8], q[10], q[12], q[14]);
-        if constexpr (BF16)
-          tmem_st_x8_nowait(st + p_col(k) + 16, q[1], q[3], q[5], q[7], q[9], q[11], q[13], q[15]);
+        const uint32_t p = st + p_col(side * (COLS / 16) + k);
+        tmem_st_x8_nowait(p, q[0], q[2], q[4], q[6], q[8], q[10], q[12], q[14]);
+        if constexpr (BF16) tmem_st_x8_nowait(p + 16, q[1], q[3], q[5], q[7], q[9], q[11], q[13], q[15]);
       }
-      l += lc[0] + lc[1];
+      float s0, s1;
+      f2_split(lsum, s0, s1);
+      l += s0 + s1;
       if (t > 0 && grow) {  // O holds P_0 V .. P_{t-1} V once the last product is done
         mbar_wait(o_done, (t - 1) & 1, abort, err);
         tc_fence_after();
 #pragma unroll 1
-        for (int cc = 0; cc < HS; cc += 32) {
+        for (int cc = 0; cc < OCOLS; cc += 32) {
           uint32_t ov[32];
-          tmem_ld_x32(tmem + lane_off + kO + cc, ov);
+          tmem_ld_x32(o_tmem + cc, ov);
 #pragma unroll
           for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-          tmem_st_x32(tmem + lane_off + kO + cc, ov);
+          tmem_st_x32(o_tmem + cc, ov);
         }
       }
       tmem_wait_st();
@@ -680,10 +693,17 @@ __global__ void __launch_bounds__(kTileThreads, HS == 256 ? 1 : 2)
       mbar_arrive(&p_full[t & 1]);
     }
     if (n > 0) {
+      // (the loop knows of the product before the last but one only: a wait for the last by its
+      // parity alone could be let through by that one)
+      if (n > 1) mbar_wait(o_done, (n - 2) & 1, abort, err);
       mbar_wait(o_done, (n - 1) & 1, abort, err);
       tc_fence_after();
     }
-    if (C > 1) ml[row] = m_used, ml[128 + row] = l;
+    // the row's sum from its halves (the two warps have the same maximum)
+    (side ? half[row].y : half[row].x) = l;
+    named_bar_sync(bar, 64);
+    l = half[row].x + half[row].y;
+    if (C > 1 && side == 0) ml[row] = m_used, ml[128 + row] = l;
   }
 
   uint16_t* out = static_cast<uint16_t*>(a.output);
@@ -691,10 +711,10 @@ __global__ void __launch_bounds__(kTileThreads, HS == 256 ? 1 : 2)
     if (warp >= 2) {
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const int64_t at = (int64_t)(it.row0 + j) * a.nh + g * a.G + row % a.G;
-      if (live && a.lse)
+      if (live && a.lse && side == 0)
         a.lse[at] = m_used == -INFINITY ? -INFINITY : (m_used + fast_log2(l)) * 0.69314718055994531f;
 #pragma unroll 1
-      for (int cc = 0; cc < HS; cc += 32) {
+      for (int cc = side * (HS / 2); cc < (side + 1) * (HS / 2); cc += 32) {
         uint32_t ov[32];
         if (n > 0) {
           tmem_ld_x32(tmem + lane_off + kO + cc, ov);
@@ -728,11 +748,11 @@ __global__ void __launch_bounds__(kTileThreads, HS == 256 ? 1 : 2)
         if (m != -INFINITY) S += fast_exp2(m - M) * ld_cluster(cluster_addr(ml + 128 + row, k));
       }
       const float f = m_used == -INFINITY ? 0.f : fast_exp2(m_used - M) / S;
-      if (rank == 0 && live && a.lse)
+      if (rank == 0 && live && a.lse && side == 0)
         a.lse[(int64_t)(it.row0 + j) * a.nh + g * a.G + row % a.G] =
             M == -INFINITY ? -INFINITY : (M + fast_log2(S)) * 0.69314718055994531f;
 #pragma unroll 1
-      for (int cc = 0; cc < HS; cc += 32) {
+      for (int cc = side * (HS / 2); cc < (side + 1) * (HS / 2); cc += 32) {
         uint32_t ov[32];
         if (n > 0) tmem_ld_x32(tmem + lane_off + kO + cc, ov);
 #pragma unroll
