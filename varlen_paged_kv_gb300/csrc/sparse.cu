@@ -408,8 +408,8 @@ struct TileSmem {
   static constexpr int kQBytes = 128 * HS * 2;
   static constexpr int kTileBytes = kSpTile * HS * 2;
   static constexpr int kRing = kQBytes;                             // K tiles, then V tiles
-  static constexpr int kBars = kRing + 2 * kStages * kTileBytes;    // 1 + 4 * kStages + 2 + 2 + 1 barriers
-  static constexpr int kNumBars = 1 + 4 * kStages + 5;
+  static constexpr int kBars = kRing + 2 * kStages * kTileBytes;    // 1 + 4 * kStages + 3 * 2 barriers
+  static constexpr int kNumBars = 1 + 4 * kStages + 6;
   static constexpr int kAbort = kBars + kNumBars * 8;               // abort flag, error word, TMEM address
   static constexpr int kItem = (kAbort + 12 + 15) / 16 * 16;
   static constexpr int kMl = kItem + 32;                            // float [2][128]: m and l of the rows
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(kTileThreads, HS == 256 ? 1 : 2)
   uint64_t* v_empty = v_full + L::kStages;
   uint64_t* s_full = v_empty + L::kStages;  // [2]
   uint64_t* p_full = s_full + 2;            // [2]
-  uint64_t* o_done = p_full + 2;
+  uint64_t* o_done = p_full + 2;            // [2]
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kAbort);
   uint32_t* err = reinterpret_cast<uint32_t*>(smem + L::kAbort + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kAbort + 8);
@@ -466,8 +466,8 @@ __global__ void __launch_bounds__(kTileThreads, HS == 256 ? 1 : 2)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 256);
+      mbar_init(&o_done[i], 1);
     }
-    mbar_init(o_done, 1);
     *abort = 0;
     *err = 0;
     fence_mbar_init();
@@ -508,33 +508,29 @@ __global__ void __launch_bounds__(kTileThreads, HS == 256 ? 1 : 2)
         for (int h = 0; h < HALVES; ++h)
           tma_load_3d(smem + h * 128 * 128, &tmQ, q_full, h * 64, g * a.G, it.row0);
       }
-      for (int t = 0; t < n; ++t) {
-        const int s = t % L::kStages;
-        const uint32_t ph = (t / L::kStages) & 1;
-        int z = oob;
-        if (lane < nseg) {
-          const int v = (t0 + t) * kSpTile + lane * seg_rows, i = v / a.bs;
-          if (i < it.n_list) z = list[i].y * a.bs + (v - i * a.bs);
-        }
-        uint8_t* dst = smem + L::kRing + s * L::kTileBytes + lane * seg_rows * 128;
+      // tiles are asked for in the order in which the products free their stages: K_{t+2} (after
+      // Q K_t) before V_{t+1} (after P V_{t-1})
+      auto slot = [&](int t) {  // this lane's segment of tile t: its first cache row
+        const int v = (t0 + t) * kSpTile + lane * seg_rows, i = v / a.bs;
+        return lane < nseg && t < n && i < it.n_list ? list[i].y * a.bs + (v - i * a.bs) : oob;
+      };
+      auto load = [&](int t, const CUtensorMap* map, uint64_t* full, uint64_t* empty, uint8_t* ring) {
+        if (t < 0 || t >= n) return;
+        const int s = t % L::kStages, z = slot(t);
         if (lane == 0) {
-          mbar_wait(&k_empty[s], ph ^ 1, abort, err);
-          mbar_arrive_expect_tx(&k_full[s], L::kTileBytes);
+          mbar_wait(&empty[s], ((t / L::kStages) & 1) ^ 1, abort, err);
+          mbar_arrive_expect_tx(&full[s], L::kTileBytes);
         }
         __syncwarp();
         if (lane < nseg)
 #pragma unroll
-          for (int h = 0; h < HALVES; ++h) tma_load_3d(dst + h * kSpTile * 128, &tmK, &k_full[s], h * 64, g, z);
-        if (lane == 0) {
-          mbar_wait(&v_empty[s], ph ^ 1, abort, err);
-          mbar_arrive_expect_tx(&v_full[s], L::kTileBytes);
-        }
+          for (int h = 0; h < HALVES; ++h)
+            tma_load_3d(ring + s * L::kTileBytes + h * kSpTile * 128 + lane * seg_rows * 128, map, &full[s], h * 64, g, z);
         __syncwarp();
-        dst += L::kStages * L::kTileBytes;
-        if (lane < nseg)
-#pragma unroll
-          for (int h = 0; h < HALVES; ++h) tma_load_3d(dst + h * kSpTile * 128, &tmV, &v_full[s], h * 64, g, z);
-        __syncwarp();
+      };
+      for (int t = -2; t < n; ++t) {
+        load(t + 2, &tmK, k_full, k_empty, smem + L::kRing);
+        load(t + 1, &tmV, v_full, v_empty, smem + L::kRing + L::kStages * L::kTileBytes);
       }
     }
   } else if (warp == 1) {
@@ -563,7 +559,7 @@ __global__ void __launch_bounds__(kTileThreads, HS == 256 ? 1 : 2)
     }
     for (int t = 0; t < n; ++t) {
       if (t + 1 < n) {
-        if (t > 0) mbar_wait(o_done, (t - 1) & 1, abort, err);  // P_{t-1}, in that S buffer, has been read
+        if (t > 0) mbar_wait(&o_done[(t - 1) & 1], ((t - 1) >> 1) & 1, abort, err);  // P_{t-1}, in that S buffer, has been read
         issue_qk(t + 1);
       }
       const int s = t % L::kStages;
@@ -592,13 +588,16 @@ __global__ void __launch_bounds__(kTileThreads, HS == 256 ? 1 : 2)
           if constexpr (BF16)
             tc_mma_ts(tmem + kO, p + p_col(kk) + 16, vd + (uint64_t)(kk * (16 * 128 >> 4)), IDESC_PV, 1u);
         }
-        tc_commit(o_done);
+        tc_commit(&o_done[t & 1]);
         tc_commit(&v_empty[s]);
       }
       __syncwarp();
     }
   } else {
     // ---- softmax ----
+    // (S, P and O each signal on two barriers in turn: not every wait is made by every warp, and a
+    // parity tells a phase from the next only, so a barrier must not be two phases ahead of or
+    // behind one that waits; P_{t-2} V is done once S_t is, and P_t V is not before this warp's P_t)
     constexpr int COLS = kSpTile / 2, OCOLS = HS / 2;
     const float c = a.scale_log2;
     const float none = c > 0.f ? -INFINITY : INFINITY;  // a score whose product with c is -inf
@@ -677,7 +676,7 @@ __global__ void __launch_bounds__(kTileThreads, HS == 256 ? 1 : 2)
       f2_split(lsum, s0, s1);
       l += s0 + s1;
       if (t > 0 && grow) {  // O holds P_0 V .. P_{t-1} V once the last product is done
-        mbar_wait(o_done, (t - 1) & 1, abort, err);
+        mbar_wait(&o_done[(t - 1) & 1], ((t - 1) >> 1) & 1, abort, err);
         tc_fence_after();
 #pragma unroll 1
         for (int cc = 0; cc < OCOLS; cc += 32) {
@@ -693,10 +692,7 @@ __global__ void __launch_bounds__(kTileThreads, HS == 256 ? 1 : 2)
       mbar_arrive(&p_full[t & 1]);
     }
     if (n > 0) {
-      // (the loop knows of the product before the last but one only: a wait for the last by its
-      // parity alone could be let through by that one)
-      if (n > 1) mbar_wait(o_done, (n - 2) & 1, abort, err);
-      mbar_wait(o_done, (n - 1) & 1, abort, err);
+      mbar_wait(&o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort, err);
       tc_fence_after();
     }
     // the row's sum from its halves (the two warps have the same maximum)
