@@ -19,6 +19,13 @@ bool cache_map_16(CUtensorMap* m, const void* base, bool bf16, int hs, int kvh, 
 bool query_block_map(CUtensorMap* m, const void* base, bool bf16, int hs, int nh, int64_t n, int64_t stride, int heads,
                      int rows);
 
+// products of packed fp32 pairs
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // ---- batch lookup without a plan -----------------------------------------------------------
 // Work units are numbered so that sequence b's begin at cum[b] / div + mul * b: a CTA finds
 // its sequence from its own index by searching that increasing function, and no kernel has to

@@ -157,11 +157,6 @@ struct SelShared {
   int found[2];
 };
 
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 template <bool BF16>
 __device__ __forceinline__ uint64_t f2_unpack(uint32_t w) {
   return f2_make(half_of<BF16>(w, 0), half_of<BF16>(w, 1));
