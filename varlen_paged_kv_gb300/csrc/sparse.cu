@@ -38,7 +38,14 @@ struct SparseItem {
 // ascending order are passed over (and reported, unless -1), pages behind the last row too.
 __device__ __forceinline__ SparseItem sparse_item(const PageArgs& a, int u, int sub, int sub_rows, int g, int2* list,
                                                   int lane) {
+  constexpr int E = 4;  // entries per lane and step: their loads, then their table loads, are in flight together
   SparseItem it{};
+  int e[E];
+  auto entries = [&](const int* sel, int i) {
+#pragma unroll
+    for (int k = 0; k < E; ++k) e[k] = i + 32 * k + lane < a.top_k ? sel[i + 32 * k + lane] : -1;
+  };
+  if (a.R == 1) entries(a.selected + ((int64_t)u * a.kvh + g) * a.top_k, 0);  // (u < N is the row)
   const int b = find_seq(a.cum, a.B, a.R, a.R == 1 ? 0 : 1, u, lane);
   if (b < 0) return it;
   const Seq s = load_seq(a.cum, a.past, b, a.N, a.max_blocks, a.bs);
@@ -54,27 +61,32 @@ __device__ __forceinline__ SparseItem sparse_item(const PageArgs& a, int u, int 
   const int* sel = a.selected + ((int64_t)(s.c0 + j0) * a.kvh + g) * a.top_k;
   const int* table = a.table + (int64_t)b * a.max_blocks;
   int kept = 0, top = -1, last_page = -1, n_whole = 0;
-  for (int i = 0; i < a.top_k; i += 32) {
-    const int e = i + lane < a.top_k ? sel[i + lane] : -1;
-    int phys = -1;
-    if (e >= 0 && e < visible) phys = table[e];
-    int m = e;  // the largest entry up to this lane
+  for (int i = 0; i < a.top_k; i += 32 * E) {
+    if (a.R != 1 || i > 0) entries(sel, i);
+    int phys[E];
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, m, d);
-      if (lane >= d) m = max(m, y);
+    for (int k = 0; k < E; ++k) phys[k] = e[k] >= 0 && e[k] < visible ? table[e[k]] : -1;
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+      if (i + 32 * k >= a.top_k) break;
+      int m = e[k];  // the largest entry up to this lane
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, m, d);
+        if (lane >= d) m = max(m, y);
+      }
+      int before = __shfl_up_sync(0xffffffffu, m, 1);
+      before = max(top, lane ? before : -1);
+      bool use = e[k] >= 0 && e[k] < visible && e[k] > before && phys[k] >= 0 && phys[k] < a.num_blocks;
+      if (!use && e[k] != -1 && a.error) atomicOr(a.error, PA_DEVERR_BAD_BLOCK);
+      use = use && (int64_t)e[k] * a.bs <= last;
+      const unsigned mask = __ballot_sync(0xffffffffu, use);
+      if (use) list[kept + __popc(mask & ((1u << lane) - 1))] = make_int2(e[k], phys[k]);
+      n_whole += __popc(__ballot_sync(0xffffffffu, use && e[k] < whole));
+      if (mask) last_page = __shfl_sync(0xffffffffu, e[k], 31 - __clz(mask));
+      kept += __popc(mask);
+      top = max(top, __shfl_sync(0xffffffffu, m, 31));
     }
-    int before = __shfl_up_sync(0xffffffffu, m, 1);
-    before = max(top, lane ? before : -1);
-    bool use = e >= 0 && e < visible && e > before && phys >= 0 && phys < a.num_blocks;
-    if (!use && e != -1 && a.error) atomicOr(a.error, PA_DEVERR_BAD_BLOCK);
-    use = use && (int64_t)e * a.bs <= last;
-    const unsigned mask = __ballot_sync(0xffffffffu, use);
-    if (use) list[kept + __popc(mask & ((1u << lane) - 1))] = make_int2(e, phys);
-    n_whole += __popc(__ballot_sync(0xffffffffu, use && e < whole));
-    if (mask) last_page = __shfl_sync(0xffffffffu, e, 31 - __clz(mask));
-    kept += __popc(mask);
-    top = max(top, __shfl_sync(0xffffffffu, m, 31));
   }
   it.n_list = kept;
   it.v_mask = n_whole * a.bs;
@@ -496,6 +508,7 @@ __global__ void __launch_bounds__(kTileThreads, HS == 256 ? 1 : 2)
   const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
   const int j = row / a.G;                  // its row in the item
   const bool live = warp >= 2 && j < it.rows && row < sub_rows * a.G;
+  const bool any_live = __any_sync(0xffffffffu, live);
   float m_used = -INFINITY, l = 0.f;
 
   if (warp == 0) {
@@ -602,7 +615,6 @@ __global__ void __launch_bounds__(kTileThreads, HS == 256 ? 1 : 2)
     const float c = a.scale_log2;
     const float none = c > 0.f ? -INFINITY : INFINITY;  // a score whose product with c is -inf
     const int lim = it.pos0 + min(j, it.rows - 1);
-    const bool any_live = __any_sync(0xffffffffu, live);
     const uint32_t o_tmem = tmem + lane_off + kO + side * OCOLS;
     const int bar = 1 + (warp & 3);  // of the two warps of a lane quarter
     for (int t = 0; t < n; ++t) {
@@ -748,7 +760,7 @@ __global__ void __launch_bounds__(kTileThreads, HS == 256 ? 1 : 2)
         a.lse[(int64_t)(it.row0 + j) * a.nh + g * a.G + row % a.G] =
             M == -INFINITY ? -INFINITY : (M + fast_log2(S)) * 0.69314718055994531f;
 #pragma unroll 1
-      for (int cc = side * (HS / 2); cc < (side + 1) * (HS / 2); cc += 32) {
+      for (int cc = side * (HS / 2); any_live && cc < (side + 1) * (HS / 2); cc += 32) {
         uint32_t ov[32];
         if (n > 0) tmem_ld_x32(tmem + lane_off + kO + cc, ov);
 #pragma unroll
