@@ -331,7 +331,7 @@ pa_status pa_paged_attention_ex(const void* query, const void* key, const void* 
 /* Most columns of a block_table whose pages pa_select_pages scores. */
 #define PA_MAX_SCORED_PAGES 32768
 /* Largest top_k. */
-#define PA_MAX_SELECTED_PAGES 4096
+#define PA_MAX_SELECTED_PAGES 2048
 
 /*
  * The step's prefix sums, positions, slots and block tables from the requests' lengths, with
@@ -446,7 +446,9 @@ pa_status pa_select_pages(const void* query, const int8_t* page_bounds, const fl
  * ascending order; -1 entries are passed over, anything else is skipped with
  * PA_DEVERR_BAD_BLOCK. A row that attends no key gives zeros and an lse of -inf. scale, output
  * and lse (fp32 (N, num_heads) or NULL) as in pa_paged_attention_lse; query rows may be strided.
- * The caches hold T and already hold this step's rows.
+ * The caches hold T and already hold this step's rows. A value row that is not finite reaches
+ * every row of a query block whose last row attends it, the rows before it among them (their
+ * weights for it are 0); cache rows behind a block's last row may hold anything.
  */
 pa_status pa_sparse_paged_attention(const void* query, const void* key_cache, const void* value_cache,
                                     const int32_t* cumulative_sequence_length, const int32_t* past_seqlens,

@@ -80,7 +80,7 @@ def test_sparse_refusals(lib, name):
                 dict(num_blocks=0), dict(max_blocks_per_sequence=0), dict(reserved=1)):
         assert call(lib, name, dims(**bad)) == 1, bad
     for bad in (dict(head_size=96), dict(block_size=24), dict(dtype=2), dict(num_blocks=1 << 26),
-                dict(max_blocks_per_sequence=1 << 26), dict(num_tokens=(1 << 31) - 5)):
+                dict(max_blocks_per_sequence=1 << 26), dict(max_blocks_per_sequence=(1 << 25) - 1), dict(num_tokens=(1 << 31) - 5)):
         assert call(lib, name, dims(**bad)) == 2, bad
     for bad in (dict(cum=0), dict(past=FAKE + 2), dict(table=0), dict(error=FAKE + 1)):
         assert call(lib, name, dims(), **bad) == 1, bad
@@ -89,7 +89,7 @@ def test_sparse_refusals(lib, name):
         return
     for bad in (dict(top_k=0), dict(query_block=0), dict(query_stride=1020), dict(query_stride=1016)):
         assert call(lib, name, dims(**bad)) == 1, bad
-    for bad in (dict(top_k=4097), dict(query_block=257)):
+    for bad in (dict(top_k=2049), dict(query_block=257)):
         assert call(lib, name, dims(**bad)) == 2, bad
     assert call(lib, name, dims(), query=FAKE + 8) == 1 and call(lib, name, dims(), sel=0) == 1
     if name == "select":

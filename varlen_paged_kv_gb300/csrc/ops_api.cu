@@ -32,8 +32,9 @@ pa_status check_batch_dims(const pa_sparse_dims* d) {
   if (d->dtype != PA_FLOAT16 && d->dtype != PA_BFLOAT16) return PA_ERR_UNSUPPORTED;
   if (d->head_size != 64 && d->head_size != 128 && d->head_size != 256) return PA_ERR_UNSUPPORTED;
   if (d->block_size % 16 != 0) return PA_ERR_UNSUPPORTED;
+  // (positions are counted in 32 bits, a tile past the last one among them)
   if ((int64_t)d->num_blocks * d->block_size > INT32_MAX ||
-      (int64_t)d->max_blocks_per_sequence * d->block_size > INT32_MAX)
+      (int64_t)d->max_blocks_per_sequence * d->block_size > INT32_MAX - 4096)
     return PA_ERR_UNSUPPORTED;
   if ((int64_t)d->num_heads * d->head_size > 65536 || d->kv_num_heads > 65535) return PA_ERR_UNSUPPORTED;
   // (query blocks and touched pages are numbered with room for every sequence)

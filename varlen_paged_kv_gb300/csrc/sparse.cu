@@ -823,7 +823,7 @@ static cudaError_t launch_rows(const PageArgs& a, const CUtensorMap& tk, const C
   const int chunks = (int)ceil_div((int64_t)a.R * a.G, 16);
   const int tiles = (int)ceil_div((int64_t)a.top_k * a.bs, kSpTile);
   const int64_t items = ceil_div(a.N, a.R) * a.kvh * chunks;
-  const int c = cluster_size(items, (int64_t)sms * (HS == 256 ? 1 : 2), tiles, 2, 16);
+  const int c = cluster_size(items, (int64_t)sms * (HS == 256 ? 1 : 2), tiles, 2, 8);
   const dim3 grid((unsigned)query_blocks(a), (unsigned)(a.kvh * chunks), (unsigned)c);
   return launch_clusters(sparse_rows_kernel<HS, BF16>, grid, kRowsThreads, RowsSmem<HS>::bytes(a.top_k), s, a, tk, tv,
                          seg, chunks);
