@@ -405,6 +405,14 @@ def test_select_pages(nh, kvh, hs, bs, R, dtype):
     assert int(b.error) == 0
 
 
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_select_of_many_blocks(dtype):
+    """Thousands of selections, so that products that round to a half on the way to their code occur by the score."""
+    b = Batch(15, dtype, 16, 4, 64, 16, [16 * 300 + 5, 16 * 150, 16 * 600], [1500, 1600, 1501])
+    b.whole_bounds()
+    assert np.array_equal(b.select(24, 4).cpu().numpy(), b.want_selected(24, 4))
+
+
 def test_select_ties_go_to_the_lowest_page():
     b = Batch(6, "fp16", 4, 2, 128, 16, [16 * 900 + 3, 16 * 3], [1, 5])
     r = np.random.default_rng(7)

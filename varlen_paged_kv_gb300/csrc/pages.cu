@@ -224,8 +224,8 @@ __device__ void query_codes(const PageArgs& a, int row0, int rows, int g, SelSha
 #pragma unroll
   for (int i = 0; i < WARPS; ++i) most = fmaxf(most, sh.warp_f[i]);
   const float fine = most > 1e-30f ? __fdiv_rn(4095.f, most) : 0.f;
-  const uint64_t fine2 = f2_make(fine, fine), magic = f2_make(12582912.f, 12582912.f),
-                 unmagic = f2_make(-12582912.f, -12582912.f);
+  const uint64_t fine2 = f2_make(fine, fine);
+  constexpr float kWhole = 12582912.f;  // 1.5 * 2^23: adding it leaves a whole number
   uint64_t sum[4];
   float mag[8];
 #pragma unroll
@@ -240,9 +240,11 @@ __device__ void query_codes(const PageArgs& a, int row0, int rows, int g, SelSha
         f2_split(x2, x0, x1);
         x2 = f2_make(isfinite(x0) ? x0 : 0.f, isfinite(x1) ? x1 : 0.f);
       }
-      const uint64_t t = f2_add(f2_add(f2_mul(x2, fine2), magic), unmagic);
-      f2_split(t, x0, x1);
-      sum[e] = f2_add(sum[e], t);
+      // (scalar sums: a product and a sum on packed pairs may become one fma, which rounds once)
+      f2_split(f2_mul(x2, fine2), x0, x1);
+      x0 = __fadd_rn(__fadd_rn(x0, kWhole), -kWhole);
+      x1 = __fadd_rn(__fadd_rn(x1, kWhole), -kWhole);
+      sum[e] = f2_add(sum[e], f2_make(x0, x1));
       mag[2 * e] += fabsf(x0);
       mag[2 * e + 1] += fabsf(x1);
     }
