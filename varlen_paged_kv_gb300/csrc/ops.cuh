@@ -144,8 +144,9 @@ cudaError_t launch_sparse(const PageArgs& a, bool bf16, int sms, cudaStream_t s)
 template <typename... KArgs, typename... Actual>
 inline cudaError_t launch_clusters(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t s,
                                    Actual&&... args) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
+  // (up to 48 KB with the kernel's static arrays need no attribute)
+  if (smem > 12 * 1024)
+    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);

@@ -163,8 +163,19 @@ pa_status pa_qk_norm_rope(const void* query, const void* key, const int32_t* pos
   a.rotary_dim = d;
   a.interleaved = interleaved != 0;
   a.eps = prep->norm_eps;
-  // the fp32 rotary table fl32(theta^(-2u/d)), formed in double and rounded once
-  for (int u = 0; u < d / 2; ++u) a.inv_freq[u] = (float)std::pow((double)prep->rope_theta, -2.0 * u / d);
+  // the fp32 rotary table fl32(theta^(-2u/d)), formed in double and rounded once; a thread's
+  // calls with one base and dimension (a model's) form it once
+  struct Table {
+    float theta = 0.f, freq[128];
+    int32_t d = 0;
+  };
+  static thread_local Table table;
+  if (d > 0 && (table.d != d || table.theta != prep->rope_theta)) {
+    for (int u = 0; u < d / 2; ++u) table.freq[u] = (float)std::pow((double)prep->rope_theta, -2.0 * u / d);
+    table.d = d;
+    table.theta = prep->rope_theta;
+  }
+  for (int u = 0; u < d / 2; ++u) a.inv_freq[u] = table.freq[u];
   return launched(pa::launch_rotate(a, dtype == PA_BFLOAT16, head_size, sms, static_cast<cudaStream_t>(stream)),
                   "rotate_kernel launch");
 }
