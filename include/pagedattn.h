@@ -410,8 +410,9 @@ typedef struct pa_sparse_dims {
  * positions past .. past + q - 1 of every sequence from key_cache (call it after the cache
  * write); a page that begins with one of them starts afresh, a page that held keys before
  * keeps their bounds. To bound a cache that is there already, pass past_seqlens of 0 and the
- * whole lengths. Sequences of one call must not write to the same page. NaN keys do not
- * count. Uses num_heads, top_k, query_block and the query stride of `dims` for nothing.
+ * whole lengths. Sequences of one call must not write to the same page. Bounds do not narrow
+ * while a page is filled: those of keys that a sequence takes back (refused drafts, past_seqlens
+ * smaller than before) stay until the page begins anew. NaN keys do not count. Uses num_heads, top_k, query_block and the query stride of `dims` for nothing.
  */
 pa_status pa_update_page_bounds(const void* key_cache, int8_t* page_bounds, const float* bound_scale,
                                 const int32_t* cumulative_sequence_length, const int32_t* past_seqlens,

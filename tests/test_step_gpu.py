@@ -742,9 +742,29 @@ def test_calls_on_two_streams_at_once():
 def test_explicit_stream_argument():
     b = Batch(22, "fp16", 4, 2, 64, 16, [300], [2])
     b.whole_bounds()
-    torch.cuda.synchronize()
     side = torch.cuda.Stream()
-    sel = b.select(5, stream=side)
-    out, lse = b.attend(sel, stream=side)
+    side.wait_stream(torch.cuda.current_stream())
+    busy = torch.randn(4096, 4096, device="cuda")
+    for _ in range(5):
+        # freed blocks of the current stream, still in use there, are not what the side stream writes to
+        junk = torch.zeros(2, 2, 5, dtype=torch.int32, device="cuda")
+        for _ in range(20):
+            busy = busy @ busy * 1e-3
+        seen = junk.clone()
+        del junk
+        sel = b.select(5, stream=side)
+        out = pa.sparse_paged_attention(b.query, b.key_cache, b.value_cache, *b.meta, sel, num_heads=4, kv_num_heads=2,
+                                        stream=side)
+        side.synchronize()
+        assert np.array_equal(sel.cpu().numpy(), b.want_selected(5))
+        want, lse = b.attend(sel)
+        assert torch.equal(out, want) and (seen == 0).all()
+        b.check(want, lse, sel.cpu().numpy())
+    q, k = b.query.contiguous(), b.query[:, :128].contiguous()
+    side.wait_stream(torch.cuda.current_stream())
+    pos = i32([5, 6])
+    torch.cuda.synchronize()
+    on = pa.qk_norm_rope(q, k, pos, num_heads=4, kv_num_heads=2, rotary_dim=64, stream=side)
     side.synchronize()
-    b.check(out, lse, sel.cpu().numpy())
+    assert all(torch.equal(x, y) for x, y in zip(on, pa.qk_norm_rope(q, k, pos, num_heads=4, kv_num_heads=2,
+                                                                     rotary_dim=64)))

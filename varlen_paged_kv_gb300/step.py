@@ -9,7 +9,8 @@
 As ``paged_attention``: argument marshalling only, for the C ABI of ``libpagedattn.so``; the
 work runs on the current stream of the tensors' device (or ``stream``), and a call can be
 captured in a CUDA graph. An int32 tensor of one element passed as ``error`` collects the
-``DEVERR_*`` bits of problems that only device data reveals.
+``DEVERR_*`` bits of problems that only device data reveals. With ``stream`` the caller orders
+that stream after the work that makes the inputs, and other streams after the call.
 """
 from __future__ import annotations
 
@@ -108,6 +109,17 @@ def _rows(t, name, width, dtype, index):
     return step if shape[0] > 1 else -(-max(width, step) // 8) * 8
 
 
+def _empty(shape, dtype, device, stream):
+    """A tensor for a kernel of ``stream`` to write: of that stream's memory, so that nothing else
+    is still using it, and not given back before work that the current stream has by then."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _call(where, index, stream, function, *args):
     """Calls function(*args, stream) with the tensors' device current; the stream is the caller's
     or that device's current one."""
@@ -149,7 +161,7 @@ def build_block_tables(past_seqlens: torch.Tensor, query_lens: torch.Tensor, blo
             raise ValueError("num_tokens must not be negative")
         # one allocation; the pieces are tensors of their own
         out = BlockTables._make(torch.unsafe_split_with_sizes(
-            torch.empty(2 * (B + num_tokens + 2), dtype=_I32, device=block_table.device), sizes))
+            _empty(2 * (B + num_tokens + 2), _I32, block_table.device, stream), sizes))
     else:
         for name, t, n in zip(BlockTables._fields, out, sizes):
             _refuse_ints(index, **{"out." + name: t})
@@ -185,12 +197,12 @@ def qk_norm_rope(query: torch.Tensor, key: torch.Tensor, positions: torch.Tensor
     qs, ks = _rows(query, "query", qw, dtype, index), _rows(key, "key", kw, dtype, index)
     device = None if query_out is not None and key_out is not None else query.device
     if query_out is None:
-        query_out = torch.empty((N, qw), dtype=dtype, device=device)
+        query_out = _empty((N, qw), dtype, device, stream)
         qos = qw
     else:
         qos = _rows(query_out, "query_out", qw, dtype, index)
     if key_out is None:
-        key_out = torch.empty((N, kw), dtype=dtype, device=device)
+        key_out = _empty((N, kw), dtype, device, stream)
         kos = kw
     else:
         kos = _rows(key_out, "key_out", kw, dtype, index)
@@ -284,7 +296,7 @@ def select_pages(query: torch.Tensor, page_bounds: torch.Tensor, bound_scale: to
     B, columns, err = _batch(index, cumulative_sequence_length, past_seqlens, block_table, error)
     N = query.shape[0]
     if selected is None:
-        selected = torch.empty((N, kv_num_heads, max(top_k, 0)), dtype=_I32, device=query.device)
+        selected = _empty((N, kv_num_heads, max(top_k, 0)), _I32, query.device, stream)
     else:
         _refuse_ints(index, selected=selected)
         if selected.shape != (N, kv_num_heads, top_k):
@@ -330,7 +342,7 @@ def sparse_paged_attention(query: torch.Tensor, key_cache: torch.Tensor, value_c
     if len(chosen) != 3 or chosen[0] != N or chosen[1] != kvh:
         raise ValueError("selected must be (rows, kv_num_heads, top_k)")
     if output is None:
-        output = torch.empty((N, num_heads * hs), dtype=dtype, device=query.device)
+        output = _empty((N, num_heads * hs), dtype, query.device, stream)
     elif output.dtype is not dtype or output.get_device() != index or output.shape != (N, num_heads * hs) or \
             not output.is_contiguous():
         raise ValueError("output must be contiguous (rows, num_heads * head_size) of the query dtype")
