@@ -739,6 +739,79 @@ def test_calls_on_two_streams_at_once():
             assert torch.equal(s2, sel) and torch.equal(o2, out) and torch.equal(z2, lse)
 
 
+class _NoFast:
+    """The compiled calls as they answer anything unusual."""
+
+    def __getattr__(self, name):
+        return lambda *a: None
+
+
+def test_both_ways_into_the_library_agree(monkeypatch):
+    """The compiled calls and the Python code behind them: the same results, types and shapes."""
+    from varlen_paged_kv_gb300 import step
+
+    def results():
+        out = []
+        for dtype, R in (("fp16", 1), ("bf16", 5)):
+            b = Batch(41, dtype, 8, 2, 128, 16, [300, 45], [1, 12], extra_rows=2, wide=256)
+            b.whole_bounds()
+            sel = b.select(6, R)
+            lse = torch.zeros(b.N, 8, device="cuda")
+            o = pa.sparse_paged_attention(b.query, b.key_cache, b.value_cache, *b.meta, sel, num_heads=8, kv_num_heads=2,
+                                          scale=0.11, query_block=R, lse=lse, error=b.error)
+            n = int(b.cum[-1])
+            w = torch.ones(128, dtype=DT[dtype], device="cuda")
+            k = b.rows[:, 1024:]
+            turned = pa.qk_norm_rope(b.query, k, i32(np.arange(b.N)), num_heads=8, kv_num_heads=2, q_norm_weight=w,
+                                     eps=1e-5, rotary_dim=64, theta=5e5, interleaved=R == 1)
+            out += [b.bounds, sel[:n], o[:n], lse[:n], b.error, *turned]
+        a = table_state(np.random.default_rng(6), 30, 16, 20, 200, 40, 0.2)
+        t, dev = run_tables(*a, 16, 700)
+        return out + list(t) + dev
+
+    fast = results()
+    assert step._fast is not None
+    monkeypatch.setattr(step, "_fast", _NoFast())
+    for x, y in zip(fast, results()):
+        assert x.dtype == y.dtype and x.shape == y.shape and x.is_contiguous() and torch.equal(x, y)
+
+
+def test_refusals_say_what_was_wrong():
+    b = Batch(42, "fp16", 4, 2, 64, 16, [100], [2])
+    kw = dict(num_heads=4, kv_num_heads=2)
+    sel = b.select(4)
+    with pytest.raises(TypeError, match="selected must be int32"):
+        pa.sparse_paged_attention(b.query, b.key_cache, b.value_cache, *b.meta, sel.long(), **kw)
+    with pytest.raises(TypeError, match="value_cache"):
+        pa.sparse_paged_attention(b.query, b.key_cache, b.value_cache.bfloat16(), *b.meta, sel, **kw)
+    with pytest.raises(ValueError, match="selected must be a contiguous"):
+        pa.sparse_paged_attention(b.query, b.key_cache, b.value_cache, *b.meta, sel.transpose(0, 1), **kw)
+    with pytest.raises(ValueError, match="lse"):
+        pa.sparse_paged_attention(b.query, b.key_cache, b.value_cache, *b.meta, sel, lse=torch.zeros(2, 3).cuda(), **kw)
+    with pytest.raises(ValueError, match="batch_size"):
+        pa.select_pages(b.query, b.bounds, b.scale, b.meta[0][:1], *b.meta[1:], block_size=16, top_k=4, **kw)
+    with pytest.raises(pa.PagedAttentionError, match="INVALID_ARGUMENT"):
+        pa.select_pages(b.query, b.bounds, b.scale, *b.meta, block_size=16, top_k=1, **kw)
+    with pytest.raises(pa.PagedAttentionError, match="UNSUPPORTED"):
+        pa.select_pages(b.query, b.bounds, b.scale, *b.meta, block_size=24, top_k=4, **kw)
+    with pytest.raises(pa.PagedAttentionError, match="INVALID_ARGUMENT"):  # rows that do not start on 16 bytes
+        wide = torch.zeros(2, 300, dtype=torch.float16, device="cuda")
+        pa.select_pages(wide[:, :256], b.bounds, b.scale, *b.meta, block_size=16, top_k=4, **kw)
+    with pytest.raises(ValueError, match="key must be"):
+        pa.qk_norm_rope(b.query, b.query, i32([0, 1]), **kw)
+    with pytest.raises(pa.PagedAttentionError, match="UNSUPPORTED"):
+        pa.qk_norm_rope(b.query, b.query[:, :128], i32([0, 1]), rotary_dim=8, **kw)
+    with pytest.raises(TypeError, match="int8"):
+        pa.update_page_bounds(b.key_cache, b.bounds.int(), b.scale, *b.meta, num_tokens=2)
+    with pytest.raises(ValueError, match="block_table"):
+        pa.build_block_tables(b.meta[1], b.meta[1], b.meta[1], b.meta[2][:0], b.meta[1], i32([0, 0]), block_size=16,
+                              num_tokens=4)
+    with pytest.raises(ValueError, match="negative"):
+        pa.build_block_tables(b.meta[1], b.meta[1], b.meta[1], b.meta[2], b.meta[1], i32([0, 0]), block_size=16,
+                              num_tokens=-1)
+    torch.cuda.synchronize()
+
+
 def test_explicit_stream_argument():
     b = Batch(22, "fp16", 4, 2, 64, 16, [300], [2])
     b.whole_bounds()

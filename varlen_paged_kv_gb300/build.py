@@ -3,7 +3,8 @@
 Each translation unit under csrc/ is compiled by nvcc in parallel, then linked into a
 shared library next to this file. Rebuilds only when a source or header is newer than
 the library. The CUDA runtime is linked statically, so the library depends on the
-driver only.
+driver only. Beside it, g++ builds csrc/binding.cpp against the installed torch: the
+Python calls of the operators around the attention call.
 """
 from __future__ import annotations
 
@@ -50,9 +51,38 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+BINDING = os.path.join(HERE, "_step_binding.so")
+
+
+def build_binding(force: bool = False) -> str:
+    """_step_binding.so: csrc/binding.cpp against the torch that imports it."""
+    src = os.path.join(CSRC, "binding.cpp")
+    deps = [src, os.path.join(INCLUDE, "pagedattn.h")]
+    if not force and os.path.exists(BINDING) and all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps):
+        return BINDING
+    import sysconfig
+
+    import torch
+
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + INCLUDE,
+           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(base, "include"),
+           "-I" + os.path.join(base, "include", "torch", "csrc", "api", "include"), "-I" + cuda, src, "-o", tmp,
+           "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {src}:\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, coverage: bool = False) -> str:
     lib = COV_LIB if coverage else LIB
     if not force and not ptxas_info and up_to_date(lib):
+        build_binding()
         return lib
     build_dir = os.path.join(BUILD, "cov") if coverage else BUILD
     os.makedirs(build_dir, exist_ok=True)
@@ -69,8 +99,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, 
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(12, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(build_binding)
         results = list(ex.map(compile_one, sources()))
+        binding.result()
     if verbose or ptxas_info:
         for _, log in results:
             if log.strip():

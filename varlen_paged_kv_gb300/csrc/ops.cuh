@@ -33,36 +33,44 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
 // sequence, with mul = 2 for one more, as rows that start inside a page touch; unused numbers
 // in between belong to no unit.) The largest b with cum[b] / div + mul * b <= u, by a whole
 // warp, 32 candidates a step; -1 if there is none.
-__device__ __forceinline__ int find_seq(const int32_t* cum, int B, int div, int mul, int u, int lane) {
-  int lo = 0, n = B;
-  while (n > 0) {
-    const int step = (n + 31) / 32, i = lo + lane * step;
-    const bool ok = i < lo + n && cum[i] / div + mul * i <= u;
-    const unsigned m = __ballot_sync(0xffffffffu, ok);
-    if (m == 0) return -1;
-    const int k = 31 - __clz(m);
-    n = min(step, lo + n - (lo + k * step));
-    lo += k * step;
-    if (step == 1) break;
-  }
-  return lo;
-}
-
+//
 // A sequence's rows and history; ok is false for lengths that do not belong to a batch
 // of N rows and tables of max_blocks pages (such a sequence is skipped).
 struct Seq {
-  int c0, q, past;
+  int b, c0, q, past;
   bool ok;
 };
-__device__ __forceinline__ Seq load_seq(const int32_t* cum, const int32_t* past, int b, int N, int max_blocks,
-                                        int bs) {
+__device__ __forceinline__ Seq make_seq(int b, int c0, int c1, int past, int N, int max_blocks, int bs) {
   Seq s;
-  s.c0 = cum[b];
-  const int c1 = cum[b + 1];
-  s.past = past[b];
-  s.q = c1 - s.c0;
-  s.ok = s.c0 >= 0 && c1 >= s.c0 && c1 <= N && s.past >= 0 && (int64_t)s.past + s.q <= (int64_t)max_blocks * bs;
+  s.b = b;
+  s.c0 = c0;
+  s.q = c1 - c0;
+  s.past = past;
+  s.ok = c0 >= 0 && c1 >= c0 && c1 <= N && past >= 0 && (int64_t)past + s.q <= (int64_t)max_blocks * bs;
   return s;
+}
+
+// The sequence of unit u: the largest b with cum[b] / div + mul * b <= u, found by a whole warp,
+// 32 candidates a step; the last step's loads bring the lengths with them. ok is false where
+// there is none.
+__device__ __forceinline__ Seq find_seq(const int32_t* cum, const int32_t* past, int B, int div, int mul, int u,
+                                        int N, int max_blocks, int bs, int lane) {
+  int lo = 0, n = B;
+  for (;;) {
+    const int step = (n + 31) / 32, i = lo + lane * step;
+    const bool in = i < lo + n;
+    const int c = in ? cum[i] : 0;
+    int c_next = 0, p = 0;
+    if (step == 1 && in) c_next = cum[i + 1], p = past[i];
+    const unsigned m = __ballot_sync(0xffffffffu, in && c / div + mul * i <= u);
+    if (m == 0) return Seq{-1, 0, 0, 0, false};
+    const int k = 31 - __clz(m);
+    if (step == 1)
+      return make_seq(lo + k, __shfl_sync(0xffffffffu, c, k), __shfl_sync(0xffffffffu, c_next, k),
+                      __shfl_sync(0xffffffffu, p, k), N, max_blocks, bs);
+    n = min(step, lo + n - (lo + k * step));
+    lo += k * step;
+  }
 }
 
 // the checks of the whole batch, by one CTA: sets PA_DEVERR_BAD_BATCH
@@ -70,7 +78,7 @@ __device__ __forceinline__ void check_batch(const int32_t* cum, const int32_t* p
                                             int bs, uint32_t* err) {
   if (!err) return;
   bool bad = threadIdx.x == 0 && cum[0] != 0;
-  for (int b = threadIdx.x; b < B; b += blockDim.x) bad |= !load_seq(cum, past, b, N, max_blocks, bs).ok;
+  for (int b = threadIdx.x; b < B; b += blockDim.x) bad |= !make_seq(b, cum[b], cum[b + 1], past[b], N, max_blocks, bs).ok;
   if (bad) atomicOr(err, PA_DEVERR_BAD_BATCH);
 }
 

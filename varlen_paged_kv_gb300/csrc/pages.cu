@@ -59,14 +59,12 @@ __global__ void __launch_bounds__(kBoundChunks * kBoundGroups) bounds_kernel(con
   const int chunk_in = threadIdx.x % kBoundChunks, group = threadIdx.x / kBoundChunks, lane = threadIdx.x & 31;
   if (blockIdx.x == 0 && blockIdx.y == 0) check_batch(a.cum, a.past, a.B, a.N, a.max_blocks, a.bs, a.error);
   const int u = blockIdx.x;
-  const int b = find_seq(a.cum, a.B, a.bs, 2, u, lane);
-  if (b < 0) return;
-  const Seq s = load_seq(a.cum, a.past, b, a.N, a.max_blocks, a.bs);
+  const Seq s = find_seq(a.cum, a.past, a.B, a.bs, 2, u, a.N, a.max_blocks, a.bs, lane);
   if (!s.ok || s.q == 0) return;
-  const int page = s.past / a.bs + (u - (s.c0 / a.bs + 2 * b));
+  const int page = s.past / a.bs + (u - (s.c0 / a.bs + 2 * s.b));
   const int end = s.past + s.q;
   if ((int64_t)page * a.bs >= end) return;
-  const int phys = a.table[(int64_t)b * a.max_blocks + page];
+  const int phys = a.table[(int64_t)s.b * a.max_blocks + page];
   if (phys < 0 || phys >= a.num_blocks) {
     if (threadIdx.x == 0 && a.error) atomicOr(a.error, PA_DEVERR_BAD_BLOCK);
     return;
@@ -154,7 +152,8 @@ struct SelShared {
   };
   int warp_a[kWarps], warp_b[kWarps];
   float warp_f[kWarps];
-  int found[2];
+  int found[3];
+  int n_close, close[32];  // the distances left when few are
 };
 
 template <bool BF16>
@@ -177,8 +176,15 @@ __device__ void query_codes(const PageArgs& a, int row0, int rows, int g, SelSha
   const int c = tid % CH * 8, group = tid / CH, total = rows * a.G;
   const uint16_t* q = a.query + (int64_t)row0 * a.q_stride + (int64_t)g * a.G * HS + c;
   uint64_t sc[4];
+  if (reinterpret_cast<uintptr_t>(a.scale) % 16 == 0) {
+    const float4 s0 = __ldg(reinterpret_cast<const float4*>(a.scale + g * HS + c));
+    const float4 s1 = __ldg(reinterpret_cast<const float4*>(a.scale + g * HS + c) + 1);
+    sc[0] = f2_make(s0.x, s0.y), sc[1] = f2_make(s0.z, s0.w), sc[2] = f2_make(s1.x, s1.y), sc[3] = f2_make(s1.z, s1.w);
+  } else {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) sc[e] = f2_make(__ldg(a.scale + g * HS + c + 2 * e), __ldg(a.scale + g * HS + c + 2 * e + 1));
+    for (int e = 0; e < 4; ++e)
+      sc[e] = f2_make(__ldg(a.scale + g * HS + c + 2 * e), __ldg(a.scale + g * HS + c + 2 * e + 1));
+  }
   auto load = [&](int r) {
     return __ldg(reinterpret_cast<const uint4*>(q + (int64_t)(r / a.G) * a.q_stride + (int64_t)(r % a.G) * HS));
   };
@@ -379,11 +385,13 @@ __global__ void __launch_bounds__(T, T == 256 ? 3 : 1024 / T) select_kernel(cons
   const int g = blockIdx.y, rank = blockIdx.z, C = gridDim.z;
   if (blockIdx.x == 0 && g == 0 && rank == 0) check_batch(a.cum, a.past, a.B, a.N, a.max_blocks, a.bs, a.error);
   const int u = blockIdx.x;
-  const int b = find_seq(a.cum, a.B, a.R, a.R == 1 ? 0 : 1, u, lane);
-  if (b < 0) return;
-  const Seq s = load_seq(a.cum, a.past, b, a.N, a.max_blocks, a.bs);
+  if (a.R == 1) {  // (the row is known: its query heads are on their way while the lengths are looked up)
+    const char* q = reinterpret_cast<const char*>(a.query + (int64_t)u * a.q_stride + (int64_t)g * a.G * HS);
+    for (int i = tid * 128; i < a.G * HS * 2; i += T * 128) prefetch_l2(q + i);
+  }
+  const Seq s = find_seq(a.cum, a.past, a.B, a.R, a.R == 1 ? 0 : 1, u, a.N, a.max_blocks, a.bs, lane);
   if (!s.ok) return;
-  const int j0 = (u - (a.R == 1 ? s.c0 : s.c0 / a.R + b)) * a.R;
+  const int j0 = (u - (a.R == 1 ? s.c0 : s.c0 / a.R + s.b)) * a.R;
   if (j0 >= s.q || j0 < 0) return;
   const int rows = min(a.R, s.q - j0);
   const int own = (s.past + j0) / a.bs, last = (s.past + j0 + rows - 1) / a.bs;
@@ -402,7 +410,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 3 : 1024 / T) select_kernel(cons
     return;
   }
   query_codes<HS, BF16, T>(a, s.c0 + j0, rows, g, sh);
-  const int* table = a.table + (int64_t)b * a.max_blocks;
+  const int* table = a.table + (int64_t)s.b * a.max_blocks;
   const int count = end - begin;
   if (C == 1) {
     score_pages<HS, T>(a, table, g, begin, end, sh, [&](int page, int d) { score[page - begin] = d; });
@@ -430,19 +438,25 @@ __global__ void __launch_bounds__(T, T == 256 ? 3 : 1024 / T) select_kernel(cons
   // distances top - score from `from` on, below `from + span`, in bins of 2^shift
   uint32_t from = 0, span = (uint32_t)(top - low) + 1;
   int ties = want;  // still to be taken among them
+  constexpr int MINE = kSelBins / T;  // bins of a thread
   for (;;) {
     const int bits = 32 - __clz(span - 1 | 1), shift = max(bits - 11, 0);
-    for (int i = tid; i < kSelBins; i += T) sh.hist[i] = 0;
+#pragma unroll
+    for (int k = 0; k < MINE; k += 4) *reinterpret_cast<int4*>(sh.hist + tid * MINE + k) = make_int4(0, 0, 0, 0);
+    if (tid == 0) sh.n_close = 0;
     __syncthreads();
     for (int i = tid; i < count; i += T) {
       const uint32_t x = (uint32_t)(top - score[i]) - from;
       if (x < span) atomicAdd(&sh.hist[x >> shift], 1);
     }
     __syncthreads();
-    constexpr int MINE = kSelBins / T;
     int h[MINE], sum = 0;
 #pragma unroll
-    for (int k = 0; k < MINE; ++k) h[k] = sh.hist[tid * MINE + k], sum += h[k];
+    for (int k = 0; k < MINE; k += 4) {
+      const int4 v = *reinterpret_cast<const int4*>(sh.hist + tid * MINE + k);
+      h[k] = v.x, h[k + 1] = v.y, h[k + 2] = v.z, h[k + 3] = v.w;
+      sum += (v.x + v.y) + (v.z + v.w);
+    }
     int inc = sum;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -458,43 +472,88 @@ __global__ void __launch_bounds__(T, T == 256 ? 3 : 1024 / T) select_kernel(cons
     if (before < ties && ties <= before + sum) {  // the want-th falls in one of this thread's bins
 #pragma unroll
       for (int k = 0; k < MINE; ++k) {
-        if (before < ties && ties <= before + h[k]) sh.found[0] = tid * MINE + k, sh.found[1] = ties - before;
+        if (before < ties && ties <= before + h[k]) {
+          sh.found[0] = tid * MINE + k, sh.found[1] = ties - before, sh.found[2] = h[k];
+        }
         before += h[k];
       }
     }
-    if (ties == 0 && tid == 0) sh.found[0] = 0, sh.found[1] = 0;  // (nothing to take: a threshold above all)
+    if (ties == 0 && tid == 0) sh.found[0] = sh.found[1] = sh.found[2] = 0;  // (nothing to take: above all)
     __syncthreads();
     from += (uint32_t)sh.found[0] << shift;
     ties = sh.found[1];
-    if (shift == 0) break;
+    if (shift == 0 || ties == 0) break;
     span = min(span - ((uint32_t)sh.found[0] << shift), 1u << shift);
     if (span == 1) break;
+    if (sh.found[2] <= 32) {
+      // few are left: every warp ranks them by comparing each with each
+      for (int i = tid; i < count; i += T) {
+        const uint32_t x = (uint32_t)(top - score[i]) - from;
+        if (x < span) sh.close[atomicAdd(&sh.n_close, 1)] = (int)x;
+      }
+      __syncthreads();
+      const int left = sh.n_close, mine = lane < left ? sh.close[lane] : INT32_MAX;
+      int rank = 0, fewer = 0;  // those before this one, and those strictly before
+      for (int j = 0; j < left; ++j) {
+        const int y = __shfl_sync(0xffffffffu, mine, j);
+        fewer += y < mine;
+        rank += y < mine || (y == mine && j < lane);
+      }
+      const unsigned m = __ballot_sync(0xffffffffu, lane < left && rank == ties - 1);
+      const int at = __ffs(m) - 1;
+      from += (uint32_t)__shfl_sync(0xffffffffu, mine, at);
+      ties -= __shfl_sync(0xffffffffu, fewer, at);
+      break;
+    }
   }
   const int cut = top - (int)from;
-  // ---- the taken pages in order, each warp a contiguous part ----
+  // ---- the taken pages in order, each warp a contiguous part: lane k keeps the masks of the
+  // part's k-th 32 scores, the warps exchange their counts, and each lane writes its own ----
   const int per = (int)align_up(ceil_div(count, WARPS), 32);
   const int i0 = min(count, warp * per), i1 = min(count, i0 + per);
-  int above = 0, at = 0;
-  for (int i = i0 + lane; i < i1; i += 32) above += score[i] > cut, at += score[i] == cut;
-  above = __reduce_add_sync(0xffffffffu, above);
-  at = __reduce_add_sync(0xffffffffu, at);
+  int n_up = 0, n_eq = 0;  // of this warp
+  constexpr int ROUNDS = 2;  // 2 * 32 * 32 scores a warp: 32768 by sixteen warps
+  unsigned up[ROUNDS], eq[ROUNDS];
+  int up_at[ROUNDS], eq_at[ROUNDS];
+#pragma unroll
+  for (int r = 0; r < ROUNDS; ++r) {
+    up[r] = eq[r] = 0;
+    for (int k = 0; k < 32; ++k) {
+      const int i = i0 + (r * 32 + k) * 32;
+      if (i >= i1) break;
+      const int x = i + lane < i1 ? score[i + lane] : INT32_MIN;
+      const unsigned u1 = __ballot_sync(0xffffffffu, x > cut), e1 = __ballot_sync(0xffffffffu, x == cut);
+      if (lane == k) up[r] = u1, eq[r] = e1;
+    }
+    int a1 = __popc(up[r]), e1 = __popc(eq[r]);
+    const int a0 = a1, e0 = e1;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, a1, d), z = __shfl_up_sync(0xffffffffu, e1, d);
+      if (lane >= d) a1 += y, e1 += z;
+    }
+    up_at[r] = n_up + a1 - a0, eq_at[r] = n_eq + e1 - e0;
+    n_up += __shfl_sync(0xffffffffu, a1, 31);
+    n_eq += __shfl_sync(0xffffffffu, e1, 31);
+  }
   __syncthreads();
-  if (lane == 0) sh.warp_a[warp] = above, sh.warp_b[warp] = at;
+  if (lane == 0) sh.warp_a[warp] = n_up, sh.warp_b[warp] = n_eq;
   __syncthreads();
-  int before_above = 0, before_at = 0;
+  int before_up = 0, before_eq = 0;
 #pragma unroll
   for (int w = 0; w < WARPS; ++w)
-    if (w < warp) before_above += sh.warp_a[w], before_at += sh.warp_b[w];
-  for (int i = i0; i < i1; i += 32) {
-    const int x = i + lane < i1 ? score[i + lane] : 0;
-    const unsigned up = __ballot_sync(0xffffffffu, i + lane < i1 && x > cut);
-    const unsigned eq = __ballot_sync(0xffffffffu, i + lane < i1 && x == cut);
-    const unsigned below = (1u << lane) - 1;
-    const int eq_rank = before_at + __popc(eq & below);
-    if ((up >> lane & 1) || ((eq >> lane & 1) && eq_rank < ties))
-      list[begin + before_above + __popc(up & below) + min(eq_rank, ties)] = begin + i + lane;
-    before_above += __popc(up);
-    before_at += __popc(eq);
+    if (w < warp) before_up += sh.warp_a[w], before_eq += sh.warp_b[w];
+#pragma unroll
+  for (int r = 0; r < ROUNDS; ++r) {
+    int above = before_up + up_at[r], equal = before_eq + eq_at[r];
+    for (unsigned m = up[r] | eq[r]; m; m &= m - 1) {
+      const int bit = __ffs(m) - 1;
+      const bool is_eq = eq[r] >> bit & 1;
+      if (!is_eq || equal < ties)
+        list[begin + above + min(equal, ties)] = begin + i0 + (r * 32 + lane) * 32 + bit;
+      if (is_eq) ++equal;
+      else ++above;
+    }
   }
   for (int i = tid; i < begin; i += T) list[i] = i;
   for (int i = end + tid; i < n; i += T) list[begin + want + i - end] = i;

@@ -46,11 +46,9 @@ __device__ __forceinline__ SparseItem sparse_item(const PageArgs& a, int u, int 
     for (int k = 0; k < E; ++k) e[k] = i + 32 * k + lane < a.top_k ? sel[i + 32 * k + lane] : -1;
   };
   if (a.R == 1) entries(a.selected + ((int64_t)u * a.kvh + g) * a.top_k, 0);  // (u < N is the row)
-  const int b = find_seq(a.cum, a.B, a.R, a.R == 1 ? 0 : 1, u, lane);
-  if (b < 0) return it;
-  const Seq s = load_seq(a.cum, a.past, b, a.N, a.max_blocks, a.bs);
+  const Seq s = find_seq(a.cum, a.past, a.B, a.R, a.R == 1 ? 0 : 1, u, a.N, a.max_blocks, a.bs, lane);
   if (!s.ok) return it;
-  const int j0 = (u - (a.R == 1 ? s.c0 : s.c0 / a.R + b)) * a.R;
+  const int j0 = (u - (a.R == 1 ? s.c0 : s.c0 / a.R + s.b)) * a.R;
   if (j0 < 0 || j0 + sub >= s.q) return it;
   it.rows = min(min(a.R - sub, sub_rows), s.q - j0 - sub);
   it.row0 = s.c0 + j0 + sub;
@@ -59,7 +57,7 @@ __device__ __forceinline__ SparseItem sparse_item(const PageArgs& a, int u, int 
   const int visible = (s.past + min(j0 + a.R, s.q) - 1) / a.bs + 1;
   const int whole = (it.pos0 + 1) / a.bs;  // pages below are seen whole by every row
   const int* sel = a.selected + ((int64_t)(s.c0 + j0) * a.kvh + g) * a.top_k;
-  const int* table = a.table + (int64_t)b * a.max_blocks;
+  const int* table = a.table + (int64_t)s.b * a.max_blocks;
   int kept = 0, top = -1, last_page = -1, n_whole = 0;
   for (int i = 0; i < a.top_k; i += 32 * E) {
     if (a.R != 1 || i > 0) entries(sel, i);

@@ -6,8 +6,10 @@
 ``select_pages``            the pages each query row attends, by a score against the bounds
 ``sparse_paged_attention``  attention over the selected pages
 
-As ``paged_attention``: argument marshalling only, for the C ABI of ``libpagedattn.so``; the
-work runs on the current stream of the tensors' device (or ``stream``), and a call can be
+As ``paged_attention``: argument marshalling only, for the C ABI of ``libpagedattn.so``. The
+common case (outputs of the call's own, the current stream and device) goes through the compiled
+``_step_binding``, whose checks take a microsecond; everything else, refusals among it, through
+the code here. The work runs on the current stream of the tensors' device (or ``stream``), and a call can be
 captured in a CUDA graph. An int32 tensor of one element passed as ``error`` collects the
 ``DEVERR_*`` bits of problems that only device data reveals. With ``stream`` the caller orders
 that stream after the work that makes the inputs, and other streams after the call.
@@ -16,6 +18,9 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.machinery
+import importlib.util
+import os
 from typing import NamedTuple, Optional
 
 import torch
@@ -43,6 +48,24 @@ class BlockTables(NamedTuple):
 
 
 _bound = _prep = None
+_fast = None  # the compiled binding, once loaded
+
+
+def _load_fast():
+    """The compiled calls (csrc/binding.cpp), given the library's entry points."""
+    global _fast
+    if _fast is None:
+        lib = _library()
+        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_step_binding.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with varlen_paged_kv_gb300.build.build()")
+        loader = importlib.machinery.ExtensionFileLoader("_step_binding", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_step_binding", loader))
+        module.bind(*[ctypes.cast(f, _p).value for f in (
+            lib.pa_build_block_tables, lib.pa_qk_norm_rope, lib.pa_update_page_bounds, lib.pa_select_pages,
+            lib.pa_sparse_paged_attention)])
+        _fast = module
+    return _fast
 
 
 def _library():
@@ -145,6 +168,11 @@ def build_block_tables(past_seqlens: torch.Tensor, query_lens: torch.Tensor, blo
     attention call for ``num_tokens`` rows (those behind the last request have slot and position
     -1). ``out``: a BlockTables to write to, as a captured step keeps it. A step that cannot be
     served changes nothing, describes an empty batch and says why in ``error``."""
+    if out is None and stream is None:
+        made = (_fast or _load_fast()).build_block_tables(past_seqlens, query_lens, blocks_held, block_table, free_blocks,
+                                                          free_state, block_size, num_tokens)
+        if made is not None:
+            return BlockTables._make(made)
     index = _index(block_table, "block_table")
     if not _ints(index, past_seqlens, query_lens, blocks_held, block_table, free_blocks, free_state):
         _refuse_ints(index, past_seqlens=past_seqlens, query_lens=query_lens, blocks_held=blocks_held,
@@ -186,6 +214,11 @@ def qk_norm_rope(query: torch.Tensor, key: torch.Tensor, positions: torch.Tensor
     may be ``query`` / ``key`` themselves. Rows with a negative position are left as they were.
     ``interleaved`` pairs components 2u and 2u + 1 instead of u and u + rotary_dim / 2. Returns
     (query_out, key_out)."""
+    if query_out is None and key_out is None and stream is None:
+        made = (_fast or _load_fast()).qk_norm_rope(query, key, positions, num_heads, kv_num_heads, q_norm_weight,
+                                                    k_norm_weight, eps, rotary_dim, theta, interleaved)
+        if made is not None:
+            return made
     index, dtype, shape = _index(query, "query"), query.dtype, query.shape
     if dtype not in _T:
         raise TypeError("query must be float16 or bfloat16")
@@ -261,6 +294,10 @@ def update_page_bounds(key_cache: torch.Tensor, page_bounds: torch.Tensor, bound
     in units of ``bound_scale`` (float32 (kv_num_heads, head_size)). ``num_tokens``: a bound on
     the step's rows, as the shape of its query. For a cache that is there already pass
     ``past_seqlens`` of 0 and the whole lengths."""
+    if stream is None and (_fast or _load_fast()).update_page_bounds(
+            key_cache, page_bounds, bound_scale, cumulative_sequence_length, past_seqlens, block_table, num_tokens,
+            error):
+        return page_bounds
     index, dtype = _index(key_cache, "key_cache"), key_cache.dtype
     if dtype not in _T:
         raise TypeError("key_cache must be float16 or bfloat16")
@@ -288,6 +325,12 @@ def select_pages(query: torch.Tensor, page_bounds: torch.Tensor, bound_scale: to
     ``sink_pages`` pages, the last ``local_pages`` up to the block's first row, the pages of its
     rows, and the best others by an upper bound of q.k summed over the block's rows and heads,
     in whole numbers. ``query`` (N, num_heads * head_size) may be a view of packed rows."""
+    if selected is None and stream is None:
+        made = (_fast or _load_fast()).select_pages(
+            query, page_bounds, bound_scale, cumulative_sequence_length, past_seqlens, block_table, num_heads,
+            kv_num_heads, block_size, top_k, query_block, sink_pages, local_pages, error)
+        if made is not None:
+            return made
     index, dtype = _index(query, "query"), query.dtype
     if dtype not in _T:
         raise TypeError("query must be float16 or bfloat16")
@@ -320,6 +363,12 @@ def sparse_paged_attention(query: torch.Tensor, key_cache: torch.Tensor, value_c
     block. The caches already hold this step's rows. Returns ``output`` (N, num_heads *
     head_size); ``lse`` (float32 (N, num_heads)) receives the rows' log-sum-exp. A row that
     attends nothing gives zeros and -inf; rows behind the last sequence are left as they were."""
+    if output is None and stream is None:
+        made = (_fast or _load_fast()).sparse_paged_attention(
+            query, key_cache, value_cache, cumulative_sequence_length, past_seqlens, block_table, selected, num_heads,
+            kv_num_heads, scale, query_block, lse, error)
+        if made is not None:
+            return made
     index, dtype = _index(query, "query"), query.dtype
     if dtype not in _T:
         raise TypeError("query must be float16 or bfloat16")
