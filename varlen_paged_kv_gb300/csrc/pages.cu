@@ -212,7 +212,8 @@ __device__ void query_codes(const PageArgs& a, int row0, int rows, int g, SelSha
   };
   auto every = [&](auto&& f) {  // the thread's pieces
 #pragma unroll
-    for (int k = 0; k < HOLD; ++k) f(held[k]);
+    for (int k = 0; k < HOLD; ++k)
+      if (k * GROUPS < total) f(held[k]);  // (a decode step has pieces for the first only)
     for (int r = group + HOLD * GROUPS; r < total; r += GROUPS) f(load(r));
   };
   every([&](const uint4& v) { widest(v, false); });
