@@ -148,7 +148,8 @@ cudaError_t launch_bounds(const PageArgs& a, bool bf16, cudaStream_t s);
 cudaError_t launch_select(const PageArgs& a, bool bf16, int sms, cudaStream_t s);
 cudaError_t launch_sparse(const PageArgs& a, bool bf16, int sms, cudaStream_t s);
 
-// A launch whose CTAs along z form one cluster each.
+// A launch that may start before the kernel before it has finished (its blocks wait for that
+// kernel's results) and whose CTAs along z form one cluster each.
 template <typename... KArgs, typename... Actual>
 inline cudaError_t launch_clusters(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t s,
                                    Actual&&... args) {
@@ -160,13 +161,15 @@ inline cudaError_t launch_clusters(void (*kernel)(KArgs...), dim3 grid, int thre
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 1;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = grid.z;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = grid.z;
   cfg.attrs = attr;
-  cfg.numAttrs = grid.z > 1 ? 1 : 0;
+  cfg.numAttrs = grid.z > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Actual&&>(args)...);
 }
 

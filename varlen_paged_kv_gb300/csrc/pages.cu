@@ -57,6 +57,8 @@ __device__ __forceinline__ float half_of(uint32_t w, int e) {
 template <bool BF16>
 __global__ void __launch_bounds__(kBoundChunks * kBoundGroups) bounds_kernel(const PageArgs a) {
   const int chunk_in = threadIdx.x % kBoundChunks, group = threadIdx.x / kBoundChunks, lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_launch_dependents();
   if (blockIdx.x == 0 && blockIdx.y == 0) check_batch(a.cum, a.past, a.B, a.N, a.max_blocks, a.bs, a.error);
   const int u = blockIdx.x;
   const Seq s = find_seq(a.cum, a.past, a.B, a.bs, 2, u, a.N, a.max_blocks, a.bs, lane);
@@ -123,9 +125,7 @@ __global__ void __launch_bounds__(kBoundChunks * kBoundGroups) bounds_kernel(con
 cudaError_t launch_bounds(const PageArgs& a, bool bf16, cudaStream_t s) {
   const int64_t units = (int64_t)a.N / a.bs + 2 * (int64_t)a.B;
   const dim3 grid((unsigned)units, (unsigned)ceil_div(a.kvh * a.hs / 8, kBoundChunks));
-  if (bf16) bounds_kernel<true><<<grid, kBoundChunks * kBoundGroups, 0, s>>>(a);
-  else bounds_kernel<false><<<grid, kBoundChunks * kBoundGroups, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(bf16 ? bounds_kernel<true> : bounds_kernel<false>, grid, dim3(kBoundChunks * kBoundGroups), 0, s, a);
 }
 
 // ---- selection -----------------------------------------------------------------------------
@@ -384,6 +384,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 3 : 1024 / T) select_kernel(cons
   int* list = score + a.max_blocks;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = blockIdx.y, rank = blockIdx.z, C = gridDim.z;
+  pdl_wait();
   if (blockIdx.x == 0 && g == 0 && rank == 0) check_batch(a.cum, a.past, a.B, a.N, a.max_blocks, a.bs, a.error);
   const int u = blockIdx.x;
   if (a.R == 1) {  // (the row is known: its query heads are on their way while the lengths are looked up)

@@ -130,6 +130,8 @@ __global__ void __launch_bounds__(kRotThreads, 7) rotate_kernel(const RotateArgs
   const int64_t w = (int64_t)blockIdx.x * (kRotThreads / 32) + (threadIdx.x >> 5);
   const int64_t row = w / a.split;
   const int part = (int)(w % a.split);
+  pdl_wait();
+  pdl_launch_dependents();
   if (row >= a.N) return;
   const int qs = (a.nh + H - 1) / H, steps = qs + (a.kvh + H - 1) / H;
   const int s0 = (int)((int64_t)steps * part / a.split), s1 = (int)((int64_t)steps * (part + 1) / a.split);
@@ -181,8 +183,7 @@ static cudaError_t launch_rotate_t(RotateArgs a, bool bf16, int sms, cudaStream_
   const int64_t grid = ceil_div((int64_t)a.N * a.split, kRotThreads / 32);
   auto kernel = bf16 ? (a.interleaved ? rotate_kernel<HS, true, true> : rotate_kernel<HS, true, false>)
                      : (a.interleaved ? rotate_kernel<HS, false, true> : rotate_kernel<HS, false, false>);
-  kernel<<<(unsigned)grid, kRotThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(kernel, dim3((unsigned)grid), dim3(kRotThreads), 0, s, a);
 }
 
 cudaError_t launch_rotate(const RotateArgs& a, bool bf16, int hs, int sms, cudaStream_t s) {

@@ -147,6 +147,7 @@ __global__ void __launch_bounds__(kRowsThreads, HS == 256 ? 1 : 2)
     *err = 0;
     fence_mbar_init();
   }
+  pdl_wait();
   if (warp == 4) {
     const SparseItem it = sparse_item(a, blockIdx.x, 0, a.R, g, list, lane);
     if (lane == 0) *item_s = it;
@@ -482,6 +483,7 @@ __global__ void __launch_bounds__(kTileThreads, HS == 256 ? 1 : 2)
     *err = 0;
     fence_mbar_init();
   }
+  pdl_wait();
   if (warp == 0) {
     const SparseItem it = sparse_item(a, u, sub, sub_rows, g, list, lane);
     if (lane == 0) *item_s = it;

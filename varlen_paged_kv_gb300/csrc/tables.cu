@@ -45,6 +45,8 @@ __global__ void __launch_bounds__(kTableThreads) tables_kernel(const TableArgs a
   __shared__ uint32_t part[3][kTableThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   bool bad = false;
+  pdl_wait();
+  pdl_launch_dependents();
   uint32_t carry[3] = {0, 0, 0};
   for (int b0 = 0; b0 < a.B; b0 += kTableThreads) {
     const int b = b0 + tid;
@@ -141,8 +143,7 @@ cudaError_t launch_tables(const TableArgs& a, int sms, cudaStream_t s) {
   const int64_t work = a.N > a.B ? a.N : a.B;
   int64_t grid = ceil_div(work, kTableThreads);
   grid = grid < 1 ? 1 : grid > sms ? sms : grid;
-  tables_kernel<<<(int)grid, kTableThreads, (size_t)smem, s>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(tables_kernel, dim3((unsigned)grid), dim3(kTableThreads), (size_t)smem, s, a);
 }
 
 }  // namespace pa
