@@ -168,8 +168,8 @@ __device__ __forceinline__ uint64_t f2_unpack(uint32_t w) {
 // HOLD * T / (HS / 8) rows are read from memory once (more are read twice). Arithmetic bounds
 // it on prompts, so it runs on packed pairs: rounding to a whole number is adding and taking
 // off 1.5 * 2^23, and the sums by sign come from those of t and |t| (whole numbers below 2^23,
-// so exact in fp32). Products that are not finite are looked for by a sum of x * 0 and left
-// out in a second form of the same steps.
+// so exact in fp32). Products that are not finite are left out in a second form of the
+// same steps.
 template <int HS, bool BF16, int T>
 __device__ void query_codes(const PageArgs& a, int row0, int rows, int g, SelShared<HS, T>& sh) {
   constexpr int CH = HS / 8, GROUPS = T / CH, HOLD = T == 256 ? 8 : 4, WARPS = T / 32;
@@ -193,22 +193,22 @@ __device__ void query_codes(const PageArgs& a, int row0, int rows, int g, SelSha
 #pragma unroll
   for (int k = 0; k < HOLD; ++k)
     held[k] = group + k * GROUPS < total ? load(group + k * GROUPS) : make_uint4(0, 0, 0, 0);
+  // Per channel the largest |q| first, on the 16-bit patterns (their order is that of the values):
+  // the scale is positive and rounding keeps the order, so its product is the largest product.
+  // A channel that reaches infinity or NaN, or whose product does, takes the exact way.
+  uint32_t widest16[4] = {0, 0, 0, 0};
   float most = 0.f;
-  uint64_t odd = f2_make(0.f, 0.f);  // NaN once a product is not finite
   auto widest = [&](const uint4& v, bool filter) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const uint64_t x2 = f2_mul(f2_unpack<BF16>(w[e]), sc[e]);
-      float x0, x1;
-      f2_split(x2, x0, x1);
-      if (filter) {
-        x0 = isfinite(x0) ? x0 : 0.f;
-        x1 = isfinite(x1) ? x1 : 0.f;
+      if (!filter) {
+        widest16[e] = max_u16x2(widest16[e], w[e] & 0x7FFF7FFFu);
       } else {
-        odd = f2_fma(x2, f2_make(0.f, 0.f), odd);
+        float x0, x1;
+        f2_split(f2_mul(f2_unpack<BF16>(w[e]), sc[e]), x0, x1);
+        most = fmax3(most, isfinite(x0) ? fabsf(x0) : 0.f, isfinite(x1) ? fabsf(x1) : 0.f);
       }
-      most = fmax3(most, fabsf(x0), fabsf(x1));
     }
   };
   auto every = [&](auto&& f) {  // the thread's pieces
@@ -218,9 +218,15 @@ __device__ void query_codes(const PageArgs& a, int row0, int rows, int g, SelSha
     for (int r = group + HOLD * GROUPS; r < total; r += GROUPS) f(load(r));
   };
   every([&](const uint4& v) { widest(v, false); });
-  float odd0, odd1;
-  f2_split(odd, odd0, odd1);
-  const bool filter = __syncthreads_or(odd0 != 0.f || odd1 != 0.f);  // (NaN compares unequal)
+  bool odd = false;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float x0, x1;
+    f2_split(f2_mul(f2_unpack<BF16>(widest16[e]), sc[e]), x0, x1);
+    odd |= !isfinite(x0) || !isfinite(x1);
+    most = fmax3(most, fabsf(x0), fabsf(x1));
+  }
+  const bool filter = __syncthreads_or(odd);
   if (filter) {
     most = 0.f;
     every([&](const uint4& v) { widest(v, true); });
