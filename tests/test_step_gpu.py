@@ -551,6 +551,55 @@ def test_sparse_attention_extreme_scores():
         b.check(out, lse, sel.cpu().numpy(), scale=scale)
 
 
+@pytest.mark.parametrize("R", [1, 3, 20])
+def test_many_sequences_most_of_them_empty(R):
+    """Sequences are found from a unit's number: through several levels of search, past runs of empty ones."""
+    r = np.random.default_rng(9)
+    B = 2600
+    q = np.where(r.random(B) < 0.85, 0, r.integers(1, 7, B))
+    q[0] = q[-1] = 0
+    q[1234] = 45
+    b = Batch(33, "bf16", 8, 2, 64, 16, r.integers(0, 120, B), q, extra_rows=5)
+    got = b.bounds.clone()
+    pa.update_page_bounds(b.key_cache, got, b.scale, *b.meta, num_tokens=b.N, error=b.error)
+    keys = b.key_cache.float().cpu().numpy()
+    assert np.array_equal(got.cpu().numpy(), ref.page_bounds(keys, np.zeros(got.shape), b.scale.cpu().numpy(), b.cum,
+                                                             b.past, b.table))
+    b.whole_bounds()
+    sel = torch.full((b.N, 2, 5), -7, dtype=torch.int32, device="cuda")
+    b.select(5, R, selected=sel)
+    assert np.array_equal(sel.cpu().numpy(), b.want_selected(5, R))
+    out, lse = b.attend(sel, R)
+    b.check(out, lse, sel.cpu().numpy(), R)
+    assert int(b.error) == 0
+
+
+@pytest.mark.parametrize("R", [1, 32])
+def test_offsets_past_32_bits(R):
+    """A cache of more than 2^32 bytes and 2^31 values per tensor: pages at its end are where they should be."""
+    kvh, hs, bs = 8, 128, 64
+    small = Batch(34, "bf16", 32, kvh, hs, bs, [bs * 20 + 3], [33], extra_pages=0)
+    small.whole_bounds()
+    sel = small.select(8, R)
+    want, wlse = small.attend(sel, R)
+    blocks = (1 << 31) // (kvh * hs * bs) + 200
+    big = [torch.empty(blocks, bs, kvh, hs, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    shift = blocks - small.blocks
+    for x, y in zip(big, (small.key_cache, small.value_cache)):
+        x[shift:] = y
+    bounds = torch.zeros(blocks, kvh, 2, hs, dtype=torch.int8, device="cuda")
+    table = i32(np.where(small.table >= 0, small.table + shift, -1))
+    total = int(small.past[0] + small.q[0])
+    pa.update_page_bounds(big[0], bounds, small.scale, i32([0, total]), i32([0]), table, num_tokens=total)
+    assert torch.equal(bounds[shift:], small.bounds) and not bounds[:shift].any()
+    kw = dict(num_heads=32, kv_num_heads=kvh, query_block=R)
+    s2 = pa.select_pages(small.query, bounds, small.scale, *small.meta[:2], table, block_size=bs, top_k=8, **kw)
+    assert torch.equal(s2, sel)
+    lse = torch.empty_like(wlse)
+    out = pa.sparse_paged_attention(small.query, *big, *small.meta[:2], table, sel, lse=lse, **kw)
+    assert torch.equal(out, want) and torch.equal(lse, wlse)
+
+
 def test_all_pages_selected_is_the_dense_attention():
     """With room for every page the sparse path is paged_attention on the same cache, within both roundings."""
     for dtype, R in (("fp16", 1), ("bf16", 8)):
