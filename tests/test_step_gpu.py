@@ -194,6 +194,17 @@ def test_qk_norm_rope(nh, kvh, hs, d, dtype, interleaved):
         assert torch.equal(rows[:, (nh + kvh) * hs:], keep[:, (nh + kvh) * hs:])
 
 
+def test_qk_norm_rope_at_far_positions():
+    """Angles of many thousand turns: the 32-bit product with the position defines them, its sine is exact to 2^-21."""
+    pos = np.array([0, 1, 105615, 105616, 131071, (1 << 24) - 1, (1 << 24) + 1, 1 << 30, (1 << 31) - 1])
+    g = torch.Generator().manual_seed(3)
+    q, k = (torch.randn(len(pos), 64 * h, generator=g).half().cuda() for h in (3, 1))
+    got = pa.qk_norm_rope(q, k, i32(pos), num_heads=3, kv_num_heads=1, rotary_dim=64, theta=1e4)
+    for x, h, y in ((q, 3, got[0]), (k, 1, got[1])):
+        want, size = ref.norm_rope(f64(x).reshape(-1, h, 64), None, 1e-6, pos, 64, 1e4, False)
+        assert (np.abs(f64(y).reshape(want.shape) - want) <= rotate_bound(want, size, "fp16")).all()
+
+
 def test_qk_norm_rope_leaves_rows_of_no_sequence():
     q = torch.randn(6, 256).half().cuda()
     k = torch.randn(6, 64).half().cuda()
