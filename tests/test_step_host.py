@@ -101,7 +101,7 @@ def test_sparse_refusals(lib, name):
         assert call(lib, name, dims(), out=0) == 1 and call(lib, name, dims(), lse=FAKE + 2) == 1
 
 
-def test_python_refuses_host_tensors_and_wrong_types():
+def test_python_refuses_host_tensors_and_wrong_types(lib):
     i = torch.zeros(2, dtype=torch.int32)
     with pytest.raises(ValueError):
         pa.build_block_tables(i, i, i, i.reshape(2, 1), i, i, block_size=16, num_tokens=1)
