@@ -308,10 +308,6 @@ pa_status launch_all(pa::Args& args, const pa_dims* d, const void* query, void* 
 // the helpers that the operators' entry points share (ops.cuh)
 namespace pa {
 pa_status cuda_fail(cudaError_t e, const char* what) { return ::cuda_fail(e, what); }
-pa_status cuda_fail_text(const char* text) {
-  g_last_error = text;
-  return PA_ERR_CUDA;
-}
 void count_launch() { ++g_launches; }
 bool device_sms(int* sms) {
   DeviceInfo info;

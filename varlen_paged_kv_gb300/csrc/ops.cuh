@@ -8,7 +8,6 @@ namespace pa {
 
 // ---- host helpers defined with the paged-attention entry points (api.cu) -------------------
 pa_status cuda_fail(cudaError_t e, const char* what);  // records the message for pa_last_error
-pa_status cuda_fail_text(const char* text);
 void count_launch();
 bool device_sms(int* sms);  // SMs of the current device
 // 3-D map over a cache of 16-bit values viewed as (head_size, kv_heads, slots), box 64 x 1 x
