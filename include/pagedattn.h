@@ -252,8 +252,10 @@ pa_status pa_static_workspace_read_device_error(void* stream, uint32_t* error_bi
  * program: the same work partition, the same SM split of a mixed batch), and `stages`
  * picks which of them this call launches. For a decode-only call that the decode kernel
  * plans itself (see pa_dims.max_query_len) PA_STAGE_PLAN is the reset of the workspace's
- * counters and PA_STAGE_PREFILL is empty; PA_STAGE_CACHE_WRITE is empty too when the
- * decode kernel writes this call's rows. The two attention kernels of a mixed batch run
+ * counters and PA_STAGE_PREFILL is empty; where the decode kernel writes this call's rows,
+ * PA_STAGE_CACHE_WRITE is empty too in a call that runs PA_STAGE_DECODE, and writes the rows
+ * in one that does not (so that PA_STAGE_PLAN | PA_STAGE_CACHE_WRITE always leaves the rows in
+ * the caches, whatever reads them next). The two attention kernels of a mixed batch run
  * side by side only when one call launches both. A stage reads what earlier stages left
  * in the workspace, so a caller that splits a call across several calls must pass the
  * same arguments and workspace to each and keep them in stage order. Used to time one

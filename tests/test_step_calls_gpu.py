@@ -1,0 +1,130 @@
+"""The operators around the attention call in the calls a serving loop makes of them: stages of the
+dense call beside them, values that are not finite, host threads, sizes at the limits."""
+import numpy as np
+import pytest
+import torch
+
+import varlen_paged_kv_gb300 as pa
+from test_step_gpu import DT, Batch, f64, i32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.fail("CUDA is required for the gpu tests")
+    from varlen_paged_kv_gb300 import build
+    build.build()
+
+
+# ---- the cache write without the dense attention ---------------------------------------------
+
+
+class Rows:
+    """A batch with new rows still outside its caches."""
+
+    def __init__(self, dtype, nh, kvh, hs, past, q, packed, bs=16):
+        self.b = b = Batch(50, dtype, nh, kvh, hs, bs, past, q)
+        b.key_cache.nan_to_num_(0)
+        b.value_cache.nan_to_num_(0)
+        g = torch.Generator().manual_seed(7)
+        rows = torch.randn(b.N, (nh + 2 * kvh) * hs, generator=g).to(DT[dtype]).cuda()
+        self.args = ((rows, None, None) if packed else
+                     tuple(x.contiguous() for x in rows.split([nh * hs, kvh * hs, kvh * hs], 1)))
+        self.new = [x.reshape(b.N, kvh, hs) for x in rows.split([nh * hs, kvh * hs, kvh * hs], 1)[1:]]
+        dims = pa.make_dims(b.N, len(past), hs, b.blocks, bs, b.table.shape[1], DT[dtype], max_query_len=max(q))
+        self.ws = torch.zeros(pa.workspace_size(dims, nh, kvh), dtype=torch.uint8, device="cuda")
+
+    def call(self, stages, meta=None, bound=None):
+        b = self.b
+        pa.paged_attention(*self.args, b.key_cache, b.value_cache, *(meta or b.meta), num_heads=b.nh,
+                           kv_num_heads=b.kvh, workspace=self.ws, max_query_len=bound or int(b.q.max()), stages=stages)
+
+    def want(self, skip=()):
+        """The caches with the new rows in their places, but those of the sequences in `skip`."""
+        b, out = self.b, []
+        for cache, rows in zip((b.key_cache, b.value_cache), self.new):
+            c = cache.clone()
+            for s in range(len(b.past)):
+                for j in range(int(b.q[s]) if s not in skip else 0):
+                    p = int(b.past[s]) + j
+                    c[b.table[s, p // b.bs], p % b.bs] = rows[int(b.cum[s]) + j]
+            out.append(c)
+        return out
+
+    def caches_are(self, want):
+        return torch.equal(self.b.key_cache, want[0]) and torch.equal(self.b.value_cache, want[1])
+
+
+STEPS = [("fp16", 8, 2, 128, [30, 50, 0, 15], [1, 1, 1, 1], False), ("bf16", 8, 2, 128, [30, 50, 0, 15], [1] * 4, True),
+         ("fp16", 4, 4, 64, [3, 0, 100], [4, 1, 3], True), ("bf16", 16, 2, 256, [200, 31], [2, 2], False),
+         ("fp16", 4, 4, 64, [20] * 300, [1] * 300, False)]  # (more sequences than plan themselves)
+
+
+@pytest.mark.parametrize("dtype,nh,kvh,hs,past,q,packed", STEPS)
+def test_the_cache_write_of_a_decode_step_stands_alone(dtype, nh, kvh, hs, past, q, packed):
+    """A decode-only call that stops before its attention (another one reads the cache next) has written its rows."""
+    for groups in ([pa.STAGE_PLAN | pa.STAGE_CACHE_WRITE], [pa.STAGE_PLAN, pa.STAGE_CACHE_WRITE],
+                   [pa.STAGE_PLAN | pa.STAGE_CACHE_WRITE | pa.STAGE_PREFILL]):
+        r = Rows(dtype, nh, kvh, hs, past, q, packed)
+        want = r.want()
+        for stages in groups:
+            r.call(stages)
+        assert pa.read_device_error(r.ws) == 0
+        assert r.caches_are(want)
+        r.call(pa.STAGE_DECODE)  # the rest of the same call
+        assert pa.read_device_error(r.ws) == 0 and r.caches_are(want)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_a_refused_decode_step_writes_nothing_and_says_so(packed):
+    past, q = [30, 50, 0, 15], [1, 1, 2, 1]
+    for cum, lens, bound in (([0, 1, 2, 4, 6], past, 2), ([0, 1, 3, 2, 5], past, 2), (None, [30, -1, 0, 15], 2),
+                             (None, [30, 5000, 0, 15], 2), (None, past, 1)):
+        r = Rows("fp16", 8, 2, 128, past, q, packed)
+        meta = (r.b.meta[0] if cum is None else i32(cum), i32(lens), r.b.meta[2])
+        want = [r.b.key_cache.clone(), r.b.value_cache.clone()]
+        r.call(pa.STAGE_PLAN | pa.STAGE_CACHE_WRITE, meta, bound)
+        assert pa.read_device_error(r.ws) == pa.DEVERR_BAD_BATCH and r.caches_are(want)
+    # a page outside the pool: its row is dropped, the others are written
+    r = Rows("fp16", 8, 2, 128, past, q, packed)
+    table = r.b.table.copy()
+    table[1, 50 // 16] = r.b.blocks
+    want = r.want(skip=(1,))
+    r.call(pa.STAGE_PLAN | pa.STAGE_CACHE_WRITE, (*r.b.meta[:2], i32(table)))
+    assert pa.read_device_error(r.ws) == pa.DEVERR_BAD_BLOCK and r.caches_are(want)
+
+
+@pytest.mark.parametrize("kv_quant", ["int8", "int4"])
+def test_a_refused_decode_step_on_integer_caches_says_so(kv_quant):
+    b = Batch(51, "fp16", 8, 2, 128, 16, [30, 50], [1, 1])
+    kc, vc = (torch.full((b.blocks, 16, 2, 128 if kv_quant == "int8" else 64), 77, dtype=torch.uint8, device="cuda")
+              for _ in range(2))
+    k = torch.randn(2, 256, device="cuda").half()
+    s = torch.full((2, 128), 0.03, device="cuda")
+    dims = pa.make_dims(2, 2, 128, b.blocks, 16, b.table.shape[1], torch.float16, max_query_len=1, kv_dtype=kv_quant)
+    ws = torch.zeros(pa.workspace_size(dims, 8, 2), dtype=torch.uint8, device="cuda")
+    pa.paged_attention(b.query.contiguous(), k, k, kc, vc, i32([0, 1, 3]), *b.meta[1:], num_heads=8, kv_num_heads=2,
+                       workspace=ws, max_query_len=1, stages=pa.STAGE_PLAN | pa.STAGE_CACHE_WRITE, kv_quant=kv_quant,
+                       k_scale=s, v_scale=s)
+    assert pa.read_device_error(ws) == pa.DEVERR_BAD_BATCH and (kc == 77).all() and (vc == 77).all()
+
+
+def test_a_sparse_decode_step_with_derived_slots():
+    """The decode call as the dense attention makes it, its attention replaced: what explicit slots give."""
+    outs = []
+    for derived in (True, False):
+        r = Rows("bf16", 8, 2, 128, [100, 47, 64], [1, 1, 1], False)
+        b = r.b
+        if derived:
+            r.call(pa.STAGE_PLAN | pa.STAGE_CACHE_WRITE)
+        else:
+            slots = i32([b.table[s, b.past[s] // 16] * 16 + b.past[s] % 16 for s in range(3)])
+            pa.paged_attention(*r.args, b.key_cache, b.value_cache, *b.meta, slots, num_heads=8, kv_num_heads=2,
+                               stages=pa.STAGE_PLAN | pa.STAGE_CACHE_WRITE)
+        b.whole_bounds()
+        sel = b.select(4)
+        outs.append((b.bounds, sel, *b.attend(sel)))
+    for x, y in zip(*outs):
+        assert torch.equal(x, y)

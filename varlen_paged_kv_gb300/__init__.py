@@ -146,7 +146,7 @@ def paged_attention(query: torch.Tensor, key: Optional[torch.Tensor], value: Opt
     ``lse`` (optional, float32 (num_tokens, num_heads)) receives each output row's natural-log
     log-sum-exp of the scaled scores.
     ``stages`` (PA_STAGE_* bits) launches only those kernels of the call's program, as
-    pa_paged_attention_stages does.
+    pa_paged_attention_stages does; STAGE_PLAN | STAGE_CACHE_WRITE is the cache write alone.
     ``qk_prep`` (optional): dict(q_norm_weight=tensor (head_size,) of the
     query dtype or None, k_norm_weight=... or None, eps=float, rotary_dim=int, theta=float):
     RMSNorm of the query and key heads, then the rotary embedding at each row's position,

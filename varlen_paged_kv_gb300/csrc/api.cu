@@ -202,8 +202,9 @@ pa_status launch_all(pa::Args& args, const pa_dims* d, const void* query, void* 
   // its own share and writes the new rows of the tiles it loads.
   // (With the Q/K preparation or integer caches the cache-write kernel still runs: it writes
   // the prepared or scaled query rows and the rows' codes, checking the batch itself.)
-  // Its stages: PA_STAGE_PLAN is that reset, PA_STAGE_CACHE_WRITE is empty when the decode
-  // kernel writes the rows, PA_STAGE_DECODE is the self-planned decode kernel.
+  // Its stages: PA_STAGE_PLAN is that reset, PA_STAGE_DECODE the self-planned decode kernel.
+  // Where the decode kernel writes the rows, PA_STAGE_CACHE_WRITE is empty in a call that runs
+  // it; a call that does not (another attention may read the cache next) writes them here.
   const bool self_plan = d->route == PA_ROUTE_AUTO && d->max_query_len > 0 &&
                          (int64_t)d->max_query_len * args.G <= pa::kDecRows && args.slot_mapping == nullptr &&
                          args.forced_split <= 0 && args.B >= 1 && args.B <= pa::self_max_b(hs) && args.N > 0 &&
@@ -217,7 +218,7 @@ pa_status launch_all(pa::Args& args, const pa_dims* d, const void* query, void* 
       ++g_launches;
       if (cudaError_t e = pa::launch_decode_prep(args, stream)) return cuda_fail(e, "decode_prep_kernel launch");
     }
-    stages &= self_write_rows ? PA_STAGE_DECODE : PA_STAGE_CACHE_WRITE | PA_STAGE_DECODE;
+    stages &= self_write_rows && (stages & PA_STAGE_DECODE) ? PA_STAGE_DECODE : PA_STAGE_CACHE_WRITE | PA_STAGE_DECODE;
   }
   if (stages & PA_STAGE_PLAN) {
     ++g_launches;

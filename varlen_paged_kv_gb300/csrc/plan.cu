@@ -1019,13 +1019,13 @@ __device__ __forceinline__ int own_mirror_base(const Args& a, int b, int lane) {
 // One instantiation per kind of write, so that each keeps only the registers it needs and
 // stays many warps deep (at most 64 registers: four blocks of 256 per SM): 0 = bit copy,
 // one warp per token, 4 = the same beside this call's planner, 5 = that with the fp16 V
-// copy; 1 = Q/K preparation, 2 = integer caches, 3 = both, over (token, unit) tasks, the
+// copy, 6 = the bit copy of a batch that no planner has checked; 1 = Q/K preparation, 2 = integer caches, 3 = both, over (token, unit) tasks, the
 // units being the token's nh query heads and then its kvh KV heads (each a short dependent
 // chain of a load, warp reductions and a store); each warp takes a contiguous run of them.
 template <int MODE>
 __global__ void __launch_bounds__(256, 4) cache_write_kernel(const Args a) {
   constexpr bool COPY = MODE == 0 || MODE >= 4;  // bit copy
-  constexpr bool early = MODE >= 4;
+  constexpr bool early = MODE == 4 || MODE == 5;
   const int lane = threadIdx.x & 31;
   const int warps = (int)((gridDim.x * blockDim.x) >> 5);
   const int gw = (int)((blockIdx.x * blockDim.x + threadIdx.x) >> 5);
@@ -1075,17 +1075,20 @@ __global__ void __launch_bounds__(256, 4) cache_write_kernel(const Args a) {
     pdl_launch_dependents();
     if (!a.hdr->valid) return;
   }
-  if constexpr (!COPY) {
+  if constexpr (!COPY || MODE == 6) {
     if (a.self_plan) {
-      // no planner ran: refuse an inconsistent batch here as well (the decode kernel, which
-      // checks it too, reports it), so that nothing is written
+      // no planner ran: refuse an inconsistent batch here as well, so that nothing is written
+      // (the decode kernel checks it too, but the call may end with this stage)
       bool bad = threadIdx.x == 0 && (a.cum[0] != 0 || a.cum[a.B] != a.N);
       for (int bb = threadIdx.x; bb < a.B; bb += blockDim.x) {
         const int64_t q = (int64_t)a.cum[bb + 1] - a.cum[bb], kv = (int64_t)a.past[bb] + q;
         bad |= q < 0 || a.past[bb] < 0 || kv > (int64_t)a.max_blocks * a.bs ||
                (a.max_query_len > 0 && q > a.max_query_len);
       }
-      if (__syncthreads_or(bad)) return;
+      if (__syncthreads_or(bad)) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&a.hdr->error, PA_DEVERR_BAD_BATCH);
+        return;
+      }
     }
   }
   if constexpr (MODE == 2) {  // integer caches without the preparation: the wider tasks
@@ -1267,6 +1270,7 @@ cudaError_t launch_cache_write(const Args& a, int sms, cudaStream_t s) {
   if (a.cw_early)
     return launch_pdl(a.mirror_keys > 0 && !a.slot_mapping ? cache_write_kernel<5> : cache_write_kernel<4>, dim3(grid),
                       dim3(256), 0, s, a);
+  if (a.self_plan) return launch_pdl(cache_write_kernel<6>, dim3(grid), dim3(256), 0, s, a);
   return launch_pdl(cache_write_kernel<0>, dim3(grid), dim3(256), 0, s, a);
 }
 
