@@ -447,7 +447,8 @@ pa_status pa_select_pages(const void* query, const int8_t* page_bounds, const fl
  * selected[cumulative_sequence_length[b] + j0][g], j0 = j - j mod query_block (the selection of
  * the block's first row; the other rows' are not read). Entries are logical pages in strictly
  * ascending order; -1 entries are passed over, anything else is skipped with
- * PA_DEVERR_BAD_BLOCK. A row that attends no key gives zeros and an lse of -inf. scale, output
+ * PA_DEVERR_BAD_BLOCK. A row that attends no key gives zeros and an lse of -inf; one that attends a
+ * key whose score is NaN gives NaN and an lse of NaN. scale, output
  * and lse (fp32 (N, num_heads) or NULL) as in pa_paged_attention_lse; query rows may be strided.
  * The caches hold T and already hold this step's rows. A value row that is not finite reaches
  * every row of a query block whose last row attends it, the rows before it among them (their

@@ -128,3 +128,63 @@ def test_a_sparse_decode_step_with_derived_slots():
         outs.append((b.bounds, sel, *b.attend(sel)))
     for x, y in zip(*outs):
         assert torch.equal(x, y)
+
+
+# ---- values that are not finite --------------------------------------------------------------
+
+
+def check_nan_rows(b, sel, R, bad, spoil, scale=0.0):
+    """After spoil() the rows `bad` are NaN with an lse of NaN, and every other row is what it was within the bounds."""
+    clean = b.attend(sel, R, scale)
+    keep = [x.clone() for x in (b.rows, b.key_cache)]
+    spoil()
+    out, lse = b.attend(sel, R, scale)
+    assert out[bad].isnan().all() and lse[bad].isnan().all()
+    b.rows.copy_(keep[0])
+    b.key_cache.copy_(keep[1])
+    out[bad], lse[bad] = clean[0][bad], clean[1][bad]
+    b.check(out, lse, sel.cpu().numpy(), R, scale)
+    assert int(b.error) == 0
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("past,q,R", [([300, 2], [1, 1], 1),             # one list per CTA pair
+                                      ([64 * 40, 700], [1, 3], 1),       # clusters
+                                      ([64 * 40], [16], 16),             # clusters of tiles
+                                      ([300, 0, 90], [20, 40, 1], 16)])
+def test_a_query_of_nan_gives_nan(past, q, R, dtype):
+    for scale in (0.0, -0.1):
+        b = Batch(52, dtype, 8, 2, 128, 64, past, q, extra_rows=1)
+        b.whole_bounds()
+        sel = b.select(30, R)
+        check_nan_rows(b, sel, R, [0], lambda: b.query[0].fill_(float("nan")), scale)
+        last = int(b.cum[-1]) - 1
+
+        def some_channels():
+            for r in (0, last):
+                b.query[r, ::16] = float("nan")
+
+        check_nan_rows(b, sel, R, [0, last], some_channels, scale)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("nh,kvh,hs,R", [(8, 2, 128, 1), (16, 2, 256, 1), (32, 2, 128, 4), (16, 2, 256, 4)])
+def test_a_key_of_nan_gives_nan(nh, kvh, hs, R, dtype):
+    """Where the key is the only one that a warp, a tile or a CTA of a cluster has, too."""
+    nan = float("nan")
+    for bs, past, n in ((16, 48, 1), (64, 64 * 20, 1), (64, 64 * 20 + 5, 130), (16, 16 * 33, 17)):
+        b = Batch(53, dtype, nh, kvh, hs, bs, [past, 200], [1, 1])
+        b.whole_bounds()
+        sel = b.select(40, R)  # every page
+
+        def spoil():
+            for p in range(past - n + 1, past + 1):  # the last n keys
+                b.key_cache[b.table[0, p // bs], p % bs] = nan
+
+        check_nan_rows(b, sel, R, [0], spoil)
+    # a key that only a block's last row sees
+    if R == 4:
+        b = Batch(54, dtype, nh, kvh, hs, 16, [47], [2])
+        b.whole_bounds()
+        sel = b.select(8, R)
+        check_nan_rows(b, sel, R, [1], lambda: b.key_cache[b.table[0, 3], 0].fill_(nan))

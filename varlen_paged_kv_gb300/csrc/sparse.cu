@@ -322,6 +322,10 @@ __global__ void __launch_bounds__(kRowsThreads, HS == 256 ? 1 : 2)
       l0 += __shfl_xor_sync(0xffffffffu, l0, d);
       l1 += __shfl_xor_sync(0xffffffffu, l1, d);
     }
+    // scores of NaN alone leave no maximum but a sum of NaN, which the merge must not take for a
+    // row without keys
+    if (m0 == -INFINITY && l0 != l0) m0 = 0.f;
+    if (m1 == -INFINITY && l1 != l1) m1 = 0.f;
     if (tq == 0) {
       ml[w * 16 + gq] = m0, ml[w * 16 + gq + 8] = m1;
       ml[64 + w * 16 + gq] = l0, ml[64 + w * 16 + gq + 8] = l1;
@@ -716,6 +720,7 @@ __global__ void __launch_bounds__(kTileThreads, HS == 256 ? 1 : 2)
     (side ? half[row].y : half[row].x) = l;
     named_bar_sync(bar, 64);
     l = half[row].x + half[row].y;
+    if (m_used == -INFINITY && l != l) m_used = 0.f;  // scores of NaN alone: not a row without keys
     if (C > 1 && side == 0) ml[row] = m_used, ml[128 + row] = l;
   }
 
