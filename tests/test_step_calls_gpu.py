@@ -188,3 +188,27 @@ def test_a_key_of_nan_gives_nan(nh, kvh, hs, R, dtype):
         b.whole_bounds()
         sel = b.select(8, R)
         check_nan_rows(b, sel, R, [1], lambda: b.key_cache[b.table[0, 3], 0].fill_(nan))
+
+
+# ---- sizes at the limits ---------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("free", [2, 0])
+def test_block_tables_of_as_many_rows_as_there_can_be(free):
+    """The last step of a loop over 2^31 - 2 rows ends past 2^31; also where the step is refused."""
+    n = 2 ** 31 - 2
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    table = i32([[5, -1], [7, -1]])
+    t = pa.build_block_tables(i32([15, 3]), i32([2, 1]), i32([1, 1]), table, i32([9, 4]), i32([1, free]), block_size=16,
+                              num_tokens=n)
+    torch.cuda.synchronize()
+    assert int(t.error) == (0 if free else pa.DEVERR_NO_BLOCKS)
+    rows = [[5 * 16 + 15, 4 * 16, 7 * 16 + 3], [15, 16, 3]] if free else [[], []]
+    for got, want in zip((t.slot_mapping, t.positions), rows):
+        assert got[: len(want)].tolist() == want
+        for at in range(len(want), n, 1 << 28):
+            assert int(got[at: at + (1 << 28)].max()) == -1 == int(got[at: at + (1 << 28)].min())
+    assert t.cumulative_sequence_length.tolist() == ([0, 2, 3] if free else [0, 0, 0])
+    assert t.blocks_held.tolist() == ([2, 1] if free else [1, 1]) and t.free_state.tolist() == ([0, 1] if free else [1, 0])
+    assert table.tolist() == ([[5, 4], [7, -1]] if free else [[5, -1], [7, -1]])

@@ -95,7 +95,8 @@ __global__ void __launch_bounds__(kTableThreads) tables_kernel(const TableArgs a
     err = PA_DEVERR_BAD_BATCH;
   else if (carry[1] > (uint32_t)count)
     err = PA_DEVERR_NO_BLOCKS;
-  const int i0 = blockIdx.x * kTableThreads + tid, step = gridDim.x * kTableThreads;
+  // (unsigned: the step past the last of up to 2^31 - 2 rows must not turn negative)
+  const uint32_t i0 = blockIdx.x * kTableThreads + tid, step = gridDim.x * kTableThreads;
   if (i0 == 0) {
     a.error[0] = err;
     a.cum[0] = 0;
@@ -103,21 +104,21 @@ __global__ void __launch_bounds__(kTableThreads) tables_kernel(const TableArgs a
     a.state_out[1] = err ? count : count - (int)carry[1] + (int)carry[2];
   }
   if (err) {  // refused: nothing changes, and the step has no rows
-    for (int b = i0; b < a.B; b += step) a.cum[b + 1] = 0, a.held_out[b] = a.held[b];
-    for (int i = i0; i < a.N; i += step) a.slots[i] = a.positions[i] = -1;
+    for (uint32_t b = i0; b < (uint32_t)a.B; b += step) a.cum[b + 1] = 0, a.held_out[b] = a.held[b];
+    for (uint32_t i = i0; i < (uint32_t)a.N; i += step) a.slots[i] = a.positions[i] = -1;
     return;
   }
-  for (int b = i0; b < a.B; b += step) {
+  for (uint32_t b = i0; b < (uint32_t)a.B; b += step) {
     a.cum[b + 1] = (int)cum[b + 1];
     a.held_out[b] = a.query_lens[b] < 0 ? 0 : a.held[b] + (int)(grow[b + 1] - grow[b]);
   }
   // rows: consecutive threads have consecutive rows, mostly of one request
   const int max_page = (0x7fffffff - (a.bs - 1)) / a.bs;
-  for (int i = i0; i < a.N; i += step) {
+  for (uint32_t i = i0; i < (uint32_t)a.N; i += step) {
     int slot = -1, pos = -1;
-    if (i < (int)carry[0]) {
+    if (i < carry[0]) {
       const int b = last_at_most(cum, a.B, i);
-      pos = a.past[b] + (i - (int)cum[b]);
+      pos = a.past[b] + (int)(i - cum[b]);
       const int col = pos / a.bs, held = a.held[b];
       const int page = col < held ? a.table[(int64_t)b * a.max_blocks + col]
                                   : a.ring[((int64_t)head + grow[b] + (col - held)) % a.cap];
@@ -126,13 +127,13 @@ __global__ void __launch_bounds__(kTableThreads) tables_kernel(const TableArgs a
     a.slots[i] = slot;
     a.positions[i] = pos;
   }
-  for (int k = i0; k < (int)carry[1]; k += step) {  // new columns
+  for (uint32_t k = i0; k < carry[1]; k += step) {  // new columns
     const int b = last_at_most(grow, a.B, k);
-    a.table[(int64_t)b * a.max_blocks + a.held[b] + (k - (int)grow[b])] = a.ring[((int64_t)head + k) % a.cap];
+    a.table[(int64_t)b * a.max_blocks + a.held[b] + (int)(k - grow[b])] = a.ring[((int64_t)head + k) % a.cap];
   }
-  for (int k = i0; k < (int)carry[2]; k += step) {  // returned pages
+  for (uint32_t k = i0; k < carry[2]; k += step) {  // returned pages
     const int b = last_at_most(back, a.B, k);
-    a.ring[((int64_t)head + count + k) % a.cap] = a.table[(int64_t)b * a.max_blocks + (k - (int)back[b])];
+    a.ring[((int64_t)head + count + k) % a.cap] = a.table[(int64_t)b * a.max_blocks + (int)(k - back[b])];
   }
 }
 
