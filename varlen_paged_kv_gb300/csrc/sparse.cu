@@ -799,9 +799,9 @@ __global__ void __launch_bounds__(kTileThreads, HS == 256 ? 1 : 2)
     }
     cluster_sync();  // no CTA leaves while another reads its shared memory
   }
-  if (threadIdx.x == 0 && *err && a.error) atomicOr(a.error, *err);
   tc_fence_before();
-  __syncthreads();
+  __syncthreads();  // (no warp waits any more: whichever gave up has said so)
+  if (threadIdx.x == 0 && *err && a.error) atomicOr(a.error, *err);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, L::kTmem);
