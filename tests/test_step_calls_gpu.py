@@ -1,11 +1,13 @@
 """The operators around the attention call in the calls a serving loop makes of them: stages of the
 dense call beside them, values that are not finite, host threads, sizes at the limits."""
+import threading
+
 import numpy as np
 import pytest
 import torch
 
 import varlen_paged_kv_gb300 as pa
-from test_step_gpu import DT, Batch, f64, i32
+from test_step_gpu import DT, Batch, i32, run_tables, table_state
 
 pytestmark = pytest.mark.gpu
 
@@ -212,3 +214,69 @@ def test_block_tables_of_as_many_rows_as_there_can_be(free):
     assert t.cumulative_sequence_length.tolist() == ([0, 2, 3] if free else [0, 0, 0])
     assert t.blocks_held.tolist() == ([2, 1] if free else [1, 1]) and t.free_state.tolist() == ([0, 1] if free else [1, 0])
     assert table.tolist() == ([[5, 4], [7, -1]] if free else [[5, -1], [7, -1]])
+
+
+# ---- host threads ----------------------------------------------------------------------------
+
+
+def in_a_new_thread(f):
+    """f() in a host thread of its own, where no other CUDA call has been made."""
+    got = []
+
+    def body():
+        try:
+            got.append(f())
+        except Exception as e:  # noqa: BLE001
+            got.append(e)
+
+    t = threading.Thread(target=body)
+    t.start()
+    t.join()
+    if isinstance(got[0], Exception):
+        raise got[0]
+    return got[0]
+
+
+@pytest.mark.parametrize("given", [False, True])  # outputs of the caller's, or of the call's
+def test_first_calls_of_a_host_thread(given):
+    """A thread's first call of the runtime gives it its context; no operator needs another call to have done so."""
+    for R in (1, 16):
+        b = Batch(61, "fp16", 8, 2, 128, 16, [300, 40], [20, 1])
+        b.whole_bounds()
+        sel = b.select(6, R)
+        out, _ = b.attend(sel, R)
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        kw = dict(num_heads=8, kv_num_heads=2, query_block=R)
+        mine = dict(output=torch.empty_like(out), stream=side) if given else {}
+        got = in_a_new_thread(lambda: pa.sparse_paged_attention(b.query, b.key_cache, b.value_cache, *b.meta, sel,
+                                                                **kw, **mine))
+        torch.cuda.synchronize()
+        assert torch.equal(got, out)
+        mine = dict(selected=torch.empty_like(sel), stream=side) if given else {}
+        got = in_a_new_thread(lambda: b.select(6, R, **mine))
+        torch.cuda.synchronize()
+        assert torch.equal(got, sel)
+    t = table_state(np.random.default_rng(8), 9, 16, 8, 60, 20, 0.2)
+    want, dev = run_tables(*t, 16, 200)
+    again = in_a_new_thread(lambda: pa.build_block_tables(*dev, block_size=16, num_tokens=200,
+                                                          out=want if given else None))
+    torch.cuda.synchronize()
+    assert torch.equal(again.slot_mapping, want.slot_mapping)
+    q = b.query.contiguous()
+    pos = i32(np.arange(len(q)))
+    want = pa.qk_norm_rope(q, q[:, :256], pos, num_heads=8, kv_num_heads=2, rotary_dim=64)
+    got = in_a_new_thread(lambda: pa.qk_norm_rope(q, q[:, :256], pos, num_heads=8, kv_num_heads=2, rotary_dim=64,
+                                                  query_out=torch.empty_like(q) if given else None))
+    kept = b.bounds.clone()
+    in_a_new_thread(b.whole_bounds)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(b.bounds, kept)
+
+
+def test_a_stage_of_the_dense_call_first_in_a_host_thread():
+    r = Rows("fp16", 8, 2, 128, [30, 50], [1, 1], False)
+    r.call(pa.STAGE_PLAN | pa.STAGE_CACHE_WRITE)
+    torch.cuda.synchronize()
+    in_a_new_thread(lambda: r.call(pa.STAGE_DECODE))
+    assert pa.read_device_error(r.ws) == 0

@@ -43,31 +43,39 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// 3-D map over a cache viewed as (head_size, kv_heads, slots); box = 64 x 1 x rows, 128B swizzle
-bool cache_map(CUtensorMap* m, void* base, pa_dtype dt, int hs, int kvh, int64_t slots, int rows) {
+// cuTensorMapEncodeTiled. It wants a current context, which a host thread has only from its
+// first runtime call on (looking up the current device is none), so a failing call is made
+// again after such a call.
+template <typename... A>
+bool encode_tiled(A... a) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
+  if (enc(a...) == CUDA_SUCCESS) return true;
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && enc(a...) == CUDA_SUCCESS;
+}
+
+// 3-D map over a cache viewed as (head_size, kv_heads, slots); box = 64 x 1 x rows, 128B swizzle
+bool cache_map(CUtensorMap* m, void* base, pa_dtype dt, int hs, int kvh, int64_t slots, int rows) {
   cuuint64_t dims[3] = {(cuuint64_t)hs, (cuuint64_t)kvh, (cuuint64_t)slots};
   cuuint64_t strides[2] = {(cuuint64_t)hs * 2, (cuuint64_t)kvh * hs * 2};
   cuuint32_t box[3] = {64, 1, (cuuint32_t)rows};
   cuuint32_t es[3] = {1, 1, 1};
-  return enc(m, dt == PA_BFLOAT16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base, dims,
-             strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_tiled(m, dt == PA_BFLOAT16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base,
+                      dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // 2-D map over the query rows (row width in elements, rows); box = 64 x 128, 128B swizzle
 bool query_map(CUtensorMap* m, const void* base, pa_dtype dt, int64_t width, int64_t rows) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
   cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)width * 2};
   cuuint32_t box[2] = {64, (cuuint32_t)pa::kPreTileQ};
   cuuint32_t es[2] = {1, 1};
-  return enc(m, dt == PA_BFLOAT16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-             const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_tiled(m, dt == PA_BFLOAT16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                      const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 int gcd(int a, int b) {
@@ -151,34 +159,30 @@ int64_t qexp_values(const pa_dims* d, int32_t nh) {
 // 3-D map over an integer cache viewed as (row bytes, kv_heads, slots), uint8 elements; box =
 // min(row bytes, 128) x 1 x rows with the swizzle of that width
 bool code_cache_map(CUtensorMap* m, void* base, int row_bytes, int kvh, int64_t slots, int rows) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
   const int box = row_bytes < 128 ? row_bytes : 128;
   cuuint64_t dims[3] = {(cuuint64_t)row_bytes, (cuuint64_t)kvh, (cuuint64_t)slots};
   cuuint64_t strides[2] = {(cuuint64_t)row_bytes, (cuuint64_t)kvh * row_bytes};
   cuuint32_t boxd[3] = {(cuuint32_t)box, 1, (cuuint32_t)rows};
   cuuint32_t es[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, boxd, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             box == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-             // a box row is one head's code row: fetch what it covers (the next head's row
-             // at the next 128 or 64 bytes belongs to another CTA's tile)
-             box == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, boxd, es,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, box == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                      // a box row is one head's code row: fetch what it covers (the next head's row
+                      // at the next 128 or 64 bytes belongs to another CTA's tile)
+                      box == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // 2-D map over an integer cache viewed as (kv_heads * row bytes, slots), uint8 elements; box =
 // 128 bytes x rows from a head's row start (that head's code row, then the next head's, read
 // and not used; zeros past the last head), 128-byte swizzle: the prefill kernel's code tiles
 bool code_tile_map(CUtensorMap* m, void* base, int row_bytes, int kvh, int64_t slots, int rows) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
   cuuint64_t dims[2] = {(cuuint64_t)kvh * row_bytes, (cuuint64_t)slots};
   cuuint64_t strides[1] = {(cuuint64_t)kvh * row_bytes};
   cuuint32_t boxd[2] = {128, (cuuint32_t)rows};
   cuuint32_t es[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, boxd, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, boxd, es,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 pa_status launch_all(pa::Args& args, const pa_dims* d, const void* query, void* kc, void* vc, uint32_t stages,
@@ -321,15 +325,13 @@ bool cache_map_16(CUtensorMap* m, const void* base, bool bf16, int hs, int kvh, 
 }
 bool query_block_map(CUtensorMap* m, const void* base, bool bf16, int hs, int nh, int64_t n, int64_t stride, int heads,
                      int rows) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
   cuuint64_t dims[3] = {(cuuint64_t)hs, (cuuint64_t)nh, (cuuint64_t)n};
   cuuint64_t strides[2] = {(cuuint64_t)hs * 2, (cuuint64_t)stride * 2};
   cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)rows};
   cuuint32_t es[3] = {1, 1, 1};
-  return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base),
-             dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_tiled(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                      const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 }  // namespace pa
 
