@@ -1,5 +1,8 @@
 """The operators around the attention call in the calls a serving loop makes of them: stages of the
 dense call beside them, values that are not finite, host threads, sizes at the limits."""
+import ctypes
+import os
+import subprocess
 import threading
 
 import numpy as np
@@ -280,3 +283,100 @@ def test_a_stage_of_the_dense_call_first_in_a_host_thread():
     torch.cuda.synchronize()
     in_a_new_thread(lambda: r.call(pa.STAGE_DECODE))
     assert pa.read_device_error(r.ws) == 0
+
+
+def table_calls(B, stream):
+    """A function that calls build_block_tables for B requests, one that says whether its answer is right, and the
+    arguments of the C entry point."""
+    with torch.cuda.stream(stream):
+        past, ones, held = (torch.full((B,), v, dtype=torch.int32, device="cuda") for v in (3, 1, 1))
+        table = torch.arange(B, dtype=torch.int32, device="cuda").reshape(B, 1)
+        ring, state = i32([0]), i32([0, 0])
+        args = (past, ones, held, table, ring, state)
+        out = pa.build_block_tables(*args, block_size=16, num_tokens=B)
+        want = out.slot_mapping.clone()
+    raw = (*args, B, B, 1, 16, 1, *out, stream.cuda_stream)
+    return lambda: pa.build_block_tables(*args, block_size=16, num_tokens=B, out=out, stream=stream), \
+        lambda: torch.equal(out.slot_mapping, want), raw
+
+
+def select_calls(columns, top_k, stream, heads=8, kvh=2, hs=64):
+    with torch.cuda.stream(stream):
+        g = torch.Generator(device="cuda").manual_seed(columns)
+        table = torch.randint(0, 64, (1, columns), generator=g, dtype=torch.int32, device="cuda")
+        bounds = torch.randint(-127, 128, (64, kvh, 2, hs), generator=g, dtype=torch.int8, device="cuda")
+        query = torch.randn(1, heads * hs, generator=g, device="cuda").half()
+        scale, cum, past = torch.full((kvh, hs), 0.03, device="cuda"), i32([0, 1]), i32([columns * 16 - 1])
+        kw = dict(num_heads=heads, kv_num_heads=kvh, block_size=16, top_k=top_k)
+        sel = pa.select_pages(query, bounds, scale, cum, past, table, **kw)
+        want = sel.clone()
+    d = pa.PaSparseDims(1, 1, heads, kvh, hs, 64, 16, columns, 0, top_k, 1, 1, 1, 0, heads * hs)
+    return lambda: pa.select_pages(query, bounds, scale, cum, past, table, selected=sel, stream=stream, **kw), \
+        lambda: torch.equal(sel, want), (query, bounds, scale, cum, past, table, d, sel, 0, stream.cuda_stream)
+
+
+def sparse_calls(top_k, R, stream):
+    with torch.cuda.stream(stream):
+        b = Batch(60, "fp16", 8, 2, 64, 16, [300], [R])
+        sel = torch.full((b.N, 2, top_k), -1, dtype=torch.int32, device="cuda")
+        sel[:, :, :19] = torch.arange(19, dtype=torch.int32, device="cuda")
+        kw = dict(num_heads=8, kv_num_heads=2, query_block=R)
+        args = (b.query, b.key_cache, b.value_cache, *b.meta, sel)
+        out = pa.sparse_paged_attention(*args, **kw)
+        want = out.clone()
+    d = pa.PaSparseDims(b.N, 1, 8, 2, 64, b.blocks, 16, b.table.shape[1], 0, top_k, R, 0, 1, 0, 8 * 64)
+    return lambda: pa.sparse_paged_attention(*args, output=out, stream=stream, **kw), \
+        lambda: torch.equal(out, want), (*args, 0, out, 0, d, 0, stream.cuda_stream)
+
+
+@pytest.fixture(scope="module")
+def native(tmp_path_factory):
+    """host_threads.cpp, compiled."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    lib = str(tmp_path_factory.mktemp("native") / "host_threads.so")
+    subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-pthread", "-I" + os.path.join(here, "..", "include"),
+                    os.path.join(here, "host_threads.cpp"), "-o", lib], check=True)
+    return ctypes.CDLL(lib)
+
+
+@pytest.mark.parametrize("which,make,sizes", [
+    (0, table_calls, [(8192,), (3000,)]), (1, select_calls, [(32000, 64), (5000, 32)]),
+    (1, select_calls, [(4000, 64), (3400, 32)]), (2, sparse_calls, [(2048, 1), (32, 1)]),
+    (2, sparse_calls, [(2048, 16), (32, 16)])])
+def test_host_threads_with_calls_of_different_sizes(native, which, make, sizes):
+    """A call's shared memory follows from its sizes; the limit that lets it launch is the function's, for all threads."""
+    from varlen_paged_kv_gb300 import step
+    calls = [make(*size, torch.cuda.Stream()) for size in sizes]
+    torch.cuda.synchronize()
+    lib = step._library()
+    entry = (lib.pa_build_block_tables, lib.pa_select_pages, lib.pa_sparse_paged_attention)[which]
+    raws = []
+    for _, _, raw in calls:
+        raws.append((ctypes.c_int64 * len(raw))(*[
+            v.data_ptr() if torch.is_tensor(v) else ctypes.addressof(v) if isinstance(v, ctypes.Structure) else v
+            for v in raw]))
+    for _ in range(10):
+        refused = native.two_threads(which, ctypes.cast(entry, ctypes.c_void_p), raws[0], raws[1], 500)
+        torch.cuda.synchronize()
+        assert refused == 0
+    assert all(right() for _, right, _ in calls)
+
+
+def test_a_graph_of_calls_of_different_sizes():
+    """Both sizes of every kernel in one graph, and other sizes called between its capture and its replays."""
+    side = torch.cuda.Stream()
+    makes = [(table_calls, (8192,)), (table_calls, (3000,)), (select_calls, (32000, 64)), (select_calls, (5000, 32)),
+             (select_calls, (40, 4)), (sparse_calls, (2048, 1)), (sparse_calls, (32, 1)), (sparse_calls, (2048, 16)),
+             (sparse_calls, (32, 16))]
+    calls = [make(*size, side) for make, size in makes]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        for call, *_ in calls:
+            call()
+    for call, *_ in reversed(calls):
+        call()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(right() for _, right, _ in calls)

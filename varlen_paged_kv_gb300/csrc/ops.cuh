@@ -148,13 +148,15 @@ cudaError_t launch_select(const PageArgs& a, bool bf16, int sms, cudaStream_t s)
 cudaError_t launch_sparse(const PageArgs& a, bool bf16, int sms, cudaStream_t s);
 
 // A launch that may start before the kernel before it has finished (its blocks wait for that
-// kernel's results) and whose CTAs along z form one cluster each.
+// kernel's results) and whose CTAs along z form one cluster each. `most` is the largest smem of
+// any call of this kernel: the limit is the function's, for all host threads, so that every
+// call sets it to the same.
 template <typename... KArgs, typename... Actual>
-inline cudaError_t launch_clusters(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t s,
-                                   Actual&&... args) {
+inline cudaError_t launch_clusters(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem, size_t most,
+                                   cudaStream_t s, Actual&&... args) {
   // (up to 48 KB with the kernel's static arrays need no attribute)
   if (smem > 12 * 1024)
-    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
+    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most)) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);

@@ -574,7 +574,8 @@ __global__ void __launch_bounds__(T, T == 256 ? 3 : 1024 / T) select_kernel(cons
 
 template <int HS, bool BF16>
 static cudaError_t launch_select_t(const PageArgs& a, int sms, cudaStream_t s) {
-  const size_t smem = ((size_t)a.max_blocks + a.top_k) * 4;
+  auto bytes = [](size_t columns, size_t top_k) { return (columns + top_k) * 4; };
+  const size_t smem = bytes(a.max_blocks, a.top_k);
   const int64_t items = ceil_div(a.N, a.R) * a.kvh;
   // CTAs that share the pages of a block: as many as run at once, each with a step of pages (at
   // most eight, the portable cluster; sixteen took 0.4 us more on one request of 2048 pages, and
@@ -587,9 +588,12 @@ static cudaError_t launch_select_t(const PageArgs& a, int sms, cudaStream_t s) {
   // threads, 67 with 256, 86 with 512; 65 pages, 64 decode rows: 8.2, 11.0, 18.4 us), long ones
   // a stream of bounds and a last CTA's passes over the scores (8193 pages, 8 decode rows: 63,
   // 41, 33 us; 1025 pages, 32 drafts of 4: 18.4, 15.4, 16.1 us).
-  if (a.max_blocks <= 768) return launch_clusters(select_kernel<HS, BF16, 128>, grid, 128, smem, s, a);
-  if (a.max_blocks <= 4096) return launch_clusters(select_kernel<HS, BF16, 256>, grid, 256, smem, s, a);
-  return launch_clusters(select_kernel<HS, BF16, 512>, grid, 512, smem, s, a);
+  auto launch = [&](auto kernel, int threads, int columns) {
+    return launch_clusters(kernel, grid, threads, smem, bytes(columns, PA_MAX_SELECTED_PAGES), s, a);
+  };
+  if (a.max_blocks <= 768) return launch(select_kernel<HS, BF16, 128>, 128, 768);
+  if (a.max_blocks <= 4096) return launch(select_kernel<HS, BF16, 256>, 256, 4096);
+  return launch(select_kernel<HS, BF16, 512>, 512, PA_MAX_SCORED_PAGES);
 }
 
 cudaError_t launch_select(const PageArgs& a, bool bf16, int sms, cudaStream_t s) {

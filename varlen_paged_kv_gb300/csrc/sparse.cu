@@ -836,8 +836,8 @@ static cudaError_t launch_rows(const PageArgs& a, const CUtensorMap& tk, const C
   const int64_t items = ceil_div(a.N, a.R) * a.kvh * chunks;
   const int c = cluster_size(items, (int64_t)sms * (HS == 256 ? 1 : 2), tiles, 2, 8);
   const dim3 grid((unsigned)query_blocks(a), (unsigned)(a.kvh * chunks), (unsigned)c);
-  return launch_clusters(sparse_rows_kernel<HS, BF16>, grid, kRowsThreads, RowsSmem<HS>::bytes(a.top_k), s, a, tk, tv,
-                         seg, chunks);
+  return launch_clusters(sparse_rows_kernel<HS, BF16>, grid, kRowsThreads, RowsSmem<HS>::bytes(a.top_k),
+                         RowsSmem<HS>::bytes(PA_MAX_SELECTED_PAGES), s, a, tk, tv, seg, chunks);
 }
 
 template <int HS, bool BF16>
@@ -848,8 +848,8 @@ static cudaError_t launch_tile(const PageArgs& a, const CUtensorMap& tq, const C
   const int64_t items = ceil_div(a.N, sub_rows) * a.kvh;
   const int c = cluster_size(items, (int64_t)sms * (HS == 256 ? 1 : 2), tiles, 4, 8);
   const dim3 grid((unsigned)(query_blocks(a) * chunks), (unsigned)a.kvh, (unsigned)c);
-  return launch_clusters(sparse_tile_kernel<HS, BF16>, grid, kTileThreads, TileSmem<HS>::bytes(a.top_k), s, a, tq, tk,
-                         tv, seg, sub_rows, chunks);
+  return launch_clusters(sparse_tile_kernel<HS, BF16>, grid, kTileThreads, TileSmem<HS>::bytes(a.top_k),
+                         TileSmem<HS>::bytes(PA_MAX_SELECTED_PAGES), s, a, tq, tk, tv, seg, sub_rows, chunks);
 }
 
 cudaError_t launch_sparse(const PageArgs& a, bool bf16, int sms, cudaStream_t s) {

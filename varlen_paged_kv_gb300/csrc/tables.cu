@@ -139,9 +139,9 @@ __global__ void __launch_bounds__(kTableThreads) tables_kernel(const TableArgs a
 
 cudaError_t launch_tables(const TableArgs& a, int sms, cudaStream_t s) {
   const int64_t smem = 3 * ((int64_t)a.B + 1) * 4;
-  if (smem > 32 * 1024)  // (less needs no attribute)
-    if (cudaError_t e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem))
-      return e;
+  constexpr int most = 3 * (PA_MAX_TABLE_REQUESTS + 1) * 4;
+  if (smem > 32 * 1024)  // (less needs no attribute; the same limit from every host thread)
+    if (cudaError_t e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most)) return e;
   const int64_t work = a.N > a.B ? a.N : a.B;
   int64_t grid = ceil_div(work, kTableThreads);
   grid = grid < 1 ? 1 : grid > sms ? sms : grid;
