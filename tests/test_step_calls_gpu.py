@@ -380,3 +380,39 @@ def test_a_graph_of_calls_of_different_sizes():
         graph.replay()
     torch.cuda.synchronize()
     assert all(right() for _, right, _ in calls)
+
+
+def test_the_compiled_calls_let_other_threads_run(native):
+    """An entry point that waits (as a launch does while the stream's queue is full) does not hold the interpreter."""
+    from varlen_paged_kv_gb300 import step
+    b = Batch(62, "fp16", 8, 2, 64, 16, [300], [2])
+    b.whole_bounds()
+    sel = b.select(5)
+    fast, lib = step._load_fast(), step._library()
+    real = [ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.pa_build_block_tables, lib.pa_qk_norm_rope, lib.pa_update_page_bounds, lib.pa_select_pages,
+        lib.pa_sparse_paged_attention)]
+    slow = ctypes.cast(native.slow_entry_point, ctypes.c_void_p).value
+    one, q = i32([1]), b.query.contiguous()
+    calls = [lambda: fast.build_block_tables(one, one, one, i32([[0]]), one, i32([0, 0]), 16, 1),
+             lambda: fast.qk_norm_rope(q, q[:, :128], i32([0, 1]), 8, 2, None, None, 1e-6, 64, 1e4, False),
+             lambda: fast.update_page_bounds(b.key_cache, b.bounds, b.scale, *b.meta, b.N, None),
+             lambda: fast.select_pages(q, b.bounds, b.scale, *b.meta, 8, 2, 16, 5, 1, 1, 1, None),
+             lambda: fast.sparse_paged_attention(q, b.key_cache, b.value_cache, *b.meta, sel, 8, 2, 0.0, 1, None, None)]
+    try:
+        for k, call in enumerate(calls):
+            native.reset()
+            fast.bind(*[slow if i == k else f for i, f in enumerate(real)])
+
+            def other():
+                while not native.has_entered():
+                    pass
+                native.release()
+
+            t = threading.Thread(target=other)
+            t.start()
+            assert call() is not None, k  # (None: the call gave up before the other thread ran)
+            t.join()
+    finally:
+        fast.bind(*real)
+    torch.cuda.synchronize()

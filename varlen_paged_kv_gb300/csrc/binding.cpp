@@ -114,6 +114,18 @@ struct Batch {
   }
 };
 
+// An entry point called without the interpreter's lock, as ctypes makes its calls: a launch
+// waits while the stream's queue is full, and what it waits for may be another Python thread.
+// (The arguments are plain values, worked out before.)
+template <typename... P, typename... A>
+pa_status unlocked(pa_status (*f)(P...), A... args) {
+  struct Unlocked {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+  } now;
+  return f(args...);
+}
+
 template <typename F>
 PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F&& f) {
   try {
@@ -140,10 +152,10 @@ PyObject* build_block_tables(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const int64_t sizes[6] = {B + 1, N, N, B, 2, 1};
     const at::Tensor all = call.empty({2 * (B + N + 2)}, at::kInt);
     int32_t* p = (int32_t*)all.data_ptr();
-    need(build_block_tables_fn(past, q, held, (int32_t*)table.data_ptr(), (int32_t*)ring.data_ptr(), state, i32(B),
-                               i32(N), i32(table.size(1)), (int32_t)integer(v[6]), i32(ring.size(0)), p, p + B + 1,
-                               p + B + 1 + N, p + B + 1 + 2 * N, p + 2 * B + 1 + 2 * N,
-                               (uint32_t*)(p + 2 * B + 3 + 2 * N), call.stream()) == PA_OK);
+    need(unlocked(build_block_tables_fn, past, q, held, (int32_t*)table.data_ptr(), (int32_t*)ring.data_ptr(), state,
+                  i32(B), i32(N), i32(table.size(1)), (int32_t)integer(v[6]), i32(ring.size(0)), p, p + B + 1,
+                  p + B + 1 + N, p + B + 1 + 2 * N, p + 2 * B + 1 + 2 * N, (uint32_t*)(p + 2 * B + 3 + 2 * N),
+                  call.stream()) == PA_OK);
     PyObject* out = PyTuple_New(6);
     need(out != nullptr);
     int64_t at = 0;
@@ -181,9 +193,9 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* v, Py_ssize_t n) {
     need(interleaved >= 0);
     const int32_t* positions = call.ints(v[2], N);
     const at::Tensor qo = call.empty({N, nh * hs}, type), ko = call.empty({N, kvh * hs}, type);
-    need(qk_norm_rope_fn(query.data_ptr(), key.data_ptr(), positions, &prep, interleaved, i32(N), i32(nh), i32(kvh),
-                         i32(hs), code, qs, ks, qo.data_ptr(), ko.data_ptr(), nh * hs, kvh * hs,
-                         call.stream()) == PA_OK);
+    need(unlocked(qk_norm_rope_fn, query.data_ptr(), key.data_ptr(), positions, &prep, interleaved, i32(N), i32(nh),
+                  i32(kvh), i32(hs), code, qs, ks, qo.data_ptr(), ko.data_ptr(), nh * hs, kvh * hs,
+                  call.stream()) == PA_OK);
     PyObject* out = PyTuple_New(2);
     need(out != nullptr);
     PyTuple_SET_ITEM(out, 0, THPVariable_Wrap(qo));
@@ -220,8 +232,8 @@ PyObject* update_page_bounds(PyObject*, PyObject* const* v, Py_ssize_t n) {
     d.block_size = i32(cache.size(1));
     d.max_blocks_per_sequence = b.columns;
     d.dtype = code;
-    need(update_page_bounds_fn(cache.data_ptr(), (int8_t*)bounds.data_ptr(), scale, b.cum, b.past, b.table, &d,
-                               call.error(v[7]), call.stream()) == PA_OK);
+    need(unlocked(update_page_bounds_fn, cache.data_ptr(), (int8_t*)bounds.data_ptr(), scale, b.cum, b.past, b.table,
+                  &d, call.error(v[7]), call.stream()) == PA_OK);
     Py_RETURN_TRUE;
   });
 }
@@ -253,8 +265,8 @@ PyObject* select_pages(PyObject*, PyObject* const* v, Py_ssize_t n) {
     d.local_pages = i32(integer(v[12]));
     uint32_t* error = call.error(v[13]);
     const at::Tensor out = call.empty({query.size(0), d.kv_num_heads, d.top_k}, at::kInt);
-    need(select_pages_fn(query.data_ptr(), (const int8_t*)bounds.data_ptr(), scale, b.cum, b.past, b.table, &d,
-                         (int32_t*)out.data_ptr(), error, call.stream()) == PA_OK);
+    need(unlocked(select_pages_fn, query.data_ptr(), (const int8_t*)bounds.data_ptr(), scale, b.cum, b.past, b.table,
+                  &d, (int32_t*)out.data_ptr(), error, call.stream()) == PA_OK);
     return THPVariable_Wrap(out);
   });
 }
@@ -294,9 +306,9 @@ PyObject* sparse_paged_attention(PyObject*, PyObject* const* v, Py_ssize_t n) {
     uint32_t* error = call.error(v[12]);
     const float scale = real(v[9]);
     const at::Tensor out = call.empty({N, d.num_heads * k.size(3)}, type);
-    need(sparse_paged_attention_fn(query.data_ptr(), k.data_ptr(), value.data_ptr(), b.cum, b.past, b.table,
-                                   (const int32_t*)selected.data_ptr(), scale, out.data_ptr(), lse, &d, error,
-                                   call.stream()) == PA_OK);
+    need(unlocked(sparse_paged_attention_fn, query.data_ptr(), k.data_ptr(), value.data_ptr(), b.cum, b.past,
+                  b.table, (const int32_t*)selected.data_ptr(), scale, out.data_ptr(), lse, &d, error,
+                  call.stream()) == PA_OK);
     return THPVariable_Wrap(out);
   });
 }
