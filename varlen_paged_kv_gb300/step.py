@@ -8,8 +8,8 @@
 
 As ``paged_attention``: argument marshalling only, for the C ABI of ``libpagedattn.so``. The
 common case (outputs of the call's own, the current stream and device) goes through the compiled
-``_step_binding``, whose checks take a microsecond; everything else, refusals among it, through
-the code here. The work runs on the current stream of the tensors' device (or ``stream``), and a call can be
+``_step_binding`` (where it is built), whose checks take a microsecond; everything else, refusals
+among it, through the code here. The work runs on the current stream of the tensors' device (or ``stream``), and a call can be
 captured in a CUDA graph. An int32 tensor of one element passed as ``error`` collects the
 ``DEVERR_*`` bits of problems that only device data reveals. With ``stream`` the caller orders
 that stream after the work that makes the inputs, and other streams after the call.
@@ -21,6 +21,7 @@ import functools
 import importlib.machinery
 import importlib.util
 import os
+import warnings
 from typing import NamedTuple, Optional
 
 import torch
@@ -51,16 +52,27 @@ _bound = _prep = None
 _fast = None  # the compiled binding, once loaded
 
 
+class _Absent:
+    """Stands in for the compiled calls where they are not built: every call is made in Python."""
+
+    def __getattr__(self, name):
+        return lambda *a: None
+
+
 def _load_fast():
     """The compiled calls (csrc/binding.cpp), given the library's entry points."""
     global _fast
     if _fast is None:
         lib = _library()
         path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_step_binding.so")
-        if not os.path.exists(path):
-            raise RuntimeError(f"{path} is missing: build it with varlen_paged_kv_gb300.build.build()")
-        loader = importlib.machinery.ExtensionFileLoader("_step_binding", path)
-        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_step_binding", loader))
+        try:
+            loader = importlib.machinery.ExtensionFileLoader("_step_binding", path)
+            module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_step_binding", loader))
+        except ImportError as e:
+            warnings.warn(f"no compiled calls, each call takes some microseconds longer: {e} "
+                          "(varlen_paged_kv_gb300.build.build() builds them)", RuntimeWarning)
+            _fast = _Absent()
+            return _fast
         module.bind(*[ctypes.cast(f, _p).value for f in (
             lib.pa_build_block_tables, lib.pa_qk_norm_rope, lib.pa_update_page_bounds, lib.pa_select_pages,
             lib.pa_sparse_paged_attention)])
