@@ -53,22 +53,32 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
-BINDING = os.path.join(HERE, "_step_binding.so")
+def binding_path(folder: str = HERE) -> str:
+    """The compiled Python calls for this interpreter and torch. They build torch's objects by its
+    headers, so the name holds what they were compiled against: another torch or Python looks
+    for another file."""
+    import sysconfig
+
+    import torch
+
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return os.path.join(folder, f"_step_binding.torch-{torch.__version__}-abi{abi}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 
 def build_binding(force: bool = False) -> str:
-    """_step_binding.so: csrc/binding.cpp against the torch that imports it."""
+    """csrc/binding.cpp against the torch that imports it."""
+    out = binding_path()
     src = os.path.join(CSRC, "binding.cpp")
     deps = [src, os.path.join(INCLUDE, "pagedattn.h")]
-    if not force and os.path.exists(BINDING) and all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps):
-        return BINDING
+    if not force and os.path.exists(out) and all(os.path.getmtime(p) <= os.path.getmtime(out) for p in deps):
+        return out
     import sysconfig
 
     import torch
 
     base = os.path.dirname(torch.__file__)
     cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
-    tmp = BINDING + f".tmp{os.getpid()}"
+    tmp = out + f".tmp{os.getpid()}"
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + INCLUDE,
            "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(base, "include"),
@@ -77,17 +87,17 @@ def build_binding(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {src}:\n{r.stderr}")
-    os.replace(tmp, BINDING)
-    return BINDING
+    os.replace(tmp, out)
+    return out
 
 
-def _try_binding() -> None:
+def _try_binding(force: bool = False) -> None:
     """build_binding, or a warning; a binding that is out of date does not stay."""
     try:
-        build_binding()
+        build_binding(force)
     except Exception as e:  # noqa: BLE001 (no compiler, no headers, an import error, ...)
-        if os.path.exists(BINDING):
-            os.unlink(BINDING)
+        if os.path.exists(binding_path()):
+            os.unlink(binding_path())
         warnings.warn(f"the compiled calls were not built, each call takes some microseconds longer: {e}", RuntimeWarning)
 
 
@@ -112,7 +122,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, 
         return obj, r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=min(12, os.cpu_count() or 4)) as ex:
-        binding = ex.submit(_try_binding)
+        binding = ex.submit(_try_binding, force)
         results = list(ex.map(compile_one, sources()))
         binding.result()
     if verbose or ptxas_info:

@@ -8,7 +8,7 @@
 
 As ``paged_attention``: argument marshalling only, for the C ABI of ``libpagedattn.so``. The
 common case (outputs of the call's own, the current stream and device) goes through the compiled
-``_step_binding`` (where it is built), whose checks take a microsecond; everything else, refusals
+``_step_binding`` (where it is built for this torch), whose checks take a microsecond; everything else, refusals
 among it, through the code here. The work runs on the current stream of the tensors' device (or ``stream``), and a call can be
 captured in a CUDA graph. An int32 tensor of one element passed as ``error`` collects the
 ``DEVERR_*`` bits of problems that only device data reveals. With ``stream`` the caller orders
@@ -25,6 +25,8 @@ import warnings
 from typing import NamedTuple, Optional
 
 import torch
+
+from .build import binding_path
 
 _I32 = torch.int32
 _T = {torch.float16: 0, torch.bfloat16: 1}  # pa_dtype
@@ -64,7 +66,7 @@ def _load_fast():
     global _fast
     if _fast is None:
         lib = _library()
-        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_step_binding.so")
+        path = binding_path(os.path.dirname(os.path.abspath(__file__)))
         try:
             loader = importlib.machinery.ExtensionFileLoader("_step_binding", path)
             module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_step_binding", loader))
