@@ -576,12 +576,12 @@ template <int HS, bool BF16>
 static cudaError_t launch_select_t(const PageArgs& a, int sms, cudaStream_t s) {
   auto bytes = [](size_t columns, size_t top_k) { return (columns + top_k) * 4; };
   const size_t smem = bytes(a.max_blocks, a.top_k);
-  const int64_t items = ceil_div(a.N, a.R) * a.kvh;
+  const int64_t items = items_of_batch(a.N, a.B, a.R, 1, 1) * a.kvh;
   // CTAs that share the pages of a block: as many as run at once, each with a step of pages (at
   // most eight, the portable cluster; sixteen took 0.4 us more on one request of 2048 pages, and
-  // twice as many as run at once 37 us instead of 30 on 8 long decode rows)
-  int c = 1;
-  while (c < 8 && items * 2 * c <= 2 * (int64_t)sms && a.max_blocks >= 2 * c * 128) c *= 2;
+  // twice as many as run at once 37 us instead of 30 on 8 long decode rows; 16 rows of 2048
+  // pages in blocks of 16, counted as one block, 25 us instead of 16)
+  const int c = cluster_size(items, 2 * (int64_t)sms, a.max_blocks, 128, 8);
   const dim3 grid((unsigned)query_blocks(a), (unsigned)a.kvh, (unsigned)c);
   // Threads by the longest history the table can hold. Short ones are chains of latencies that
   // more CTAs per SM overlap (tables of 544 pages, 4 prompts of 2048 rows: 58 us with 128

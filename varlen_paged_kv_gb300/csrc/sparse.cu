@@ -819,21 +819,17 @@ static int common_divisor(int a, int b) {
   return a;
 }
 
-// CTAs that share an item's tiles: as many as run at once, at most `most`, each with at least
-// `least` tiles of a full list. (Twice as many as run at once cost more than they balance: 8 long
-// decode rows 26.6 us instead of 18.5, 32 drafts of 4 in 256-wide heads 39.2 instead of 29.5.)
-static int cluster_size(int64_t items, int64_t slots, int tiles, int least, int most) {
-  int c = 1;
-  while (2 * c <= most && items * 2 * c <= slots && tiles >= 2 * c * least) c *= 2;
-  return c;
-}
-
+// The CTAs of a cluster share an item's tiles, as many as run at once. (More cost more than they
+// balance: twice as many 8 long decode rows 26.6 us instead of 18.5 and 32 drafts of 4 in 256-wide
+// heads 39.2 instead of 29.5, eight times as many 64 one-row sequences in blocks of 16, of 32 pages of
+// 64, 208 us instead of 90. Idle sequences that are counted cost less: a chunk of 512 in blocks of
+// 32 beside 63 of them takes 43.9 us in clusters of one instead of 40.1 of two.)
 template <int HS, bool BF16>
 static cudaError_t launch_rows(const PageArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int seg, int sms,
                                cudaStream_t s) {
   const int chunks = (int)ceil_div((int64_t)a.R * a.G, 16);
   const int tiles = (int)ceil_div((int64_t)a.top_k * a.bs, kSpTile);
-  const int64_t items = ceil_div(a.N, a.R) * a.kvh * chunks;
+  const int64_t items = items_of_batch(a.N, a.B, a.R, chunks, ceil_div(a.G, 16)) * a.kvh;
   const int c = cluster_size(items, (int64_t)sms * (HS == 256 ? 1 : 2), tiles, 2, 8);
   const dim3 grid((unsigned)query_blocks(a), (unsigned)(a.kvh * chunks), (unsigned)c);
   return launch_clusters(sparse_rows_kernel<HS, BF16>, grid, kRowsThreads, RowsSmem<HS>::bytes(a.top_k),
@@ -845,7 +841,7 @@ static cudaError_t launch_tile(const PageArgs& a, const CUtensorMap& tq, const C
                                int seg, int sub_rows, int sms, cudaStream_t s) {
   const int chunks = (int)ceil_div(a.R, sub_rows);
   const int tiles = (int)ceil_div((int64_t)a.top_k * a.bs, kSpTile);
-  const int64_t items = ceil_div(a.N, sub_rows) * a.kvh;
+  const int64_t items = items_of_batch(a.N, a.B, sub_rows, 1, 1) * a.kvh;
   const int c = cluster_size(items, (int64_t)sms * (HS == 256 ? 1 : 2), tiles, 4, 8);
   const dim3 grid((unsigned)(query_blocks(a) * chunks), (unsigned)a.kvh, (unsigned)c);
   return launch_clusters(sparse_tile_kernel<HS, BF16>, grid, kTileThreads, TileSmem<HS>::bytes(a.top_k),
