@@ -416,3 +416,28 @@ def test_the_compiled_calls_let_other_threads_run(native):
     finally:
         fast.bind(*real)
     torch.cuda.synchronize()
+
+
+def test_sizes_past_32_bits_are_refused():
+    """Not taken for their low 32 bits, which would be sizes that exist."""
+    big = 1 << 32
+    b = Batch(63, "fp16", 4, 2, 64, 16, [300], [2])
+    b.whole_bounds()
+    kw = dict(num_heads=4, kv_num_heads=2)
+    sel = b.select(5)
+    one = i32([1])
+    for v in (big, -big):
+        with pytest.raises(ValueError, match="block_size"):
+            pa.build_block_tables(one, one, one, i32([[0]]), one, i32([0, 0]), block_size=16 + v, num_tokens=1)
+        with pytest.raises(ValueError, match="rotary_dim"):
+            pa.qk_norm_rope(b.query, b.query[:, :128], i32([0, 1]), rotary_dim=64 + v, **kw)
+        with pytest.raises(ValueError, match="num_tokens"):
+            pa.update_page_bounds(b.key_cache, b.bounds, b.scale, *b.meta, num_tokens=2 + v)
+        with pytest.raises(ValueError, match="query_block"):
+            pa.sparse_paged_attention(b.query, b.key_cache, b.value_cache, *b.meta, sel, query_block=1 + v, **kw)
+        for name, x in (("block_size", 16), ("top_k", 5), ("query_block", 1), ("sink_pages", 1), ("local_pages", 1)):
+            with pytest.raises(ValueError, match=name):
+                pa.select_pages(b.query, b.bounds, b.scale, *b.meta, **kw, **(dict(block_size=16, top_k=5) | {name: x + v}))
+    with pytest.raises(ValueError, match="num_tokens"):
+        pa.build_block_tables(one, one, one, i32([[0]]), one, i32([0, 0]), block_size=16, num_tokens=big + 1)
+    torch.cuda.synchronize()

@@ -102,9 +102,17 @@ def _library():
     return _bound
 
 
+def _sizes(**sizes):
+    """Refuses what the C ABI's 32-bit fields cannot hold (ctypes would keep the low bits)."""
+    for name, v in sizes.items():
+        if not -(1 << 31) <= v < 1 << 31:
+            raise ValueError(f"{name} must fit 32 bits")
+
+
 # (the records hold sizes and scalars only)
 @functools.lru_cache(maxsize=256)
 def _dims(*v) -> PaSparseDims:
+    _sizes(**{n: x for (n, t), x in zip(PaSparseDims._fields_, v) if t is _i32})
     return PaSparseDims(*v)
 
 
@@ -197,6 +205,8 @@ def build_block_tables(past_seqlens: torch.Tensor, query_lens: torch.Tensor, blo
         raise ValueError("past_seqlens, query_lens and blocks_held must be (B,), block_table (B, columns), "
                          "free_blocks 1-D and free_state (2,)")
     B = shape[0]
+    _sizes(requests=B, num_tokens=num_tokens, columns=table[1], block_size=block_size,
+           free_blocks=free_blocks.shape[0])
     sizes = (B + 1, num_tokens, num_tokens, B, 2, 1)
     if out is None:
         if num_tokens < 0:
@@ -240,6 +250,7 @@ def qk_norm_rope(query: torch.Tensor, key: torch.Tensor, positions: torch.Tensor
         raise ValueError("query must be (rows, num_heads * head_size)")
     N, qw = shape
     head_size = qw // num_heads
+    _sizes(rows=N, num_heads=num_heads, kv_num_heads=kv_num_heads, head_size=head_size, rotary_dim=rotary_dim)
     kw = kv_num_heads * head_size
     qs, ks = _rows(query, "query", qw, dtype, index), _rows(key, "key", kw, dtype, index)
     device = None if query_out is not None and key_out is not None else query.device
@@ -352,14 +363,14 @@ def select_pages(query: torch.Tensor, page_bounds: torch.Tensor, bound_scale: to
     stride = _rows(query, "query", num_heads * hs, dtype, index)
     B, columns, err = _batch(index, cumulative_sequence_length, past_seqlens, block_table, error)
     N = query.shape[0]
+    d = _dims(N, B, num_heads, kv_num_heads, hs, blocks, block_size, columns, _T[dtype], top_k, query_block,
+              sink_pages, local_pages, 0, stride)
     if selected is None:
         selected = _empty((N, kv_num_heads, max(top_k, 0)), _I32, query.device, stream)
     else:
         _refuse_ints(index, selected=selected)
         if selected.shape != (N, kv_num_heads, top_k):
             raise ValueError("selected must be (rows, kv_num_heads, top_k)")
-    d = _dims(N, B, num_heads, kv_num_heads, hs, blocks, block_size, columns, _T[dtype], top_k, query_block,
-              sink_pages, local_pages, 0, stride)
     _call("pa_select_pages", index, stream, _library().pa_select_pages, query.data_ptr(), page_bounds.data_ptr(),
           bound_scale.data_ptr(), cumulative_sequence_length.data_ptr(), past_seqlens.data_ptr(),
           block_table.data_ptr(), d, selected.data_ptr(), err)
