@@ -48,3 +48,13 @@ def test_clusters_are_no_more_than_run_at_once(rules):
     assert rules.cluster(rules.items(64, 64, 16, 1, 1) * 8, 304, 32, 4, 8) == 1
     assert rules.cluster(8, 304, 32, 4, 8) == 8 and rules.cluster(64, 304, 32, 4, 8) == 4
     assert rules.cluster(8, 304, 31, 4, 8) == 4 and rules.cluster(1, 304, 7, 4, 8) == 1
+
+
+def test_more_tiles_than_can_be_numbered_are_refused():
+    """2^28 sequences of blocks of 15 tiles each: the grid would be taken for its low 32 bits."""
+    import varlen_paged_kv_gb300 as pa
+    from varlen_paged_kv_gb300 import build, step
+    build.build()
+    d = pa.PaSparseDims(16, 1 << 28, 68, 1, 64, 64, 64, 16, 0, 4, 15, 0, 1, 0, 68 * 64)
+    p = 1 << 20  # aligned and never dereferenced: the call is refused before any launch
+    assert step._library().pa_sparse_paged_attention(p, p, p, p, p, p, p, 0.0, p, None, d, None, None) == 2

@@ -233,6 +233,11 @@ pa_status pa_sparse_paged_attention(const void* query, const void* key_cache, co
                                     float* lse, const pa_sparse_dims* dims, uint32_t* error, void* stream) {
   if (pa_status st = check_batch_dims(dims)) return st;
   if (pa_status st = check_selection_dims(dims)) return st;
+  // (a query block's tiles are numbered in 32 bits, with room for every sequence)
+  const int32_t R = dims->query_block, G = dims->num_heads / dims->kv_num_heads;
+  if (!pa::takes_rows_kernel(R, G) &&
+      ((int64_t)dims->num_tokens / R + dims->batch_size) * pa::ceil_div(R, pa::rows_of_tile(R, G)) > INT32_MAX)
+    return PA_ERR_UNSUPPORTED;
   if (dims->num_tokens == 0) return PA_OK;
   if (!all_aligned(16, {query, key_cache, value_cache, output}) ||
       !all_aligned(4, {cumulative_sequence_length, past_seqlens, block_table, selected}) ||

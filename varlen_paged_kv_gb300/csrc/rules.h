@@ -15,6 +15,12 @@ inline int64_t items_of_batch(int64_t N, int64_t B, int64_t rows, int64_t full, 
   return long_ones > short_ones ? long_ones : short_ones;
 }
 
+// Rows of a query block of R rows and G heads that one tile of 128 takes, G at most 128.
+inline int rows_of_tile(int R, int G) { return R * G <= 128 ? R : 128 / G; }
+
+// Whether the sparse attention takes the warp-level kernel (sparse.cu has the reason).
+inline bool takes_rows_kernel(int R, int G) { return R * G <= 16 || G > 128; }
+
 // CTAs that share an item's pieces (tiles of keys, pages): as many as run at once in `slots`
 // places, at most `most`, each with at least `least` pieces.
 inline int cluster_size(int64_t items, int64_t slots, int64_t pieces, int least, int most) {

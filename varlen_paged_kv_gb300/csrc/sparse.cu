@@ -859,12 +859,12 @@ cudaError_t launch_sparse(const PageArgs& a, bool bf16, int sms, cudaStream_t s)
   // kernel, whatever share of its 128 rows they fill: 64 decode requests with 16 pages of 64 take
   // 46.9 us against 51.8 with 4 rows, 52.2 against 55.6 with 16, and 65.5 against 55.7 with 20 (a
   // second pass over the list). Groups of over 128 heads are more than a tile's rows.
-  if (a.R * a.G <= 16 || a.G > 128) {
+  if (takes_rows_kernel(a.R, a.G)) {
 #define PA_ROWS(HS) (bf16 ? launch_rows<HS, true>(a, tk, tv, seg, sms, s) : launch_rows<HS, false>(a, tk, tv, seg, sms, s))
     return a.hs == 64 ? PA_ROWS(64) : a.hs == 128 ? PA_ROWS(128) : PA_ROWS(256);
 #undef PA_ROWS
   }
-  const int sub_rows = a.R * a.G <= 128 ? a.R : 128 / a.G;
+  const int sub_rows = rows_of_tile(a.R, a.G);
   if (!query_block_map(&tq, a.query, bf16, a.hs, a.nh, a.N, a.q_stride, a.G, sub_rows)) return cudaErrorInvalidValue;
 #define PA_TILE(HS)                                                    \
   (bf16 ? launch_tile<HS, true>(a, tq, tk, tv, seg, sub_rows, sms, s) \
