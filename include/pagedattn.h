@@ -360,6 +360,8 @@ pa_status pa_paged_attention_ex(const void* query, const void* key, const void* 
  * (lengths that are negative, exceed the table row or num_tokens, or a free_state that does
  * not fit the ring). A refused step changes neither table nor ring, repeats the state, and
  * describes an empty batch. A call repeated on the same inputs gives the same results.
+ * pa_paged_attention takes only a batch that ends at its num_tokens: where the rows are a fixed
+ * number (a captured step), give those left over to a spare request with past_seqlens 0.
  */
 pa_status pa_build_block_tables(const int32_t* past_seqlens, const int32_t* query_lens, const int32_t* blocks_held,
                                 int32_t* block_table, int32_t* free_blocks, const int32_t* free_state,

@@ -441,3 +441,42 @@ def test_sizes_past_32_bits_are_refused():
     with pytest.raises(ValueError, match="num_tokens"):
         pa.build_block_tables(one, one, one, i32([[0]]), one, i32([0, 0]), block_size=16, num_tokens=big + 1)
     torch.cuda.synchronize()
+
+
+# ---- a step of a fixed number of rows --------------------------------------------------------
+
+
+@pytest.mark.parametrize("stages", [pa.STAGE_ALL, pa.STAGE_PLAN | pa.STAGE_CACHE_WRITE])
+def test_a_padded_step(stages):
+    """16 rows for requests that fill 9: the dense call refuses the batch as it is; with a spare request for the other 7
+    it writes and attends, and the others' rows are what they are without padding."""
+    nh, kvh, hs, n = 8, 2, 64, 16
+    g = torch.Generator().manual_seed(5)
+    rows = torch.randn(n, (nh + 2 * kvh) * hs, generator=g).half().cuda()
+    cache = [torch.randn(12, 16, kvh, hs, generator=g).half().cuda() for _ in range(2)]
+
+    def step(past, q, held, n):
+        B = len(past)
+        kc, vc = (c.clone() for c in cache)
+        table = i32([[3, 1, -1], [0, -1, -1], [-1, -1, -1]][:B])
+        t = pa.build_block_tables(i32(past), i32(q), i32(held), table, i32([2, 4, 5, 6, 7, 8]), i32([0, 6]),
+                                  block_size=16, num_tokens=n)
+        assert int(t.error) == 0
+        dims = pa.make_dims(n, B, hs, 12, 16, 3, torch.float16)
+        ws = torch.zeros(pa.workspace_size(dims, nh, kvh), dtype=torch.uint8, device="cuda")
+        out = torch.zeros(n, nh * hs, dtype=torch.float16, device="cuda")
+        pa.paged_attention(rows[:n], None, None, kc, vc, t.cumulative_sequence_length, i32(past), table, t.slot_mapping,
+                           num_heads=nh, kv_num_heads=kvh, output=out, workspace=ws, stages=stages)
+        return kc, vc, out, pa.read_device_error(ws)
+
+    kc, vc, out, error = step([30, 9], [4, 5], [2, 1], n)
+    assert error == pa.DEVERR_BAD_BATCH and torch.equal(kc, cache[0]) and torch.equal(vc, cache[1]) and not out.any()
+    want = step([30, 9], [4, 5], [2, 1], 9)
+    got = step([30, 9, 0], [4, 5, 7], [2, 1, 0], n)
+    assert want[3] == got[3] == 0
+    mine = [3, 1, 0, 2]  # the two requests' pages; the spare one has taken 4
+    for x, y in zip(want[:2], got[:2]):
+        assert torch.equal(x[mine], y[mine]) and not torch.equal(x[4], y[4])
+        assert not torch.equal(x, cache[0])
+    if stages == pa.STAGE_ALL:
+        assert torch.equal(got[2][:9], want[2][:9])

@@ -187,8 +187,10 @@ def build_block_tables(past_seqlens: torch.Tensor, query_lens: torch.Tensor, blo
     pages go back. ``blocks_held`` (B): pages each request holds. ``block_table`` (B, columns)
     and ``free_blocks`` (a ring of page numbers with ``free_state`` = [head, count]) are updated
     in place; the new ``blocks_held`` and ``free_state`` are returned, with the arguments of the
-    attention call for ``num_tokens`` rows (those behind the last request have slot and position
-    -1). ``out``: a BlockTables to write to, as a captured step keeps it. A step that cannot be
+    attention call for ``num_tokens`` rows. Rows behind the last request have slot and position
+    -1 and are left alone by the operators here; ``paged_attention`` refuses a batch that ends
+    before its rows (DEVERR_BAD_BATCH, nothing written), so where the rows of a captured step are
+    a fixed number, a spare request with ``past_seqlens`` 0 takes those left over. ``out``: a BlockTables to write to, as a captured step keeps it. A step that cannot be
     served changes nothing, describes an empty batch and says why in ``error``."""
     if out is None and stream is None:
         made = (_fast or _load_fast()).build_block_tables(past_seqlens, query_lens, blocks_held, block_table, free_blocks,
