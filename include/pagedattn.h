@@ -325,7 +325,8 @@ pa_status pa_paged_attention_ex(const void* query, const void* key, const void* 
  * PA_DEVERR_BAD_BATCH for a sequence whose lengths do not fit the batch or its table row,
  * PA_DEVERR_BAD_BLOCK for a page outside the pool (or a selection entry that is not a page
  * of the row's history in ascending order); what is bad is skipped, the rest is computed.
- * Calls on the same tensors follow their stream's order; calls share no other state.
+ * Calls on the same tensors follow their stream's order; calls share no other state, whatever
+ * host threads make them.
  */
 
 /* Most requests of one pa_build_block_tables call. */
@@ -449,12 +450,14 @@ pa_status pa_select_pages(const void* query, const int8_t* page_bounds, const fl
  * selected[cumulative_sequence_length[b] + j0][g], j0 = j - j mod query_block (the selection of
  * the block's first row; the other rows' are not read). Entries are logical pages in strictly
  * ascending order; -1 entries are passed over, anything else is skipped with
- * PA_DEVERR_BAD_BLOCK. A row that attends no key gives zeros and an lse of -inf; one that attends a
- * key whose score is NaN gives NaN and an lse of NaN. scale, output
- * and lse (fp32 (N, num_heads) or NULL) as in pa_paged_attention_lse; query rows may be strided.
+ * PA_DEVERR_BAD_BLOCK. A row that attends no key gives zeros and an lse of -inf; one that attends
+ * a key whose score is NaN gives NaN and an lse of NaN. scale, output and lse (fp32 (N, num_heads)
+ * or NULL) as in pa_paged_attention_lse; query rows may be strided.
  * The caches hold T and already hold this step's rows. A value row that is not finite reaches
  * every row of a query block whose last row attends it, the rows before it among them (their
- * weights for it are 0); cache rows behind a block's last row may hold anything.
+ * weights for it are 0); cache rows behind a block's last row may hold anything. A pipeline wait
+ * that runs out sets PA_DEVERR_TIMEOUT in `error` and nowhere else: with NULL the block's undefined
+ * rows come without a sign.
  */
 pa_status pa_sparse_paged_attention(const void* query, const void* key_cache, const void* value_cache,
                                     const int32_t* cumulative_sequence_length, const int32_t* past_seqlens,

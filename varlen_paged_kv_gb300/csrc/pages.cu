@@ -10,8 +10,8 @@
 // page's bounds (in units of the scales); with q split by sign it is sum_c q+_c hi_c - q-_c
 // lo_c, linear in (q+, q-), so the sum of the bounds over the block's R rows and the group's
 // G heads is one product with the summed parts: the cost does not grow with R or G. The
-// summed parts enter as 8-bit codes, so a score is a whole number below 2^24 and the
-// selection is exact: the top_k pages by (score, lowest index), always with the first
+// summed parts enter as 8-bit codes, so a score is a whole number below 2^24 (an estimate of
+// that bound: codes are rounded to the nearest and clipped, not outward) and the selection is exact: the top_k pages by (score, lowest index), always with the first
 // `sink` pages, the last `local` pages up to the block's first row, and the pages that hold
 // the block's rows.
 #include "ops.cuh"
@@ -165,9 +165,9 @@ __device__ __forceinline__ uint64_t f2_unpack(uint32_t w) {
 // The block's codes into sh.code: 12-bit codes t of every row in units of the block's largest
 // product, summed by sign, rescaled to 8 bits. A thread holds up to HOLD 16-byte pieces of
 // the rows in registers between finding the largest value and rounding by it, so that up to
-// HOLD * T / (HS / 8) rows are read from memory once (more are read twice). Arithmetic bounds
-// it on prompts, so it runs on packed pairs: rounding to a whole number is adding and taking
-// off 1.5 * 2^23, and the sums by sign come from those of t and |t| (whole numbers below 2^23,
+// HOLD * T / (HS / 8) rows are read from memory once (more are read twice). On prompts its
+// instructions are most of the kernel's (issue slots 59% busy, the rest mostly waits for those
+// rows), so it runs on packed pairs: rounding to a whole number is adding and taking off 1.5 * 2^23, and the sums by sign come from those of t and |t| (whole numbers below 2^23,
 // so exact in fp32). Products that are not finite are left out in a second form of the
 // same steps.
 template <int HS, bool BF16, int T>
@@ -383,8 +383,8 @@ __device__ void score_pages(const PageArgs& a, const int* table, int g, int i0, 
 // most 32 scores are ranked directly, more go through further histograms. Bytes bound the
 // scoring of long histories (2 HS bytes a page and head: 8 rows with up to 8192 pages read 84 MB
 // and take 30 us, of which the scores 16); short ones are a chain of latencies (64 rows with up
-// to 65 pages 8.1 us); prompts the query rows, read twice (4 prompts of 2048 in blocks of 32:
-// 60 us).
+// to 65 pages 8.1 us); prompts wait in turn for the query rows, which are read twice, and for the
+// arithmetic on them (4 prompts of 2048 in blocks of 32: 59 us; DRAM 15%, issue slots 59% busy).
 template <int HS, bool BF16, int T>
 __global__ void __launch_bounds__(T, T == 256 ? 3 : 1024 / T) select_kernel(const PageArgs a) {
   constexpr int WARPS = T / 32;
@@ -587,7 +587,10 @@ static cudaError_t launch_select_t(const PageArgs& a, int sms, cudaStream_t s) {
   // more CTAs per SM overlap (tables of 544 pages, 4 prompts of 2048 rows: 58 us with 128
   // threads, 67 with 256, 86 with 512; 65 pages, 64 decode rows: 8.2, 11.0, 18.4 us), long ones
   // a stream of bounds and a last CTA's passes over the scores (8193 pages, 8 decode rows: 63,
-  // 41, 33 us; 1025 pages, 32 drafts of 4: 18.4, 15.4, 16.1 us).
+  // 41, 33 us; 1025 pages, 32 drafts of 4: 18.4, 15.4, 16.1 us). The host knows the table's width,
+  // not the histories: short ones in a wide table take the long ones' threads and shared memory (64 decode rows of
+  // up to 65 pages: 8.1 us in 66 to 768 columns, 9.8 up to 4096, 16.9 in 8192, 23.4 in 32768), so
+  // a table cut to the longest history of the step is worth its while.
   auto launch = [&](auto kernel, int threads, int columns) {
     return launch_clusters(kernel, grid, threads, smem, bytes(columns, PA_MAX_SELECTED_PAGES), s, a);
   };

@@ -350,8 +350,8 @@ def select_pages(query: torch.Tensor, page_bounds: torch.Tensor, bound_scale: to
     (pa_select_pages): int32 (N, kv_num_heads, top_k), logical pages in ascending order, then -1.
     Rows [j R, (j + 1) R) of a sequence, R = ``query_block``, share a selection: the first
     ``sink_pages`` pages, the last ``local_pages`` up to the block's first row, the pages of its
-    rows, and the best others by an upper bound of q.k summed over the block's rows and heads,
-    in whole numbers. ``query`` (N, num_heads * head_size) may be a view of packed rows."""
+    rows, and the best others by an estimate from the bounds of the largest q.k, summed over the
+    block's rows and heads, in whole numbers. ``query`` (N, num_heads * head_size) may be a view of packed rows."""
     if selected is None and stream is None:
         made = (_fast or _load_fast()).select_pages(
             query, page_bounds, bound_scale, cumulative_sequence_length, past_seqlens, block_table, num_heads,
@@ -389,7 +389,9 @@ def sparse_paged_attention(query: torch.Tensor, key_cache: torch.Tensor, value_c
     row attends the keys up to its own position that lie in the pages ``selected`` for its query
     block. The caches already hold this step's rows. Returns ``output`` (N, num_heads *
     head_size); ``lse`` (float32 (N, num_heads)) receives the rows' log-sum-exp. A row that
-    attends nothing gives zeros and -inf; rows behind the last sequence are left as they were."""
+    attends nothing gives zeros and -inf; rows behind the last sequence are left as they were.
+    A pipeline wait that runs out (DEVERR_TIMEOUT, the rows of its block undefined) is told by
+    ``error`` only, as there is no workspace to keep it: pass one where that matters."""
     if output is None and stream is None:
         made = (_fast or _load_fast()).sparse_paged_attention(
             query, key_cache, value_cache, cumulative_sequence_length, past_seqlens, block_table, selected, num_heads,
