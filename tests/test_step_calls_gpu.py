@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import varlen_paged_kv_gb300 as pa
-from test_step_gpu import DT, Batch, i32, run_tables, table_state
+from test_step_gpu import DT, Batch, f64, i32, run_tables, table_state
 
 pytestmark = pytest.mark.gpu
 
@@ -480,3 +480,48 @@ def test_a_padded_step(stages):
         assert not torch.equal(x, cache[0])
     if stages == pa.STAGE_ALL:
         assert torch.equal(got[2][:9], want[2][:9])
+
+
+# ---- weights of very different sizes ---------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("bits", [16.3, 24.4, 26.7, 30.2])
+@pytest.mark.parametrize("nh,kvh,hs,R", [(8, 2, 64, 1), (8, 2, 64, 8), (16, 2, 256, 1), (16, 2, 256, 4)])
+def test_small_weights_beside_a_large_one(nh, kvh, hs, R, bits, dtype):
+    """One key with nearly all of the weight and a value of 0 beside thousands of 2^-bits each with values of 1 to 2:
+    they make the output."""
+    n, bs = 60 * 256, 256
+    b = Batch(70, dtype, nh, kvh, hs, bs, [n - R], [R])
+    b.whole_bounds()
+    b.query.zero_()
+    b.query[:, ::hs] = 16
+    b.key_cache.zero_()
+    g = torch.Generator().manual_seed(1)
+    b.value_cache.copy_((1 + torch.rand(b.value_cache.shape, generator=g)).to(DT[dtype]))
+    for at in (0, 100 * bs // 3, n - R):  # the large one: first, on the way, last for the block's first row
+        page, off = b.table[0, at // bs], at % bs
+        value = b.value_cache[page, off].clone()
+        b.key_cache[page, off, :, 0], b.value_cache[page, off] = 16, 0
+        scale = bits * np.log(2) / 256
+        sel = i32(np.tile(np.arange(60), (R, kvh, 1)))
+        out, lse = b.attend(sel, R, scale)
+        k = np.arange(n)
+        v = f64(b.value_cache[b.table[0, k // bs], torch.from_numpy(k % bs)])[:, None]          # (n, 1, kvh, hs)
+        w = np.where(k[:, None] > n - R + np.arange(R), 0.0, 2.0 ** -bits)
+        w[at] = 1.0
+        total = w.sum(0)
+        want = np.einsum("kr,kgc->rgc", w, v[:, 0]) / total[:, None, None]
+        # the scores are exact but for the scale's rounding and the exponential's: 2^-22 of a score of `bits` each in
+        # fp32, 2^-18 of a weight; a weight is rounded to fp16 (2^-11) or, below the subnormals' border, off by 2^-36
+        # of the largest, or to two bf16 terms (2^-16); sums 2^-17; one rounding of the result
+        half = torch.finfo(DT[dtype]).eps / 2
+        weight = 2.0 ** -11 if dtype == "fp16" else 2.0 ** -16
+        small = 2 * n * 2.0 ** -36 if dtype == "fp16" else 0.0  # (values up to 2)
+        bound = want * (half * (1 + 2.0 ** -7) + weight + 2.0 ** -18 + 2.0 ** -17) + small / total[:, None, None] + (
+            2.0 ** -25 if dtype == "fp16" else 0.0)
+        got = f64(out).reshape(R, kvh, nh // kvh, hs)
+        assert (np.abs(got - want[:, :, None]) <= bound[:, :, None]).all(), (np.abs(got - want[:, :, None]) / bound[:, :, None]).max()
+        z = np.log(total) + 256 * scale
+        assert (np.abs(f64(lse) - z[:, None]) <= 2.0 ** -17 * (1 + np.abs(z[:, None]))).all()
+        b.key_cache[page, off, :, 0], b.value_cache[page, off] = 0, value

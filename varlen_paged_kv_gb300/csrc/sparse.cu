@@ -126,6 +126,7 @@ __global__ void __launch_bounds__(kRowsThreads, HS == 256 ? 1 : 2)
                        const __grid_constant__ CUtensorMap tmV, const int seg_rows, const int chunks) {
   using L = RowsSmem<HS>;
   constexpr int NKS = HS / 16, ND = HS / 8;
+  constexpr float kLift = BF16 ? 1.f : 32768.f;  // of the weights on their way into P V
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   float* ml = reinterpret_cast<float*>(smem + L::kMl);
@@ -272,8 +273,10 @@ __global__ void __launch_bounds__(kRowsThreads, HS == 256 ? 1 : 2)
         l0 = l0 * al0 + ((p[0][0] + p[0][1]) + (p[1][0] + p[1][1]));
         l1 = l1 * al1 + ((p[0][2] + p[0][3]) + (p[1][2] + p[1][3]));
         // P as the A operand: fp16 rounds the weights once (2^-11, the output's own rounding and the
-        // dense call's choice; errors of 2.8e-4 where weights of 32 bits leave 2.1e-4 on 64 decode rows);
-        // bf16, whose one rounding would be 2^-8, keeps them as two terms
+        // dense call's choice; errors of 2.8e-4 where weights of 32 bits leave 2.1e-4 on 64 decode rows),
+        // lifted from at most 1 to at most 2^15, so that only those below 2^-29 of the largest are
+        // subnormal and have absolute errors, of 2^-40: without it many small ones beside a large
+        // one were lost; bf16, whose one rounding would be 2^-8, keeps them as two terms
         uint32_t ph[4], pl[4];
         if constexpr (BF16) {
           split_bf16x2(p[0][0], p[0][1], ph[0], pl[0]);
@@ -281,10 +284,10 @@ __global__ void __launch_bounds__(kRowsThreads, HS == 256 ? 1 : 2)
           split_bf16x2(p[1][0], p[1][1], ph[2], pl[2]);
           split_bf16x2(p[1][2], p[1][3], ph[3], pl[3]);
         } else {
-          ph[0] = pack2<false>(p[0][0], p[0][1]);
-          ph[1] = pack2<false>(p[0][2], p[0][3]);
-          ph[2] = pack2<false>(p[1][0], p[1][1]);
-          ph[3] = pack2<false>(p[1][2], p[1][3]);
+          ph[0] = pack2<false>(p[0][0] * kLift, p[0][1] * kLift);
+          ph[1] = pack2<false>(p[0][2] * kLift, p[0][3] * kLift);
+          ph[2] = pack2<false>(p[1][0] * kLift, p[1][1] * kLift);
+          ph[3] = pack2<false>(p[1][2] * kLift, p[1][3] * kLift);
         }
         if (!__all_sync(0xffffffffu, al0 == 1.f && al1 == 1.f)) {
 #pragma unroll
@@ -350,7 +353,7 @@ __global__ void __launch_bounds__(kRowsThreads, HS == 256 ? 1 : 2)
       const int r = gq + 8 * i;
       const float M = fmaxf(fmaxf(ml[r], ml[16 + r]), fmaxf(ml[32 + r], ml[48 + r]));
       const float m = i ? m1 : m0;
-      f[i] = m == -INFINITY ? 0.f : fast_exp2(m - M);
+      f[i] = m == -INFINITY ? 0.f : fast_exp2(m - M) * (1.f / kLift);
     }
     float* dst = part + warp * 16 * L::kStride;
 #pragma unroll
@@ -418,7 +421,7 @@ __global__ void __launch_bounds__(kRowsThreads, HS == 256 ? 1 : 2)
 // two S buffers in TMEM and O += P_t V_t, warps 2 .. 9 are the softmax: two threads share a
 // row (TMEM lets a warp at 32 of the 128 lanes), read 32 of its 64 scores each, exchange their
 // maxima through shared memory, write P over the scores (fp16, or bf16 hi and lo terms) and
-// rescale O in TMEM when the maximum grew by more than 2^8. S_{t+1} is issued before P_t is waited for, so
+// rescale O in TMEM when the maximum grew by more than 2^8 (fp16: 2^4). S_{t+1} is issued before P_t is waited for, so
 // the tensor core works during the softmax; two CTAs share an SM (one with 256-wide heads)
 // and fill each other's gaps, the prologue included. 4 prompts of 2048 rows in blocks of 32, 32
 // pages of 64, bf16: 335 us (821 TFLOP/s, P V counted once); its loads alone take 206 us (10.5
@@ -457,6 +460,10 @@ __global__ void __launch_bounds__(kTileThreads, HS == 256 ? 1 : 2)
   constexpr int HALVES = HS / 64, KSTEPS = HS / 16;
   constexpr uint32_t IDESC_QK = idesc_f16(BF16, 128, kSpTile, false), IDESC_PV = idesc_f16(BF16, 128, HS, true);
   constexpr uint32_t kO = 128;  // TMEM column of O
+  // The row's reference m_used may lag behind its maximum by kLag before O is rescaled. fp16
+  // weights are lifted by 2^kLift, to 2^15 at most, so that only those below 2^-25 of the largest
+  // are subnormal and have absolute errors, of 2^-36; l is lifted with them.
+  constexpr float kLag = BF16 ? 8.f : 4.f, kLift = BF16 ? 0.f : 11.f, kUnlift = BF16 ? 1.f : 1.f / 2048;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + L::kBars);
@@ -669,14 +676,16 @@ __global__ void __launch_bounds__(kTileThreads, HS == 256 ? 1 : 2)
       named_bar_sync(bar, 64);
       const float2 both = *hx;
       const float m_new = fmaxf(m_used, fmaxf(both.x, both.y));
-      const bool grow = __any_sync(0xffffffffu, live && m_new > m_used + 8.f);
+      const bool grow = __any_sync(0xffffffffu, live && m_new > m_used + kLag);
       float alpha = 1.f;
       if (grow) {
-        alpha = m_new == -INFINITY ? 1.f : fast_exp2(m_used - m_new);  // 0 on a row's first keys
-        m_used = m_new;
+        // (fp16: a whole number, which kLift is taken off exactly)
+        const float to = BF16 ? m_new : ceilf(m_new);
+        alpha = m_new == -INFINITY ? 1.f : fast_exp2(m_used - to);  // 0 on a row's first keys
+        m_used = to;
         l *= alpha;
       }
-      const float neg_m = m_used == -INFINITY ? 0.f : -m_used;  // (no key yet: every weight is 0)
+      const float neg_m = m_used == -INFINITY ? 0.f : kLift - m_used;  // (no key yet: every weight is 0)
       const uint64_t c2 = f2_make(c, c), nm2 = f2_make(neg_m, neg_m);
       uint64_t lsum = f2_make(0.f, 0.f);
 #pragma unroll
@@ -732,7 +741,7 @@ __global__ void __launch_bounds__(kTileThreads, HS == 256 ? 1 : 2)
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const int64_t at = (int64_t)(it.row0 + j) * a.nh + g * a.G + row % a.G;
       if (live && a.lse && side == 0)
-        a.lse[at] = m_used == -INFINITY ? -INFINITY : (m_used + fast_log2(l)) * 0.69314718055994531f;
+        a.lse[at] = m_used == -INFINITY ? -INFINITY : (m_used + fast_log2(l * kUnlift)) * 0.69314718055994531f;
 #pragma unroll 1
       for (int cc = side * (HS / 2); cc < (side + 1) * (HS / 2); cc += 32) {
         uint32_t ov[32];
@@ -770,7 +779,7 @@ __global__ void __launch_bounds__(kTileThreads, HS == 256 ? 1 : 2)
       const float f = m_used == -INFINITY ? 0.f : fast_exp2(m_used - M) / S;
       if (rank == 0 && live && a.lse && side == 0)
         a.lse[(int64_t)(it.row0 + j) * a.nh + g * a.G + row % a.G] =
-            M == -INFINITY ? -INFINITY : (M + fast_log2(S)) * 0.69314718055994531f;
+            M == -INFINITY ? -INFINITY : (M + fast_log2(S * kUnlift)) * 0.69314718055994531f;
 #pragma unroll 1
       for (int cc = side * (HS / 2); any_live && cc < (side + 1) * (HS / 2); cc += 32) {
         uint32_t ov[32];
