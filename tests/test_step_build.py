@@ -45,6 +45,16 @@ def test_the_library_is_built_where_the_compiled_calls_cannot_be(tree):
     assert os.path.exists(build.LIB)
 
 
+def test_the_library_is_built_where_there_is_no_torch(tree, monkeypatch):
+    def absent():
+        raise ImportError("no torch")
+
+    monkeypatch.setattr(build, "binding_path", absent)
+    with pytest.warns(RuntimeWarning, match="no torch"):
+        assert build.build() == build.LIB
+    assert os.path.exists(build.LIB)
+
+
 def test_the_calls_are_made_in_python_where_the_compiled_ones_are_missing(monkeypatch, tmp_path):
     build.build()
     monkeypatch.setattr(step, "_fast", None)

@@ -93,11 +93,13 @@ def build_binding(force: bool = False) -> str:
 
 def _try_binding(force: bool = False) -> None:
     """build_binding, or a warning; a binding that is out of date does not stay."""
+    out = None
     try:
+        out = binding_path()
         build_binding(force)
-    except Exception as e:  # noqa: BLE001 (no compiler, no headers, an import error, ...)
-        if os.path.exists(binding_path()):
-            os.unlink(binding_path())
+    except Exception as e:  # noqa: BLE001 (no torch, no compiler, no headers, ...)
+        if out is not None and os.path.exists(out):
+            os.unlink(out)
         warnings.warn(f"the compiled calls were not built, each call takes some microseconds longer: {e}", RuntimeWarning)
 
 
