@@ -525,3 +525,45 @@ def test_small_weights_beside_a_large_one(nh, kvh, hs, R, bits, dtype):
         z = np.log(total) + 256 * scale
         assert (np.abs(f64(lse) - z[:, None]) <= 2.0 ** -17 * (1 + np.abs(z[:, None]))).all()
         b.key_cache[page, off, :, 0], b.value_cache[page, off] = 0, value
+
+
+def test_host_threads_each_with_its_own_steps():
+    """Four threads, each with its stream, its batch and every operator: what each gives alone."""
+    jobs = []
+    for seed, (dtype, nh, kvh, hs, R, top_k) in enumerate([("fp16", 8, 2, 128, 1, 9), ("bf16", 16, 2, 256, 4, 30),
+                                                           ("fp16", 8, 2, 64, 32, 200), ("bf16", 8, 8, 64, 1, 40)]):
+        b = Batch(80 + seed, dtype, nh, kvh, hs, 16, [1500, 3000, 700], [1, 33, 2])
+        b.whole_bounds()
+        q, pos = b.query.contiguous(), i32(np.arange(b.N))
+        tables = run_tables(*table_state(np.random.default_rng(seed), 30 * (seed + 1), 16, 20, 200, 40, 0.2), 16, 6000)[1]
+
+        def job(b=b, q=q, pos=pos, tables=tables, R=R, top_k=top_k):
+            sel = b.select(top_k, R)
+            out = pa.sparse_paged_attention(b.query, b.key_cache, b.value_cache, *b.meta, sel, num_heads=b.nh,
+                                            kv_num_heads=b.kvh, query_block=R)
+            turned = pa.qk_norm_rope(q, q[:, : b.kvh * b.hs], pos, num_heads=b.nh, kv_num_heads=b.kvh, rotary_dim=b.hs)
+            bounds = pa.update_page_bounds(b.key_cache, b.bounds.clone(), b.scale, *b.meta, num_tokens=b.N)
+            return [sel, out, *turned, bounds, *pa.build_block_tables(*tables, block_size=16, num_tokens=6000)]
+
+        jobs.append((job, job()))
+    torch.cuda.synchronize()
+    wrong, start = [], threading.Barrier(len(jobs))
+
+    def loop(job, want):
+        start.wait()
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(100):
+                    got = job()
+                    torch.cuda.current_stream().synchronize()
+                    if not all(torch.equal(x, y) for x, y in zip(got, want)):
+                        wrong.append("differs")
+        except Exception as e:  # noqa: BLE001
+            wrong.append(e)
+
+    threads = [threading.Thread(target=loop, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong[:3]

@@ -1019,9 +1019,10 @@ __device__ __forceinline__ int own_mirror_base(const Args& a, int b, int lane) {
 // One instantiation per kind of write, so that each keeps only the registers it needs and
 // stays many warps deep (at most 64 registers: four blocks of 256 per SM): 0 = bit copy,
 // one warp per token, 4 = the same beside this call's planner, 5 = that with the fp16 V
-// copy, 6 = the bit copy of a batch that no planner has checked; 1 = Q/K preparation, 2 = integer caches, 3 = both, over (token, unit) tasks, the
-// units being the token's nh query heads and then its kvh KV heads (each a short dependent
-// chain of a load, warp reductions and a store); each warp takes a contiguous run of them.
+// copy, 6 = the bit copy of a batch that no planner has checked; 1 = Q/K preparation, 2 =
+// integer caches, 3 = both, over (token, unit) tasks, the units being the token's nh query
+// heads and then its kvh KV heads (each a short dependent chain of a load, warp reductions
+// and a store); each warp takes a contiguous run of them.
 template <int MODE>
 __global__ void __launch_bounds__(256, 4) cache_write_kernel(const Args a) {
   constexpr bool COPY = MODE == 0 || MODE >= 4;  // bit copy
