@@ -464,6 +464,163 @@ pa_status pa_sparse_paged_attention(const void* query, const void* key_cache, co
                                     const int32_t* block_table, const int32_t* selected, float scale, void* output,
                                     float* lse, const pa_sparse_dims* dims, uint32_t* error, void* stream);
 
+/* ======================= pages that are shared, copied and moved ======================= */
+
+/* Most pages of a pool that the two entry points below take, and most tensors of one copy. */
+#define PA_MAX_POOL_PAGES (1 << 20)
+#define PA_MAX_COPY_TENSORS 256
+
+/* Bytes of the device workspace (16-byte aligned) of pa_fork_block_tables and
+ * pa_compact_block_tables for a pool of num_blocks pages; 0 for sizes they refuse. Calls that
+ * share a workspace must be ordered. It holds nothing between calls. */
+size_t pa_pool_workspace_size(int32_t num_blocks);
+
+/*
+ * The rows of a new batch from rows of the old one: beams that survive, samples of one prompt,
+ * requests that end. Row b of the new batch continues row parents[b] of the old one, whose pages
+ * it shares; pages that nothing holds any more go back to the ring of free pages.
+ *
+ *   parents        int32 (new_batch_size): a row of the old batch, any number of times and in any
+ *                  order, or -1: the new row is empty.
+ *   past_seqlens, blocks_held, block_table, free_blocks, free_state
+ *                  as for pa_build_block_tables (batch_size old rows). Rows may share pages.
+ *   pinned         uint8 (num_blocks) or NULL: not 0 for pages that something else holds as well
+ *                  (a prefix cache): they are shared like any page, but never written to by a new
+ *                  row nor given back.
+ *
+ * Row b gets past_seqlens_out = past, blocks_held_out = ceil(past / block_size) pages and the
+ * parent's table entries for them, -1 behind (an empty row: 0, 0 and -1). Pages that its
+ * parent held beyond those (for tokens that were taken back) are not kept. Its next token is written into the
+ * last of them where past mod block_size is not 0, so of the new rows whose last page that is the
+ * lowest keeps it, and only if no new row holds it as a whole page and it is not pinned; every
+ * other one takes the next free page at the ring's head, rows in order, and the pair (old page,
+ * new page) joins copies, int32 (new_batch_size, 2) with (-1, -1) behind the last: pa_copy_pages
+ * makes them, before anything else is written to either page. Pages in the first blocks_held
+ * columns of the old rows that no new row holds and that are not pinned are appended behind the
+ * last free page in ascending order; none of them is given out by the same call.
+ *
+ * free_blocks is updated in place, free_state_out (2) is the state for the next step; the other
+ * outputs are in memory of their own. error (1), not accumulated: 0, or why the fork was refused:
+ * PA_DEVERR_NO_BLOCKS (fewer free pages than copies), PA_DEVERR_BAD_BLOCK (a held entry outside
+ * the pool) or PA_DEVERR_BAD_BATCH (a parent, length or count out of range, a parent that holds
+ * less than its past, a free_state that does not fit the ring). A refused fork changes neither
+ * the old batch nor the ring, repeats free_state and describes new_batch_size empty rows without
+ * copies. A call repeated on the same inputs gives the same results. (A request that shares pages
+ * is ended by a -1 here, not in pa_build_block_tables, which gives back all pages of a finished
+ * request.)
+ */
+pa_status pa_fork_block_tables(const int32_t* parents, const int32_t* past_seqlens, const int32_t* blocks_held,
+                               const int32_t* block_table, int32_t* free_blocks, const int32_t* free_state,
+                               const uint8_t* pinned, int32_t batch_size, int32_t new_batch_size,
+                               int32_t max_blocks_per_sequence, int32_t block_size, int32_t num_blocks,
+                               int32_t free_capacity, int32_t* past_seqlens_out, int32_t* blocks_held_out,
+                               int32_t* block_table_out, int32_t* copies, int32_t* free_state_out, uint32_t* error,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Moves pages down so that the pool's tail falls free. In use are the pages in the first
+ * blocks_held columns of the rows, and the pinned ones, which do not move; all others are free
+ * (so whatever holds pages outside this table pins them). The r-th highest page that may
+ * move goes to the r-th lowest free page for r = 0, 1, .. while r < max_moves and the free page is
+ * the lower one. block_table_out (which may be block_table) has the held entries renamed and the
+ * others as they were; copies, int32 (max_moves, 2), has the pairs (from, to) in that order, then
+ * (-1, -1): pa_copy_pages makes them before the new table is used. free_blocks (a ring of
+ * free_capacity entries) receives all pages that are free after the moves in ascending order,
+ * with free_state_out = {0, their count}; its other entries stay. pages_end (1): one more than the
+ * highest page still in use.
+ *
+ * error (1), not accumulated: 0, or why nothing was moved: PA_DEVERR_BAD_BLOCK (a held entry
+ * outside the pool) or PA_DEVERR_BAD_BATCH (blocks_held out of range, more free pages than
+ * free_capacity). Then the table is repeated, there are no copies, the ring is left as it was,
+ * free_state_out is {0, 0} (the caller's own state still holds) and pages_end 0.
+ */
+pa_status pa_compact_block_tables(const int32_t* blocks_held, const int32_t* block_table, int32_t* free_blocks,
+                                  const uint8_t* pinned, int32_t batch_size, int32_t max_blocks_per_sequence,
+                                  int32_t num_blocks, int32_t free_capacity, int32_t max_moves,
+                                  int32_t* block_table_out, int32_t* copies, int32_t* free_state_out,
+                                  int32_t* pages_end, uint32_t* error, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/* A tensor of pages: num_blocks pages of page_bytes bytes one after the other (a key or value
+ * cache of any element type, page bounds). data 16-byte aligned, page_bytes a multiple of 16. */
+typedef struct pa_page_tensor {
+  void* data;
+  int64_t page_bytes;
+} pa_page_tensor;
+
+/*
+ * Page copies[i][1] of every tensor becomes a copy of page copies[i][0], for all i < num_copies of
+ * which neither is -1. `tensors` is host memory, read by the call. No page may be the target of
+ * two entries, or the target of one and the source of another (what pa_fork_block_tables and
+ * pa_compact_block_tables give never is). Entries outside the pool are skipped with
+ * PA_DEVERR_BAD_BLOCK in `error` (which may be NULL).
+ */
+pa_status pa_copy_pages(const pa_page_tensor* tensors, int32_t num_tensors, int32_t num_blocks, const int32_t* copies,
+                        int32_t num_copies, uint32_t* error, void* stream);
+
+/* ================= attention with capped or biased scores and ranges of keys =========== */
+
+/* What pa_biased_paged_attention does to the scores, and which keys a row sees. All device
+ * pointers may be NULL. */
+typedef struct pa_score_rules {
+  float softcap;               /* c > 0: a score s becomes c * tanh(s / c); 0: no cap */
+  int32_t window;              /* w > 0: a row at position p sees no key before p - w + 1; 0: no window */
+  const float* slopes;         /* fp32 (num_heads): slopes[h] * |p - t| is taken off the score of key t */
+  const int32_t* first_keys;   /* int32 (num_tokens): a row sees no key before its own first one (packed
+                                  documents); one beyond the row's last key leaves it none */
+  const int32_t* prefix_lens;  /* int32 (batch_size): every row sees the sequence's first prefix_lens[b]
+                                  keys, those after its own position too, up to the sequence's end */
+  int64_t reserved;            /* 0 */
+} pa_score_rules;
+
+/* Host-side sizes, as in pa_sparse_dims. */
+typedef struct pa_biased_dims {
+  int32_t num_tokens;
+  int32_t batch_size;
+  int32_t num_heads;
+  int32_t kv_num_heads;
+  int32_t head_size;               /* 64, 128 or 256 */
+  int32_t num_blocks;
+  int32_t block_size;              /* a positive multiple of 16 */
+  int32_t max_blocks_per_sequence;
+  int32_t dtype;                   /* pa_dtype of T */
+  int32_t max_query_len;           /* 0, or a bound on every sequence's new rows: a batch that it proves to be
+                                      of few rows launches fewer kernels; longer sequences are skipped with
+                                      PA_DEVERR_BAD_BATCH */
+  int64_t query_stride;            /* elements between rows of query: a multiple of 8 */
+  int64_t reserved;                /* 0 */
+} pa_biased_dims;
+
+/* Most CTAs whose partial results the workspace has room for. */
+#define PA_BIASED_CTAS 320
+/* Bytes of the device workspace (16-byte aligned) of pa_biased_paged_attention; 0 for a head size
+ * that it refuses. Calls that share a workspace must be ordered. It holds nothing between calls. */
+size_t pa_biased_workspace_size(int32_t head_size);
+
+/*
+ * pa_paged_attention's read path with other scores and other masks. Row j of sequence b, at position
+ * p = past_seqlens[b] + j, sees the keys t in [lo, hi),
+ *   lo = max(0, first_keys[row], p - window + 1),
+ *   hi = min(past_seqlens[b] + q_len, max(p + 1, prefix_lens[b])),
+ * (of the terms that are given) with scores scale * q.k, capped, then biased, as pa_score_rules says. Softmax and accumulation are
+ * fp32, the output is rounded once to T; lse (fp32 (N, num_heads) or NULL) is the natural-log
+ * log-sum-exp of those scores. A row that sees no key gives zeros and an lse of -inf. scale and
+ * query rows as in pa_sparse_paged_attention; the caches hold T and already hold this step's rows.
+ *
+ * Pages that no row of a sequence sees are not looked up (their table entries may be anything, as
+ * those that a window has left behind), and what masked keys hold reaches no score. Rows of a
+ * sequence are worked on in blocks of up to 128 / (num_heads / kv_num_heads): a value row that is
+ * not finite and that one row of a block sees may reach the others of that block; value rows
+ * that none of them sees, before the first or behind the last key, reach none.
+ * A page outside the pool reads as zeros, with PA_DEVERR_BAD_BLOCK in `error`; a pipeline wait that
+ * runs out sets PA_DEVERR_TIMEOUT there and nowhere else.
+ */
+pa_status pa_biased_paged_attention(const void* query, const void* key_cache, const void* value_cache,
+                                    const int32_t* cumulative_sequence_length, const int32_t* past_seqlens,
+                                    const int32_t* block_table, float scale, const pa_score_rules* rules, void* output,
+                                    float* lse, const pa_biased_dims* dims, uint32_t* error, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. Never NULL. */
 const char* pa_status_string(pa_status status);
 

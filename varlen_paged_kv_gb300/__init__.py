@@ -253,7 +253,11 @@ def paged_attention(query: torch.Tensor, key: Optional[torch.Tensor], value: Opt
 
 from .step import (BlockTables, PaSparseDims, build_block_tables, qk_norm_rope, select_pages,  # noqa: E402
                    sparse_paged_attention, update_page_bounds)
+from .pool import (CompactedTables, ForkedTables, compact_block_tables, copy_pages, fork_block_tables,  # noqa: E402
+                   pool_workspace_size)
+from .biased import biased_paged_attention, biased_workspace_size  # noqa: E402
 
-__all__ = ["BlockTables", "PaSparseDims", "build_block_tables", "qk_norm_rope", "select_pages",
+__all__ = ["CompactedTables", "ForkedTables", "compact_block_tables", "copy_pages", "fork_block_tables",
+           "pool_workspace_size", "biased_paged_attention", "biased_workspace_size", "BlockTables", "PaSparseDims", "build_block_tables", "qk_norm_rope", "select_pages",
            "sparse_paged_attention", "update_page_bounds", "KV_SAME", "KV_INT8", "KV_INT4", "paged_attention", "workspace_size", "make_dims", "PaQkPrep", "PaExtensions", "read_device_error", "kernel_launch_count",
            "load_library", "PagedAttentionError", "PaDims", "LIBRARY_PATH"]

@@ -1,0 +1,634 @@
+// Attention over the paged cache with capped scores, biases that grow with the distance, and a
+// range of keys for every row.
+//
+// Row j of a sequence is at position p = past + j and sees the keys [lo, hi): lo the largest of 0,
+// first_keys[row] and p - window + 1, hi the smaller of past + q and max(p + 1, prefix). Its score
+// of key t for head h is s = scale q.k, then cap * tanh(s / cap), then - slope_h |p - t|; softmax
+// and P V in fp32, rounded once to T. A row without keys gives zeros and an lse of -inf. Keys that
+// no row of an item sees are not read, so their pages need not be there (a window's old pages).
+//
+// Two kernels, by the rows that share a KV head's keys:
+//   biased_rows_kernel  sequences of up to 16 such rows (decode steps, short drafts): bound by the
+//                       bytes of K and V; the work is cut into equal shares whatever the lengths,
+//                       and biased_merge_kernel joins what a cut went through;
+//   biased_tile_kernel  longer ones (prompts, wide groups): tcgen05, 128 rows against tiles of 64 keys.
+#include "ops.cuh"
+
+namespace pa {
+
+constexpr int kBiTile = 64;          // keys per tile
+constexpr int kBiThreads = 160;      // rows kernel: four consumer warps and a producer
+constexpr int kBiCost = 3;           // what an item costs beside its tiles, in tiles
+constexpr int kMergeThreads = 128;
+
+// ---- scores --------------------------------------------------------------------------------
+// tanh on |u| <= 0.75 as u times a polynomial in u^2 (minimax by weighted least squares on 4000
+// Chebyshev points: 9.5e-9 off at most, below fp32's rounding), beyond it from the exponential;
+// the instruction tanh.approx is 5e-4 off, which a cap of 50 would turn into scores 0.02 off.
+constexpr float kTanhReach = 0.75f;
+__device__ constexpr float kTanh[6] = {0.99999983f, -0.33332471f, 0.1332058f, -0.05314926f, 0.01923724f, -0.00449346f};
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float tanh_far(float u) {  // 1 - 2 / (1 + e^2|u|), with u's sign
+  return copysignf(1.f - 2.f * rcp_approx(1.f + fast_exp2(fabsf(u) * 2.8853900818f)), u);
+}
+__device__ __forceinline__ float tanh_near(float u) {
+  const float z = u * u;
+  float y = kTanh[5];
+#pragma unroll
+  for (int i = 4; i >= 0; --i) y = fmaf(y, z, kTanh[i]);
+  return u * y;
+}
+__device__ __forceinline__ float tanh_of(float u) { return fabsf(u) <= kTanhReach ? tanh_near(u) : tanh_far(u); }
+
+// ---- ranges --------------------------------------------------------------------------------
+struct Keys {
+  int lo, hi;  // (lo >= hi: none, then lo = INT32_MAX and hi = 0)
+};
+__device__ __forceinline__ Keys keys_of_row(const BiasedArgs& a, const Seq& s, int prefix, int j) {
+  const int p = s.past + j;
+  Keys k;
+  k.lo = a.first ? max(a.first[s.c0 + j], 0) : 0;
+  if (a.window) k.lo = max(k.lo, p - a.window + 1);
+  k.hi = min(max(p + 1, prefix), s.past + s.q);
+  if (k.lo >= k.hi) k.lo = INT32_MAX, k.hi = 0;
+  return k;
+}
+__device__ __forceinline__ Keys join(Keys x, Keys y) { return {min(x.lo, y.lo), max(x.hi, y.hi)}; }
+
+__device__ __forceinline__ Seq seq_at(const BiasedArgs& a, int b) {
+  Seq s = make_seq(b, a.cum[b], a.cum[b + 1], a.past[b], a.N, a.max_blocks, a.bs);
+  s.ok = s.ok && (a.max_rows == 0 || s.q <= a.max_rows);
+  return s;
+}
+// whether a sequence is the rows kernel's
+__device__ __forceinline__ bool short_rows(const BiasedArgs& a, const Seq& s) {
+  return s.ok && s.q > 0 && (a.G > 128 || (int64_t)s.q * a.G <= 16);
+}
+
+// the checks of the whole batch, by one CTA
+__device__ __forceinline__ void check_biased_batch(const BiasedArgs& a) {
+  if (!a.error) return;
+  bool bad = threadIdx.x == 0 && a.cum[0] != 0;
+  for (int b = threadIdx.x; b < a.B; b += blockDim.x) bad |= !seq_at(a, b).ok;
+  if (bad) atomicOr(a.error, PA_DEVERR_BAD_BATCH);
+}
+
+// ---- few rows: equal shares of all tiles ----------------------------------------------------
+// All (sequence, KV head, 16 rows) units stand in a row, each as long as its 64-key tiles and
+// kBiCost; CTA c of C takes the c-th C-th of that. What a CTA has of a unit is an item: its
+// tiles go through a ring of K and V tiles (TMA, one box per page segment, 128-byte swizzle);
+// each of four consumer warps takes 16 keys of every tile (S = Q K^T by mma.sync, an online
+// softmax in registers, O += P V, bf16 with P as two bf16 terms); the warps' (m, l, O) meet in
+// shared memory. A whole unit is written out, a piece of one goes to one of the CTA's two slots
+// (2c: its unit began with an earlier CTA; 2c + 1: it goes on with the next) and the merge
+// kernel joins the slots in order. Every warp walks the units by itself.
+template <int HS>
+struct BiRows {
+  static constexpr int kStages = 3;
+  static constexpr int kTileBytes = kBiTile * HS * 2;
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kStride = HS + 4;                      // floats between rows of a partial result
+  static constexpr int kComb = kStages * kStageBytes;         // float [16][kStride]
+  static constexpr int kMl = kComb + 16 * kStride * 4;        // float [2][4][16]: m and l of the warps
+  static constexpr int kPre = kMl + 2 * 4 * 16 * 4;           // int64 [kBiThreads + 1]: costs before each thread's sequences
+  static constexpr int kBars = kPre + (kBiThreads + 2) * 8;
+  static constexpr int kAbort = kBars + 2 * kStages * 8;      // abort flag, error word
+  static constexpr int kBytes = kAbort + 16 + 1024;
+};
+static_assert(2 * (BiRows<128>::kBytes + 1024) <= 233472 && BiRows<256>::kBytes <= 232448, "rows kernel's shared memory");
+
+struct BiItem {
+  int b, c0, q, past, prefix;
+  int r_first, n_rows, g;  // rows r = j * G + head of the sequence, from r_first
+  int ta, te;              // tiles
+  Keys keys;               // of all rows of the sequence
+  bool first, last;        // the unit's first, last tiles
+};
+
+// the tiles of a sequence's rows
+__device__ __forceinline__ int2 tiles_of(Keys k) {
+  return k.hi > 0 ? make_int2(k.lo / kBiTile, (k.hi + kBiTile - 1) / kBiTile) : make_int2(0, 0);
+}
+
+struct BiWalk {
+  int64_t pos, end, base;  // the CTA's share; where sequence b begins
+  int b, u;                // the next unit
+  bool loaded;
+  Seq s;
+  Keys keys;
+  int prefix, units, chunks, t0, nt;
+
+  // by a whole warp: the sequence's lengths and keys
+  __device__ __forceinline__ void load(const BiasedArgs& a, int lane) {
+    s = seq_at(a, b);
+    units = 0;
+    loaded = true;
+    if (!short_rows(a, s)) return;
+    prefix = a.prefix ? a.prefix[b] : 0;
+    keys = {INT32_MAX, 0};
+    if (a.first) {
+      for (int j = lane; j < s.q; j += 32) keys = join(keys, keys_of_row(a, s, prefix, j));
+      keys.lo = __reduce_min_sync(0xffffffffu, keys.lo);
+      keys.hi = __reduce_max_sync(0xffffffffu, keys.hi);
+    } else {
+      keys = join(keys_of_row(a, s, prefix, 0), keys_of_row(a, s, prefix, s.q - 1));
+    }
+    const int2 t = tiles_of(keys);
+    t0 = t.x;
+    nt = t.y - t.x;
+    chunks = (int)(((int64_t)s.q * a.G + 15) / 16);
+    units = a.kvh * chunks;
+  }
+  __device__ __forceinline__ bool next(const BiasedArgs& a, int lane, BiItem& it) {
+    for (;;) {
+      if (b >= a.B || base >= end) return false;
+      if (!loaded) {
+        load(a, lane);
+        u = base < pos && units ? (int)((pos - base) / (nt + kBiCost)) : 0;
+      }
+      const int cost = nt + kBiCost;
+      if (u >= units) {
+        if (units) base += (int64_t)units * cost;
+        ++b;
+        loaded = false;
+        continue;
+      }
+      const int64_t start = base + (int64_t)u * cost;
+      if (start >= end) return false;
+      const int unit = u++;
+      int64_t x = 0, y = 0;
+      if (nt == 0) {
+        if (start < pos) continue;
+      } else {
+        x = max(max(pos, start) - start - kBiCost, (int64_t)0);
+        y = max(min(end, start + cost) - start - kBiCost, (int64_t)0);
+        if (y <= x) continue;
+      }
+      it.b = b, it.c0 = s.c0, it.q = s.q, it.past = s.past, it.prefix = prefix;
+      it.g = unit / chunks;
+      it.r_first = unit % chunks * 16;
+      it.n_rows = min(16, s.q * a.G - it.r_first);
+      it.ta = t0 + (int)x, it.te = t0 + (int)y;
+      it.keys = keys;
+      it.first = x == 0, it.last = y == nt;
+      return true;
+    }
+  }
+};
+
+template <int HS, bool BF16>
+__global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
+    biased_rows_kernel(const BiasedArgs a, const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV, const int seg_rows) {
+  using L = BiRows<HS>;
+  constexpr int NKS = HS / 16, ND = HS / 8;
+  constexpr float kLift = BF16 ? 1.f : 32768.f;  // of the weights on their way into P V
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  float* comb = reinterpret_cast<float*>(smem + L::kComb);
+  float* ml = reinterpret_cast<float*>(smem + L::kMl);
+  int64_t* pre = reinterpret_cast<int64_t*>(smem + L::kPre);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBars);
+  uint64_t* empty = full + L::kStages;
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kAbort);
+  uint32_t* err = reinterpret_cast<uint32_t*>(smem + L::kAbort + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 4);
+    }
+    *abort = 0;
+    *err = 0;
+    fence_mbar_init();
+  }
+  pdl_wait();
+  // the costs of all sequences, each thread those of a run of them
+  const int run = (a.B + kBiThreads - 1) / kBiThreads;
+  {
+    int64_t mine = 0;
+    for (int i = 0; i < run; ++i) {
+      const int b = threadIdx.x * run + i;
+      if (b >= a.B) break;
+      const Seq s = seq_at(a, b);
+      if (!short_rows(a, s)) continue;
+      const int prefix = a.prefix ? a.prefix[b] : 0;
+      Keys k = join(keys_of_row(a, s, prefix, 0), keys_of_row(a, s, prefix, s.q - 1));
+      if (a.first)
+        for (int j = 1; j < s.q - 1; ++j) k = join(k, keys_of_row(a, s, prefix, j));
+      const int2 t = tiles_of(k);
+      mine += (int64_t)a.kvh * (((int64_t)s.q * a.G + 15) / 16) * (t.y - t.x + kBiCost);
+    }
+    pre[threadIdx.x + 1] = mine;
+  }
+  if (blockIdx.x == 0) check_biased_batch(a);
+  __syncthreads();
+  if (warp == 0) {  // sums, five threads' costs a lane
+    int64_t v[kBiThreads / 32], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kBiThreads / 32; ++i) sum += pre[lane * (kBiThreads / 32) + i + 1], v[i] = sum;
+    int64_t x = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
+    }
+#pragma unroll
+    for (int i = 0; i < kBiThreads / 32; ++i) pre[lane * (kBiThreads / 32) + i + 1] = x - sum + v[i];
+    if (lane == 0) pre[0] = 0;
+  }
+  __syncthreads();
+  const int64_t W = pre[kBiThreads];
+  const int C = (int)min((int64_t)gridDim.x, max(W / (kBiCost + 1), (int64_t)1));
+  const int c = blockIdx.x;
+  BiWalk walk;
+  walk.pos = c < C ? W * c / C : W;
+  walk.end = c < C ? W * (c + 1) / C : W;
+  walk.loaded = false;
+  {  // the thread whose sequences hold the share's beginning
+    int k = 0;
+#pragma unroll
+    for (int i = 0; i < kBiThreads / 32; ++i) k += __popc(__ballot_sync(0xffffffffu, pre[i * 32 + lane + 1] <= walk.pos));
+    k = min(k, kBiThreads - 1);
+    walk.b = k * run;
+    walk.base = pre[k];
+  }
+  if (walk.pos >= walk.end) {
+    if (threadIdx.x == 0) a.records[2 * c] = make_int4(0, 0, 0, 0), a.records[2 * c + 1] = make_int4(0, 0, 0, 0);
+    return;
+  }
+  BiItem it;
+  int n = 0;  // tiles so far
+
+  if (warp == 4) {
+    // ---- producer ----
+    const int nseg = kBiTile / seg_rows, oob = a.num_blocks * a.bs;
+    int4 head = make_int4(0, 0, 0, 0);
+    int cont = 0;
+    while (walk.next(a, lane, it)) {
+      if (it.first && !it.last) head = make_int4(it.n_rows, it.c0, it.r_first, it.g);
+      if (!it.first) cont = it.last ? 2 : 1;
+      const int* table = a.table + (int64_t)it.b * a.max_blocks;
+      auto slot = [&](int t) {  // this lane's segment of tile t: its first cache row
+        const int v = t * kBiTile + lane * seg_rows;
+        if (lane >= nseg || t >= it.te || v >= it.keys.hi || v + seg_rows <= it.keys.lo) return oob;
+        const int page = v / a.bs, phys = table[page];
+        if (phys < 0 || phys >= a.num_blocks) {
+          atomicOr(err, PA_DEVERR_BAD_BLOCK);
+          return oob;
+        }
+        return phys * a.bs + (v - page * a.bs);
+      };
+      int z = slot(it.ta);
+      for (int t = it.ta; t < it.te; ++t, ++n) {
+        const int s = n % L::kStages, z_next = slot(t + 1);
+        if (lane == 0) {
+          mbar_wait(&empty[s], ((n / L::kStages) & 1) ^ 1, abort, err);
+          mbar_arrive_expect_tx(&full[s], L::kStageBytes);
+        }
+        __syncwarp();
+        if (lane < nseg) {
+          uint8_t* dst = smem + s * L::kStageBytes + lane * seg_rows * 128;
+#pragma unroll
+          for (int h = 0; h < HS / 64; ++h) {
+            tma_load_3d(dst + h * kBiTile * 128, &tmK, &full[s], h * 64, it.g, z);
+            tma_load_3d(dst + L::kTileBytes + h * kBiTile * 128, &tmV, &full[s], h * 64, it.g, z);
+          }
+        }
+        __syncwarp();
+        z = z_next;
+      }
+    }
+    if (lane == 0) a.records[2 * c] = head, a.records[2 * c + 1] = make_int4(cont, 0, 0, 0);
+  } else {
+    // ---- consumers: warp w has keys 16w .. 16w + 15 of every tile ----
+    const int w = warp, tq = lane & 3, gq = lane >> 2;
+    const int mi = lane >> 3, rr = lane & 7;
+    while (walk.next(a, lane, it)) {
+      Seq sq;
+      sq.c0 = it.c0, sq.q = it.q, sq.past = it.past;
+      uint32_t qa[NKS][4];  // Q as the A operand: rows gq and gq + 8
+      Keys k[2];
+      int pos[2];
+      float slope[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = it.r_first + gq + 8 * i, rc = min(r, it.r_first + it.n_rows - 1);  // (padding rows borrow the last row's keys)
+        const int j = rc / a.G, h = it.g * a.G + rc % a.G;
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(a.query + (int64_t)(it.c0 + j) * a.q_stride + (int64_t)h * HS + tq * 2);
+#pragma unroll
+        for (int ks = 0; ks < NKS; ++ks) {
+          qa[ks][i] = rc == r ? __ldg(p + ks * 8) : 0u;
+          qa[ks][i + 2] = rc == r ? __ldg(p + ks * 8 + 4) : 0u;
+        }
+        k[i] = keys_of_row(a, sq, it.prefix, j);
+        pos[i] = it.past + j;
+        slope[i] = a.slopes ? a.slopes[h] * 1.4426950408889634f : 0.f;
+      }
+      // keys that some row sees, and those that all see
+      const int some_lo = __reduce_min_sync(0xffffffffu, min(k[0].lo, k[1].lo));
+      const int some_hi = __reduce_max_sync(0xffffffffu, max(k[0].hi, k[1].hi));
+      const int all_lo = __reduce_max_sync(0xffffffffu, max(k[0].lo, k[1].lo));
+      const int all_hi = __reduce_min_sync(0xffffffffu, min(k[0].hi, k[1].hi));
+      float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+      float o[ND][4];
+#pragma unroll
+      for (int d = 0; d < ND; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
+      for (int t = it.ta; t < it.te; ++t, ++n) {
+        const int s = n % L::kStages;
+        mbar_wait(&full[s], (n / L::kStages) & 1, abort, err);
+        const uint32_t kb = smem_u32(smem + s * L::kStageBytes), vb = kb + L::kTileBytes;
+        const int v0 = t * kBiTile + 16 * w;  // the warp's first key
+        if (v0 < some_hi && v0 + 16 > some_lo) {
+          float sa[2][4] = {}, sb[2][4] = {};  // keys 0-7 and 8-15; even and odd k-steps
+          {
+            const int key = 16 * w + (mi >> 1) * 8 + rr;
+#pragma unroll
+            for (int ks = 0; ks < NKS; ++ks) {
+              const int cc = ks * 2 + (mi & 1);
+              uint32_t b0, b1, b2, b3;
+              ldsm_x4(kb + (cc >> 3) * (kBiTile * 128) + key * 128 + (((cc & 7) ^ (key & 7)) << 4), b0, b1, b2, b3);
+              mma16816<BF16>((ks & 1) ? sb[0] : sa[0], qa[ks], b0, b1);
+              mma16816<BF16>((ks & 1) ? sb[1] : sa[1], qa[ks], b2, b3);
+            }
+          }
+          float x[2][4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[i][e] = sa[i][e] + sb[i][e];
+          if (a.cap_log2 != 0.f) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[i][e] = a.cap_log2 * tanh_of(x[i][e] * a.scale_cap);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[i][e] *= a.scale_log2;
+          }
+          if (a.slopes) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int away = abs(pos[e >> 1] - (v0 + i * 8 + tq * 2 + (e & 1)));
+                x[i][e] = fmaf(-slope[e >> 1], (float)away, x[i][e]);
+              }
+          }
+          if (v0 < all_lo || v0 + 16 > all_hi) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int key = v0 + i * 8 + tq * 2 + (e & 1);
+                if (key < k[e >> 1].lo || key >= k[e >> 1].hi) x[i][e] = -INFINITY;
+              }
+          }
+          float mx0 = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
+          float mx1 = fmaxf(fmaxf(x[0][2], x[0][3]), fmaxf(x[1][2], x[1][3]));
+#pragma unroll
+          for (int d = 1; d < 4; d <<= 1) {
+            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, d));
+            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, d));
+          }
+          const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
+          const float ms0 = mn0 == -INFINITY ? 0.f : mn0, ms1 = mn1 == -INFINITY ? 0.f : mn1;  // (no key yet)
+          const float al0 = fast_exp2(m0 - ms0), al1 = fast_exp2(m1 - ms1);
+          m0 = mn0;
+          m1 = mn1;
+          float p[2][4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            p[i][0] = fast_exp2(x[i][0] - ms0);
+            p[i][1] = fast_exp2(x[i][1] - ms0);
+            p[i][2] = fast_exp2(x[i][2] - ms1);
+            p[i][3] = fast_exp2(x[i][3] - ms1);
+          }
+          l0 = l0 * al0 + ((p[0][0] + p[0][1]) + (p[1][0] + p[1][1]));
+          l1 = l1 * al1 + ((p[0][2] + p[0][3]) + (p[1][2] + p[1][3]));
+          // P as the A operand: fp16 rounds the weights once (2^-11, as the output is rounded), lifted
+          // to at most 2^15 so that only those below 2^-29 of the largest are subnormal; bf16, whose
+          // one rounding would be 2^-8, keeps them as two terms
+          uint32_t ph[4], pl[4];
+          if constexpr (BF16) {
+            split_bf16x2(p[0][0], p[0][1], ph[0], pl[0]);
+            split_bf16x2(p[0][2], p[0][3], ph[1], pl[1]);
+            split_bf16x2(p[1][0], p[1][1], ph[2], pl[2]);
+            split_bf16x2(p[1][2], p[1][3], ph[3], pl[3]);
+          } else {
+            ph[0] = pack2<false>(p[0][0] * kLift, p[0][1] * kLift);
+            ph[1] = pack2<false>(p[0][2] * kLift, p[0][3] * kLift);
+            ph[2] = pack2<false>(p[1][0] * kLift, p[1][1] * kLift);
+            ph[3] = pack2<false>(p[1][2] * kLift, p[1][3] * kLift);
+          }
+          if (!__all_sync(0xffffffffu, al0 == 1.f && al1 == 1.f)) {
+#pragma unroll
+            for (int d = 0; d < ND; ++d) o[d][0] *= al0, o[d][1] *= al0, o[d][2] *= al1, o[d][3] *= al1;
+          }
+          // keys that no row sees may be unwritten cache rows: their V is cleared, so that no NaN
+          // meets a weight of 0
+          const int key = 16 * w + (mi & 1) * 8 + rr;
+          auto pv = [&](uint32_t mlo, uint32_t mhi) {
+#pragma unroll
+            for (int dp = 0; dp < ND / 2; ++dp) {
+              const int cc = 2 * dp + (mi >> 1);
+              uint32_t w0, w1, w2, w3;
+              ldsm_x4_t(vb + (cc >> 3) * (kBiTile * 128) + key * 128 + (((cc & 7) ^ (key & 7)) << 4), w0, w1, w2, w3);
+              w0 &= mlo, w2 &= mlo, w1 &= mhi, w3 &= mhi;
+              mma16816<BF16>(o[2 * dp], ph, w0, w1);
+              mma16816<BF16>(o[2 * dp + 1], ph, w2, w3);
+              if constexpr (BF16) {
+                mma16816<BF16>(o[2 * dp], pl, w0, w1);
+                mma16816<BF16>(o[2 * dp + 1], pl, w2, w3);
+              }
+            }
+          };
+          if (v0 >= some_lo && v0 + 16 <= some_hi) {
+            pv(0xffffffffu, 0xffffffffu);
+          } else {
+            auto keep = [&](int first_key) {  // the two keys of a register
+              return (first_key >= some_lo && first_key < some_hi ? 0xFFFFu : 0u) |
+                     (first_key + 1 >= some_lo && first_key + 1 < some_hi ? 0xFFFF0000u : 0u);
+            };
+            pv(keep(v0 + 2 * tq), keep(v0 + 8 + 2 * tq));
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[s]);
+      }
+      // ---- the four warps' results of the item ----
+#pragma unroll
+      for (int d = 1; d < 4; d <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+      }
+      // scores of NaN alone leave no maximum but a sum of NaN, which must not be taken for a row
+      // without keys
+      if (m0 == -INFINITY && l0 != l0) m0 = 0.f;
+      if (m1 == -INFINITY && l1 != l1) m1 = 0.f;
+      if (tq == 0) {
+        ml[w * 16 + gq] = m0, ml[w * 16 + gq + 8] = m1;
+        ml[64 + w * 16 + gq] = l0, ml[64 + w * 16 + gq + 8] = l1;
+      }
+      named_bar_sync(1, 128);
+      float f[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = gq + 8 * i;
+        const float M = fmaxf(fmaxf(ml[r], ml[16 + r]), fmaxf(ml[32 + r], ml[48 + r]));
+        const float m = i ? m1 : m0;
+        f[i] = m == -INFINITY ? 0.f : fast_exp2(m - M) * (1.f / kLift);
+      }
+      // up to four rows: the warps' side by side; more: the warps in turn add into the same rows
+      const bool side = it.n_rows <= 4;
+      for (int turn = 0; turn < (side ? 1 : 4); ++turn) {
+        if (side || turn == w) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int r = gq + 8 * i;
+            if (r >= it.n_rows) continue;
+            float* dst = comb + (side ? w * 4 + r : r) * L::kStride + tq * 2;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+              float2 y = f[i] != 0.f ? make_float2(o[d][2 * i] * f[i], o[d][2 * i + 1] * f[i]) : make_float2(0.f, 0.f);
+              if (!side && turn > 0) {
+                const float2 old = *reinterpret_cast<float2*>(dst + d * 8);
+                y.x += old.x, y.y += old.y;
+              }
+              *reinterpret_cast<float2*>(dst + d * 8) = y;
+            }
+          }
+        }
+        named_bar_sync(1, 128);
+      }
+      const bool whole = it.first && it.last;
+      const int slot = 2 * c + (it.first ? 1 : 0);
+      for (int i = threadIdx.x; i < it.n_rows * (HS / 4); i += 128) {
+        const int r = i / (HS / 4), cc = i % (HS / 4) * 4;
+        float4 x = *reinterpret_cast<float4*>(comb + r * L::kStride + cc);
+        if (side)
+          for (int v = 1; v < 4; ++v) {
+            const float4 y = *reinterpret_cast<float4*>(comb + (v * 4 + r) * L::kStride + cc);
+            x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+          }
+        const float M = fmaxf(fmaxf(ml[r], ml[16 + r]), fmaxf(ml[32 + r], ml[48 + r]));
+        float S = 0.f;
+        for (int v = 0; v < 4; ++v)
+          if (ml[v * 16 + r] != -INFINITY) S += ml[64 + v * 16 + r] * fast_exp2(ml[v * 16 + r] - M);
+        if (whole) {
+          const int rs = it.r_first + r;
+          const int64_t at = (int64_t)(it.c0 + rs / a.G) * a.nh + it.g * a.G + rs % a.G;
+          const float inv = M == -INFINITY ? 0.f : 1.f / S;
+          uint2 out = make_uint2(pack2<BF16>(x.x * inv, x.y * inv), pack2<BF16>(x.z * inv, x.w * inv));
+          if (M == -INFINITY) out = make_uint2(0, 0);
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.output) + at * HS + cc) = out;
+          if (a.lse && cc == 0) a.lse[at] = M == -INFINITY ? -INFINITY : (M + fast_log2(S)) * 0.69314718055994531f;
+        } else {
+          *reinterpret_cast<float4*>(a.part_o + ((int64_t)slot * 16 + r) * HS + cc) = x;
+          if (cc == 0) *reinterpret_cast<float2*>(a.part_ml + (slot * 16 + r) * 2) = make_float2(M, S);
+        }
+      }
+      named_bar_sync(1, 128);  // the combining buffers are free again
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && *err && a.error) atomicOr(a.error, *err);
+}
+
+// The pieces of the units that the cuts between CTAs went through, in order: CTA c of the rows
+// kernel began such a unit (record 2c), its next ones went on with it (record 2k + 1: 1, and 2 for
+// the last). A thread has four columns of a row.
+template <int HS, bool BF16>
+__global__ void __launch_bounds__(kMergeThreads) biased_merge_kernel(const BiasedArgs a, const int ctas) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int c = blockIdx.x;
+  const int4 head = a.records[2 * c];
+  if (head.x == 0) return;
+  const int i = blockIdx.y * kMergeThreads + threadIdx.x, r = i / (HS / 4), cc = i % (HS / 4) * 4;
+  if (r >= head.x) return;
+  float M = -INFINITY, S = 0.f;
+  float x[4] = {0.f, 0.f, 0.f, 0.f};
+  auto add = [&](int slot) {
+    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (slot * 16 + r) * 2);
+    const float4 y = *reinterpret_cast<const float4*>(a.part_o + ((int64_t)slot * 16 + r) * HS + cc);
+    if (ml.x == -INFINITY) return;
+    const float m = fmaxf(M, ml.x), f = fast_exp2(M - m), g = fast_exp2(ml.x - m);  // (0 on the first piece with keys)
+    M = m;
+    S = S * f + ml.y * g;
+    x[0] = x[0] * f + y.x * g, x[1] = x[1] * f + y.y * g, x[2] = x[2] * f + y.z * g, x[3] = x[3] * f + y.w * g;
+  };
+  add(2 * c + 1);
+  int k = c + 1;
+  for (; k < ctas && a.records[2 * k + 1].x == 1; ++k) add(2 * k);
+  if (k < ctas && a.records[2 * k + 1].x == 2) add(2 * k);
+  const int rs = head.z + r;
+  const int64_t at = (int64_t)(head.y + rs / a.G) * a.nh + head.w * a.G + rs % a.G;
+  const float inv = M == -INFINITY ? 0.f : 1.f / S;
+  uint2 out = make_uint2(pack2<BF16>(x[0] * inv, x[1] * inv), pack2<BF16>(x[2] * inv, x[3] * inv));
+  if (M == -INFINITY) out = make_uint2(0, 0);
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.output) + at * HS + cc) = out;
+  if (a.lse && cc == 0) a.lse[at] = M == -INFINITY ? -INFINITY : (M + fast_log2(S)) * 0.69314718055994531f;
+}
+
+#include "biased_tile.cuh"
+
+// ---- host ----------------------------------------------------------------------------------
+int biased_ctas(int hs, int sms) {
+  const int n = sms * (hs == 256 ? 1 : 2);
+  return n < PA_BIASED_CTAS ? n : PA_BIASED_CTAS;
+}
+
+static int divisor(int a, int b) {
+  while (b) {
+    const int t = a % b;
+    a = b;
+    b = t;
+  }
+  return a;
+}
+
+template <int HS, bool BF16>
+static cudaError_t launch_biased_rows(const BiasedArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int seg,
+                                      int sms, cudaStream_t s) {
+  const int ctas = biased_ctas(HS, sms);
+  constexpr int smem = BiRows<HS>::kBytes;
+  if (cudaError_t e = cudaFuncSetAttribute(biased_rows_kernel<HS, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))
+    return e;
+  if (cudaError_t e = launch_pdl(biased_rows_kernel<HS, BF16>, dim3(ctas), dim3(kBiThreads), smem, s, a, tk, tv, seg)) return e;
+  return launch_pdl(biased_merge_kernel<HS, BF16>, dim3(ctas, 16 * (HS / 4) / kMergeThreads), dim3(kMergeThreads), 0, s, a,
+                    ctas);
+}
+
+cudaError_t launch_biased(const BiasedArgs& a, bool bf16, int sms, cudaStream_t s) {
+  const int seg = divisor(a.bs, kBiTile);
+  const int64_t slots = (int64_t)a.num_blocks * a.bs;
+  CUtensorMap tk, tv, tq;
+  if (!cache_map_16(&tk, a.key_cache, bf16, a.hs, a.kvh, slots, seg) ||
+      !cache_map_16(&tv, a.value_cache, bf16, a.hs, a.kvh, slots, seg))
+    return cudaErrorInvalidValue;
+  // Sequences of up to 16 rows per KV head are the rows kernel's, longer ones the tile kernel's (groups
+  // of over 128 heads, more than a tile's rows, are all the rows kernel's); a kernel that can have none is not launched.
+  if (a.G <= 16 || a.G > 128) {
+#define PA_ROWS(HS) (bf16 ? launch_biased_rows<HS, true>(a, tk, tv, seg, sms, s) : launch_biased_rows<HS, false>(a, tk, tv, seg, sms, s))
+    if (cudaError_t e = a.hs == 64 ? PA_ROWS(64) : a.hs == 128 ? PA_ROWS(128) : PA_ROWS(256)) return e;
+#undef PA_ROWS
+  }
+  if (a.G > 128 || (a.max_rows > 0 && (int64_t)a.max_rows * a.G <= 16)) return cudaSuccess;
+  const int rows = 128 / a.G;
+  if (!query_block_map(&tq, a.query, bf16, a.hs, a.nh, a.N, a.q_stride, a.G, rows)) return cudaErrorInvalidValue;
+#define PA_TILE(HS)                                                       \
+  (bf16 ? launch_biased_tile<HS, true>(a, tq, tk, tv, seg, rows, sms, s)  \
+        : launch_biased_tile<HS, false>(a, tq, tk, tv, seg, rows, sms, s))
+  return a.hs == 64 ? PA_TILE(64) : a.hs == 128 ? PA_TILE(128) : PA_TILE(256);
+#undef PA_TILE
+}
+
+}  // namespace pa

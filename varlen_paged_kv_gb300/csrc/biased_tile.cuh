@@ -1,0 +1,496 @@
+// biased_tile_kernel: sequences of more than 16 rows per KV head (included by biased.cu, in its namespace).
+//
+// The up to 128 rows r = j * G + head of 128 / G consecutive rows of a sequence are one M = 128
+// tile (TMA lays them out so from a (channel, head, row) view of the query; rows past the item are
+// computed and not stored). Warp 0 loads K and V tiles of 64 keys (two stages), warp 1 issues
+// S_t = Q K_t^T into one of two S buffers in TMEM and O += P_t V_t, warps 2 .. 9 are the softmax:
+// two threads share a row (TMEM lets a warp at 32 of the 128 lanes), take 32 of its 64 scores each
+// through the cap, the bias and the mask, exchange their maxima through shared memory, write P
+// over the scores (fp16, or bf16 hi and lo terms) and rescale O in TMEM when the maximum grew by
+// more than 2^8 (fp16: 2^4). S_{t+1} is issued before P_t is waited for, so the tensor core works
+// during the softmax; two CTAs share an SM (one with 256-wide heads) and fill each other's gaps.
+// Where a batch has few tiles of rows, the CTAs of a cluster share an item's keys and add their
+// results through each other's shared memory.
+template <int HS>
+struct BiTile {
+  static constexpr int kStages = 2;
+  static constexpr int kQBytes = 128 * HS * 2;
+  static constexpr int kTileBytes = kBiTile * HS * 2;
+  static constexpr int kRing = kQBytes;                             // K tiles, then V tiles
+  static constexpr int kBars = kRing + 2 * kStages * kTileBytes;    // 1 + 4 * kStages + 3 * 2 barriers
+  static constexpr int kNumBars = 1 + 4 * kStages + 6;
+  static constexpr int kAbort = kBars + kNumBars * 8;               // abort flag, error word, TMEM address
+  static constexpr int kItem = (kAbort + 12 + 15) / 16 * 16;
+  static constexpr int kMl = kItem + 64;                            // float [2][128]: m and l of the rows
+  static constexpr int kX = kMl + 2 * 128 * 4;                      // float [2][128][2]: maxima and sums of half rows
+  static constexpr uint32_t kTmem = HS == 256 ? 512 : 256;          // S, S, O at columns 0, 64, 128
+  static_assert(128 * HS * 4 <= 2 * kStages * kTileBytes, "the cluster's partial result lies over the ring");
+  // At least a third of an SM's shared memory, so that no more CTAs share an SM than find TMEM
+  // there: a CTA that waited for TMEM while its cluster waits for it could wait for ever.
+  static constexpr int kNeed = kX + 2 * 128 * 2 * 4 + 1024;
+  static constexpr int kBytes = kNeed < 80 * 1024 ? 80 * 1024 : kNeed;
+};
+constexpr int kBiTileThreads = 320;
+
+// a CTA's work item: some rows of one sequence
+struct TileItem {
+  int rows, row0, pos0, b;  // rows of the batch (0: none), the first of them, its position, the sequence
+  int prefix, total;        // keys of the sequence
+  int lo, hi;               // keys that some row sees
+  int all_lo, all_hi;       // keys that all rows see
+};
+
+__device__ __forceinline__ TileItem tile_item(const BiasedArgs& a, int u, int sub_rows, int lane) {
+  TileItem it{};
+  Seq s = find_seq(a.cum, a.past, a.B, sub_rows, 1, u, a.N, a.max_blocks, a.bs, lane);
+  s.ok = s.ok && (a.max_rows == 0 || s.q <= a.max_rows);
+  if (!s.ok || short_rows(a, s)) return it;
+  const int j0 = (u - (s.c0 / sub_rows + s.b)) * sub_rows;
+  if (j0 < 0 || j0 >= s.q) return it;
+  it.rows = min(sub_rows, s.q - j0);
+  it.row0 = s.c0 + j0;
+  it.pos0 = s.past + j0;
+  it.b = s.b;
+  it.prefix = a.prefix ? a.prefix[s.b] : 0;
+  it.total = s.past + s.q;
+  Keys some{INT32_MAX, 0}, all{0, INT32_MAX};
+  for (int j = lane; j < it.rows; j += 32) {
+    const Keys k = keys_of_row(a, s, it.prefix, j0 + j);
+    some = join(some, k);
+    all = {max(all.lo, k.lo), min(all.hi, k.hi)};
+  }
+  it.lo = __reduce_min_sync(0xffffffffu, some.lo);
+  it.hi = __reduce_max_sync(0xffffffffu, some.hi);
+  it.all_lo = __reduce_max_sync(0xffffffffu, all.lo);
+  it.all_hi = __reduce_min_sync(0xffffffffu, all.hi);
+  return it;
+}
+
+template <int HS, bool BF16>
+__global__ void __launch_bounds__(kBiTileThreads, HS == 256 ? 1 : 2)
+    biased_tile_kernel(const BiasedArgs a, const __grid_constant__ CUtensorMap tmQ,
+                       const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                       const int seg_rows, const int sub_rows) {
+  using L = BiTile<HS>;
+  constexpr int HALVES = HS / 64, KSTEPS = HS / 16;
+  constexpr uint32_t IDESC_QK = idesc_f16(BF16, 128, kBiTile, false), IDESC_PV = idesc_f16(BF16, 128, HS, true);
+  constexpr uint32_t kO = 128;  // TMEM column of O
+  // The row's reference m_used may lag behind its maximum by kLag before O is rescaled. fp16
+  // weights are lifted by 2^kLift, to 2^15 at most, so that only those below 2^-25 of the largest
+  // are subnormal and have absolute errors, of 2^-36; l is lifted with them.
+  constexpr float kLag = BF16 ? 8.f : 4.f, kLift = BF16 ? 0.f : 11.f, kUnlift = BF16 ? 1.f : 1.f / 2048;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + L::kBars);
+  uint64_t* k_full = q_full + 1;
+  uint64_t* k_empty = k_full + L::kStages;
+  uint64_t* v_full = k_empty + L::kStages;
+  uint64_t* v_empty = v_full + L::kStages;
+  uint64_t* s_full = v_empty + L::kStages;  // [2]
+  uint64_t* p_full = s_full + 2;            // [2]
+  uint64_t* o_done = p_full + 2;            // [2]
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kAbort);
+  uint32_t* err = reinterpret_cast<uint32_t*>(smem + L::kAbort + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kAbort + 8);
+  TileItem* item_s = reinterpret_cast<TileItem*>(smem + L::kItem);
+  float* ml = reinterpret_cast<float*>(smem + L::kMl);
+  float2* half = reinterpret_cast<float2*>(smem + L::kX);  // [2][128]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // later rows see more keys, so their items start first
+  const int g = blockIdx.y, u = gridDim.x - 1 - blockIdx.x;
+  const int rank = blockIdx.z, C = gridDim.z;  // the cluster is a column of the grid
+  if (threadIdx.x == 32) {
+    mbar_init(q_full, 1);
+    for (int i = 0; i < L::kStages; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 256);
+      mbar_init(&o_done[i], 1);
+    }
+    *abort = 0;
+    *err = 0;
+    fence_mbar_init();
+  }
+  pdl_wait();
+  if (warp == 0) {
+    const TileItem it = tile_item(a, u, sub_rows, lane);
+    if (lane == 0) *item_s = it;
+  }
+  if (blockIdx.x == 0 && g == 0 && rank == 0) check_biased_batch(a);
+  __syncthreads();
+  const TileItem it = *item_s;
+  if (it.rows <= 0) return;  // (all CTAs of a cluster agree)
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, L::kTmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int2 tiles = tiles_of(Keys{it.lo, it.hi});
+  const int t0 = tiles.x + (int)((int64_t)(tiles.y - tiles.x) * rank / C);
+  const int n = tiles.x + (int)((int64_t)(tiles.y - tiles.x) * (rank + 1) / C) - t0;
+
+  const int row = (warp & 3) * 32 + lane;  // (softmax warps) the thread's TMEM lane
+  const int side = warp >= 6;              // and its half of the row's columns
+  const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+  const int j = row / a.G;                  // its row in the item
+  const bool live = warp >= 2 && j < it.rows && row < sub_rows * a.G;
+  const bool any_live = __any_sync(0xffffffffu, live);
+  float m_used = -INFINITY, l = 0.f;
+
+  if (warp == 0) {
+    // ---- producer ----
+    if (n > 0) {
+      const int nseg = kBiTile / seg_rows, oob = a.num_blocks * a.bs;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(q_full, (uint32_t)(sub_rows * a.G * HS * 2));
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h)
+          tma_load_3d(smem + h * 128 * 128, &tmQ, q_full, h * 64, g * a.G, it.row0);
+      }
+      const int* table = a.table + (int64_t)it.b * a.max_blocks;
+      auto slot = [&](int t) {  // this lane's segment of tile t: its first cache row
+        const int v = (t0 + t) * kBiTile + lane * seg_rows;
+        if (lane >= nseg || t >= n || v >= it.hi || v + seg_rows <= it.lo) return oob;
+        const int page = v / a.bs, phys = table[page];
+        if (phys < 0 || phys >= a.num_blocks) {
+          atomicOr(err, PA_DEVERR_BAD_BLOCK);
+          return oob;
+        }
+        return phys * a.bs + (v - page * a.bs);
+      };
+      auto load = [&](int t, int z, const CUtensorMap* map, uint64_t* full, uint64_t* empty, uint8_t* ring) {
+        if (t < 0 || t >= n) return;
+        const int s = t % L::kStages;
+        if (lane == 0) {
+          mbar_wait(&empty[s], ((t / L::kStages) & 1) ^ 1, abort, err);
+          mbar_arrive_expect_tx(&full[s], L::kTileBytes);
+        }
+        __syncwarp();
+        if (lane < nseg)
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h)
+            tma_load_3d(ring + s * L::kTileBytes + h * kBiTile * 128 + lane * seg_rows * 128, map, &full[s], h * 64, g, z);
+        __syncwarp();
+      };
+      // tiles are asked for in the order in which the products free their stages: K_{t+2} (after
+      // Q K_t) before V_{t+1} (after P V_{t-1}); a tile's pages are looked up a step before
+      int z1 = oob, z2 = slot(0);  // of tiles t + 1 and t + 2
+      for (int t = -2; t < n; ++t) {
+        const int z3 = slot(t + 3);
+        load(t + 2, z2, &tmK, k_full, k_empty, smem + L::kRing);
+        load(t + 1, z1, &tmV, v_full, v_empty, smem + L::kRing + L::kStages * L::kTileBytes);
+        z1 = z2;
+        z2 = z3;
+      }
+    }
+  } else if (warp == 1) {
+    // ---- MMA issuer ----
+    const uint64_t qdesc = sdesc_sw128(smem_u32(smem), 16, 1024);
+    const uint64_t kdesc = sdesc_sw128(smem_u32(smem + L::kRing), 16, 1024);
+    const uint64_t vdesc = sdesc_sw128(smem_u32(smem + L::kRing + L::kStages * L::kTileBytes), kBiTile * 128, 1024);
+    auto issue_qk = [&](int t) {
+      const int s = t % L::kStages;
+      mbar_wait(&k_full[s], (t / L::kStages) & 1, abort, err);
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t kd = kdesc + (uint64_t)((s * L::kTileBytes) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < KSTEPS; ++kk)
+          tc_mma_ss(tmem + (t & 1) * kBiTile, qdesc + (uint64_t)((kk >> 2) * (128 * 128 >> 4) + (kk & 3) * 2),
+                    kd + (uint64_t)((kk >> 2) * (kBiTile * 128 >> 4) + (kk & 3) * 2), IDESC_QK, kk > 0 ? 1u : 0u);
+        tc_commit(&s_full[t & 1]);
+        tc_commit(&k_empty[s]);
+      }
+      __syncwarp();
+    };
+    if (n > 0) {
+      mbar_wait(q_full, 0, abort, err);
+      issue_qk(0);
+    }
+    for (int t = 0; t < n; ++t) {
+      if (t + 1 < n) {
+        if (t > 0) mbar_wait(&o_done[(t - 1) & 1], ((t - 1) >> 1) & 1, abort, err);  // P_{t-1}, in that S buffer, has been read
+        issue_qk(t + 1);
+      }
+      const int s = t % L::kStages;
+      mbar_wait(&v_full[s], (t / L::kStages) & 1, abort, err);
+      // rows that no row of the item sees may be unwritten: cleared, so that no NaN meets a
+      // weight of 0 (whole 128-byte rows: the swizzle stays inside)
+      const int k0 = (t0 + t) * kBiTile, front = max(it.lo - k0, 0), back = min(it.hi - k0, kBiTile);
+      if (front > 0 || back < kBiTile) {
+        uint8_t* vt = smem + L::kRing + (L::kStages + s) * L::kTileBytes;
+        const int rows = front + kBiTile - back;
+        for (int c = lane; c < rows * 8 * HALVES; c += 32) {
+          const int r = c % (rows * 8) / 8;
+          *reinterpret_cast<uint4*>(vt + c / (rows * 8) * (kBiTile * 128) + (r < front ? r : back + r - front) * 128 +
+                                    c % 8 * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+      }
+      mbar_wait(&p_full[t & 1], (t >> 1) & 1, abort, err);
+      __syncwarp();
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t vd = vdesc + (uint64_t)((s * L::kTileBytes) >> 4);
+        const uint32_t p = tmem + (t & 1) * kBiTile;
+#pragma unroll
+        for (int kk = 0; kk < kBiTile / 16; ++kk) {
+          tc_mma_ts(tmem + kO, p + p_col(kk), vd + (uint64_t)(kk * (16 * 128 >> 4)), IDESC_PV,
+                    kk > 0 || t > 0 ? 1u : 0u);
+          if constexpr (BF16)
+            tc_mma_ts(tmem + kO, p + p_col(kk) + 16, vd + (uint64_t)(kk * (16 * 128 >> 4)), IDESC_PV, 1u);
+        }
+        tc_commit(&o_done[t & 1]);
+        tc_commit(&v_empty[s]);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ---- softmax ----
+    // (S, P and O each signal on two barriers in turn: not every wait is made by every warp, and a
+    // parity tells a phase from the next only, so a barrier must not be two phases ahead of or
+    // behind one that waits; P_{t-2} V is done once S_t is, and P_t V is not before this warp's P_t)
+    constexpr int COLS = kBiTile / 2, OCOLS = HS / 2;
+    const int jc = min(j, it.rows - 1), h = g * a.G + min(row % a.G, a.G - 1);  // (rows past the item borrow the last row's keys)
+    Seq sq;
+    sq.c0 = it.row0, sq.past = it.pos0, sq.q = it.total - it.pos0;  // (the item's rows counted from 0)
+    const Keys keys = keys_of_row(a, sq, it.prefix, jc);
+    const int pos = it.pos0 + jc;
+    const bool cap = a.cap_log2 != 0.f, bias = a.slopes != nullptr;
+    const float slope = bias ? -a.slopes[h] * 1.4426950408889634f : 0.f;
+    const float c = cap || bias ? 1.f : a.scale_log2;  // what the scores below are still multiplied by
+    const float none = c > 0.f ? -INFINITY : INFINITY;  // a score whose product with c is -inf
+    const uint32_t o_tmem = tmem + lane_off + kO + side * OCOLS;
+    const int bar = 1 + (warp & 3);  // of the two warps of a lane quarter
+    for (int t = 0; t < n; ++t) {
+      mbar_wait(&s_full[t & 1], (t >> 1) & 1, abort, err);
+      if (!any_live) {  // rows past the item: whatever their P holds stays in their rows of O
+        mbar_arrive(&p_full[t & 1]);
+        continue;
+      }
+      tc_fence_after();
+      const uint32_t st = tmem + lane_off + (t & 1) * kBiTile;
+      uint32_t r[COLS];
+      tmem_ld_x32(st + side * COLS, r);
+      const int v0 = (t0 + t) * kBiTile + side * COLS;
+      if (cap) {
+        float most[2] = {0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < COLS; e += 4)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            most[k] = fmax3(most[k], fabsf(__uint_as_float(r[e + 2 * k])), fabsf(__uint_as_float(r[e + 2 * k + 1])));
+        const bool near = __all_sync(0xffffffffu, fmaxf(most[0], most[1]) * fabsf(a.scale_cap) <= kTanhReach);
+        if (near) {
+          const uint64_t sc = f2_make(a.scale_cap, a.scale_cap), cl = f2_make(a.cap_log2, a.cap_log2);
+#pragma unroll
+          for (int e = 0; e < COLS; e += 2) {
+            const uint64_t x = f2_mul(f2_make(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), sc), z = f2_mul(x, x);
+            uint64_t y = f2_make(kTanh[5], kTanh[5]);
+#pragma unroll
+            for (int k = 4; k >= 0; --k) y = f2_fma(y, z, f2_make(kTanh[k], kTanh[k]));
+            float y0, y1;
+            f2_split(f2_mul(f2_mul(x, cl), y), y0, y1);
+            r[e] = __float_as_uint(y0), r[e + 1] = __float_as_uint(y1);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < COLS; ++e)
+            r[e] = __float_as_uint(a.cap_log2 * tanh_of(__uint_as_float(r[e]) * a.scale_cap));
+        }
+      }
+      if (bias) {
+        const float first = cap ? 1.f : a.scale_log2, away = (float)(pos - v0);
+#pragma unroll
+        for (int e = 0; e < COLS; ++e)
+          r[e] = __float_as_uint(fmaf(slope, fabsf(away - (float)e), __uint_as_float(r[e]) * first));
+      }
+      if (v0 < it.all_lo || v0 + COLS > it.all_hi) {
+        const int lo = keys.lo - v0, hi = keys.hi - v0;
+#pragma unroll
+        for (int e = 0; e < COLS; ++e)
+          if (e < lo || e >= hi) r[e] = __float_as_uint(none);
+      }
+      float mc[4] = {none, none, none, none};
+      if (c > 0.f) {
+#pragma unroll
+        for (int e = 0; e < COLS; e += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mc[k] = fmax3(mc[k], __uint_as_float(r[e + 2 * k]), __uint_as_float(r[e + 2 * k + 1]));
+      } else {
+#pragma unroll
+        for (int e = 0; e < COLS; e += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mc[k] = fmin3(mc[k], __uint_as_float(r[e + 2 * k]), __uint_as_float(r[e + 2 * k + 1]));
+      }
+      const float best = c > 0.f ? fmax3(fmaxf(mc[0], mc[1]), mc[2], mc[3]) : fmin3(fminf(mc[0], mc[1]), mc[2], mc[3]);
+      float2* hx = half + (t & 1) * 128 + row;
+      (side ? hx->y : hx->x) = best * c;
+      named_bar_sync(bar, 64);
+      const float2 both = *hx;
+      const float m_new = fmaxf(m_used, fmaxf(both.x, both.y));
+      const bool grow = __any_sync(0xffffffffu, live && m_new > m_used + kLag);
+      float alpha = 1.f;
+      if (grow) {
+        // (fp16: a whole number, which kLift is taken off exactly)
+        const float to = BF16 ? m_new : ceilf(m_new);
+        alpha = m_new == -INFINITY ? 1.f : fast_exp2(m_used - to);  // 0 on a row's first keys
+        m_used = to;
+        l *= alpha;
+      }
+      const float neg_m = m_used == -INFINITY ? 0.f : kLift - m_used;  // (no key yet: every weight is 0)
+      const uint64_t c2 = f2_make(c, c), nm2 = f2_make(neg_m, neg_m);
+      uint64_t lsum = f2_make(0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < COLS / 16; ++k) {
+        uint32_t* q = r + k * 16;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float x0, x1;
+          f2_split(f2_fma(f2_make(__uint_as_float(q[2 * e]), __uint_as_float(q[2 * e + 1])), c2, nm2), x0, x1);
+          const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+          lsum = f2_add(lsum, f2_make(p0, p1));
+          if constexpr (BF16) split_bf16x2(p0, p1, q[2 * e], q[2 * e + 1]);
+          else q[2 * e] = pack2<false>(p0, p1);
+        }
+        const uint32_t p = st + p_col(side * (COLS / 16) + k);
+        tmem_st_x8_nowait(p, q[0], q[2], q[4], q[6], q[8], q[10], q[12], q[14]);
+        if constexpr (BF16) tmem_st_x8_nowait(p + 16, q[1], q[3], q[5], q[7], q[9], q[11], q[13], q[15]);
+      }
+      float s0, s1;
+      f2_split(lsum, s0, s1);
+      l += s0 + s1;
+      if (t > 0 && grow) {  // O holds P_0 V .. P_{t-1} V once the last product is done
+        mbar_wait(&o_done[(t - 1) & 1], ((t - 1) >> 1) & 1, abort, err);
+        tc_fence_after();
+#pragma unroll 1
+        for (int cc = 0; cc < OCOLS; cc += 32) {
+          uint32_t ov[32];
+          tmem_ld_x32(o_tmem + cc, ov);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+          tmem_st_x32(o_tmem + cc, ov);
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&p_full[t & 1]);
+    }
+    if (n > 0) {
+      mbar_wait(&o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort, err);
+      tc_fence_after();
+    }
+    // the row's sum from its halves (the two warps have the same maximum)
+    (side ? half[row].y : half[row].x) = l;
+    named_bar_sync(bar, 64);
+    l = half[row].x + half[row].y;
+    if (m_used == -INFINITY && l != l) m_used = 0.f;  // scores of NaN alone: not a row without keys
+    if (C > 1 && side == 0) ml[row] = m_used, ml[128 + row] = l;
+  }
+
+  uint16_t* out = static_cast<uint16_t*>(a.output);
+  if (C == 1) {
+    if (warp >= 2) {
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const int64_t at = (int64_t)(it.row0 + j) * a.nh + g * a.G + row % a.G;
+      if (live && a.lse && side == 0)
+        a.lse[at] = m_used == -INFINITY ? -INFINITY : (m_used + fast_log2(l * kUnlift)) * 0.69314718055994531f;
+#pragma unroll 1
+      for (int cc = side * (HS / 2); cc < (side + 1) * (HS / 2); cc += 32) {
+        uint32_t ov[32];
+        if (n > 0) {
+          tmem_ld_x32(tmem + lane_off + kO + cc, ov);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) ov[e] = 0u;
+        }
+        if (live) {
+          const bool some = m_used != -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = some ? pack2<BF16>(__uint_as_float(ov[e + 2 * k]) * inv, __uint_as_float(ov[e + 2 * k + 1]) * inv) : 0u;
+            *reinterpret_cast<uint4*>(out + at * HS + cc + e) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+    }
+  } else {
+    // every row's share of the cluster's result: O 2^(m - M) / L, quads of a row rotated by the
+    // row so that a warp's stores spread over the banks
+    cluster_sync();  // all (m, l)
+    float* part = reinterpret_cast<float*>(smem + L::kRing);
+    if (warp >= 2) {
+      float M = -INFINITY, S = 0.f;
+      for (int k = 0; k < C; ++k) M = fmaxf(M, ld_cluster(cluster_addr(ml + row, k)));
+      for (int k = 0; k < C; ++k) {
+        const float m = ld_cluster(cluster_addr(ml + row, k));
+        if (m != -INFINITY) S += fast_exp2(m - M) * ld_cluster(cluster_addr(ml + 128 + row, k));
+      }
+      const float f = m_used == -INFINITY ? 0.f : fast_exp2(m_used - M) / S;
+      if (rank == 0 && live && a.lse && side == 0)
+        a.lse[(int64_t)(it.row0 + j) * a.nh + g * a.G + row % a.G] =
+            M == -INFINITY ? -INFINITY : (M + fast_log2(S * kUnlift)) * 0.69314718055994531f;
+#pragma unroll 1
+      for (int cc = side * (HS / 2); any_live && cc < (side + 1) * (HS / 2); cc += 32) {
+        uint32_t ov[32];
+        if (n > 0) tmem_ld_x32(tmem + lane_off + kO + cc, ov);
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (n > 0 && f != 0.f)
+            x = make_float4(__uint_as_float(ov[e]) * f, __uint_as_float(ov[e + 1]) * f, __uint_as_float(ov[e + 2]) * f,
+                            __uint_as_float(ov[e + 3]) * f);
+          const int quad = ((cc + e) / 4 + row) % (HS / 4);
+          *reinterpret_cast<float4*>(part + row * HS + quad * 4) = x;
+        }
+      }
+    }
+    cluster_sync();
+    const int M = it.rows * a.G;  // rows of the item, a share of them summed by each CTA
+    const int r0 = M * rank / C, r1 = M * (rank + 1) / C;
+    for (int i = threadIdx.x; i < (r1 - r0) * (HS / 4); i += kBiTileThreads) {
+      const int r = r0 + i / (HS / 4), quad = i % (HS / 4);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < C; ++k) {
+        const float4 y = ld_cluster4(cluster_addr(part + r * HS + (quad + r) % (HS / 4) * 4, k));
+        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+      }
+      const int64_t at = (int64_t)(it.row0 + r / a.G) * a.nh + g * a.G + r % a.G;
+      *reinterpret_cast<uint2*>(out + at * HS + quad * 4) = make_uint2(pack2<BF16>(x.x, x.y), pack2<BF16>(x.z, x.w));
+    }
+    cluster_sync();  // no CTA leaves while another reads its shared memory
+  }
+  tc_fence_before();
+  __syncthreads();  // (no warp waits any more: whichever gave up has said so)
+  if (threadIdx.x == 0 && *err && a.error) atomicOr(a.error, *err);
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::kTmem);
+  }
+}
+
+// The CTAs of a cluster share an item's tiles, as many as run at once.
+template <int HS, bool BF16>
+static cudaError_t launch_biased_tile(const BiasedArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
+                                      const CUtensorMap& tv, int seg, int sub_rows, int sms, cudaStream_t s) {
+  int64_t keys = (int64_t)a.max_blocks * a.bs;
+  if (a.window && !a.prefix && (int64_t)a.window + sub_rows < keys) keys = (int64_t)a.window + sub_rows;
+  const int64_t items = items_of_batch(a.N, a.B, sub_rows, 1, 1) * a.kvh;
+  const int c = cluster_size(items, (int64_t)sms * (HS == 256 ? 1 : 2), ceil_div(keys, kBiTile), 4, 8);
+  const dim3 grid((unsigned)(a.N / sub_rows + a.B), (unsigned)a.kvh, (unsigned)c);
+  return launch_clusters(biased_tile_kernel<HS, BF16>, grid, kBiTileThreads, BiTile<HS>::kBytes, BiTile<HS>::kBytes, s, a,
+                         tq, tk, tv, seg, sub_rows);
+}

@@ -142,6 +142,76 @@ struct PageArgs {
   float scale_log2;
 };
 
+// forks and compactions of block tables (pool.cu)
+struct PoolArgs {
+  const int32_t *parents, *past, *held, *table, *state;
+  const uint8_t* pinned;  // per page, or null
+  int32_t *ring, *past_out, *held_out, *table_out, *state_out, *pages_end;
+  int2* copies;
+  uint32_t* error;
+  // the workspace: the error word and the marks, cleared first (clear_words 16-byte words), then
+  // the words of bits and the chunks' totals
+  uint4* clear;
+  int64_t clear_words;
+  uint32_t* ws_error;
+  uint8_t *marks, *old_marks;  // per page
+  int32_t* keeper;             // per page
+  uint4* words;
+  int2* chunks;
+  int32_t B, Bn, max_blocks, bs, num_blocks, num_chunks, cap, max_moves;
+};
+// bytes of the workspace of num_blocks pages; fills in its pointers where `a` is given
+inline size_t pool_workspace(int32_t num_blocks, bool fork, PoolArgs* a, uint8_t* base) {
+  const size_t chunks = (size_t)ceil_div(num_blocks, 1024), pages = chunks * 1024;
+  size_t off = 16;
+  const size_t marks = off, old_marks = off += pages, keeper = off += fork ? pages : 0;
+  off += fork ? 4 * pages : 0;
+  const size_t words = off, totals = words + pages / 2, end = align_up(totals + 8 * chunks, 16);
+  if (a) {
+    a->clear = reinterpret_cast<uint4*>(base);
+    a->clear_words = (int64_t)(words / 16);
+    a->ws_error = reinterpret_cast<uint32_t*>(base);
+    a->marks = base + marks;
+    a->old_marks = base + old_marks;
+    a->keeper = reinterpret_cast<int32_t*>(base + keeper);
+    a->words = reinterpret_cast<uint4*>(base + words);
+    a->chunks = reinterpret_cast<int2*>(base + totals);
+    a->num_chunks = (int32_t)chunks;
+  }
+  return end;
+}
+
+struct CopyArgs {
+  uint8_t* data[PA_MAX_COPY_TENSORS];
+  int64_t bytes[PA_MAX_COPY_TENSORS];  // of a page
+  const int2* copies;
+  uint32_t* error;
+  int32_t n, num_tensors, num_blocks, pieces;
+};
+
+// attention with capped or biased scores and ranges of keys (biased.cu)
+struct BiasedArgs {
+  const uint16_t *query, *key_cache, *value_cache;
+  const int32_t *cum, *past, *table, *first, *prefix;  // first, prefix: or null
+  const float* slopes;                                 // or null
+  void* output;
+  float* lse;
+  uint32_t* error;
+  int64_t q_stride;
+  int32_t N, B, nh, kvh, G, hs, num_blocks, bs, max_blocks;
+  int32_t window, max_rows;  // 0: none
+  // s log2(e) of a score q.k is q.k * scale_log2, or with a cap cap_log2 * tanh(q.k * scale_cap)
+  float scale_log2, scale_cap, cap_log2;
+  // split pieces of the rows kernel: two slots per CTA, and what they hold
+  float *part_o, *part_ml;
+  int4* records;
+};
+
+cudaError_t launch_fork(const PoolArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_compact(const PoolArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_copy_pages(CopyArgs& a, int sms, cudaStream_t s);
+int biased_ctas(int hs, int sms);  // CTAs of the rows kernel
+cudaError_t launch_biased(const BiasedArgs& a, bool bf16, int sms, cudaStream_t s);
 cudaError_t launch_tables(const TableArgs& a, int sms, cudaStream_t s);
 cudaError_t launch_rotate(const RotateArgs& a, bool bf16, int hs, int sms, cudaStream_t s);
 cudaError_t launch_bounds(const PageArgs& a, bool bf16, cudaStream_t s);

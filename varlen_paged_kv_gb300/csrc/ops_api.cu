@@ -1,5 +1,5 @@
 // C ABI of the operators around paged attention (include/pagedattn.h): argument checks and
-// launches. No allocation, no synchronisation, no workspace.
+// launches. No allocation and no synchronisation; a workspace only where the caller gives one.
 #include <cmath>
 #include <initializer_list>
 
@@ -15,9 +15,9 @@ bool all_aligned(uintptr_t a, std::initializer_list<const void*> ps) {
   return true;
 }
 
-pa_status launched(cudaError_t e, const char* what) {
+pa_status launched(cudaError_t e, const char* what, int kernels = 1) {
   if (e) return pa::cuda_fail(e, what);
-  pa::count_launch();
+  while (kernels-- > 0) pa::count_launch();
   return PA_OK;
 }
 
@@ -257,6 +257,195 @@ pa_status pa_sparse_paged_attention(const void* query, const void* key_cache, co
   a.scale_log2 = sc * 1.4426950408889634f;
   return launched(pa::launch_sparse(a, dims->dtype == PA_BFLOAT16, sms, static_cast<cudaStream_t>(stream)),
                   "sparse attention launch");
+}
+
+size_t pa_pool_workspace_size(int32_t num_blocks) {
+  if (num_blocks <= 0 || num_blocks > PA_MAX_POOL_PAGES) return 0;
+  return pa::pool_workspace(num_blocks, true, nullptr, nullptr);
+}
+
+pa_status pa_fork_block_tables(const int32_t* parents, const int32_t* past_seqlens, const int32_t* blocks_held,
+                               const int32_t* block_table, int32_t* free_blocks, const int32_t* free_state,
+                               const uint8_t* pinned, int32_t batch_size, int32_t new_batch_size,
+                               int32_t max_blocks_per_sequence, int32_t block_size, int32_t num_blocks,
+                               int32_t free_capacity, int32_t* past_seqlens_out, int32_t* blocks_held_out,
+                               int32_t* block_table_out, int32_t* copies, int32_t* free_state_out, uint32_t* error,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  if (batch_size < 0 || new_batch_size < 0 || max_blocks_per_sequence <= 0 || block_size <= 0 || num_blocks <= 0 ||
+      free_capacity <= 0)
+    return PA_ERR_INVALID_ARGUMENT;
+  if (batch_size > PA_MAX_TABLE_REQUESTS || new_batch_size > PA_MAX_TABLE_REQUESTS || num_blocks > PA_MAX_POOL_PAGES ||
+      (int64_t)max_blocks_per_sequence * block_size > INT32_MAX ||
+      (int64_t)batch_size * max_blocks_per_sequence > INT32_MAX ||
+      (int64_t)new_batch_size * max_blocks_per_sequence > INT32_MAX || free_capacity > (1 << 30))
+    return PA_ERR_UNSUPPORTED;
+  if (!all_aligned(4, {free_blocks, free_state, free_state_out, error}) || !aligned(workspace, 16))
+    return PA_ERR_INVALID_ARGUMENT;
+  if (batch_size > 0 && !all_aligned(4, {past_seqlens, blocks_held, block_table})) return PA_ERR_INVALID_ARGUMENT;
+  if (new_batch_size > 0 &&
+      (!all_aligned(4, {parents, past_seqlens_out, blocks_held_out, block_table_out}) || !aligned(copies, 8)))
+    return PA_ERR_INVALID_ARGUMENT;
+  // rows are read while others are written
+  if (free_state_out == free_state ||
+      (batch_size > 0 && new_batch_size > 0 &&
+       (past_seqlens_out == past_seqlens || blocks_held_out == blocks_held || block_table_out == block_table)))
+    return PA_ERR_INVALID_ARGUMENT;
+  if (workspace_bytes < pa::pool_workspace(num_blocks, true, nullptr, nullptr)) return PA_ERR_WORKSPACE_TOO_SMALL;
+  int sms = 0;
+  if (!pa::device_sms(&sms)) return pa::cuda_fail(cudaGetLastError(), "device query");
+  pa::PoolArgs a{};
+  pa::pool_workspace(num_blocks, true, &a, static_cast<uint8_t*>(workspace));
+  a.parents = parents;
+  a.past = past_seqlens;
+  a.held = blocks_held;
+  a.table = block_table;
+  a.ring = free_blocks;
+  a.state = free_state;
+  a.pinned = pinned;
+  a.past_out = past_seqlens_out;
+  a.held_out = blocks_held_out;
+  a.table_out = block_table_out;
+  a.copies = reinterpret_cast<int2*>(copies);
+  a.state_out = free_state_out;
+  a.error = error;
+  a.B = batch_size;
+  a.Bn = new_batch_size;
+  a.max_blocks = max_blocks_per_sequence;
+  a.bs = block_size;
+  a.num_blocks = num_blocks;
+  a.cap = free_capacity;
+  return launched(pa::launch_fork(a, sms, static_cast<cudaStream_t>(stream)), "fork launch", 4);
+}
+
+pa_status pa_compact_block_tables(const int32_t* blocks_held, const int32_t* block_table, int32_t* free_blocks,
+                                  const uint8_t* pinned, int32_t batch_size, int32_t max_blocks_per_sequence,
+                                  int32_t num_blocks, int32_t free_capacity, int32_t max_moves,
+                                  int32_t* block_table_out, int32_t* copies, int32_t* free_state_out,
+                                  int32_t* pages_end, uint32_t* error, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  if (batch_size < 0 || max_blocks_per_sequence <= 0 || num_blocks <= 0 || free_capacity <= 0 || max_moves < 0)
+    return PA_ERR_INVALID_ARGUMENT;
+  if (batch_size > PA_MAX_TABLE_REQUESTS || num_blocks > PA_MAX_POOL_PAGES || max_moves > PA_MAX_POOL_PAGES ||
+      (int64_t)batch_size * max_blocks_per_sequence > INT32_MAX || free_capacity > (1 << 30))
+    return PA_ERR_UNSUPPORTED;
+  if (!all_aligned(4, {free_blocks, free_state_out, pages_end, error}) || !aligned(workspace, 16))
+    return PA_ERR_INVALID_ARGUMENT;
+  if (batch_size > 0 && !all_aligned(4, {blocks_held, block_table, block_table_out})) return PA_ERR_INVALID_ARGUMENT;
+  if (max_moves > 0 && !aligned(copies, 8)) return PA_ERR_INVALID_ARGUMENT;
+  if (workspace_bytes < pa::pool_workspace(num_blocks, false, nullptr, nullptr)) return PA_ERR_WORKSPACE_TOO_SMALL;
+  int sms = 0;
+  if (!pa::device_sms(&sms)) return pa::cuda_fail(cudaGetLastError(), "device query");
+  pa::PoolArgs a{};
+  pa::pool_workspace(num_blocks, false, &a, static_cast<uint8_t*>(workspace));
+  a.held = blocks_held;
+  a.table = block_table;
+  a.ring = free_blocks;
+  a.pinned = pinned;
+  a.table_out = block_table_out;
+  a.copies = reinterpret_cast<int2*>(copies);
+  a.state_out = free_state_out;
+  a.pages_end = pages_end;
+  a.error = error;
+  a.B = batch_size;
+  a.max_blocks = max_blocks_per_sequence;
+  a.num_blocks = num_blocks;
+  a.cap = free_capacity;
+  a.max_moves = max_moves;
+  return launched(pa::launch_compact(a, sms, static_cast<cudaStream_t>(stream)), "compaction launch", 4);
+}
+
+pa_status pa_copy_pages(const pa_page_tensor* tensors, int32_t num_tensors, int32_t num_blocks, const int32_t* copies,
+                        int32_t num_copies, uint32_t* error, void* stream) {
+  if (num_tensors < 0 || num_blocks < 0 || num_copies < 0) return PA_ERR_INVALID_ARGUMENT;
+  if (num_tensors > PA_MAX_COPY_TENSORS) return PA_ERR_UNSUPPORTED;
+  if (num_tensors == 0 || num_copies == 0) return PA_OK;
+  if (!tensors || !aligned(copies, 8) || (error && !aligned(error, 4))) return PA_ERR_INVALID_ARGUMENT;
+  pa::CopyArgs a{};
+  for (int32_t t = 0; t < num_tensors; ++t) {
+    const int64_t bytes = tensors[t].page_bytes;
+    if (bytes <= 0 || !aligned(tensors[t].data, 16)) return PA_ERR_INVALID_ARGUMENT;
+    if (bytes % 16 != 0 || bytes > INT32_MAX) return PA_ERR_UNSUPPORTED;
+    a.data[t] = static_cast<uint8_t*>(tensors[t].data);
+    a.bytes[t] = bytes;
+  }
+  int sms = 0;
+  if (!pa::device_sms(&sms)) return pa::cuda_fail(cudaGetLastError(), "device query");
+  a.copies = reinterpret_cast<const int2*>(copies);
+  a.error = error;
+  a.n = num_copies;
+  a.num_tensors = num_tensors;
+  a.num_blocks = num_blocks;
+  return launched(pa::launch_copy_pages(a, sms, static_cast<cudaStream_t>(stream)), "copy_pages_kernel launch");
+}
+
+// the rows kernel's two slots per CTA: partial results, their (m, l), and the CTAs' records
+size_t pa_biased_workspace_size(int32_t head_size) {
+  if (head_size != 64 && head_size != 128 && head_size != 256) return 0;
+  const size_t slots = 2 * (size_t)PA_BIASED_CTAS;
+  return slots * 16 * (size_t)head_size * 4 + slots * 16 * 8 + slots * 16;
+}
+
+pa_status pa_biased_paged_attention(const void* query, const void* key_cache, const void* value_cache,
+                                    const int32_t* cumulative_sequence_length, const int32_t* past_seqlens,
+                                    const int32_t* block_table, float scale, const pa_score_rules* rules, void* output,
+                                    float* lse, const pa_biased_dims* dims, uint32_t* error, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+  if (!dims || dims->reserved != 0 || !rules || rules->reserved != 0) return PA_ERR_INVALID_ARGUMENT;
+  const pa_sparse_dims d = {dims->num_tokens, dims->batch_size, dims->num_heads, dims->kv_num_heads, dims->head_size,
+                            dims->num_blocks, dims->block_size, dims->max_blocks_per_sequence, dims->dtype,
+                            1, 1, 0, 1, 0, dims->query_stride};
+  if (pa_status st = check_batch_dims(&d)) return st;
+  if (pa_status st = check_selection_dims(&d)) return st;
+  if (!(rules->softcap >= 0.f) || !(rules->softcap <= 1e30f) || rules->window < 0 || dims->max_query_len < 0 || !std::isfinite(scale))
+    return PA_ERR_INVALID_ARGUMENT;
+  // (rows, heads and blocks of rows are numbered in 32 bits)
+  if ((int64_t)dims->num_tokens * dims->num_heads > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  if (dims->num_tokens == 0) return PA_OK;
+  if (!all_aligned(16, {query, key_cache, value_cache, output, workspace}) ||
+      !all_aligned(4, {cumulative_sequence_length, past_seqlens, block_table}) || (lse && !aligned(lse, 4)) ||
+      (error && !aligned(error, 4)) || (rules->slopes && !aligned(rules->slopes, 4)) ||
+      (rules->first_keys && !aligned(rules->first_keys, 4)) || (rules->prefix_lens && !aligned(rules->prefix_lens, 4)))
+    return PA_ERR_INVALID_ARGUMENT;
+  if (workspace_bytes < pa_biased_workspace_size(dims->head_size)) return PA_ERR_WORKSPACE_TOO_SMALL;
+  int sms = 0;
+  if (!pa::device_sms(&sms)) return pa::cuda_fail(cudaGetLastError(), "device query");
+  pa::BiasedArgs a{};
+  a.query = static_cast<const uint16_t*>(query);
+  a.key_cache = static_cast<const uint16_t*>(key_cache);
+  a.value_cache = static_cast<const uint16_t*>(value_cache);
+  a.cum = cumulative_sequence_length;
+  a.past = past_seqlens;
+  a.table = block_table;
+  a.first = rules->first_keys;
+  a.prefix = rules->prefix_lens;
+  a.slopes = rules->slopes;
+  a.output = output;
+  a.lse = lse;
+  a.error = error;
+  a.q_stride = dims->query_stride;
+  a.N = dims->num_tokens;
+  a.B = dims->batch_size;
+  a.nh = dims->num_heads;
+  a.kvh = dims->kv_num_heads;
+  a.G = dims->num_heads / dims->kv_num_heads;
+  a.hs = dims->head_size;
+  a.num_blocks = dims->num_blocks;
+  a.bs = dims->block_size;
+  a.max_blocks = dims->max_blocks_per_sequence;
+  a.window = rules->window;
+  a.max_rows = dims->max_query_len;
+  const float sc = scale == 0.0f ? 1.0f / std::sqrt((float)dims->head_size) : scale;
+  a.scale_log2 = sc * 1.4426950408889634f;
+  if (rules->softcap > 0.f) {
+    a.scale_cap = sc / rules->softcap;
+    a.cap_log2 = rules->softcap * 1.4426950408889634f;
+  }
+  const size_t slots = 2 * (size_t)PA_BIASED_CTAS;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = a.part_o + slots * 16 * (size_t)dims->head_size;
+  a.records = reinterpret_cast<int4*>(a.part_ml + slots * 16 * 2);
+  return launched(pa::launch_biased(a, dims->dtype == PA_BFLOAT16, sms, static_cast<cudaStream_t>(stream)),
+                  "biased attention launch");
 }
 
 }  // extern "C"
