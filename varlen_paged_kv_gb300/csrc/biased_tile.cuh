@@ -37,7 +37,7 @@ struct TileItem {
   int rows, row0, pos0, b;  // rows of the batch (0: none), the first of them, its position, the sequence
   int prefix, total;        // keys of the sequence
   int lo, hi;               // keys that some row sees
-  int all_lo, all_hi;       // keys that all rows see
+  int all_lo, all_hi;       // keys that all rows see that see any
 };
 
 __device__ __forceinline__ TileItem tile_item(const BiasedArgs& a, int u, int sub_rows, int lane) {
@@ -57,13 +57,89 @@ __device__ __forceinline__ TileItem tile_item(const BiasedArgs& a, int u, int su
   for (int j = lane; j < it.rows; j += 32) {
     const Keys k = keys_of_row(a, s, it.prefix, j0 + j);
     some = join(some, k);
-    all = {max(all.lo, k.lo), min(all.hi, k.hi)};
+    if (k.hi > 0) all = {max(all.lo, k.lo), min(all.hi, k.hi)};
   }
   it.lo = __reduce_min_sync(0xffffffffu, some.lo);
   it.hi = __reduce_max_sync(0xffffffffu, some.hi);
   it.all_lo = __reduce_max_sync(0xffffffffu, all.lo);
   it.all_hi = __reduce_min_sync(0xffffffffu, all.hi);
   return it;
+}
+
+// 32 products q.k of a row as scores in powers of two, consecutive keys from the tile's first: capped
+// (`level`: not at all, by tanh's short form, its longer one, or wherever they are) and less their
+// distance's share (`slope` is minus the slope, `away` the distance of the first key; with `after`
+// some keys may lie behind the row). On packed pairs: a score takes 4.5 instruction slots at level 1
+// with a bias, where one score at a time with a six-term tanh took 13.
+template <bool BIAS>
+__device__ __forceinline__ void bend_scores(const BiasedArgs& a, uint32_t* r, int level, float slope, float away, bool after) {
+  constexpr int N = 32;
+  // without a key behind the row the bias is slope * away - slope * e, exact enough in this form: its
+  // rounding, 2^-24 of the bias, only shows where the bias itself has not made the weight small
+  const uint64_t base = f2_make(slope * away, slope * away), step = f2_make(-slope, -slope);
+  auto bias_of = [&](int e) { return BIAS ? f2_fma(step, f2_make((float)e, (float)(e + 1)), base) : f2_make(0.f, 0.f); };
+  auto pair = [&](int e) { return f2_make(__uint_as_float(r[e]), __uint_as_float(r[e + 1])); };
+  auto put = [&](int e, uint64_t v) {
+    float x, y;
+    f2_split(v, x, y);
+    r[e] = __float_as_uint(x), r[e + 1] = __float_as_uint(y);
+  };
+  const float scale = level == 0 ? a.scale_log2 : a.scale_cap, cl = a.cap_log2;
+  const uint64_t sc = f2_make(scale, scale);
+  if (BIAS && after) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const float x = __uint_as_float(r[e]) * scale;
+      r[e] = __float_as_uint(fmaf(slope, fabsf(away - (float)e), level == 0 ? x : cl * tanh_of(x)));
+    }
+  } else if (level == 0) {
+#pragma unroll
+    for (int e = 0; e < N; e += 2) put(e, f2_fma(pair(e), sc, bias_of(e)));
+  } else if (level == 1) {
+    const uint64_t c0 = f2_make(kTanh3[0] * cl, kTanh3[0] * cl), c1 = f2_make(kTanh3[1] * cl, kTanh3[1] * cl),
+                   c2 = f2_make(kTanh3[2] * cl, kTanh3[2] * cl);
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+      const uint64_t x = f2_mul(pair(e), sc), z = f2_mul(x, x);
+      put(e, f2_fma(f2_fma(f2_fma(c2, z, c1), z, c0), x, bias_of(e)));
+    }
+  } else if (level == 2) {
+    uint64_t c[6];
+#pragma unroll
+    for (int k = 0; k < 6; ++k) c[k] = f2_make(kTanh[k] * cl, kTanh[k] * cl);
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+      const uint64_t x = f2_mul(pair(e), sc), z = f2_mul(x, x);
+      uint64_t y = c[5];
+#pragma unroll
+      for (int k = 4; k >= 0; --k) y = f2_fma(y, z, c[k]);
+      put(e, f2_fma(y, x, bias_of(e)));
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+      const float x = cl * tanh_of(__uint_as_float(r[e]) * scale), y = cl * tanh_of(__uint_as_float(r[e + 1]) * scale);
+      put(e, f2_add(f2_make(x, y), bias_of(e)));
+    }
+  }
+}
+
+// two weights as bf16 pairs hi + lo: hi their upper 16 bits as they are, lo the rest rounded, so that
+// the sum is 2^-17 off at most
+__device__ __forceinline__ void cut_bf16x2(uint64_t p, uint32_t& hi, uint32_t& lo) {
+  float p0, p1;
+  f2_split(p, p0, p1);
+  const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
+  hi = prmt(u0, u1, 0x7632u);
+  float r0, r1;  // (weights are not negative: the sign bit set is minus the upper part)
+  f2_split(f2_add(p, f2_make(__uint_as_float((u0 & 0xFFFF0000u) | 0x80000000u), __uint_as_float((u1 & 0xFFFF0000u) | 0x80000000u))), r0, r1);
+  lo = pack2<true>(r0, r1);
+}
+
+__device__ __forceinline__ Keys keys_of_item_row(const BiasedArgs& a, const TileItem& it, int j) {
+  Seq s;
+  s.c0 = it.row0, s.past = it.pos0, s.q = it.total - it.pos0;  // (the item's rows counted from 0)
+  return keys_of_row(a, s, it.prefix, j);
 }
 
 template <int HS, bool BF16>
@@ -260,9 +336,8 @@ __global__ void __launch_bounds__(kBiTileThreads, HS == 256 ? 1 : 2)
     // behind one that waits; P_{t-2} V is done once S_t is, and P_t V is not before this warp's P_t)
     constexpr int COLS = kBiTile / 2, OCOLS = HS / 2;
     const int jc = min(j, it.rows - 1), h = g * a.G + min(row % a.G, a.G - 1);  // (rows past the item borrow the last row's keys)
-    Seq sq;
-    sq.c0 = it.row0, sq.past = it.pos0, sq.q = it.total - it.pos0;  // (the item's rows counted from 0)
-    const Keys keys = keys_of_row(a, sq, it.prefix, jc);
+    const Keys keys = keys_of_item_row(a, it, jc);
+    const bool seeing = keys.hi > 0;  // (a row without keys is worked on as its neighbours, its result dropped)
     const int pos = it.pos0 + jc;
     const bool cap = a.cap_log2 != 0.f, bias = a.slopes != nullptr;
     const float slope = bias ? -a.slopes[h] * 1.4426950408889634f : 0.f;
@@ -281,43 +356,33 @@ __global__ void __launch_bounds__(kBiTileThreads, HS == 256 ? 1 : 2)
       uint32_t r[COLS];
       tmem_ld_x32(st + side * COLS, r);
       const int v0 = (t0 + t) * kBiTile + side * COLS;
-      if (cap) {
-        float most[2] = {0.f, 0.f};
+      if (cap || bias) {
+        int level = 0;  // how the cap bends the scores: not at all, or by which form of tanh
+        if (cap) {
+          float most[2] = {0.f, 0.f};
 #pragma unroll
-        for (int e = 0; e < COLS; e += 4)
+          for (int e = 0; e < COLS; e += 4)
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            most[k] = fmax3(most[k], fabsf(__uint_as_float(r[e + 2 * k])), fabsf(__uint_as_float(r[e + 2 * k + 1])));
-        const bool near = __all_sync(0xffffffffu, fmaxf(most[0], most[1]) * fabsf(a.scale_cap) <= kTanhReach);
-        if (near) {
-          const uint64_t sc = f2_make(a.scale_cap, a.scale_cap), cl = f2_make(a.cap_log2, a.cap_log2);
-#pragma unroll
-          for (int e = 0; e < COLS; e += 2) {
-            const uint64_t x = f2_mul(f2_make(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), sc), z = f2_mul(x, x);
-            uint64_t y = f2_make(kTanh[5], kTanh[5]);
-#pragma unroll
-            for (int k = 4; k >= 0; --k) y = f2_fma(y, z, f2_make(kTanh[k], kTanh[k]));
-            float y0, y1;
-            f2_split(f2_mul(f2_mul(x, cl), y), y0, y1);
-            r[e] = __float_as_uint(y0), r[e + 1] = __float_as_uint(y1);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < COLS; ++e)
-            r[e] = __float_as_uint(a.cap_log2 * tanh_of(__uint_as_float(r[e]) * a.scale_cap));
+            for (int k = 0; k < 2; ++k)
+              most[k] = fmax3(most[k], fabsf(__uint_as_float(r[e + 2 * k])), fabsf(__uint_as_float(r[e + 2 * k + 1])));
+          const float u = fmaxf(most[0], most[1]) * fabsf(a.scale_cap);
+          level = __all_sync(0xffffffffu, u <= kTanhNear) ? 1 : __all_sync(0xffffffffu, u <= kTanhReach) ? 2 : 3;
         }
+        if (!bias) bend_scores<false>(a, r, level, 0.f, 0.f, false);
+        else bend_scores<true>(a, r, level, slope, (float)(pos - v0), v0 + COLS > it.pos0 && it.prefix > it.pos0);
       }
-      if (bias) {
-        const float first = cap ? 1.f : a.scale_log2, away = (float)(pos - v0);
+      // (v0 and the bounds of all rows are the warp's: most tiles need neither side, few need both)
+      if (v0 < it.all_lo) {
+        const int lo = keys.lo - v0;
 #pragma unroll
         for (int e = 0; e < COLS; ++e)
-          r[e] = __float_as_uint(fmaf(slope, fabsf(away - (float)e), __uint_as_float(r[e]) * first));
+          if (e < lo) r[e] = __float_as_uint(none);
       }
-      if (v0 < it.all_lo || v0 + COLS > it.all_hi) {
-        const int lo = keys.lo - v0, hi = keys.hi - v0;
+      if (v0 + COLS > it.all_hi) {
+        const int hi = keys.hi - v0;
 #pragma unroll
         for (int e = 0; e < COLS; ++e)
-          if (e < lo || e >= hi) r[e] = __float_as_uint(none);
+          if (e >= hi) r[e] = __float_as_uint(none);
       }
       float mc[4] = {none, none, none, none};
       if (c > 0.f) {
@@ -339,7 +404,7 @@ __global__ void __launch_bounds__(kBiTileThreads, HS == 256 ? 1 : 2)
       named_bar_sync(bar, 64);
       const float2 both = *hx;
       const float m_new = fmaxf(m_used, fmaxf(both.x, both.y));
-      const bool grow = __any_sync(0xffffffffu, live && m_new > m_used + kLag);
+      const bool grow = __any_sync(0xffffffffu, live && seeing && m_new > m_used + kLag);
       float alpha = 1.f;
       if (grow) {
         // (fp16: a whole number, which kLift is taken off exactly)
@@ -359,8 +424,9 @@ __global__ void __launch_bounds__(kBiTileThreads, HS == 256 ? 1 : 2)
           float x0, x1;
           f2_split(f2_fma(f2_make(__uint_as_float(q[2 * e]), __uint_as_float(q[2 * e + 1])), c2, nm2), x0, x1);
           const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-          lsum = f2_add(lsum, f2_make(p0, p1));
-          if constexpr (BF16) split_bf16x2(p0, p1, q[2 * e], q[2 * e + 1]);
+          const uint64_t pp = f2_make(p0, p1);
+          lsum = f2_add(lsum, pp);
+          if constexpr (BF16) cut_bf16x2(pp, q[2 * e], q[2 * e + 1]);
           else q[2 * e] = pack2<false>(p0, p1);
         }
         const uint32_t p = st + p_col(side * (COLS / 16) + k);
@@ -395,6 +461,7 @@ __global__ void __launch_bounds__(kBiTileThreads, HS == 256 ? 1 : 2)
     named_bar_sync(bar, 64);
     l = half[row].x + half[row].y;
     if (m_used == -INFINITY && l != l) m_used = 0.f;  // scores of NaN alone: not a row without keys
+    if (!seeing) m_used = -INFINITY, l = 0.f;
     if (C > 1 && side == 0) ml[row] = m_used, ml[128 + row] = l;
   }
 
