@@ -7,7 +7,7 @@
 // two threads share a row (TMEM lets a warp at 32 of the 128 lanes), take 32 of its 64 scores each
 // through the cap, the bias and the mask, exchange their maxima through shared memory, write P
 // over the scores (fp16, or bf16 hi and lo terms) and rescale O in TMEM when the maximum grew by
-// more than 2^8 (fp16: 2^4). S_{t+1} is issued before P_t is waited for, so the tensor core works
+// more than 2^8 (fp16: 2^7). S_{t+1} is issued before P_t is waited for, so the tensor core works
 // during the softmax; two CTAs share an SM (one with 256-wide heads) and fill each other's gaps.
 // Where a batch has few tiles of rows, the CTAs of a cluster share an item's keys and add their
 // results through each other's shared memory.
@@ -30,7 +30,14 @@ struct BiTile {
   static constexpr int kNeed = kX + 2 * 128 * 2 * 4 + 1024;
   static constexpr int kBytes = kNeed < 80 * 1024 ? 80 * 1024 : kNeed;
 };
-constexpr int kBiTileThreads = 320;
+// (where the compiler lays the rarer path out of line: the softmax's code is long, and what it jumps
+// over costs fetches)
+__device__ __forceinline__ bool likely(bool x) { return __builtin_expect(x, 1); }
+__device__ __forceinline__ bool unlikely(bool x) { return __builtin_expect(x, 0); }
+
+// softmax threads that share a row, and the threads of a CTA
+__host__ __device__ constexpr int bi_sides(int hs) { return hs == 256 ? 2 : 1; }
+__host__ __device__ constexpr int bi_threads(int hs) { return 64 + 128 * bi_sides(hs); }
 
 // a CTA's work item: some rows of one sequence
 struct TileItem {
@@ -66,18 +73,14 @@ __device__ __forceinline__ TileItem tile_item(const BiasedArgs& a, int u, int su
   return it;
 }
 
-// 32 products q.k of a row as scores in powers of two, consecutive keys from the tile's first: capped
-// (`level`: not at all, by tanh's short form, its longer one, or wherever they are) and less their
-// distance's share (`slope` is minus the slope, `away` the distance of the first key; with `after`
-// some keys may lie behind the row). On packed pairs: a score takes 4.5 instruction slots at level 1
-// with a bias, where one score at a time with a six-term tanh took 13.
-template <bool BIAS>
-__device__ __forceinline__ void bend_scores(const BiasedArgs& a, uint32_t* r, int level, float slope, float away, bool after) {
-  constexpr int N = 32;
-  // without a key behind the row the bias is slope * away - slope * e, exact enough in this form: its
-  // rounding, 2^-24 of the bias, only shows where the bias itself has not made the weight small
-  const uint64_t base = f2_make(slope * away, slope * away), step = f2_make(-slope, -slope);
-  auto bias_of = [&](int e) { return BIAS ? f2_fma(step, f2_make((float)e, (float)(e + 1)), base) : f2_make(0.f, 0.f); };
+// N products q.k of a row as scores in powers of two, consecutive keys from v0 on: capped (`level`: not
+// at all, by tanh's short form, by its longer one, or wherever they are), less their distance's share
+// (`slope` is minus the slope, `away` the distance of the first key; with `after` some keys may lie behind
+// the row), plus `shift`. On packed pairs: a score takes 2.5 instruction slots at level 1, 3 with a
+// bias, where one score at a time with a six-term tanh took 13.
+template <bool BIAS, int N>
+__device__ __forceinline__ void bend_scores(const BiasedArgs& a, uint32_t* r, int level, float slope, float away, bool after,
+                                            float shift) {
   auto pair = [&](int e) { return f2_make(__uint_as_float(r[e]), __uint_as_float(r[e + 1])); };
   auto put = [&](int e, uint64_t v) {
     float x, y;
@@ -85,25 +88,48 @@ __device__ __forceinline__ void bend_scores(const BiasedArgs& a, uint32_t* r, in
     r[e] = __float_as_uint(x), r[e + 1] = __float_as_uint(y);
   };
   const float scale = level == 0 ? a.scale_log2 : a.scale_cap, cl = a.cap_log2;
-  const uint64_t sc = f2_make(scale, scale);
-  if (BIAS && after) {
+  if (BIAS && unlikely(after)) {
 #pragma unroll
     for (int e = 0; e < N; ++e) {
       const float x = __uint_as_float(r[e]) * scale;
-      r[e] = __float_as_uint(fmaf(slope, fabsf(away - (float)e), level == 0 ? x : cl * tanh_of(x)));
+      r[e] = __float_as_uint(fmaf(slope, fabsf(away - (float)e), level == 0 ? x : cl * tanh_of(x)) + shift);
+    }
+    return;
+  }
+  // without a key behind the row the bias is slope * away - slope * e, exact enough in this form: its
+  // rounding, 2^-23 of the bias, only shows where the bias itself has not made the weight small
+  const float base = fmaf(slope, away, shift);
+  const uint64_t all = f2_make(base, base);
+  uint64_t eight[4] = {};  // the bias of the eight keys from each eighth one on, and of that key
+  if constexpr (BIAS) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) eight[k] = f2_make(-slope * (float)(2 * k), -slope * (float)(2 * k + 1));
+  }
+  uint64_t from = all;
+  auto bias_of = [&](int e) {
+    if constexpr (!BIAS) return all;
+    if (e % 8 == 0) {
+      const float x = fmaf(-slope, (float)e, base);
+      from = f2_make(x, x);
+    }
+    return f2_add(eight[e % 8 / 2], from);
+  };
+  const uint64_t sc = f2_make(scale, scale);
+  if (likely(level == 1)) {
+    // cap * tanh(u) with u = scale * r as r times a polynomial in r^2 (level 1 is for scales whose fifth
+    // power is a normal number)
+    const float s1 = cl * scale, s2 = scale * scale, s3 = s1 * s2, s5 = s3 * s2;
+    const uint64_t c0 = f2_make(kTanh3[0] * s1, kTanh3[0] * s1), c1 = f2_make(kTanh3[1] * s3, kTanh3[1] * s3),
+                   c2 = f2_make(kTanh3[2] * s5, kTanh3[2] * s5);
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+      const uint64_t x = pair(e), z = f2_mul(x, x);
+      put(e, f2_fma(f2_fma(f2_fma(c2, z, c1), z, c0), x, bias_of(e)));
     }
   } else if (level == 0) {
 #pragma unroll
     for (int e = 0; e < N; e += 2) put(e, f2_fma(pair(e), sc, bias_of(e)));
-  } else if (level == 1) {
-    const uint64_t c0 = f2_make(kTanh3[0] * cl, kTanh3[0] * cl), c1 = f2_make(kTanh3[1] * cl, kTanh3[1] * cl),
-                   c2 = f2_make(kTanh3[2] * cl, kTanh3[2] * cl);
-#pragma unroll
-    for (int e = 0; e < N; e += 2) {
-      const uint64_t x = f2_mul(pair(e), sc), z = f2_mul(x, x);
-      put(e, f2_fma(f2_fma(f2_fma(c2, z, c1), z, c0), x, bias_of(e)));
-    }
-  } else if (level == 2) {
+  } else if (likely(level == 2)) {
     uint64_t c[6];
 #pragma unroll
     for (int k = 0; k < 6; ++k) c[k] = f2_make(kTanh[k] * cl, kTanh[k] * cl);
@@ -136,6 +162,37 @@ __device__ __forceinline__ void cut_bf16x2(uint64_t p, uint32_t& hi, uint32_t& l
   lo = pack2<true>(r0, r1);
 }
 
+// The weights 2^(r c + shift) (c is 1 where SCALED is not set, and the shift 0) of COLS scores, written to
+// TMEM from column `p` on as the A operand of P V: fp16, or bf16 hi and lo terms. Returns their sum.
+template <int COLS, bool BF16, bool SCALED>
+__device__ __forceinline__ float weigh(uint32_t* r, float c, float shift, uint32_t p, int first_block) {
+  const uint64_t c2 = f2_make(c, c), sh = f2_make(shift, shift);
+  uint64_t sum = f2_make(0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < COLS / 16; ++k) {
+    uint32_t* q = r + k * 16;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float x0 = __uint_as_float(q[2 * e]), x1 = __uint_as_float(q[2 * e + 1]);
+      if constexpr (SCALED) f2_split(f2_fma(f2_make(x0, x1), c2, sh), x0, x1);
+      const uint64_t w = f2_make(fast_exp2(x0), fast_exp2(x1));
+      sum = f2_add(sum, w);
+      if constexpr (BF16) {
+        cut_bf16x2(w, q[2 * e], q[2 * e + 1]);
+      } else {
+        f2_split(w, x0, x1);
+        q[2 * e] = pack2<false>(x0, x1);
+      }
+    }
+    const uint32_t at = p + p_col(first_block + k);
+    tmem_st_x8_nowait(at, q[0], q[2], q[4], q[6], q[8], q[10], q[12], q[14]);
+    if constexpr (BF16) tmem_st_x8_nowait(at + 16, q[1], q[3], q[5], q[7], q[9], q[11], q[13], q[15]);
+  }
+  float s0, s1;
+  f2_split(sum, s0, s1);
+  return s0 + s1;
+}
+
 __device__ __forceinline__ Keys keys_of_item_row(const BiasedArgs& a, const TileItem& it, int j) {
   Seq s;
   s.c0 = it.row0, s.past = it.pos0, s.q = it.total - it.pos0;  // (the item's rows counted from 0)
@@ -143,18 +200,18 @@ __device__ __forceinline__ Keys keys_of_item_row(const BiasedArgs& a, const Tile
 }
 
 template <int HS, bool BF16>
-__global__ void __launch_bounds__(kBiTileThreads, HS == 256 ? 1 : 2)
+__global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
     biased_tile_kernel(const BiasedArgs a, const __grid_constant__ CUtensorMap tmQ,
                        const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const int seg_rows, const int sub_rows) {
   using L = BiTile<HS>;
-  constexpr int HALVES = HS / 64, KSTEPS = HS / 16;
+  constexpr int HALVES = HS / 64, KSTEPS = HS / 16, SIDES = bi_sides(HS), THREADS = bi_threads(HS);
   constexpr uint32_t IDESC_QK = idesc_f16(BF16, 128, kBiTile, false), IDESC_PV = idesc_f16(BF16, 128, HS, true);
   constexpr uint32_t kO = 128;  // TMEM column of O
   // The row's reference m_used may lag behind its maximum by kLag before O is rescaled. fp16
-  // weights are lifted by 2^kLift, to 2^15 at most, so that only those below 2^-25 of the largest
-  // are subnormal and have absolute errors, of 2^-36; l is lifted with them.
-  constexpr float kLag = BF16 ? 8.f : 4.f, kLift = BF16 ? 0.f : 11.f, kUnlift = BF16 ? 1.f : 1.f / 2048;
+  // weights are lifted by 2^kLift, to 2^15 at most, so that only those below 2^-22 of the reference
+  // are subnormal and have absolute errors, of 2^-33; l is lifted with them.
+  constexpr float kLag = BF16 ? 8.f : 7.f, kLift = BF16 ? 0.f : 8.f, kUnlift = BF16 ? 1.f : 1.f / 256;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + L::kBars);
@@ -185,7 +242,7 @@ __global__ void __launch_bounds__(kBiTileThreads, HS == 256 ? 1 : 2)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 256);
+      mbar_init(&p_full[i], 128 * SIDES);
       mbar_init(&o_done[i], 1);
     }
     *abort = 0;
@@ -212,9 +269,13 @@ __global__ void __launch_bounds__(kBiTileThreads, HS == 256 ? 1 : 2)
   const int2 tiles = tiles_of(Keys{it.lo, it.hi});
   const int t0 = tiles.x + (int)((int64_t)(tiles.y - tiles.x) * rank / C);
   const int n = tiles.x + (int)((int64_t)(tiles.y - tiles.x) * (rank + 1) / C) - t0;
+  // Tiles are taken from the last to the first: with a bias the near keys' scores are the large ones, and
+  // in this order a row's maximum is there from the beginning (in the other it grows with every tile,
+  // and O is rescaled with it: 4 prompts of 2048 with everything 1031 us instead of 760).
+  const int last = t0 + n - 1;
 
   const int row = (warp & 3) * 32 + lane;  // (softmax warps) the thread's TMEM lane
-  const int side = warp >= 6;              // and its half of the row's columns
+  const int side = SIDES == 2 && warp >= 6;  // and, where two threads share a row, its half of the columns
   const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
   const int j = row / a.G;                  // its row in the item
   const bool live = warp >= 2 && j < it.rows && row < sub_rows * a.G;
@@ -233,7 +294,7 @@ __global__ void __launch_bounds__(kBiTileThreads, HS == 256 ? 1 : 2)
       }
       const int* table = a.table + (int64_t)it.b * a.max_blocks;
       auto slot = [&](int t) {  // this lane's segment of tile t: its first cache row
-        const int v = (t0 + t) * kBiTile + lane * seg_rows;
+        const int v = (last - t) * kBiTile + lane * seg_rows;
         if (lane >= nseg || t >= n || v >= it.hi || v + seg_rows <= it.lo) return oob;
         const int page = v / a.bs, phys = table[page];
         if (phys < 0 || phys >= a.num_blocks) {
@@ -300,7 +361,7 @@ __global__ void __launch_bounds__(kBiTileThreads, HS == 256 ? 1 : 2)
       mbar_wait(&v_full[s], (t / L::kStages) & 1, abort, err);
       // rows that no row of the item sees may be unwritten: cleared, so that no NaN meets a
       // weight of 0 (whole 128-byte rows: the swizzle stays inside)
-      const int k0 = (t0 + t) * kBiTile, front = max(it.lo - k0, 0), back = min(it.hi - k0, kBiTile);
+      const int k0 = (last - t) * kBiTile, front = max(it.lo - k0, 0), back = min(it.hi - k0, kBiTile);
       if (front > 0 || back < kBiTile) {
         uint8_t* vt = smem + L::kRing + (L::kStages + s) * L::kTileBytes;
         const int rows = front + kBiTile - back;
@@ -334,17 +395,19 @@ __global__ void __launch_bounds__(kBiTileThreads, HS == 256 ? 1 : 2)
     // (S, P and O each signal on two barriers in turn: not every wait is made by every warp, and a
     // parity tells a phase from the next only, so a barrier must not be two phases ahead of or
     // behind one that waits; P_{t-2} V is done once S_t is, and P_t V is not before this warp's P_t)
-    constexpr int COLS = kBiTile / 2, OCOLS = HS / 2;
+    constexpr int COLS = kBiTile / SIDES, OCOLS = HS / SIDES;
     const int jc = min(j, it.rows - 1), h = g * a.G + min(row % a.G, a.G - 1);  // (rows past the item borrow the last row's keys)
     const Keys keys = keys_of_item_row(a, it, jc);
     const bool seeing = keys.hi > 0;  // (a row without keys is worked on as its neighbours, its result dropped)
     const int pos = it.pos0 + jc;
-    const bool cap = a.cap_log2 != 0.f, bias = a.slopes != nullptr;
+    const bool cap = a.cap_log2 != 0.f, bias = a.slopes != nullptr, bent = cap || bias;
+    const float span = fabsf(a.scale_cap);
+    const int near = span > 1e-6f && span < 1e6f && a.cap_log2 < 1e6f ? 1 : 2;  // (the short tanh's coefficients hold)
     const float slope = bias ? -a.slopes[h] * 1.4426950408889634f : 0.f;
-    const float c = cap || bias ? 1.f : a.scale_log2;  // what the scores below are still multiplied by
+    const float c = bent ? 1.f : a.scale_log2;  // what the scores below are still multiplied by
     const float none = c > 0.f ? -INFINITY : INFINITY;  // a score whose product with c is -inf
     const uint32_t o_tmem = tmem + lane_off + kO + side * OCOLS;
-    const int bar = 1 + (warp & 3);  // of the two warps of a lane quarter
+    [[maybe_unused]] const int bar = 1 + (warp & 3);  // of the two warps of a lane quarter
     for (int t = 0; t < n; ++t) {
       mbar_wait(&s_full[t & 1], (t >> 1) & 1, abort, err);
       if (!any_live) {  // rows past the item: whatever their P holds stays in their rows of O
@@ -354,89 +417,92 @@ __global__ void __launch_bounds__(kBiTileThreads, HS == 256 ? 1 : 2)
       tc_fence_after();
       const uint32_t st = tmem + lane_off + (t & 1) * kBiTile;
       uint32_t r[COLS];
-      tmem_ld_x32(st + side * COLS, r);
-      const int v0 = (t0 + t) * kBiTile + side * COLS;
-      if (cap || bias) {
-        int level = 0;  // how the cap bends the scores: not at all, or by which form of tanh
+      if constexpr (SIDES == 2) tmem_ld_x32(st + side * COLS, r);
+      else tmem_ld_x64(st, r);
+      const int v0 = (last - t) * kBiTile + side * COLS;
+      // With a cap or a bias the scores are bent first. The largest |q.k| of the row's keys tells how far
+      // the cap bends them and bounds the scores from above, so that a maximum is only looked for where
+      // the bound is over what the row's reference may lag behind; else the reference goes into the
+      // bend (where two threads share a row they would have to agree: there it is always looked for).
+      bool find_max = true;
+      if (bent) {
+        float most[2] = {0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < COLS; e += 4)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            most[k] = fmax3(most[k], fabsf(__uint_as_float(r[e + 2 * k])), fabsf(__uint_as_float(r[e + 2 * k + 1])));
+        const float u = fmaxf(most[0], most[1]) * fabsf(cap ? a.scale_cap : a.scale_log2), away = (float)(pos - v0);
+        float top = u;
+        int level = 0;
         if (cap) {
-          float most[2] = {0.f, 0.f};
-#pragma unroll
-          for (int e = 0; e < COLS; e += 4)
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              most[k] = fmax3(most[k], fabsf(__uint_as_float(r[e + 2 * k])), fabsf(__uint_as_float(r[e + 2 * k + 1])));
-          const float u = fmaxf(most[0], most[1]) * fabsf(a.scale_cap);
-          level = __all_sync(0xffffffffu, u <= kTanhNear) ? 1 : __all_sync(0xffffffffu, u <= kTanhReach) ? 2 : 3;
+          level = __all_sync(0xffffffffu, u <= kTanhNear) ? near : __all_sync(0xffffffffu, u <= kTanhReach) ? 2 : 3;
+          top = a.cap_log2 * fminf(u, 1.f);
         }
-        if (!bias) bend_scores<false>(a, r, level, 0.f, 0.f, false);
-        else bend_scores<true>(a, r, level, slope, (float)(pos - v0), v0 + COLS > it.pos0 && it.prefix > it.pos0);
+        const bool after = v0 + COLS > it.pos0 && it.prefix > it.pos0;
+        if constexpr (SIDES == 1) {
+          // (the bias of the nearest or farthest key, whichever is more; a key behind the row may be as near as 0)
+          const float far = after ? fmaxf(fabsf(away), fabsf(away - (COLS - 1))) : away;
+          top += fmaxf(slope * far, slope * (after ? 0.f : fmaxf(away - (COLS - 1), 0.f)));
+          find_max = __any_sync(0xffffffffu, live && seeing && !(top <= m_used + kLag));
+        }
+        const float shift = find_max || m_used == -INFINITY ? 0.f : kLift - m_used;
+        if (!bias) bend_scores<false, COLS>(a, r, level, 0.f, 0.f, false, shift);
+        else bend_scores<true, COLS>(a, r, level, slope, away, after, shift);
       }
       // (v0 and the bounds of all rows are the warp's: most tiles need neither side, few need both)
-      if (v0 < it.all_lo) {
+      if (unlikely(v0 < it.all_lo)) {
         const int lo = keys.lo - v0;
 #pragma unroll
         for (int e = 0; e < COLS; ++e)
           if (e < lo) r[e] = __float_as_uint(none);
       }
-      if (v0 + COLS > it.all_hi) {
+      if (unlikely(v0 + COLS > it.all_hi)) {
         const int hi = keys.hi - v0;
 #pragma unroll
         for (int e = 0; e < COLS; ++e)
           if (e >= hi) r[e] = __float_as_uint(none);
       }
-      float mc[4] = {none, none, none, none};
-      if (c > 0.f) {
-#pragma unroll
-        for (int e = 0; e < COLS; e += 8)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mc[k] = fmax3(mc[k], __uint_as_float(r[e + 2 * k]), __uint_as_float(r[e + 2 * k + 1]));
-      } else {
-#pragma unroll
-        for (int e = 0; e < COLS; e += 8)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mc[k] = fmin3(mc[k], __uint_as_float(r[e + 2 * k]), __uint_as_float(r[e + 2 * k + 1]));
-      }
-      const float best = c > 0.f ? fmax3(fmaxf(mc[0], mc[1]), mc[2], mc[3]) : fmin3(fminf(mc[0], mc[1]), mc[2], mc[3]);
-      float2* hx = half + (t & 1) * 128 + row;
-      (side ? hx->y : hx->x) = best * c;
-      named_bar_sync(bar, 64);
-      const float2 both = *hx;
-      const float m_new = fmaxf(m_used, fmaxf(both.x, both.y));
-      const bool grow = __any_sync(0xffffffffu, live && seeing && m_new > m_used + kLag);
+      bool grow = false;
       float alpha = 1.f;
-      if (grow) {
-        // (fp16: a whole number, which kLift is taken off exactly)
-        const float to = BF16 ? m_new : ceilf(m_new);
-        alpha = m_new == -INFINITY ? 1.f : fast_exp2(m_used - to);  // 0 on a row's first keys
-        m_used = to;
-        l *= alpha;
-      }
-      const float neg_m = m_used == -INFINITY ? 0.f : kLift - m_used;  // (no key yet: every weight is 0)
-      const uint64_t c2 = f2_make(c, c), nm2 = f2_make(neg_m, neg_m);
-      uint64_t lsum = f2_make(0.f, 0.f);
+      if (find_max) {
+        float mc[4] = {none, none, none, none};
+        if (c > 0.f) {
 #pragma unroll
-      for (int k = 0; k < COLS / 16; ++k) {
-        uint32_t* q = r + k * 16;
+          for (int e = 0; e < COLS; e += 8)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float x0, x1;
-          f2_split(f2_fma(f2_make(__uint_as_float(q[2 * e]), __uint_as_float(q[2 * e + 1])), c2, nm2), x0, x1);
-          const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-          const uint64_t pp = f2_make(p0, p1);
-          lsum = f2_add(lsum, pp);
-          if constexpr (BF16) cut_bf16x2(pp, q[2 * e], q[2 * e + 1]);
-          else q[2 * e] = pack2<false>(p0, p1);
+            for (int k = 0; k < 4; ++k)
+              mc[k] = fmax3(mc[k], __uint_as_float(r[e + 2 * k]), __uint_as_float(r[e + 2 * k + 1]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < COLS; e += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mc[k] = fmin3(mc[k], __uint_as_float(r[e + 2 * k]), __uint_as_float(r[e + 2 * k + 1]));
         }
-        const uint32_t p = st + p_col(side * (COLS / 16) + k);
-        tmem_st_x8_nowait(p, q[0], q[2], q[4], q[6], q[8], q[10], q[12], q[14]);
-        if constexpr (BF16) tmem_st_x8_nowait(p + 16, q[1], q[3], q[5], q[7], q[9], q[11], q[13], q[15]);
+        const float best = c > 0.f ? fmax3(fmaxf(mc[0], mc[1]), mc[2], mc[3]) : fmin3(fminf(mc[0], mc[1]), mc[2], mc[3]);
+        float m_new = fmaxf(m_used, best * c);
+        if constexpr (SIDES == 2) {
+          float2* hx = half + (t & 1) * 128 + row;
+          (side ? hx->y : hx->x) = best * c;
+          named_bar_sync(bar, 64);
+          const float2 both = *hx;
+          m_new = fmaxf(m_used, fmaxf(both.x, both.y));
+        }
+        grow = __any_sync(0xffffffffu, live && seeing && m_new > m_used + kLag);
+        if (unlikely(grow)) {
+          // (fp16: a whole number, which kLift is taken off exactly)
+          const float to = BF16 ? m_new : ceilf(m_new);
+          alpha = m_new == -INFINITY ? 1.f : fast_exp2(m_used - to);  // 0 on a row's first keys
+          m_used = to;
+          l *= alpha;
+        }
+        const float neg_m = m_used == -INFINITY ? 0.f : kLift - m_used;  // (no key yet: every weight is 0)
+        l += weigh<COLS, BF16, true>(r, c, neg_m, st, side * (COLS / 16));
+      } else {
+        l += weigh<COLS, BF16, false>(r, 1.f, 0.f, st, 0);
       }
-      float s0, s1;
-      f2_split(lsum, s0, s1);
-      l += s0 + s1;
-      if (t > 0 && grow) {  // O holds P_0 V .. P_{t-1} V once the last product is done
+      if (unlikely(t > 0 && grow)) {  // O holds P_0 V .. P_{t-1} V once the last product is done
         mbar_wait(&o_done[(t - 1) & 1], ((t - 1) >> 1) & 1, abort, err);
         tc_fence_after();
 #pragma unroll 1
@@ -456,10 +522,11 @@ __global__ void __launch_bounds__(kBiTileThreads, HS == 256 ? 1 : 2)
       mbar_wait(&o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort, err);
       tc_fence_after();
     }
-    // the row's sum from its halves (the two warps have the same maximum)
-    (side ? half[row].y : half[row].x) = l;
-    named_bar_sync(bar, 64);
-    l = half[row].x + half[row].y;
+    if constexpr (SIDES == 2) {  // the row's sum from its halves (the two warps have the same maximum)
+      (side ? half[row].y : half[row].x) = l;
+      named_bar_sync(bar, 64);
+      l = half[row].x + half[row].y;
+    }
     if (m_used == -INFINITY && l != l) m_used = 0.f;  // scores of NaN alone: not a row without keys
     if (!seeing) m_used = -INFINITY, l = 0.f;
     if (C > 1 && side == 0) ml[row] = m_used, ml[128 + row] = l;
@@ -473,7 +540,7 @@ __global__ void __launch_bounds__(kBiTileThreads, HS == 256 ? 1 : 2)
       if (live && a.lse && side == 0)
         a.lse[at] = m_used == -INFINITY ? -INFINITY : (m_used + fast_log2(l * kUnlift)) * 0.69314718055994531f;
 #pragma unroll 1
-      for (int cc = side * (HS / 2); cc < (side + 1) * (HS / 2); cc += 32) {
+      for (int cc = side * (HS / SIDES); cc < (side + 1) * (HS / SIDES); cc += 32) {
         uint32_t ov[32];
         if (n > 0) {
           tmem_ld_x32(tmem + lane_off + kO + cc, ov);
@@ -511,7 +578,7 @@ __global__ void __launch_bounds__(kBiTileThreads, HS == 256 ? 1 : 2)
         a.lse[(int64_t)(it.row0 + j) * a.nh + g * a.G + row % a.G] =
             M == -INFINITY ? -INFINITY : (M + fast_log2(S * kUnlift)) * 0.69314718055994531f;
 #pragma unroll 1
-      for (int cc = side * (HS / 2); any_live && cc < (side + 1) * (HS / 2); cc += 32) {
+      for (int cc = side * (HS / SIDES); any_live && cc < (side + 1) * (HS / SIDES); cc += 32) {
         uint32_t ov[32];
         if (n > 0) tmem_ld_x32(tmem + lane_off + kO + cc, ov);
 #pragma unroll
@@ -528,7 +595,7 @@ __global__ void __launch_bounds__(kBiTileThreads, HS == 256 ? 1 : 2)
     cluster_sync();
     const int M = it.rows * a.G;  // rows of the item, a share of them summed by each CTA
     const int r0 = M * rank / C, r1 = M * (rank + 1) / C;
-    for (int i = threadIdx.x; i < (r1 - r0) * (HS / 4); i += kBiTileThreads) {
+    for (int i = threadIdx.x; i < (r1 - r0) * (HS / 4); i += THREADS) {
       const int r = r0 + i / (HS / 4), quad = i % (HS / 4);
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int k = 0; k < C; ++k) {
@@ -558,6 +625,6 @@ static cudaError_t launch_biased_tile(const BiasedArgs& a, const CUtensorMap& tq
   const int64_t items = items_of_batch(a.N, a.B, sub_rows, 1, 1) * a.kvh;
   const int c = cluster_size(items, (int64_t)sms * (HS == 256 ? 1 : 2), ceil_div(keys, kBiTile), 4, 8);
   const dim3 grid((unsigned)(a.N / sub_rows + a.B), (unsigned)a.kvh, (unsigned)c);
-  return launch_clusters(biased_tile_kernel<HS, BF16>, grid, kBiTileThreads, BiTile<HS>::kBytes, BiTile<HS>::kBytes, s, a,
+  return launch_clusters(biased_tile_kernel<HS, BF16>, grid, bi_threads(HS), BiTile<HS>::kBytes, BiTile<HS>::kBytes, s, a,
                          tq, tk, tv, seg, sub_rows);
 }
