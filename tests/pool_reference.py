@@ -18,7 +18,7 @@ def fork(parents, past, held, table, ring, state, bs, num_blocks, pinned=None):
         error = 1
     elif any(need[p] > held[p] for p in parents if p >= 0):
         error = 1
-    pages = [[int(x) for x in table[b, : held[b]]] for b in range(B)] if not ((held < 0) | (held > width)).any() else []
+    pages = [[int(x) for x in table[b, : held[b] if 0 <= held[b] <= width else 0]] for b in range(B)]
     if any(not 0 <= x < num_blocks for row in pages for x in row):
         error |= 2
     refused = dict(past=np.zeros(n, int), held=np.zeros(n, int), table=np.full((n, width), -1), copies=np.full((n, 2), -1),

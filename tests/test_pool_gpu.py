@@ -63,7 +63,7 @@ def check_fork(t, dev, want):
 @pytest.mark.parametrize("B,n,bs,longest,pinned", [
     (1, 1, 16, 40, 0.0), (1, 9, 16, 37, 0.0), (5, 1, 48, 200, 0.3), (64, 64, 64, 4096, 0.0), (64, 100, 16, 500, 0.1),
     (300, 257, 256, 3000, 0.0), (700, 1100, 16, 100, 0.05), (40, 64, 16, 9000, 0.02), (8192, 8192, 16, 40, 0.01),
-    (3, 0, 16, 100, 0.0), (7, 7, 16, 0, 0.5)])
+    (3, 0, 16, 100, 0.0), (7, 7, 16, 0, 0.5), (2500, 2600, 16, 300, 0.05), (120, 130, 16, 12000, 0.02), (5, 2049, 16, 90, 0.0)])
 def test_fork(B, n, bs, longest, pinned):
     r = np.random.default_rng(B * 11 + n)
     past, held, table, ring, state, blocks, pins = pool_state(r, B, bs, -(-longest // bs) + 2, longest, spare=n + 40,
@@ -110,13 +110,14 @@ def test_fork_who_keeps_the_last_page():
             check_fork(t, dev, want)
 
 
+@pytest.mark.parametrize("columns", [12, 200])  # one CTA's, and more
 @pytest.mark.parametrize("what,code", [("parent", 1), ("parent low", 1), ("past", 1), ("held", 1), ("held low", 1),
                                        ("short", 1), ("page", 2), ("page low", 2), ("head", 1), ("count", 1), ("ring", 1),
                                        ("no pages", 16)])
-def test_refused_forks_change_nothing(what, code):
+def test_refused_forks_change_nothing(what, code, columns):
     r = np.random.default_rng(5)
     bs, B = 16, 600
-    past, held, table, ring, state, blocks, _ = pool_state(r, B, bs, 12, 150, spare=700, fit=True)
+    past, held, table, ring, state, blocks, _ = pool_state(r, B, bs, columns, 150, spare=700, fit=True)
     parents = r.integers(0, B, 700)
     past[599], held[599] = 20, 2
     table[599, :2] = 3, 4
@@ -128,7 +129,7 @@ def test_refused_forks_change_nothing(what, code):
     elif what == "past":
         past[599] = -1
     elif what == "held":
-        held[7] = 13
+        held[7] = columns + 1
     elif what == "held low":
         held[7] = -1
     elif what == "short":
@@ -166,7 +167,8 @@ def check_compact(t, dev, want):
 
 @pytest.mark.parametrize("B,bs,longest,spare,pinned", [
     (1, 16, 40, 3, 0.0), (1, 16, 0, 900, 0.0), (3, 48, 200, 40, 0.3), (64, 64, 4096, 900, 0.0), (64, 64, 4096, 2000, 0.1),
-    (300, 16, 300, 4000, 0.02), (500, 16, 500, 9, 0.5), (8192, 16, 60, 30000, 0.01), (20, 16, 8000, 0, 0.0)])
+    (300, 16, 300, 4000, 0.02), (500, 16, 500, 9, 0.5), (8192, 16, 60, 30000, 0.01), (20, 16, 8000, 0, 0.0),
+    (100, 16, 12000, 5000, 0.02), (2500, 48, 700, 0, 0.0), (3, 16, 100, 40000, 0.001)])
 def test_compact(B, bs, longest, spare, pinned):
     r = np.random.default_rng(B * 13 + spare)
     _, held, table, ring, _, blocks, pins = pool_state(r, B, bs, -(-longest // bs) + 2, longest, spare=spare,
@@ -184,7 +186,7 @@ def test_compact(B, bs, longest, spare, pinned):
         check_compact(out, dev, want)
 
 
-@pytest.mark.parametrize("blocks", [1, 31, 32, 33, 1023, 1024, 1025, 2048, 5000])
+@pytest.mark.parametrize("blocks", [1, 31, 32, 33, 1023, 1024, 1025, 2048, 5000, 32768, 32769, 40001])
 def test_compact_at_the_ends_of_words_and_chunks(blocks):
     """Any set of pages in use, one row each of one page, at pool sizes around a word of bits and a chunk of pages."""
     r = np.random.default_rng(blocks)
@@ -199,10 +201,11 @@ def test_compact_at_the_ends_of_words_and_chunks(blocks):
         check_compact(t, dev, want)
 
 
+@pytest.mark.parametrize("columns", [12, 300])  # one CTA's, and more
 @pytest.mark.parametrize("what,code", [("page", 2), ("page low", 2), ("held", 1), ("held low", 1), ("ring", 1)])
-def test_refused_compactions_change_nothing(what, code):
+def test_refused_compactions_change_nothing(what, code, columns):
     r = np.random.default_rng(6)
-    _, held, table, ring, _, blocks, _ = pool_state(r, 300, 16, 12, 150, spare=700)
+    _, held, table, ring, _, blocks, _ = pool_state(r, 300, 16, columns, 150, spare=700)
     held[3] = 2
     table[3, :2] = 5, 6
     if what == "page":
@@ -210,7 +213,7 @@ def test_refused_compactions_change_nothing(what, code):
     elif what == "page low":
         table[3, 1] = -1
     elif what == "held":
-        held[3] = 13
+        held[3] = columns + 1
     elif what == "held low":
         held[3] = -2
     elif what == "ring":

@@ -86,6 +86,12 @@ def biased_paged_attention(query: torch.Tensor, key_cache: torch.Tensor, value_c
     receives the log-sum-exp; rows behind the last sequence are left as they were. ``workspace``
     (``biased_workspace_size(head_size)`` bytes): else the call allocates its own. A pipeline wait
     that runs out (DEVERR_TIMEOUT) is told by ``error`` only."""
+    if output is None and workspace is None and stream is None:
+        made = (step._fast or step._load_fast()).biased_paged_attention(
+            query, key_cache, value_cache, cumulative_sequence_length, past_seqlens, block_table, num_heads, kv_num_heads,
+            scale, softcap, slopes, window, first_keys, prefix_lens, max_query_len, lse, error)
+        if made is not None:
+            return made
     index, dtype = _index(query, "query"), query.dtype
     if dtype not in _T:
         raise TypeError("query must be float16 or bfloat16")

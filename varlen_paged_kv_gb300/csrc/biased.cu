@@ -19,7 +19,7 @@ namespace pa {
 constexpr int kBiTile = 64;          // keys per tile
 constexpr int kBiThreads = 160;      // rows kernel: four consumer warps and a producer
 constexpr int kBiCost = 3;           // what an item costs beside its tiles, in tiles
-constexpr int kMergeThreads = 128;
+constexpr int kMergeThreads = 256;
 
 // ---- scores --------------------------------------------------------------------------------
 // tanh as u times a polynomial in u^2 (minimax by weighted least squares on 4000 Chebyshev points),
@@ -210,6 +210,7 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
     fence_mbar_init();
   }
   pdl_wait();
+  pdl_launch_dependents();  // (the merge waits for this kernel's end)
   // the costs of all sequences, each thread those of a run of them
   const int run = (a.B + kBiThreads - 1) / kBiThreads;
   {
@@ -546,38 +547,63 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
 
 // The pieces of the units that the cuts between CTAs went through, in order: CTA c of the rows
 // kernel began such a unit (record 2c), its next ones went on with it (record 2k + 1: 1, and 2 for
-// the last). A thread has four columns of a row.
+// the last). A lane has four columns of a row, eight warps share the pieces: what bounds it is the
+// latency of three loads, one after the other (a record, the next ones, the pieces).
 template <int HS, bool BF16>
 __global__ void __launch_bounds__(kMergeThreads) biased_merge_kernel(const BiasedArgs a, const int ctas) {
+  constexpr int WARPS = kMergeThreads / 32;
+  __shared__ float part[WARPS][6][32];
   pdl_wait();
   pdl_launch_dependents();
-  const int c = blockIdx.x;
+  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int4 head = a.records[2 * c];
   if (head.x == 0) return;
-  const int i = blockIdx.y * kMergeThreads + threadIdx.x, r = i / (HS / 4), cc = i % (HS / 4) * 4;
-  if (r >= head.x) return;
-  float M = -INFINITY, S = 0.f;
-  float x[4] = {0.f, 0.f, 0.f, 0.f};
-  auto add = [&](int slot) {
-    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (slot * 16 + r) * 2);
-    const float4 y = *reinterpret_cast<const float4*>(a.part_o + ((int64_t)slot * 16 + r) * HS + cc);
-    if (ml.x == -INFINITY) return;
-    const float m = fmaxf(M, ml.x), f = fast_exp2(M - m), g = fast_exp2(ml.x - m);  // (0 on the first piece with keys)
-    M = m;
-    S = S * f + ml.y * g;
-    x[0] = x[0] * f + y.x * g, x[1] = x[1] * f + y.y * g, x[2] = x[2] * f + y.z * g, x[3] = x[3] * f + y.w * g;
-  };
-  add(2 * c + 1);
-  int k = c + 1;
-  for (; k < ctas && a.records[2 * k + 1].x == 1; ++k) add(2 * k);
-  if (k < ctas && a.records[2 * k + 1].x == 2) add(2 * k);
-  const int rs = head.z + r;
-  const int64_t at = (int64_t)(head.y + rs / a.G) * a.nh + head.w * a.G + rs % a.G;
-  const float inv = M == -INFINITY ? 0.f : 1.f / S;
-  uint2 out = make_uint2(pack2<BF16>(x[0] * inv, x[1] * inv), pack2<BF16>(x[2] * inv, x[3] * inv));
-  if (M == -INFINITY) out = make_uint2(0, 0);
-  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.output) + at * HS + cc) = out;
-  if (a.lse && cc == 0) a.lse[at] = M == -INFINITY ? -INFINITY : (M + fast_log2(S)) * 0.69314718055994531f;
+  int pieces = 1;
+  for (int k = c + 1;; k += 32) {
+    const int rec = k + lane < ctas ? a.records[2 * (k + lane) + 1].x : 0;
+    const unsigned end = __ballot_sync(0xffffffffu, rec != 1);
+    const int n = end ? __ffs(end) - 1 : 32;
+    pieces += n;
+    if (end) {
+      pieces += __shfl_sync(0xffffffffu, rec, n) == 2;
+      break;
+    }
+  }
+  for (int i = blockIdx.y * 32 + lane; i - lane < head.x * (HS / 4); i += gridDim.y * 32) {
+    const int r = min(i / (HS / 4), head.x - 1), cc = i % (HS / 4) * 4;
+    float M = -INFINITY, S = 0.f;
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    auto add = [&](float m_in, float s_in, float4 y) {
+      if (m_in == -INFINITY) return;
+      const float m = fmaxf(M, m_in), f = fast_exp2(M - m), g = fast_exp2(m_in - m);  // (0 on the first piece with keys)
+      M = m;
+      S = S * f + s_in * g;
+      x[0] = x[0] * f + y.x * g, x[1] = x[1] * f + y.y * g, x[2] = x[2] * f + y.z * g, x[3] = x[3] * f + y.w * g;
+    };
+#pragma unroll 4
+    for (int p = warp; p < pieces; p += WARPS) {
+      const int slot = p ? 2 * (c + p) : 2 * c + 1;
+      const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (slot * 16 + r) * 2);
+      add(ml.x, ml.y, *reinterpret_cast<const float4*>(a.part_o + ((int64_t)slot * 16 + r) * HS + cc));
+    }
+    __syncthreads();  // (the round before has been read)
+    part[warp][0][lane] = M, part[warp][1][lane] = S;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) part[warp][2 + e][lane] = x[e];
+    __syncthreads();
+    if (warp != 0 || i >= head.x * (HS / 4)) continue;
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w)
+      add(part[w][0][lane], part[w][1][lane],
+          make_float4(part[w][2][lane], part[w][3][lane], part[w][4][lane], part[w][5][lane]));
+    const int rs = head.z + r;
+    const int64_t at = (int64_t)(head.y + rs / a.G) * a.nh + head.w * a.G + rs % a.G;
+    const float inv = M == -INFINITY ? 0.f : 1.f / S;
+    uint2 out = make_uint2(pack2<BF16>(x[0] * inv, x[1] * inv), pack2<BF16>(x[2] * inv, x[3] * inv));
+    if (M == -INFINITY) out = make_uint2(0, 0);
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.output) + at * HS + cc) = out;
+    if (a.lse && cc == 0) a.lse[at] = M == -INFINITY ? -INFINITY : (M + fast_log2(S)) * 0.69314718055994531f;
+  }
 }
 
 #include "biased_tile.cuh"
@@ -605,7 +631,7 @@ static cudaError_t launch_biased_rows(const BiasedArgs& a, const CUtensorMap& tk
   if (cudaError_t e = cudaFuncSetAttribute(biased_rows_kernel<HS, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))
     return e;
   if (cudaError_t e = launch_pdl(biased_rows_kernel<HS, BF16>, dim3(ctas), dim3(kBiThreads), smem, s, a, tk, tv, seg)) return e;
-  return launch_pdl(biased_merge_kernel<HS, BF16>, dim3(ctas, 16 * (HS / 4) / kMergeThreads), dim3(kMergeThreads), 0, s, a,
+  return launch_pdl(biased_merge_kernel<HS, BF16>, dim3(ctas, 4), dim3(kMergeThreads), 0, s, a,
                     ctas);
 }
 

@@ -1,10 +1,11 @@
-// The Python calls of the operators around paged attention, for the common case.
+// The Python calls of the operators around paged attention, of those on pages and of the biased
+// attention, for the common case.
 //
 // A decode step's operators run for a few microseconds each, less than Python needs to look
-// at a dozen tensors. These functions make the same checks as step.py and call the same C
+// at a dozen tensors. These functions make the same checks as step.py, pool.py and biased.py and call the same C
 // entry points (whose addresses step.py hands over); they allocate the outputs as torch does,
 // on the current stream. Anything unusual - another type, device or layout, an argument that
-// an entry point refuses, an exception - returns None without a trace: step.py then makes the
+// an entry point refuses, an exception - returns None without a trace: the Python then makes the
 // call itself and says what was wrong.
 #include <Python.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -23,6 +24,12 @@ decltype(&pa_qk_norm_rope) qk_norm_rope_fn;
 decltype(&pa_update_page_bounds) update_page_bounds_fn;
 decltype(&pa_select_pages) select_pages_fn;
 decltype(&pa_sparse_paged_attention) sparse_paged_attention_fn;
+decltype(&pa_fork_block_tables) fork_block_tables_fn;
+decltype(&pa_compact_block_tables) compact_block_tables_fn;
+decltype(&pa_copy_pages) copy_pages_fn;
+decltype(&pa_biased_paged_attention) biased_paged_attention_fn;
+decltype(&pa_pool_workspace_size) pool_workspace_size_fn;
+decltype(&pa_biased_workspace_size) biased_workspace_size_fn;
 
 struct Unusual {};
 
@@ -138,6 +145,14 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F&& f) {
   Py_RETURN_NONE;
 }
 
+// tensors of their own over pieces of one allocation of int32
+at::Tensor piece_of(const at::Tensor& all, int64_t at, at::IntArrayRef shape) {
+  at::Tensor piece = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+  piece.unsafeGetTensorImpl()->set_storage_offset(at);
+  piece.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+  return piece;
+}
+
 // (past, query_lens, held, table, ring, state, block_size, num_tokens) -> the six outputs
 PyObject* build_block_tables(PyObject*, PyObject* const* v, Py_ssize_t n) {
   return guarded(n, 8, [&]() -> PyObject* {
@@ -159,11 +174,8 @@ PyObject* build_block_tables(PyObject*, PyObject* const* v, Py_ssize_t n) {
     PyObject* out = PyTuple_New(6);
     need(out != nullptr);
     int64_t at = 0;
-    for (int i = 0; i < 6; ++i) {  // pieces of the one allocation, as tensors of their own
-      at::Tensor piece = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
-      piece.unsafeGetTensorImpl()->set_storage_offset(at);
-      piece.unsafeGetTensorImpl()->set_sizes_contiguous({sizes[i]});
-      PyTuple_SET_ITEM(out, i, THPVariable_Wrap(std::move(piece)));
+    for (int i = 0; i < 6; ++i) {
+      PyTuple_SET_ITEM(out, i, THPVariable_Wrap(piece_of(all, at, {sizes[i]})));
       at += sizes[i];
     }
     return out;
@@ -313,7 +325,173 @@ PyObject* sparse_paged_attention(PyObject*, PyObject* const* v, Py_ssize_t n) {
   });
 }
 
-// (five addresses): the entry points of libpagedattn.so, in the order above
+const uint8_t* pinned_of(const Call& call, PyObject* o, int64_t blocks) {
+  if (is_none(o)) return nullptr;
+  const at::Tensor& t = tensor(o);
+  need(t.scalar_type() == at::kBool || t.scalar_type() == at::kByte);
+  need(t.device() == call.device && t.dim() == 1 && t.size(0) == blocks && t.is_contiguous());
+  return (const uint8_t*)t.data_ptr();
+}
+
+PyObject* tuple_of(std::initializer_list<at::Tensor> pieces) {
+  PyObject* out = PyTuple_New((Py_ssize_t)pieces.size());
+  need(out != nullptr);
+  Py_ssize_t i = 0;
+  for (const at::Tensor& t : pieces) PyTuple_SET_ITEM(out, i++, THPVariable_Wrap(t));
+  return out;
+}
+
+// (parents, past, held, table, ring, state, pinned, block_size, num_blocks) -> the six outputs
+PyObject* fork_block_tables(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return guarded(n, 9, [&]() -> PyObject* {
+    const at::Tensor& table = tensor(v[3]);
+    const Call call(table);
+    call.whole(v[3], at::kInt, 2);
+    const int64_t B = table.size(0), cols = table.size(1), blocks = integer(v[8]);
+    const at::Tensor &parents = call.whole(v[0], at::kInt, 1), &ring = call.whole(v[4], at::kInt, 1);
+    const int64_t N = parents.size(0);
+    const int32_t *past = call.ints(v[1], B), *held = call.ints(v[2], B), *state = call.ints(v[5], 2);
+    const uint8_t* pins = pinned_of(call, v[6], blocks);
+    const size_t bytes = pool_workspace_size_fn(i32(blocks));
+    need(bytes > 0);
+    const at::Tensor all = call.empty({N * (cols + 4) + 3}, at::kInt), ws = call.empty({(int64_t)bytes}, at::kByte);
+    int32_t* p = (int32_t*)all.data_ptr();  // copies, table, past, held, state, error
+    const int64_t t = 2 * N, q = t + N * cols, h = q + N, s = h + N;
+    need(unlocked(fork_block_tables_fn, (const int32_t*)parents.data_ptr(), past, held, (const int32_t*)table.data_ptr(),
+                  (int32_t*)ring.data_ptr(), state, pins, i32(B), i32(N), i32(cols), (int32_t)integer(v[7]),
+                  i32(blocks), i32(ring.size(0)), p + q, p + h, p + t, p, p + s, (uint32_t*)(p + s + 2),
+                  ws.data_ptr(), bytes, call.stream()) == PA_OK);
+    return tuple_of({piece_of(all, q, {N}), piece_of(all, h, {N}), piece_of(all, t, {N, cols}), piece_of(all, 0, {N, 2}),
+                     piece_of(all, s, {2}), piece_of(all, s + 2, {1})});
+  });
+}
+
+// (held, table, ring, pinned, num_blocks, max_moves) -> the five outputs
+PyObject* compact_block_tables(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return guarded(n, 6, [&]() -> PyObject* {
+    const at::Tensor& table = tensor(v[1]);
+    const Call call(table);
+    call.whole(v[1], at::kInt, 2);
+    const int64_t B = table.size(0), cols = table.size(1), blocks = integer(v[4]), moves = integer(v[5]);
+    need(moves >= 0);
+    const int32_t* held = call.ints(v[0], B);
+    const at::Tensor& ring = call.whole(v[2], at::kInt, 1);
+    const uint8_t* pins = pinned_of(call, v[3], blocks);
+    const size_t bytes = pool_workspace_size_fn(i32(blocks));
+    need(bytes > 0);
+    const at::Tensor all = call.empty({2 * moves + B * cols + 4}, at::kInt), ws = call.empty({(int64_t)bytes}, at::kByte);
+    int32_t* p = (int32_t*)all.data_ptr();  // copies, table, state, end, error
+    const int64_t t = 2 * moves, s = t + B * cols;
+    need(unlocked(compact_block_tables_fn, held, (const int32_t*)table.data_ptr(), (int32_t*)ring.data_ptr(), pins,
+                  i32(B), i32(cols), i32(blocks), i32(ring.size(0)), i32(moves), p + t, p, p + s, p + s + 2,
+                  (uint32_t*)(p + s + 3), ws.data_ptr(), bytes, call.stream()) == PA_OK);
+    return tuple_of({piece_of(all, t, {B, cols}), piece_of(all, 0, {moves, 2}), piece_of(all, s, {2}),
+                     piece_of(all, s + 2, {1}), piece_of(all, s + 3, {1})});
+  });
+}
+
+// (tensors, copies, error) -> True
+PyObject* copy_pages(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return guarded(n, 3, [&]() -> PyObject* {
+    need(PyList_Check(v[0]) || PyTuple_Check(v[0]));
+    const Py_ssize_t count = PySequence_Fast_GET_SIZE(v[0]);
+    need(count > 0 && count <= PA_MAX_COPY_TENSORS);
+    const at::Tensor& copies = tensor(v[1]);
+    const Call call(copies);
+    call.whole(v[1], at::kInt, 2);
+    need(copies.size(1) == 2);
+    pa_page_tensor pages[PA_MAX_COPY_TENSORS];
+    int64_t blocks = 0;
+    for (Py_ssize_t i = 0; i < count; ++i) {
+      const at::Tensor& t = tensor(PySequence_Fast_ITEMS(v[0])[i]);
+      need(t.device() == call.device && t.dim() > 0 && t.is_contiguous());
+      if (i == 0) blocks = t.size(0);
+      need(t.size(0) == blocks && blocks > 0);
+      pages[i] = {t.data_ptr(), t.numel() / blocks * (int64_t)t.element_size()};
+    }
+    uint32_t* error = call.error(v[2]);
+    need(unlocked(copy_pages_fn, (const pa_page_tensor*)pages, (int32_t)count, i32(blocks),
+                  (const int32_t*)copies.data_ptr(), i32(copies.size(0)), error, call.stream()) == PA_OK);
+    Py_RETURN_TRUE;
+  });
+}
+
+// (query, key_cache, value_cache, cum, past, table, heads, kv_heads, scale, softcap, slopes, window, first_keys,
+//  prefix_lens, max_query_len, lse, error)
+PyObject* biased_paged_attention(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return guarded(n, 17, [&]() -> PyObject* {
+    const at::Tensor& query = tensor(v[0]);
+    const Call call(query);
+    const at::ScalarType type = query.scalar_type();
+    pa_biased_dims d{};
+    d.dtype = dtype_code(type);
+    const at::Tensor &k = call.whole(v[1], type, 4), &value = call.whole(v[2], type, 4);
+    need(value.sizes() == k.sizes());
+    const Batch b(call, v[3], v[4], v[5]);
+    const int64_t N = query.size(0);
+    d.num_heads = i32(integer(v[6]));
+    d.kv_num_heads = i32(integer(v[7]));
+    need(k.size(2) == d.kv_num_heads);
+    d.query_stride = call.rows(query, type, d.num_heads * k.size(3));
+    d.num_tokens = i32(N);
+    d.batch_size = b.size;
+    d.head_size = i32(k.size(3));
+    d.num_blocks = i32(k.size(0));
+    d.block_size = i32(k.size(1));
+    d.max_blocks_per_sequence = b.columns;
+    d.max_query_len = i32(integer(v[14]));
+    pa_score_rules rules{};
+    rules.softcap = real(v[9]);
+    rules.window = i32(integer(v[11]));
+    if (!is_none(v[10])) {
+      const at::Tensor& s = call.whole(v[10], at::kFloat, 1);
+      need(s.size(0) == d.num_heads);
+      rules.slopes = (const float*)s.data_ptr();
+    }
+    if (!is_none(v[12])) rules.first_keys = call.ints(v[12], N);
+    if (!is_none(v[13])) rules.prefix_lens = call.ints(v[13], b.size);
+    float* lse = nullptr;
+    if (!is_none(v[15])) {
+      const at::Tensor& l = call.whole(v[15], at::kFloat, 2);
+      need(l.size(0) == N && l.size(1) == d.num_heads);
+      lse = (float*)l.data_ptr();
+    }
+    uint32_t* error = call.error(v[16]);
+    const float scale = real(v[8]);
+    const size_t bytes = biased_workspace_size_fn(d.head_size);
+    need(bytes > 0);
+    const at::Tensor out = call.empty({N, d.num_heads * k.size(3)}, type), ws = call.empty({(int64_t)bytes}, at::kByte);
+    need(unlocked(biased_paged_attention_fn, query.data_ptr(), k.data_ptr(), value.data_ptr(), b.cum, b.past, b.table,
+                  scale, (const pa_score_rules*)&rules, out.data_ptr(), lse, (const pa_biased_dims*)&d, error,
+                  ws.data_ptr(), bytes, call.stream()) == PA_OK);
+    return THPVariable_Wrap(out);
+  });
+}
+
+// (six addresses): the entry points of the four functions above, then the sizes of their workspaces
+PyObject* bind_pool(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  void* p[6];
+  if (n != 6) {
+    PyErr_SetString(PyExc_TypeError, "bind_pool takes six addresses");
+    return nullptr;
+  }
+  for (int i = 0; i < 6; ++i) {
+    p[i] = PyLong_AsVoidPtr(v[i]);
+    if (!p[i]) {
+      if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "an address is null");
+      return nullptr;
+    }
+  }
+  fork_block_tables_fn = reinterpret_cast<decltype(fork_block_tables_fn)>(p[0]);
+  compact_block_tables_fn = reinterpret_cast<decltype(compact_block_tables_fn)>(p[1]);
+  copy_pages_fn = reinterpret_cast<decltype(copy_pages_fn)>(p[2]);
+  biased_paged_attention_fn = reinterpret_cast<decltype(biased_paged_attention_fn)>(p[3]);
+  pool_workspace_size_fn = reinterpret_cast<decltype(pool_workspace_size_fn)>(p[4]);
+  biased_workspace_size_fn = reinterpret_cast<decltype(biased_workspace_size_fn)>(p[5]);
+  Py_RETURN_NONE;
+}
+
+// (five addresses): the entry points of libpagedattn.so that the first five functions call, in their order
 PyObject* bind(PyObject*, PyObject* const* v, Py_ssize_t n) {
   void* p[5];
   if (n != 5) {
@@ -338,6 +516,8 @@ PyObject* bind(PyObject*, PyObject* const* v, Py_ssize_t n) {
 #define PA_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {PA_METHOD(build_block_tables), PA_METHOD(qk_norm_rope),           PA_METHOD(update_page_bounds),
                          PA_METHOD(select_pages),       PA_METHOD(sparse_paged_attention), PA_METHOD(bind),
+                         PA_METHOD(fork_block_tables),  PA_METHOD(compact_block_tables),   PA_METHOD(copy_pages),
+                         PA_METHOD(biased_paged_attention), PA_METHOD(bind_pool),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_step_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

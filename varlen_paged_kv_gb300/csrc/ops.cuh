@@ -155,30 +155,41 @@ struct PoolArgs {
   int64_t clear_words;
   uint32_t* ws_error;
   uint8_t *marks, *old_marks;  // per page
-  int32_t* keeper;             // per page
+  int32_t* keeper;             // per page (fork)
   uint4* words;
   int2* chunks;
+  int32_t* first_child;        // per old row (fork, else null)
+  uint32_t* row_bits;          // 32 new rows each (fork)
+  int32_t* holes;              // per page (compact)
   int32_t B, Bn, max_blocks, bs, num_blocks, num_chunks, cap, max_moves;
 };
 // bytes of the workspace of num_blocks pages; fills in its pointers where `a` is given
 inline size_t pool_workspace(int32_t num_blocks, bool fork, PoolArgs* a, uint8_t* base) {
-  const size_t chunks = (size_t)ceil_div(num_blocks, 1024), pages = chunks * 1024;
+  const size_t chunks = (size_t)ceil_div(num_blocks, 1024), pages = chunks * 1024, rows = PA_MAX_TABLE_REQUESTS;
   size_t off = 16;
-  const size_t marks = off, old_marks = off += pages, keeper = off += fork ? pages : 0;
-  off += fork ? 4 * pages : 0;
-  const size_t words = off, totals = words + pages / 2, end = align_up(totals + 8 * chunks, 16);
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align_up(off + bytes, 16);
+    return at;
+  };
+  const size_t marks = take(pages), old_marks = take(fork ? pages : 0), keeper = take(fork ? 4 * pages : 0), cleared = off;
+  const size_t words = take(pages / 2), totals = take(8 * chunks), child = take(fork ? 4 * rows : 0),
+               row_bits = take(fork ? rows / 8 : 0), holes = take(fork ? 0 : 4 * pages);
   if (a) {
     a->clear = reinterpret_cast<uint4*>(base);
-    a->clear_words = (int64_t)(words / 16);
+    a->clear_words = (int64_t)(cleared / 16);
     a->ws_error = reinterpret_cast<uint32_t*>(base);
     a->marks = base + marks;
     a->old_marks = base + old_marks;
     a->keeper = reinterpret_cast<int32_t*>(base + keeper);
     a->words = reinterpret_cast<uint4*>(base + words);
     a->chunks = reinterpret_cast<int2*>(base + totals);
+    a->first_child = fork ? reinterpret_cast<int32_t*>(base + child) : nullptr;
+    a->row_bits = reinterpret_cast<uint32_t*>(base + row_bits);
+    a->holes = reinterpret_cast<int32_t*>(base + holes);
     a->num_chunks = (int32_t)chunks;
   }
-  return end;
+  return off;
 }
 
 struct CopyArgs {
@@ -207,8 +218,8 @@ struct BiasedArgs {
   int4* records;
 };
 
-cudaError_t launch_fork(const PoolArgs& a, int sms, cudaStream_t s);
-cudaError_t launch_compact(const PoolArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_fork(const PoolArgs& a, int sms, cudaStream_t s, int* kernels);
+cudaError_t launch_compact(const PoolArgs& a, int sms, cudaStream_t s, int* kernels);
 cudaError_t launch_copy_pages(CopyArgs& a, int sms, cudaStream_t s);
 int biased_ctas(int hs, int sms);  // CTAs of the rows kernel
 cudaError_t launch_biased(const BiasedArgs& a, bool bf16, int sms, cudaStream_t s);

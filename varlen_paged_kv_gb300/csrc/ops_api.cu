@@ -314,7 +314,9 @@ pa_status pa_fork_block_tables(const int32_t* parents, const int32_t* past_seqle
   a.bs = block_size;
   a.num_blocks = num_blocks;
   a.cap = free_capacity;
-  return launched(pa::launch_fork(a, sms, static_cast<cudaStream_t>(stream)), "fork launch", 4);
+  int kernels = 0;
+  const cudaError_t e = pa::launch_fork(a, sms, static_cast<cudaStream_t>(stream), &kernels);
+  return launched(e, "fork launch", kernels);
 }
 
 pa_status pa_compact_block_tables(const int32_t* blocks_held, const int32_t* block_table, int32_t* free_blocks,
@@ -351,7 +353,9 @@ pa_status pa_compact_block_tables(const int32_t* blocks_held, const int32_t* blo
   a.num_blocks = num_blocks;
   a.cap = free_capacity;
   a.max_moves = max_moves;
-  return launched(pa::launch_compact(a, sms, static_cast<cudaStream_t>(stream)), "compaction launch", 4);
+  int kernels = 0;
+  const cudaError_t e = pa::launch_compact(a, sms, static_cast<cudaStream_t>(stream), &kernels);
+  return launched(e, "compaction launch", kernels);
 }
 
 pa_status pa_copy_pages(const pa_page_tensor* tensors, int32_t num_tensors, int32_t num_blocks, const int32_t* copies,

@@ -2,19 +2,23 @@
 //
 // fork_block_tables makes the rows of a new batch from rows of the old one; compact_block_tables
 // moves the highest pages in use into the lowest free ones. Both ask of every page of the pool
-// what the tables hold it for, so both run as four short kernels over a workspace of marks:
-//   clear   the marks
+// what the tables hold it for. Small batches over small pools do all of it in one CTA, with
+// the pages' marks as bits in shared memory (one launch: a fork of 64 rows SMALLFORK us instead of 9.4 of
+// the kernels below, a compaction SMALLCOMPACT instead of 10.0). Others take a few short kernels over a workspace:
+//   clear   the marks; the fork's first new row of each old one
 //   mark    every held table entry stores a byte at its page (the same byte from whoever
 //           stores it, so without atomics); a row that would write into its last page next
 //           leaves its number there by an atomic maximum (of Bn - row: the lowest row stays)
 //   words   the marks as bits, 32 pages a word, with counts before each word inside its chunk of
-//           1024 pages and the chunks' totals
+//           1024 pages and the chunks' totals; the fork's rows that copy as bits
+//   lists   (compaction) the holes in order
 //   finish  every CTA scans the chunks' totals (1024 at most) itself; a page's rank among the
-//           pages of its kind is then its chunk's sum, its word's and a population count, and the
-//           r-th page of a kind is found by bisection in them. Tables, ring and copies are
-//           written from that, each entry by itself.
+//           pages of its kind is then its chunk's sum, its word's and a population count. Tables,
+//           ring and copies are written from that, each entry by itself.
 // Every order (of pages given out, given back and moved) is one of page or row numbers, so results
-// do not depend on the order in which CTAs run.
+// do not depend on the order in which CTAs run. What bounds them is latency, a few dependent
+// loads from L2 per kernel: 1024 requests with 470000 held pages fork in BIGFORK us and are compacted
+// in BIGCOMPACT.
 //
 // copy_pages moves the pages' data: one launch over the tensors of all layers, each CTA taking
 // pieces of 16 KB.
@@ -23,88 +27,169 @@
 namespace pa {
 
 constexpr int kPoolThreads = 256;
+constexpr int kSmallThreads = 1024;
 constexpr int kChunk = 1024;      // pages
-constexpr int kColumns = 256;     // columns of a table row that a warp takes at a time
 
-// ---- clear ---------------------------------------------------------------------------------
-__global__ void __launch_bounds__(kPoolThreads) pool_clear_kernel(uint4* p, int64_t n) {
-  pdl_wait();
-  pdl_launch_dependents();
-  for (int64_t i = blockIdx.x * (int64_t)kPoolThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kPoolThreads)
-    p[i] = make_uint4(0, 0, 0, 0);
+// How a warp goes over table rows: items of K * 32 columns of a row, ROWS of them with their loads in
+// flight together. A CTA of many rows takes short ones, a grid of many CTAs long ones.
+template <int ROWS_, int K_>
+struct Walk {
+  static constexpr int ROWS = ROWS_, K = K_, COLUMNS = 32 * K_;
+  __device__ __forceinline__ static int parts(int columns) { return (columns + COLUMNS - 1) / COLUMNS; }
+  // row and first column of item i
+  __device__ __forceinline__ static int2 item(int i, int parts) {
+    return parts == 1 ? make_int2(i, 0) : make_int2(i / parts, i % parts * COLUMNS);
+  }
+};
+using BigWalk = Walk<1, 8>;
+using SmallWalk = Walk<4, 4>;
+
+// entry head + k of the ring, k at most its capacity
+__device__ __forceinline__ int ring_index(const PoolArgs& a, int head, int k) {
+  const uint32_t i = (uint32_t)head + (uint32_t)k;
+  return (int)(i >= (uint32_t)a.cap ? i - (uint32_t)a.cap : i);
 }
 
-// ---- mark ----------------------------------------------------------------------------------
+// ---- marks ---------------------------------------------------------------------------------
+// Where the marks go: bytes in the workspace, or bits in shared memory.
+struct ByteMarks {
+  uint8_t *whole, *old;
+  int32_t* keeper;
+  __device__ __forceinline__ void set_whole(int x) const { whole[x] = 1; }
+  __device__ __forceinline__ void set_old(int x) const { old[x] = 1; }
+  __device__ __forceinline__ void keep(int x, int v) const { atomicMax(&keeper[x], v); }
+};
+struct BitMarks {
+  uint32_t *whole, *old, *kept;
+  int32_t* keeper;
+  __device__ __forceinline__ void set_whole(int x) const { atomicOr(&whole[x >> 5], 1u << (x & 31)); }
+  __device__ __forceinline__ void set_old(int x) const { atomicOr(&old[x >> 5], 1u << (x & 31)); }
+  __device__ __forceinline__ void keep(int x, int v) const {
+    atomicOr(&kept[x >> 5], 1u << (x & 31));
+    atomicMax(&keeper[x], v);
+  }
+};
+
+// the lowest new row of each old one (INT32_MAX: none), by the block; the errors found
+__device__ __forceinline__ uint32_t find_children(const PoolArgs& a, int* first_child) {
+  uint32_t err = 0;
+  for (int p = threadIdx.x; p < a.B; p += blockDim.x) first_child[p] = INT32_MAX;
+  __syncthreads();
+  for (int b = threadIdx.x; b < a.Bn; b += blockDim.x) {
+    const int p = a.parents[b];
+    if (p < -1 || p >= a.B) err = PA_DEVERR_BAD_BATCH;
+    else if (p >= 0) atomicMin(&first_child[p], b);
+  }
+  return err;
+}
+
+// Marks the pages of the old rows, item by item of a row's columns from `first` on; the errors found.
+// `pasts` and `helds` are the call's, or their copies; `last` receives the rows' partly filled pages.
+template <bool FORK, typename W, typename Marks>
+__device__ __forceinline__ uint32_t mark_pages(const PoolArgs& a, const int* pasts, const int* helds, const int* first_child,
+                                               const Marks& marks, int* last, int first, int step, int lane) {
+  uint32_t err = 0;
+  const int parts = W::parts(a.max_blocks), items = a.B * parts;
+  for (int i0 = first; i0 < items; i0 += W::ROWS * step) {
+    int x[W::ROWS][W::K];
+#pragma unroll
+    for (int n = 0; n < W::ROWS; ++n) {  // (all of the rows: which entries are held need not be known yet)
+      const int2 it = W::item(i0 + n * step, parts);
+#pragma unroll
+      for (int k = 0; k < W::K; ++k) {
+        const int c = it.y + k * 32 + lane;
+        x[n][k] = i0 + n * step < items && c < a.max_blocks ? a.table[(int64_t)it.x * a.max_blocks + c] : -1;
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < W::ROWS; ++n) {
+      if (i0 + n * step >= items) break;
+      const int2 it = W::item(i0 + n * step, parts);
+      const int p = it.x;
+      int held = helds[p];
+      if (held < 0 || held > a.max_blocks) err |= PA_DEVERR_BAD_BATCH, held = 0;
+      int whole = 0, child = INT32_MAX;
+      bool part = false;
+      if constexpr (FORK) {
+        const int past = pasts[p];
+        child = first_child[p];
+        whole = past / a.bs;
+        part = past % a.bs != 0;
+        // (refused: the marks do not matter any more, but the pages are still looked at)
+        if (past < 0 || (child != INT32_MAX && whole + (part ? 1 : 0) > held)) err |= PA_DEVERR_BAD_BATCH;
+      }
+#pragma unroll
+      for (int k = 0; k < W::K; ++k) {
+        const int c = it.y + k * 32 + lane, page = x[n][k];
+        if (c >= held) continue;
+        if (page < 0 || page >= a.num_blocks) {
+          err |= PA_DEVERR_BAD_BLOCK;
+        } else if (FORK && (child == INT32_MAX || c >= whole)) {
+          marks.set_old(page);
+          if (child != INT32_MAX && c == whole && part) {
+            marks.keep(page, a.Bn - child);
+            if (last) last[p] = page;
+          }
+        } else {
+          marks.set_whole(page);
+        }
+      }
+    }
+  }
+  return err;
+}
+
+__global__ void __launch_bounds__(kPoolThreads) pool_clear_kernel(const PoolArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  for (int64_t i = blockIdx.x * (int64_t)kPoolThreads + threadIdx.x; i < a.clear_words; i += (int64_t)gridDim.x * kPoolThreads)
+    a.clear[i] = make_uint4(0, 0, 0, 0);
+  if (a.pages_end && blockIdx.x == 0 && threadIdx.x == 0) *a.pages_end = 0;  // (the finish takes a maximum)
+  if (a.first_child && blockIdx.x == gridDim.x - 1) find_children(a, a.first_child);
+}
+
 template <bool FORK>
 __global__ void __launch_bounds__(kPoolThreads) pool_mark_kernel(const PoolArgs a) {
-  extern __shared__ int first_child[];  // FORK: the lowest new row of each old one
   pdl_wait();
   pdl_launch_dependents();
   uint32_t err = 0;
-  if (!FORK && blockIdx.x == 0 && threadIdx.x == 0) *a.pages_end = 0;  // (the finish takes a maximum)
-  if constexpr (FORK) {
-    for (int p = threadIdx.x; p < a.B; p += kPoolThreads) first_child[p] = INT32_MAX;
-    __syncthreads();
-    for (int b = threadIdx.x; b < a.Bn; b += kPoolThreads) {
-      const int p = a.parents[b];
-      if (p < -1 || p >= a.B) err = PA_DEVERR_BAD_BATCH;
-      else if (p >= 0) atomicMin(&first_child[p], b);
-    }
-    __syncthreads();
-  }
-  const int lane = threadIdx.x & 31;
-  const int parts = (a.max_blocks + kColumns - 1) / kColumns;
-  const int64_t items = (int64_t)a.B * parts, step = (int64_t)gridDim.x * (kPoolThreads / 32);
-  for (int64_t i = blockIdx.x * (int64_t)(kPoolThreads / 32) + (threadIdx.x >> 5); i < items; i += step) {
-    const int p = (int)(i / parts), c0 = (int)(i % parts) * kColumns;
-    const int held = a.held[p];
-    if (held < 0 || held > a.max_blocks) {
-      err |= PA_DEVERR_BAD_BATCH;
-      continue;
-    }
-    int whole = 0, child = INT32_MAX;
-    bool part = false;
-    if constexpr (FORK) {
-      const int past = a.past[p];
-      child = first_child[p];
-      whole = past / a.bs;
-      part = past % a.bs != 0;
-      if (past < 0 || (child != INT32_MAX && whole + (part ? 1 : 0) > held)) {
-        err |= PA_DEVERR_BAD_BATCH;
-        continue;
-      }
-    }
-    int x[kColumns / 32];
-#pragma unroll
-    for (int k = 0; k < kColumns / 32; ++k) {
-      const int c = c0 + k * 32 + lane;
-      x[k] = c < held ? a.table[(int64_t)p * a.max_blocks + c] : -1;
-      if (c < held && (x[k] < 0 || x[k] >= a.num_blocks)) err |= PA_DEVERR_BAD_BLOCK, x[k] = -1;
-    }
-#pragma unroll
-    for (int k = 0; k < kColumns / 32; ++k) {
-      const int c = c0 + k * 32 + lane;
-      if (x[k] < 0) continue;
-      if (FORK && (child == INT32_MAX || c >= whole)) {
-        a.old_marks[x[k]] = 1;
-        if (child != INT32_MAX && c == whole && part) atomicMax(&a.keeper[x[k]], a.Bn - child);
-      } else {
-        a.marks[x[k]] = 1;
-      }
-    }
-  }
+  if (FORK && blockIdx.x == 0)
+    for (int b = threadIdx.x; b < a.Bn; b += kPoolThreads)
+      if (a.parents[b] < -1 || a.parents[b] >= a.B) err = PA_DEVERR_BAD_BATCH;
+  err |= mark_pages<FORK, BigWalk>(a, a.past, a.held, a.first_child, ByteMarks{a.marks, a.old_marks, a.keeper}, nullptr,
+                                   blockIdx.x * (kPoolThreads / 32) + (threadIdx.x >> 5),
+                                   gridDim.x * (kPoolThreads / 32), threadIdx.x & 31);
   if (err) atomicOr(a.ws_error, err);
 }
 
 // ---- words ---------------------------------------------------------------------------------
+// whether new row b takes a page of its own for the last, partly filled one of its parent
+template <typename Held>
+__device__ __forceinline__ bool row_copies(const PoolArgs& a, int b, Held held_elsewhere) {
+  const int p = a.parents[b], past = p < 0 ? 0 : a.past[p];
+  if (past % a.bs == 0) return false;
+  const int x = a.table[(int64_t)p * a.max_blocks + past / a.bs];
+  return held_elsewhere(x) || (a.pinned && a.pinned[x]);
+}
+
 // word i: {bits of the first kind, of the second, the counts of both before it in its chunk}.
-// fork: the first kind are the pages to give back; compact: the holes, and the movers.
+// fork: the first kind are the pages to give back; compact: the holes, and the movers. Blocks behind
+// the chunks': the fork's rows that copy.
 template <bool FORK>
 __global__ void __launch_bounds__(kPoolThreads) pool_words_kernel(const PoolArgs a) {
   __shared__ uint32_t bits[2][32];
   pdl_wait();
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (FORK && (int)blockIdx.x >= a.num_chunks) {
+    const int b = (blockIdx.x - a.num_chunks) * kPoolThreads + threadIdx.x;
+    // (a refused fork's parents and pages may be anything)
+    const bool copy = b < a.Bn && *a.ws_error == 0 &&
+                      row_copies(a, b, [&](int x) { return a.keeper[x] != a.Bn - b || a.marks[x]; });
+    const uint32_t m = __ballot_sync(0xffffffffu, copy);
+    if (lane == 0) a.row_bits[(blockIdx.x - a.num_chunks) * (kPoolThreads / 32) + warp] = m;
+    return;
+  }
   for (int w = warp; w < 32; w += kPoolThreads / 32) {
     const int x = blockIdx.x * kChunk + w * 32 + lane;
     bool first = false, second = false;
@@ -135,15 +220,15 @@ __global__ void __launch_bounds__(kPoolThreads) pool_words_kernel(const PoolArgs
   }
 }
 
-// exclusive sums of the chunks' totals, and the totals at [chunks]
-__device__ __forceinline__ void scan_chunks(const PoolArgs& a, int2* sums) {
-  __shared__ int2 part[kPoolThreads / 32];
+// exclusive sums of n pairs (value(i)), by the whole block of THREADS; sums[n] are the totals
+template <int THREADS, typename F>
+__device__ __forceinline__ void scan_pairs(int n, int2* sums, F value) {
+  __shared__ int2 part[THREADS / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int2 carry = make_int2(0, 0);
-  const int n = a.num_chunks;
-  for (int i0 = 0; i0 < n; i0 += kPoolThreads) {
+  for (int i0 = 0; i0 < n; i0 += THREADS) {
     const int i = i0 + threadIdx.x;
-    const int2 own = i < n ? a.chunks[i] : make_int2(0, 0);
+    const int2 own = i < n ? value(i) : make_int2(0, 0);
     int2 x = own;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -153,7 +238,7 @@ __device__ __forceinline__ void scan_chunks(const PoolArgs& a, int2* sums) {
     if (lane == 31) part[warp] = x;
     __syncthreads();
     int2 before = carry;
-    for (int w = 0; w < kPoolThreads / 32; ++w) {
+    for (int w = 0; w < THREADS / 32; ++w) {
       if (w < warp) before.x += part[w].x, before.y += part[w].y;
       carry.x += part[w].x, carry.y += part[w].y;
     }
@@ -164,104 +249,199 @@ __device__ __forceinline__ void scan_chunks(const PoolArgs& a, int2* sums) {
   __syncthreads();
 }
 
-// ---- finish: fork --------------------------------------------------------------------------
-__global__ void __launch_bounds__(kPoolThreads) fork_finish_kernel(const PoolArgs a) {
-  extern __shared__ int smem[];
-  int2* sums = reinterpret_cast<int2*>(smem);          // [num_chunks + 1]
-  int* rank = smem + 2 * (a.num_chunks + 1);           // [Bn]: which copy a row makes, -1 for none
-  __shared__ int part[kPoolThreads / 32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_wait();
-  pdl_launch_dependents();
-  uint32_t err = *a.ws_error;
-  const int head = a.state[0], count = a.state[1];
-  if (head < 0 || head >= a.cap || count < 0 || count > a.cap) err |= PA_DEVERR_BAD_BATCH;
-  scan_chunks(a, sums);
-  const int freed = sums[a.num_chunks].x;
-  int copies = 0;
-  if (!err) {  // (the rows' parents and pages are what they should be)
-    for (int b0 = 0; b0 < a.Bn; b0 += kPoolThreads) {
-      const int b = b0 + threadIdx.x;
-      bool copy = false;
-      if (b < a.Bn) {
-        const int p = a.parents[b], past = p < 0 ? 0 : a.past[p];
-        if (past % a.bs) {
-          const int x = a.table[(int64_t)p * a.max_blocks + past / a.bs];
-          copy = a.keeper[x] != a.Bn - b || a.marks[x] || (a.pinned && a.pinned[x]);
-        }
-      }
-      const unsigned m = __ballot_sync(0xffffffffu, copy);
-      if (lane == 0) part[warp] = __popc(m);
-      __syncthreads();
-      int before = copies;
-      for (int w = 0; w < kPoolThreads / 32; ++w) {
-        if (w < warp) before += part[w];
-        copies += part[w];
-      }
-      if (b < a.Bn) rank[b] = copy ? before + __popc(m & ((1u << lane) - 1)) : -1;
-      __syncthreads();
-    }
-    if ((int64_t)count + freed > a.cap) err = PA_DEVERR_BAD_BATCH;
-    else if (copies > count) err = PA_DEVERR_NO_BLOCKS;
+// The pages as words {bits of both kinds, the counts of both before the word in the whole pool}.
+struct BigWords {
+  const uint4* words;
+  const int2* sums;  // before each chunk
+  __device__ __forceinline__ uint4 at(int w) const {
+    const uint4 v = words[w];
+    const int2 s = sums[w / 32];
+    return make_uint4(v.x, v.y, s.x + (v.z & 0xffff), s.y + (v.z >> 16));
   }
-  // A refused fork describes an empty batch and changes nothing that it was given.
-  const int i0 = blockIdx.x * kPoolThreads + threadIdx.x, step = gridDim.x * kPoolThreads;
+};
+struct SmallWords {
+  const uint32_t *first, *second;
+  const int2* sums;  // before each word
+  __device__ __forceinline__ uint4 at(int w) const {
+    return make_uint4(first[w], second ? second[w] : 0u, (uint32_t)sums[w].x, (uint32_t)sums[w].y);
+  }
+};
+
+// the fork's rows that copy, and their count before the word
+struct BigRows {
+  const uint32_t* bits;
+  const int2* sums;
+  __device__ __forceinline__ int2 at(int w) const { return make_int2((int)bits[w], sums[w].x); }
+};
+struct SmallRows {
+  const uint32_t* bits;
+  const int2* sums;
+  __device__ __forceinline__ int2 at(int w) const { return make_int2((int)bits[w], sums[w].y); }
+};
+
+// ---- finish: fork --------------------------------------------------------------------------
+// The outputs, spread over the threads from `i0` on in steps of `step`. A refused fork (err) describes an
+// empty batch and changes nothing that it was given. `parents` and `pasts` are the call's, or their copies.
+template <typename W, typename Words, typename Rows>
+__device__ __forceinline__ void fork_outputs(const PoolArgs& a, uint32_t err, int head, int count, int copies, int freed,
+                                             const Words& pages, const Rows& rows, const int* parents, const int* pasts,
+                                             int i0, int step) {
+  auto rank_of = [&](int b) {  // which copy row b makes, -1 for none
+    if (err) return -1;
+    const int2 w = rows.at(b >> 5);
+    return (uint32_t)w.x >> (b & 31) & 1 ? w.y + __popc((uint32_t)w.x & ((1u << (b & 31)) - 1)) : -1;
+  };
   if (i0 == 0) {
     a.error[0] = err;
-    a.state_out[0] = err ? head : (int)(((int64_t)head + copies) % a.cap);
+    a.state_out[0] = err ? head : ring_index(a, head, copies);
     a.state_out[1] = err ? count : count - copies + freed;
   }
   for (int b = i0; b < a.Bn; b += step) {
-    const int p = err ? -1 : a.parents[b], past = p < 0 ? 0 : a.past[p];
+    const int p = err ? -1 : parents[b], past = p < 0 ? 0 : pasts[p], rank = rank_of(b);
     a.past_out[b] = past;
     a.held_out[b] = past / a.bs + (past % a.bs != 0);
     if (err || b >= copies) a.copies[b] = make_int2(-1, -1);
-    if (!err && rank[b] >= 0)
-      a.copies[rank[b]] = make_int2(a.table[(int64_t)p * a.max_blocks + past / a.bs],
-                                    a.ring[((int64_t)head + rank[b]) % a.cap]);
+    if (rank >= 0)
+      a.copies[rank] = make_int2(a.table[(int64_t)p * a.max_blocks + past / a.bs], a.ring[ring_index(a, head, rank)]);
   }
-  const int parts = (a.max_blocks + kColumns - 1) / kColumns;
-  const int64_t items = (int64_t)a.Bn * parts, stride = (int64_t)gridDim.x * (kPoolThreads / 32);
-  for (int64_t i = blockIdx.x * (int64_t)(kPoolThreads / 32) + warp; i < items; i += stride) {
-    const int b = (int)(i / parts), c0 = (int)(i % parts) * kColumns;
-    const int p = err ? -1 : a.parents[b], past = p < 0 ? 0 : a.past[p];
-    const int whole = past / a.bs, need = whole + (past % a.bs != 0);
-    const int fresh = !err && rank[b] >= 0 && whole >= c0 && whole < c0 + kColumns
-                          ? a.ring[((int64_t)head + rank[b]) % a.cap] : -1;
-    int x[kColumns / 32];
+  const int parts = W::parts(a.max_blocks), items = a.Bn * parts, lane = threadIdx.x & 31, warps = step / 32;
+  for (int j0 = i0 / 32; j0 < items; j0 += W::ROWS * warps) {
+    int x[W::ROWS][W::K];
 #pragma unroll
-    for (int k = 0; k < kColumns / 32; ++k) {
-      const int c = c0 + k * 32 + lane;
-      x[k] = c < need ? a.table[(int64_t)p * a.max_blocks + c] : -1;
-      if (!err && rank[b] >= 0 && c == whole) x[k] = fresh;
+    for (int n = 0; n < W::ROWS; ++n) {
+      if (j0 + n * warps >= items) break;
+      const int2 it = W::item(j0 + n * warps, parts);
+      const int b = it.x, p = err ? -1 : parents[b], past = p < 0 ? 0 : pasts[p], rank = rank_of(b);
+      const int whole = past / a.bs, need = whole + (past % a.bs != 0);
+#pragma unroll
+      for (int k = 0; k < W::K; ++k) {
+        const int c = it.y + k * 32 + lane;
+        x[n][k] = c >= need ? -1 : rank >= 0 && c == whole ? a.ring[ring_index(a, head, rank)]
+                                                           : a.table[(int64_t)p * a.max_blocks + c];
+      }
     }
 #pragma unroll
-    for (int k = 0; k < kColumns / 32; ++k) {
-      const int c = c0 + k * 32 + lane;
-      if (c < a.max_blocks) a.table_out[(int64_t)b * a.max_blocks + c] = x[k];
+    for (int n = 0; n < W::ROWS; ++n) {
+      if (j0 + n * warps >= items) break;
+      const int2 it = W::item(j0 + n * warps, parts);
+#pragma unroll
+      for (int k = 0; k < W::K; ++k) {
+        const int c = it.y + k * 32 + lane;
+        if (c < a.max_blocks) a.table_out[(int64_t)it.x * a.max_blocks + c] = x[n][k];
+      }
     }
   }
   if (err) return;
   for (int x = i0; x < a.num_blocks; x += step) {  // the pages given back, behind the last free one
-    const uint4 w = a.words[x >> 5];
+    const uint4 w = pages.at(x >> 5);
     if (w.x >> (x & 31) & 1) {
-      const int r = sums[x / kChunk].x + (w.z & 0xffff) + __popc(w.x & ((1u << (x & 31)) - 1));
-      a.ring[((int64_t)head + count + r) % a.cap] = x;
+      const int r = (int)w.z + __popc(w.x & ((1u << (x & 31)) - 1));
+      a.ring[ring_index(a, head, count + r)] = x;
     }
   }
+}
+
+__device__ __forceinline__ uint32_t fork_refusal(const PoolArgs& a, uint32_t err, int head, int count, int copies, int freed) {
+  if (head < 0 || head >= a.cap || count < 0 || count > a.cap) err |= PA_DEVERR_BAD_BATCH;
+  if (err) return err;
+  return (int64_t)count + freed > a.cap ? PA_DEVERR_BAD_BATCH : copies > count ? PA_DEVERR_NO_BLOCKS : 0;
+}
+
+__global__ void __launch_bounds__(kPoolThreads) fork_finish_kernel(const PoolArgs a) {
+  extern __shared__ int2 smem2[];
+  int2* sums = smem2;                       // [num_chunks + 1]
+  int2* before = sums + a.num_chunks + 1;   // [words of rows + 1]
+  pdl_wait();
+  pdl_launch_dependents();
+  const int row_words = (a.Bn + 31) / 32;
+  const int head = a.state[0], count = a.state[1];
+  scan_pairs<kPoolThreads>(a.num_chunks, sums, [&](int i) { return a.chunks[i]; });
+  scan_pairs<kPoolThreads>(row_words, before, [&](int i) { return make_int2(__popc(a.row_bits[i]), 0); });
+  const int freed = sums[a.num_chunks].x, copies = before[row_words].x;
+  const uint32_t err = fork_refusal(a, *a.ws_error, head, count, copies, freed);
+  fork_outputs<BigWalk>(a, err, head, count, copies, freed, BigWords{a.words, sums}, BigRows{a.row_bits, before}, a.parents, a.past,
+               blockIdx.x * kPoolThreads + threadIdx.x, gridDim.x * kPoolThreads);
+}
+
+// Everything in one CTA: lengths, parents and pins are loaded at once, the table's entries after them,
+// and the outputs need one more round of loads; between them all is in shared memory.
+__global__ void __launch_bounds__(kSmallThreads) fork_small_kernel(const PoolArgs a) {
+  extern __shared__ int2 smem2[];
+  const int words = (a.num_blocks + 31) / 32, row_words = (a.Bn + 31) / 32, n_sums = max(words, row_words);
+  int2* sums = smem2;                                                   // [n_sums + 1]: pages given back, rows that copy
+  uint32_t* whole = reinterpret_cast<uint32_t*>(sums + n_sums + 1);     // [words] each
+  uint32_t *old = whole + words, *kept = old + words, *pinned = kept + words;
+  uint32_t* rows = pinned + words;                                      // [row_words]
+  int* keeper = reinterpret_cast<int*>(rows + row_words);               // [num_blocks]
+  int* first_child = keeper + a.num_blocks;                             // [B] each
+  int *past = first_child + a.B, *held = past + a.B, *last = held + a.B;  // last: the partly filled page
+  int* parent = last + a.B;                                             // [Bn]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < 3 * words; i += kSmallThreads) whole[i] = 0;
+  for (int i = threadIdx.x; i < a.num_blocks; i += kSmallThreads) keeper[i] = 0;
+  for (int p = threadIdx.x; p < a.B; p += kSmallThreads) first_child[p] = INT32_MAX;
+  pdl_wait();
+  pdl_launch_dependents();
+  uint32_t err = 0;
+  const int head = a.state[0], count = a.state[1];
+  for (int p = threadIdx.x; p < a.B; p += kSmallThreads) past[p] = a.past[p], held[p] = a.held[p];
+  for (int b = threadIdx.x; b < a.Bn; b += kSmallThreads) {
+    const int p = a.parents[b];
+    if (p < -1 || p >= a.B) err = PA_DEVERR_BAD_BATCH;
+    parent[b] = p < 0 || p >= a.B ? -1 : p;
+  }
+  for (int w = warp; w < words; w += kSmallThreads / 32) {
+    const int x = w * 32 + lane;
+    const uint32_t m = __ballot_sync(0xffffffffu, a.pinned && x < a.num_blocks && a.pinned[x]);
+    if (lane == 0) pinned[w] = m;
+  }
+  __syncthreads();
+  for (int b = threadIdx.x; b < a.Bn; b += kSmallThreads)
+    if (parent[b] >= 0) atomicMin(&first_child[parent[b]], b);
+  __syncthreads();
+  const BitMarks marks{whole, old, kept, keeper};
+  err |= mark_pages<true, SmallWalk>(a, past, held, first_child, marks, last, warp, kSmallThreads / 32, lane);
+  const bool batch = __syncthreads_or(err & PA_DEVERR_BAD_BATCH), block = __syncthreads_or(err & PA_DEVERR_BAD_BLOCK);
+  err = (batch ? PA_DEVERR_BAD_BATCH : 0) | (block ? PA_DEVERR_BAD_BLOCK : 0);
+  for (int b0 = 0; b0 < a.Bn; b0 += kSmallThreads) {
+    const int b = b0 + threadIdx.x;
+    bool copy = false;
+    if (b < a.Bn && !err && parent[b] >= 0 && past[parent[b]] % a.bs) {
+      const int x = last[parent[b]];
+      copy = keeper[x] != a.Bn - b || ((whole[x >> 5] | pinned[x >> 5]) >> (x & 31) & 1);
+    }
+    const uint32_t m = __ballot_sync(0xffffffffu, copy);
+    if (lane == 0 && b < a.Bn) rows[b >> 5] = m;
+  }
+  for (int w = threadIdx.x; w < words; w += kSmallThreads) old[w] &= ~(whole[w] | kept[w] | pinned[w]);
+  __syncthreads();
+  scan_pairs<kSmallThreads>(n_sums, sums, [&](int i) {
+    return make_int2(i < words ? __popc(old[i]) : 0, i < row_words ? __popc(rows[i]) : 0);
+  });
+  const int freed = sums[n_sums].x, copies = sums[n_sums].y;
+  err = fork_refusal(a, err, head, count, copies, freed);
+  fork_outputs<SmallWalk>(a, err, head, count, copies, freed, SmallWords{old, nullptr, sums}, SmallRows{rows, sums}, parent, past,
+               threadIdx.x, kSmallThreads);
 }
 
 // ---- finish: compact -----------------------------------------------------------------------
 // The r-th highest mover x_r goes to the r-th lowest hole h_r while h_r < x_r: x_r falls and h_r
 // rises with r, so the pairs that move are the first D, and D is the number of movers x with
 //   holes below x > movers above x.
-struct Compaction {
-  int holes, movers, moves;
-};
+// the movers of a word for which that holds; w as Words::at gives it, M movers in all
+__device__ __forceinline__ int moving_in(const uint4& w, int M) {
+  int n = 0;
+  for (uint32_t rest = w.y; rest; rest &= rest - 1) {
+    const uint32_t below = (rest & -rest) - 1;
+    n += (int)w.z + __popc(w.x & below) + (int)w.w + __popc(w.y & below) + 1 > M;
+  }
+  return n;
+}
 
-// by the whole block; `sums` as scan_chunks leaves it
-__device__ __forceinline__ int count_moves(const PoolArgs& a, const int2* sums) {
+// by the whole block
+__device__ __forceinline__ int count_moves(const PoolArgs& a, const BigWords& pages) {
   __shared__ int found;
+  const int2* sums = pages.sums;
   const int M = sums[a.num_chunks].y;
   if (threadIdx.x == 0) found = a.num_chunks;
   __syncthreads();
@@ -273,66 +453,17 @@ __device__ __forceinline__ int count_moves(const PoolArgs& a, const int2* sums) 
   __syncthreads();
   if (c == a.num_chunks) return 0;
   if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
-    const uint4 w = a.words[c * 32 + lane];
-    const int h0 = sums[c].x + (w.z & 0xffff), m0 = sums[c].y + (w.z >> 16);
-    int n = 0;  // movers of this word that move
-    for (uint32_t rest = w.y; rest; rest &= rest - 1) {
-      const uint32_t below = (rest & -rest) - 1;
-      n += h0 + __popc(w.x & below) + m0 + __popc(w.y & below) + 1 > M;
-    }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
-    if (lane == 0) found = M - sums[c + 1].y + n;
+    const int n = __reduce_add_sync(0xffffffffu, moving_in(pages.at(c * 32 + threadIdx.x), M));
+    if (threadIdx.x == 0) found = M - sums[c + 1].y + n;
   }
   __syncthreads();
   return min(found, a.max_moves);
 }
 
-// the r-th hole
-__device__ __forceinline__ int hole_at(const PoolArgs& a, const int2* sums, int r) {
-  int lo = 0, n = a.num_chunks;  // the last chunk with at most r holes before it
-  while (n > 1) {
-    const int half = n >> 1;
-    if (sums[lo + half].x <= r) lo += half, n -= half;
-    else n = half;
-  }
-  r -= sums[lo].x;
-  int w = lo * 32;
-#pragma unroll
-  for (int d = 16; d; d >>= 1)
-    if ((int)(a.words[w + d].z & 0xffff) <= r) w += d;
-  const uint4 word = a.words[w];
-  r -= word.z & 0xffff;
-  uint32_t bits = word.x;
-  int at = 0;
-#pragma unroll
-  for (int d = 16; d; d >>= 1) {
-    const int low = __popc(bits & ((1u << d) - 1));
-    if (low <= r) r -= low, at += d, bits >>= d;
-  }
-  return w * 32 + at;
-}
-
-__global__ void __launch_bounds__(kPoolThreads) compact_finish_kernel(const PoolArgs a) {
-  extern __shared__ int smem[];
-  int2* sums = reinterpret_cast<int2*>(smem);  // [num_chunks + 1]
-  const int lane = threadIdx.x & 31;
-  pdl_wait();
-  pdl_launch_dependents();
-  scan_chunks(a, sums);
-  uint32_t err = *a.ws_error;
-  const int holes = sums[a.num_chunks].x, movers = sums[a.num_chunks].y;
-  if (!err && holes > a.cap) err = PA_DEVERR_BAD_BATCH;
-  const int moves = err ? 0 : count_moves(a, sums);
-  // where page x goes: itself, or the hole of its rank from above
-  auto moved = [&](int x) {
-    const uint4 w = a.words[x >> 5];
-    if (!(w.y >> (x & 31) & 1)) return x;
-    const int above = movers - 1 - (sums[x / kChunk].y + (int)(w.z >> 16) + __popc(w.y & ((1u << (x & 31)) - 1)));
-    return above < moves ? hole_at(a, sums, above) : x;
-  };
-  const int i0 = blockIdx.x * kPoolThreads + threadIdx.x, step = gridDim.x * kPoolThreads;
+// The outputs, spread over the threads from `i0` on in steps of `step`; hole(r) is the r-th hole.
+template <typename W, typename Words, typename Hole>
+__device__ __forceinline__ int compact_outputs(const PoolArgs& a, uint32_t err, int holes, int movers, int moves,
+                                               const Words& pages, Hole hole, int i0, int step) {
   if (i0 == 0) {
     a.error[0] = err;
     a.state_out[0] = 0;
@@ -342,17 +473,16 @@ __global__ void __launch_bounds__(kPoolThreads) compact_finish_kernel(const Pool
   int end = 0;
   if (!err)
     for (int x = i0; x < a.num_blocks; x += step) {
-      const uint4 w = a.words[x >> 5];
+      const uint4 w = pages.at(x >> 5);
       const uint32_t bit = 1u << (x & 31);
-      const int h = sums[x / kChunk].x + (w.z & 0xffff) + __popc(w.x & (bit - 1));
-      const int m = sums[x / kChunk].y + (int)(w.z >> 16) + __popc(w.y & (bit - 1));
+      const int h = (int)w.z + __popc(w.x & (bit - 1)), m = (int)w.w + __popc(w.y & (bit - 1));
       bool free = false;
       if (w.x & bit) {
         free = h >= moves;
       } else if (w.y & bit) {
         const int above = movers - 1 - m;
         if (above < moves) {
-          a.copies[above] = make_int2(x, hole_at(a, sums, above));
+          a.copies[above] = make_int2(x, hole(above));
           free = true;
         }
       }
@@ -360,21 +490,123 @@ __global__ void __launch_bounds__(kPoolThreads) compact_finish_kernel(const Pool
       if (free) a.ring[max(0, h - moves) + max(0, m - (movers - moves))] = x;
       else end = max(end, x + 1);
     }
-  end = __reduce_max_sync(0xffffffffu, end);
-  if (lane == 0 && end) atomicMax(a.pages_end, end);
-  const int parts = (a.max_blocks + kColumns - 1) / kColumns;
-  const int64_t items = (int64_t)a.B * parts, stride = (int64_t)gridDim.x * (kPoolThreads / 32);
-  for (int64_t i = blockIdx.x * (int64_t)(kPoolThreads / 32) + (threadIdx.x >> 5); i < items; i += stride) {
-    const int b = (int)(i / parts), c0 = (int)(i % parts) * kColumns;
-    const int held = err ? 0 : a.held[b];
+  const int parts = W::parts(a.max_blocks), items = a.B * parts, lane = threadIdx.x & 31, warps = step / 32;
+  for (int j0 = i0 / 32; j0 < items; j0 += W::ROWS * warps) {
+    int x[W::ROWS][W::K], held[W::ROWS];
 #pragma unroll
-    for (int k = 0; k < kColumns / 32; ++k) {
-      const int c = c0 + k * 32 + lane;
-      if (c >= a.max_blocks) break;
-      const int x = a.table[(int64_t)b * a.max_blocks + c];
-      a.table_out[(int64_t)b * a.max_blocks + c] = c < held ? moved(x) : x;
+    for (int n = 0; n < W::ROWS; ++n) {
+      if (j0 + n * warps >= items) break;
+      const int2 it = W::item(j0 + n * warps, parts);
+      held[n] = err ? 0 : a.held[it.x];
+#pragma unroll
+      for (int k = 0; k < W::K; ++k) {
+        const int c = it.y + k * 32 + lane;
+        x[n][k] = c < a.max_blocks ? a.table[(int64_t)it.x * a.max_blocks + c] : 0;
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < W::ROWS; ++n) {
+      if (j0 + n * warps >= items) break;
+      const int2 it = W::item(j0 + n * warps, parts);
+      int to[W::K];
+#pragma unroll
+      for (int k = 0; k < W::K; ++k) {  // the rank from above of the pages that move, -1 for others
+        to[k] = -1;
+        if (it.y + k * 32 + lane >= held[n]) continue;
+        const uint4 w = pages.at(x[n][k] >> 5);
+        const uint32_t bit = 1u << (x[n][k] & 31);
+        const int above = movers - 1 - ((int)w.w + __popc(w.y & (bit - 1)));
+        if ((w.y & bit) && above < moves) to[k] = above;
+      }
+#pragma unroll
+      for (int k = 0; k < W::K; ++k)
+        if (to[k] >= 0) x[n][k] = hole(to[k]);
+#pragma unroll
+      for (int k = 0; k < W::K; ++k) {
+        const int c = it.y + k * 32 + lane;
+        if (c < a.max_blocks) a.table_out[(int64_t)it.x * a.max_blocks + c] = x[n][k];
+      }
     }
   }
+  return end;
+}
+
+// the holes in order
+__global__ void __launch_bounds__(kPoolThreads) compact_lists_kernel(const PoolArgs a) {
+  extern __shared__ int2 smem2[];
+  pdl_wait();
+  pdl_launch_dependents();
+  scan_pairs<kPoolThreads>(a.num_chunks, smem2, [&](int i) { return a.chunks[i]; });
+  const BigWords pages{a.words, smem2};
+  for (int x = blockIdx.x * kPoolThreads + threadIdx.x; x < a.num_blocks; x += gridDim.x * kPoolThreads) {
+    const uint4 w = pages.at(x >> 5);
+    if (w.x >> (x & 31) & 1) a.holes[(int)w.z + __popc(w.x & ((1u << (x & 31)) - 1))] = x;
+  }
+}
+
+__global__ void __launch_bounds__(kPoolThreads) compact_finish_kernel(const PoolArgs a) {
+  extern __shared__ int2 smem2[];  // [num_chunks + 1]
+  pdl_wait();
+  pdl_launch_dependents();
+  scan_pairs<kPoolThreads>(a.num_chunks, smem2, [&](int i) { return a.chunks[i]; });
+  uint32_t err = *a.ws_error;
+  const int holes = smem2[a.num_chunks].x, movers = smem2[a.num_chunks].y;
+  if (!err && holes > a.cap) err = PA_DEVERR_BAD_BATCH;
+  const BigWords pages{a.words, smem2};
+  const int moves = err ? 0 : count_moves(a, pages);
+  int end = compact_outputs<BigWalk>(a, err, holes, movers, moves, pages, [&](int r) { return a.holes[r]; },
+                            blockIdx.x * kPoolThreads + threadIdx.x, gridDim.x * kPoolThreads);
+  end = __reduce_max_sync(0xffffffffu, end);
+  if ((threadIdx.x & 31) == 0 && end) atomicMax(a.pages_end, end);
+}
+
+// everything in one CTA
+__global__ void __launch_bounds__(kSmallThreads) compact_small_kernel(const PoolArgs a) {
+  extern __shared__ int2 smem2[];
+  __shared__ int total[2];  // pages that move, the highest page in use
+  const int words = (a.num_blocks + 31) / 32;
+  int2* sums = smem2;                                               // [words + 1]
+  uint32_t* movers = reinterpret_cast<uint32_t*>(sums + words + 1);  // [words] each
+  uint32_t *holes = movers + words, *pinned = holes + words;
+  int* list = reinterpret_cast<int*>(pinned + words);               // [num_blocks]: the holes in order
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < words; i += kSmallThreads) movers[i] = 0;
+  if (threadIdx.x < 2) total[threadIdx.x] = 0;
+  pdl_wait();
+  pdl_launch_dependents();
+  __syncthreads();
+  for (int w = warp; w < words; w += kSmallThreads / 32) {
+    const int x = w * 32 + lane;
+    const uint32_t m = __ballot_sync(0xffffffffu, a.pinned && x < a.num_blocks && a.pinned[x]);
+    if (lane == 0) pinned[w] = m;
+  }
+  uint32_t err = mark_pages<false, SmallWalk>(a, nullptr, a.held, nullptr, BitMarks{movers, nullptr, nullptr, nullptr}, nullptr, warp,
+                                   kSmallThreads / 32, lane);
+  const bool batch = __syncthreads_or(err & PA_DEVERR_BAD_BATCH), block = __syncthreads_or(err & PA_DEVERR_BAD_BLOCK);
+  err = (batch ? PA_DEVERR_BAD_BATCH : 0) | (block ? PA_DEVERR_BAD_BLOCK : 0);
+  for (int w = threadIdx.x; w < words; w += kSmallThreads) {
+    const uint32_t there = a.num_blocks - w * 32 >= 32 ? 0xffffffffu : (1u << (a.num_blocks & 31)) - 1, used = movers[w] | pinned[w];
+    holes[w] = there & ~used;
+    movers[w] = used & ~pinned[w];
+  }
+  __syncthreads();
+  scan_pairs<kSmallThreads>(words, sums, [&](int i) { return make_int2(__popc(holes[i]), __popc(movers[i])); });
+  const int H = sums[words].x, M = sums[words].y;
+  if (!err && H > a.cap) err = PA_DEVERR_BAD_BATCH;
+  const SmallWords pages{holes, movers, sums};
+  int n = 0;
+  for (int w = threadIdx.x; w < words; w += kSmallThreads) {
+    n += moving_in(pages.at(w), M);
+    int r = sums[w].x;
+    for (uint32_t rest = holes[w]; rest; rest &= rest - 1) list[r++] = w * 32 + __ffs(rest) - 1;
+  }
+  if (n) atomicAdd(&total[0], n);
+  __syncthreads();
+  const int moves = err ? 0 : min(total[0], a.max_moves);
+  const int end = compact_outputs<SmallWalk>(a, err, H, M, moves, pages, [&](int r) { return list[r]; }, threadIdx.x, kSmallThreads);
+  if (end) atomicMax(&total[1], end);
+  __syncthreads();
+  if (threadIdx.x == 0) *a.pages_end = total[1];
 }
 
 // ---- copies --------------------------------------------------------------------------------
@@ -442,29 +674,53 @@ static int grid_of(int64_t work, int sms, int per_sm) {
   return (int)(g < 1 ? 1 : g > (int64_t)sms * per_sm ? (int64_t)sms * per_sm : g);
 }
 
+// One CTA's shared memory holds the marks of 32768 pages, and it reads and writes about 65536 table
+// entries in the time of the launches that it saves.
+constexpr int kSmallPages = 32768, kSmallRows = 2048, kSmallEntries = 65536;
+static int small_smem(int num_blocks, int B, int Bn, bool fork) {
+  const int words = (int)ceil_div(num_blocks, 32), row_words = (int)ceil_div(Bn, 32);
+  return fork ? 8 * ((words > row_words ? words : row_words) + 1) + 4 * (4 * words + row_words + num_blocks + 4 * B + Bn)
+              : 8 * (words + 1) + 4 * (3 * words + num_blocks);
+}
+static bool is_small(const PoolArgs& a) {
+  return a.num_blocks <= kSmallPages && a.B <= kSmallRows && a.Bn <= kSmallRows &&
+         (int64_t)a.B * a.max_blocks <= kSmallEntries && (int64_t)a.Bn * a.max_blocks <= kSmallEntries;
+}
+
 // (at most PA_MAX_TABLE_REQUESTS rows and PA_MAX_POOL_PAGES / 1024 chunks)
-constexpr int kMarkSmem = PA_MAX_TABLE_REQUESTS * 4;
-constexpr int kFinishSmem = 8 * (PA_MAX_POOL_PAGES / kChunk + 1) + PA_MAX_TABLE_REQUESTS * 4;
-static_assert(kMarkSmem <= 48 * 1024 && kFinishSmem <= 48 * 1024 - 256, "no attribute is needed");
+constexpr int kFinishSmem = 8 * (PA_MAX_POOL_PAGES / kChunk + 1) + 8 * (PA_MAX_TABLE_REQUESTS / 32 + 1);
+static_assert(kFinishSmem <= 48 * 1024 - 1024, "no attribute is needed");
 
 template <bool FORK>
-static cudaError_t launch_pool(const PoolArgs& a, int sms, cudaStream_t s) {
+static cudaError_t launch_pool(const PoolArgs& a, int sms, cudaStream_t s, int* kernels) {
+  if (is_small(a)) {
+    auto kernel = FORK ? fork_small_kernel : compact_small_kernel;
+    const int smem = small_smem(a.num_blocks, a.B, a.Bn, FORK);
+    *kernels = 1;
+    if (smem > 32 * 1024)  // (less needs no attribute; the same limit from every host thread)
+      if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               small_smem(kSmallPages, kSmallRows, kSmallRows, FORK)))
+        return e;
+    return launch_pdl(kernel, dim3(1), dim3(kSmallThreads), (size_t)smem, s, a);
+  }
   const dim3 block(kPoolThreads);
-  if (cudaError_t e = launch_pdl(pool_clear_kernel, dim3(grid_of(a.clear_words, sms, 4)), block, 0, s, a.clear, a.clear_words)) return e;
-  const int64_t parts = ceil_div(a.max_blocks, kColumns) * 32;
-  if (cudaError_t e = launch_pdl(pool_mark_kernel<FORK>, dim3(grid_of(a.B * parts, sms, 4)), block,
-                                 FORK ? (size_t)a.B * 4 : 0, s, a))
-    return e;
-  if (cudaError_t e = launch_pdl(pool_words_kernel<FORK>, dim3(a.num_chunks), block, 0, s, a)) return e;
+  const size_t sums = 8 * ((size_t)a.num_chunks + 1), rows_smem = FORK ? 8 * ((size_t)ceil_div(a.Bn, 32) + 1) : 0;
+  *kernels = FORK ? 4 : 5;
+  if (cudaError_t e = launch_pdl(pool_clear_kernel, dim3(grid_of(a.clear_words, sms, 4)), block, 0, s, a)) return e;
+  const int64_t parts = ceil_div(a.max_blocks, BigWalk::COLUMNS) * 32;
+  if (cudaError_t e = launch_pdl(pool_mark_kernel<FORK>, dim3(grid_of(a.B * parts, sms, 4)), block, 0, s, a)) return e;
+  const int64_t row_blocks = FORK ? ceil_div(a.Bn, kPoolThreads) : 0;
+  if (cudaError_t e = launch_pdl(pool_words_kernel<FORK>, dim3((unsigned)(a.num_chunks + row_blocks)), block, 0, s, a)) return e;
   const int64_t rows = FORK ? a.Bn : a.B, work = rows * parts > a.num_blocks ? rows * parts : a.num_blocks;
-  if constexpr (FORK)
-    return launch_pdl(fork_finish_kernel, dim3(grid_of(work, sms, 4)), block,
-                      8 * ((size_t)a.num_chunks + 1) + (size_t)a.Bn * 4, s, a);
-  else
-    return launch_pdl(compact_finish_kernel, dim3(grid_of(work, sms, 4)), block, 8 * ((size_t)a.num_chunks + 1), s, a);
+  if constexpr (FORK) {
+    return launch_pdl(fork_finish_kernel, dim3(grid_of(work, sms, 4)), block, sums + rows_smem, s, a);
+  } else {
+    if (cudaError_t e = launch_pdl(compact_lists_kernel, dim3(grid_of(a.num_blocks, sms, 4)), block, sums, s, a)) return e;
+    return launch_pdl(compact_finish_kernel, dim3(grid_of(work, sms, 4)), block, sums, s, a);
+  }
 }
-cudaError_t launch_fork(const PoolArgs& a, int sms, cudaStream_t s) { return launch_pool<true>(a, sms, s); }
-cudaError_t launch_compact(const PoolArgs& a, int sms, cudaStream_t s) { return launch_pool<false>(a, sms, s); }
+cudaError_t launch_fork(const PoolArgs& a, int sms, cudaStream_t s, int* kernels) { return launch_pool<true>(a, sms, s, kernels); }
+cudaError_t launch_compact(const PoolArgs& a, int sms, cudaStream_t s, int* kernels) { return launch_pool<false>(a, sms, s, kernels); }
 
 cudaError_t launch_copy_pages(CopyArgs& a, int sms, cudaStream_t s) {
   int64_t most = 0;

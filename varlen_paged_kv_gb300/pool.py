@@ -4,8 +4,9 @@
 ``compact_block_tables``  the highest pages in use into the lowest free ones
 ``copy_pages``            the copies that either names, in the caches of all layers
 
-As the operators of ``step``: argument marshalling for the C ABI, on the current stream of the
-tensors' device (or ``stream``), and a call can be captured in a CUDA graph.
+As the operators of ``step``: argument marshalling for the C ABI (through the compiled calls where
+they are built), on the current stream of the tensors' device (or ``stream``), and a call can be
+captured in a CUDA graph.
 """
 from __future__ import annotations
 
@@ -111,6 +112,11 @@ def fork_block_tables(parents: torch.Tensor, past_seqlens: torch.Tensor, blocks_
     write to, in memory other than the old batch's. A fork that cannot be served changes nothing,
     describes empty rows and says why in ``error``. A request that shares pages is ended by a -1
     here; ``build_block_tables`` gives every page of a finished request back, shared or not."""
+    if out is None and workspace is None and stream is None:
+        made = (step._fast or step._load_fast()).fork_block_tables(parents, past_seqlens, blocks_held, block_table,
+                                                                   free_blocks, free_state, pinned, block_size, num_blocks)
+        if made is not None:
+            return ForkedTables._make(made)
     index = _index(block_table, "block_table")
     if not _ints(index, parents, past_seqlens, blocks_held, block_table, free_blocks, free_state):
         _refuse_ints(index, parents=parents, past_seqlens=past_seqlens, blocks_held=blocks_held,
@@ -153,6 +159,11 @@ def compact_block_tables(blocks_held: torch.Tensor, block_table: torch.Tensor, f
     is used; the ring ``free_blocks`` is rebuilt in place from all free pages in ascending order.
     From ``pages_end`` on the pool is free. ``out``: a CompactedTables to write to; its
     ``block_table`` may be ``block_table`` itself."""
+    if out is None and workspace is None and stream is None:
+        made = (step._fast or step._load_fast()).compact_block_tables(blocks_held, block_table, free_blocks, pinned,
+                                                                      num_blocks, max_moves)
+        if made is not None:
+            return CompactedTables._make(made)
     index = _index(block_table, "block_table")
     if not _ints(index, blocks_held, block_table, free_blocks):
         _refuse_ints(index, blocks_held=blocks_held, block_table=block_table, free_blocks=free_blocks)
@@ -187,6 +198,8 @@ def copy_pages(tensors: Sequence[torch.Tensor], copies: torch.Tensor, *, error: 
     (pa_copy_pages), entries of -1 passed over. ``tensors``: up to 256 contiguous tensors whose
     first extent counts the same pages, of any type: the key and value caches of all layers, page
     bounds. A page may be the target of one entry only, and then the source of none."""
+    if stream is None and (step._fast or step._load_fast()).copy_pages(tensors, copies, error):
+        return
     if not len(tensors):
         return
     index = _index(copies, "copies")

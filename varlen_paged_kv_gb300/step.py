@@ -78,6 +78,12 @@ def _load_fast():
         module.bind(*[ctypes.cast(f, _p).value for f in (
             lib.pa_build_block_tables, lib.pa_qk_norm_rope, lib.pa_update_page_bounds, lib.pa_select_pages,
             lib.pa_sparse_paged_attention)])
+        from .biased import _library as biased_library
+        from .pool import _library as pool_library
+        pool_library(), biased_library()
+        module.bind_pool(*[ctypes.cast(f, _p).value for f in (
+            lib.pa_fork_block_tables, lib.pa_compact_block_tables, lib.pa_copy_pages, lib.pa_biased_paged_attention,
+            lib.pa_pool_workspace_size, lib.pa_biased_workspace_size)])
         _fast = module
     return _fast
 
