@@ -190,8 +190,9 @@ __global__ void __launch_bounds__(kPoolThreads) pool_words_kernel(const PoolArgs
     if (lane == 0) a.row_bits[(blockIdx.x - a.num_chunks) * (kPoolThreads / 32) + warp] = m;
     return;
   }
-  for (int w = warp; w < 32; w += kPoolThreads / 32) {
-    const int x = blockIdx.x * kChunk + w * 32 + lane;
+#pragma unroll
+  for (int i = 0; i < 32 / (kPoolThreads / 32); ++i) {
+    const int w = warp + i * (kPoolThreads / 32), x = blockIdx.x * kChunk + w * 32 + lane;
     bool first = false, second = false;
     if (x < a.num_blocks) {
       const bool pinned = a.pinned && a.pinned[x], mark = a.marks[x];
@@ -220,13 +221,13 @@ __global__ void __launch_bounds__(kPoolThreads) pool_words_kernel(const PoolArgs
   }
 }
 
-// exclusive sums of n pairs (value(i)), by the whole block of THREADS; sums[n] are the totals
-template <int THREADS, typename F>
+// exclusive sums of n pairs (value(i)), by the whole block; sums[n] are the totals
+template <typename F>
 __device__ __forceinline__ void scan_pairs(int n, int2* sums, F value) {
-  __shared__ int2 part[THREADS / 32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ int2 part[32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, threads = blockDim.x;
   int2 carry = make_int2(0, 0);
-  for (int i0 = 0; i0 < n; i0 += THREADS) {
+  for (int i0 = 0; i0 < n; i0 += threads) {
     const int i = i0 + threadIdx.x;
     const int2 own = i < n ? value(i) : make_int2(0, 0);
     int2 x = own;
@@ -237,11 +238,12 @@ __device__ __forceinline__ void scan_pairs(int n, int2* sums, F value) {
     }
     if (lane == 31) part[warp] = x;
     __syncthreads();
+    const int2 all = lane * 32 < threads ? part[lane] : make_int2(0, 0);
     int2 before = carry;
-    for (int w = 0; w < THREADS / 32; ++w) {
-      if (w < warp) before.x += part[w].x, before.y += part[w].y;
-      carry.x += part[w].x, carry.y += part[w].y;
-    }
+    before.x += __reduce_add_sync(0xffffffffu, lane < warp ? all.x : 0);
+    before.y += __reduce_add_sync(0xffffffffu, lane < warp ? all.y : 0);
+    carry.x += __reduce_add_sync(0xffffffffu, all.x);
+    carry.y += __reduce_add_sync(0xffffffffu, all.y);
     if (i < n) sums[i] = make_int2(before.x + x.x - own.x, before.y + x.y - own.y);
     __syncthreads();
   }
@@ -254,7 +256,7 @@ struct BigWords {
   const uint4* words;
   const int2* sums;  // before each chunk
   __device__ __forceinline__ uint4 at(int w) const {
-    const uint4 v = words[w];
+    const uint4 v = __ldg(words + w);  // (of a kernel before)
     const int2 s = sums[w / 32];
     return make_uint4(v.x, v.y, s.x + (v.z & 0xffff), s.y + (v.z >> 16));
   }
@@ -332,6 +334,7 @@ __device__ __forceinline__ void fork_outputs(const PoolArgs& a, uint32_t err, in
     }
   }
   if (err) return;
+#pragma unroll 4
   for (int x = i0; x < a.num_blocks; x += step) {  // the pages given back, behind the last free one
     const uint4 w = pages.at(x >> 5);
     if (w.x >> (x & 31) & 1) {
@@ -355,8 +358,8 @@ __global__ void __launch_bounds__(kPoolThreads) fork_finish_kernel(const PoolArg
   pdl_launch_dependents();
   const int row_words = (a.Bn + 31) / 32;
   const int head = a.state[0], count = a.state[1];
-  scan_pairs<kPoolThreads>(a.num_chunks, sums, [&](int i) { return a.chunks[i]; });
-  scan_pairs<kPoolThreads>(row_words, before, [&](int i) { return make_int2(__popc(a.row_bits[i]), 0); });
+  scan_pairs(a.num_chunks, sums, [&](int i) { return a.chunks[i]; });
+  scan_pairs(row_words, before, [&](int i) { return make_int2(__popc(a.row_bits[i]), 0); });
   const int freed = sums[a.num_chunks].x, copies = before[row_words].x;
   const uint32_t err = fork_refusal(a, *a.ws_error, head, count, copies, freed);
   fork_outputs<BigWalk>(a, err, head, count, copies, freed, BigWords{a.words, sums}, BigRows{a.row_bits, before}, a.parents, a.past,
@@ -376,34 +379,34 @@ __global__ void __launch_bounds__(kSmallThreads) fork_small_kernel(const PoolArg
   int* first_child = keeper + a.num_blocks;                             // [B] each
   int *past = first_child + a.B, *held = past + a.B, *last = held + a.B;  // last: the partly filled page
   int* parent = last + a.B;                                             // [Bn]
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < 3 * words; i += kSmallThreads) whole[i] = 0;
-  for (int i = threadIdx.x; i < a.num_blocks; i += kSmallThreads) keeper[i] = 0;
-  for (int p = threadIdx.x; p < a.B; p += kSmallThreads) first_child[p] = INT32_MAX;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, threads = blockDim.x, warps = threads / 32;
+  for (int i = threadIdx.x; i < 3 * words; i += threads) whole[i] = 0;
+  for (int i = threadIdx.x; i < a.num_blocks; i += threads) keeper[i] = 0;
+  for (int p = threadIdx.x; p < a.B; p += threads) first_child[p] = INT32_MAX;
   pdl_wait();
   pdl_launch_dependents();
   uint32_t err = 0;
   const int head = a.state[0], count = a.state[1];
-  for (int p = threadIdx.x; p < a.B; p += kSmallThreads) past[p] = a.past[p], held[p] = a.held[p];
-  for (int b = threadIdx.x; b < a.Bn; b += kSmallThreads) {
+  for (int p = threadIdx.x; p < a.B; p += threads) past[p] = a.past[p], held[p] = a.held[p];
+  for (int b = threadIdx.x; b < a.Bn; b += threads) {
     const int p = a.parents[b];
     if (p < -1 || p >= a.B) err = PA_DEVERR_BAD_BATCH;
     parent[b] = p < 0 || p >= a.B ? -1 : p;
   }
-  for (int w = warp; w < words; w += kSmallThreads / 32) {
+  for (int w = warp; w < words; w += warps) {
     const int x = w * 32 + lane;
     const uint32_t m = __ballot_sync(0xffffffffu, a.pinned && x < a.num_blocks && a.pinned[x]);
     if (lane == 0) pinned[w] = m;
   }
   __syncthreads();
-  for (int b = threadIdx.x; b < a.Bn; b += kSmallThreads)
+  for (int b = threadIdx.x; b < a.Bn; b += threads)
     if (parent[b] >= 0) atomicMin(&first_child[parent[b]], b);
   __syncthreads();
   const BitMarks marks{whole, old, kept, keeper};
-  err |= mark_pages<true, SmallWalk>(a, past, held, first_child, marks, last, warp, kSmallThreads / 32, lane);
+  err |= mark_pages<true, SmallWalk>(a, past, held, first_child, marks, last, warp, warps, lane);
   const bool batch = __syncthreads_or(err & PA_DEVERR_BAD_BATCH), block = __syncthreads_or(err & PA_DEVERR_BAD_BLOCK);
   err = (batch ? PA_DEVERR_BAD_BATCH : 0) | (block ? PA_DEVERR_BAD_BLOCK : 0);
-  for (int b0 = 0; b0 < a.Bn; b0 += kSmallThreads) {
+  for (int b0 = 0; b0 < a.Bn; b0 += threads) {
     const int b = b0 + threadIdx.x;
     bool copy = false;
     if (b < a.Bn && !err && parent[b] >= 0 && past[parent[b]] % a.bs) {
@@ -413,15 +416,15 @@ __global__ void __launch_bounds__(kSmallThreads) fork_small_kernel(const PoolArg
     const uint32_t m = __ballot_sync(0xffffffffu, copy);
     if (lane == 0 && b < a.Bn) rows[b >> 5] = m;
   }
-  for (int w = threadIdx.x; w < words; w += kSmallThreads) old[w] &= ~(whole[w] | kept[w] | pinned[w]);
+  for (int w = threadIdx.x; w < words; w += threads) old[w] &= ~(whole[w] | kept[w] | pinned[w]);
   __syncthreads();
-  scan_pairs<kSmallThreads>(n_sums, sums, [&](int i) {
+  scan_pairs(n_sums, sums, [&](int i) {
     return make_int2(i < words ? __popc(old[i]) : 0, i < row_words ? __popc(rows[i]) : 0);
   });
   const int freed = sums[n_sums].x, copies = sums[n_sums].y;
   err = fork_refusal(a, err, head, count, copies, freed);
   fork_outputs<SmallWalk>(a, err, head, count, copies, freed, SmallWords{old, nullptr, sums}, SmallRows{rows, sums}, parent, past,
-               threadIdx.x, kSmallThreads);
+               threadIdx.x, threads);
 }
 
 // ---- finish: compact -----------------------------------------------------------------------
@@ -472,6 +475,7 @@ __device__ __forceinline__ int compact_outputs(const PoolArgs& a, uint32_t err, 
   for (int r = moves + i0; r < a.max_moves; r += step) a.copies[r] = make_int2(-1, -1);
   int end = 0;
   if (!err)
+#pragma unroll 4
     for (int x = i0; x < a.num_blocks; x += step) {
       const uint4 w = pages.at(x >> 5);
       const uint32_t bit = 1u << (x & 31);
@@ -536,8 +540,9 @@ __global__ void __launch_bounds__(kPoolThreads) compact_lists_kernel(const PoolA
   extern __shared__ int2 smem2[];
   pdl_wait();
   pdl_launch_dependents();
-  scan_pairs<kPoolThreads>(a.num_chunks, smem2, [&](int i) { return a.chunks[i]; });
+  scan_pairs(a.num_chunks, smem2, [&](int i) { return a.chunks[i]; });
   const BigWords pages{a.words, smem2};
+#pragma unroll 4
   for (int x = blockIdx.x * kPoolThreads + threadIdx.x; x < a.num_blocks; x += gridDim.x * kPoolThreads) {
     const uint4 w = pages.at(x >> 5);
     if (w.x >> (x & 31) & 1) a.holes[(int)w.z + __popc(w.x & ((1u << (x & 31)) - 1))] = x;
@@ -548,13 +553,13 @@ __global__ void __launch_bounds__(kPoolThreads) compact_finish_kernel(const Pool
   extern __shared__ int2 smem2[];  // [num_chunks + 1]
   pdl_wait();
   pdl_launch_dependents();
-  scan_pairs<kPoolThreads>(a.num_chunks, smem2, [&](int i) { return a.chunks[i]; });
+  scan_pairs(a.num_chunks, smem2, [&](int i) { return a.chunks[i]; });
   uint32_t err = *a.ws_error;
   const int holes = smem2[a.num_chunks].x, movers = smem2[a.num_chunks].y;
   if (!err && holes > a.cap) err = PA_DEVERR_BAD_BATCH;
   const BigWords pages{a.words, smem2};
   const int moves = err ? 0 : count_moves(a, pages);
-  int end = compact_outputs<BigWalk>(a, err, holes, movers, moves, pages, [&](int r) { return a.holes[r]; },
+  int end = compact_outputs<BigWalk>(a, err, holes, movers, moves, pages, [&](int r) { return __ldg(a.holes + r); },
                             blockIdx.x * kPoolThreads + threadIdx.x, gridDim.x * kPoolThreads);
   end = __reduce_max_sync(0xffffffffu, end);
   if ((threadIdx.x & 31) == 0 && end) atomicMax(a.pages_end, end);
@@ -569,33 +574,33 @@ __global__ void __launch_bounds__(kSmallThreads) compact_small_kernel(const Pool
   uint32_t* movers = reinterpret_cast<uint32_t*>(sums + words + 1);  // [words] each
   uint32_t *holes = movers + words, *pinned = holes + words;
   int* list = reinterpret_cast<int*>(pinned + words);               // [num_blocks]: the holes in order
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < words; i += kSmallThreads) movers[i] = 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, threads = blockDim.x, warps = threads / 32;
+  for (int i = threadIdx.x; i < words; i += threads) movers[i] = 0;
   if (threadIdx.x < 2) total[threadIdx.x] = 0;
   pdl_wait();
   pdl_launch_dependents();
   __syncthreads();
-  for (int w = warp; w < words; w += kSmallThreads / 32) {
+  for (int w = warp; w < words; w += warps) {
     const int x = w * 32 + lane;
     const uint32_t m = __ballot_sync(0xffffffffu, a.pinned && x < a.num_blocks && a.pinned[x]);
     if (lane == 0) pinned[w] = m;
   }
   uint32_t err = mark_pages<false, SmallWalk>(a, nullptr, a.held, nullptr, BitMarks{movers, nullptr, nullptr, nullptr}, nullptr, warp,
-                                   kSmallThreads / 32, lane);
+                                   warps, lane);
   const bool batch = __syncthreads_or(err & PA_DEVERR_BAD_BATCH), block = __syncthreads_or(err & PA_DEVERR_BAD_BLOCK);
   err = (batch ? PA_DEVERR_BAD_BATCH : 0) | (block ? PA_DEVERR_BAD_BLOCK : 0);
-  for (int w = threadIdx.x; w < words; w += kSmallThreads) {
+  for (int w = threadIdx.x; w < words; w += threads) {
     const uint32_t there = a.num_blocks - w * 32 >= 32 ? 0xffffffffu : (1u << (a.num_blocks & 31)) - 1, used = movers[w] | pinned[w];
     holes[w] = there & ~used;
     movers[w] = used & ~pinned[w];
   }
   __syncthreads();
-  scan_pairs<kSmallThreads>(words, sums, [&](int i) { return make_int2(__popc(holes[i]), __popc(movers[i])); });
+  scan_pairs(words, sums, [&](int i) { return make_int2(__popc(holes[i]), __popc(movers[i])); });
   const int H = sums[words].x, M = sums[words].y;
   if (!err && H > a.cap) err = PA_DEVERR_BAD_BATCH;
   const SmallWords pages{holes, movers, sums};
   int n = 0;
-  for (int w = threadIdx.x; w < words; w += kSmallThreads) {
+  for (int w = threadIdx.x; w < words; w += threads) {
     n += moving_in(pages.at(w), M);
     int r = sums[w].x;
     for (uint32_t rest = holes[w]; rest; rest &= rest - 1) list[r++] = w * 32 + __ffs(rest) - 1;
@@ -603,7 +608,7 @@ __global__ void __launch_bounds__(kSmallThreads) compact_small_kernel(const Pool
   if (n) atomicAdd(&total[0], n);
   __syncthreads();
   const int moves = err ? 0 : min(total[0], a.max_moves);
-  const int end = compact_outputs<SmallWalk>(a, err, H, M, moves, pages, [&](int r) { return list[r]; }, threadIdx.x, kSmallThreads);
+  const int end = compact_outputs<SmallWalk>(a, err, H, M, moves, pages, [&](int r) { return list[r]; }, threadIdx.x, threads);
   if (end) atomicMax(&total[1], end);
   __syncthreads();
   if (threadIdx.x == 0) *a.pages_end = total[1];
@@ -674,17 +679,18 @@ static int grid_of(int64_t work, int sms, int per_sm) {
   return (int)(g < 1 ? 1 : g > (int64_t)sms * per_sm ? (int64_t)sms * per_sm : g);
 }
 
-// One CTA's shared memory holds the marks of 32768 pages, and it reads and writes about 65536 table
-// entries in the time of the launches that it saves.
-constexpr int kSmallPages = 32768, kSmallRows = 2048, kSmallEntries = 65536;
+// One CTA takes batches of up to about 10000 table entries and pages together: one SM's instruction rate
+// bounds it (64 rows of 66 columns over 1707 pages 7.6 us, of 130 over 3340 12.6, 250 of 66 over 7096
+// 14.5), where the kernels of many CTAs take about 12 us whatever there is below 50000.
+constexpr int kSmallPages = 8192, kSmallRows = 2048, kSmallWork = 10000;
 static int small_smem(int num_blocks, int B, int Bn, bool fork) {
   const int words = (int)ceil_div(num_blocks, 32), row_words = (int)ceil_div(Bn, 32);
   return fork ? 8 * ((words > row_words ? words : row_words) + 1) + 4 * (4 * words + row_words + num_blocks + 4 * B + Bn)
               : 8 * (words + 1) + 4 * (3 * words + num_blocks);
 }
 static bool is_small(const PoolArgs& a) {
-  return a.num_blocks <= kSmallPages && a.B <= kSmallRows && a.Bn <= kSmallRows &&
-         (int64_t)a.B * a.max_blocks <= kSmallEntries && (int64_t)a.Bn * a.max_blocks <= kSmallEntries;
+  const int64_t rows = a.B > a.Bn ? a.B : a.Bn;
+  return a.num_blocks <= kSmallPages && rows <= kSmallRows && rows * a.max_blocks + a.num_blocks <= kSmallWork;
 }
 
 // (at most PA_MAX_TABLE_REQUESTS rows and PA_MAX_POOL_PAGES / 1024 chunks)
@@ -708,7 +714,7 @@ static cudaError_t launch_pool(const PoolArgs& a, int sms, cudaStream_t s, int* 
   *kernels = FORK ? 4 : 5;
   if (cudaError_t e = launch_pdl(pool_clear_kernel, dim3(grid_of(a.clear_words, sms, 4)), block, 0, s, a)) return e;
   const int64_t parts = ceil_div(a.max_blocks, BigWalk::COLUMNS) * 32;
-  if (cudaError_t e = launch_pdl(pool_mark_kernel<FORK>, dim3(grid_of(a.B * parts, sms, 4)), block, 0, s, a)) return e;
+  if (cudaError_t e = launch_pdl(pool_mark_kernel<FORK>, dim3(grid_of(a.B * parts, sms, 8)), block, 0, s, a)) return e;
   const int64_t row_blocks = FORK ? ceil_div(a.Bn, kPoolThreads) : 0;
   if (cudaError_t e = launch_pdl(pool_words_kernel<FORK>, dim3((unsigned)(a.num_chunks + row_blocks)), block, 0, s, a)) return e;
   const int64_t rows = FORK ? a.Bn : a.B, work = rows * parts > a.num_blocks ? rows * parts : a.num_blocks;
