@@ -97,7 +97,8 @@ struct BiRows {
   static constexpr int kStride = HS + 4;                      // floats between rows of a partial result
   static constexpr int kComb = kStages * kStageBytes;         // float [16][kStride]
   static constexpr int kMl = kComb + 16 * kStride * 4;        // float [2][4][16]: m and l of the warps
-  static constexpr int kPre = kMl + 2 * 4 * 16 * 4;           // int64 [kBiThreads + 1]: costs before each thread's sequences
+  static constexpr int kCl = kMl + 2 * 4 * 16 * 4;            // float [2][16]: m and l of the CTA
+  static constexpr int kPre = kCl + 2 * 16 * 4;               // int64 [kBiThreads + 1]: costs before each thread's sequences
   static constexpr int kBars = kPre + (kBiThreads + 2) * 8;
   static constexpr int kAbort = kBars + 2 * kStages * 8;      // abort flag, error word
   static constexpr int kBytes = kAbort + 16 + 1024;
@@ -146,6 +147,19 @@ struct BiWalk {
     chunks = (int)(((int64_t)s.q * a.G + 15) / 16);
     units = a.kvh * chunks;
   }
+  // the rank-th of C equal shares of the sequence's tiles (`loaded` is taken back: the only item)
+  __device__ __forceinline__ bool only(const BiasedArgs& a, int g, int rank, int C, BiItem& it) {
+    if (!loaded) return false;
+    loaded = false;
+    it.b = b, it.c0 = s.c0, it.q = s.q, it.past = s.past, it.prefix = prefix;
+    it.g = g;
+    it.r_first = 0;
+    it.n_rows = s.q * a.G;
+    it.ta = t0 + (int)((int64_t)nt * rank / C), it.te = t0 + (int)((int64_t)nt * (rank + 1) / C);
+    it.keys = keys;
+    it.first = it.last = true;
+    return true;
+  }
   __device__ __forceinline__ bool next(const BiasedArgs& a, int lane, BiItem& it) {
     for (;;) {
       if (b >= a.B || base >= end) return false;
@@ -183,7 +197,12 @@ struct BiWalk {
   }
 };
 
-template <int HS, bool BF16>
+//
+// CLUSTER: few units over short tables. The CTAs of a cluster (a column of the grid) share one unit's
+// tiles, no costs are summed up and no merge follows: every CTA learns all (m, l) of the cluster and
+// sums a share of the columns over it. One row of 2048 keys: 9.3 us where equal shares and a merge
+// take 12.6; but a cluster's CTAs are at most eight, and a unit is not cut between clusters.
+template <int HS, bool BF16, bool CLUSTER>
 __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
     biased_rows_kernel(const BiasedArgs a, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const int seg_rows) {
@@ -194,6 +213,7 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   float* comb = reinterpret_cast<float*>(smem + L::kComb);
   float* ml = reinterpret_cast<float*>(smem + L::kMl);
+  float* cl = reinterpret_cast<float*>(smem + L::kCl);
   int64_t* pre = reinterpret_cast<int64_t*>(smem + L::kPre);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBars);
   uint64_t* empty = full + L::kStages;
@@ -210,60 +230,70 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
     fence_mbar_init();
   }
   pdl_wait();
-  pdl_launch_dependents();  // (the merge waits for this kernel's end)
-  // the costs of all sequences, each thread those of a run of them
-  const int run = (a.B + kBiThreads - 1) / kBiThreads;
-  {
-    int64_t mine = 0;
-    for (int i = 0; i < run; ++i) {
-      const int b = threadIdx.x * run + i;
-      if (b >= a.B) break;
-      const Seq s = seq_at(a, b);
-      if (!short_rows(a, s)) continue;
-      const int prefix = a.prefix ? a.prefix[b] : 0;
-      Keys k = join(keys_of_row(a, s, prefix, 0), keys_of_row(a, s, prefix, s.q - 1));
-      if (a.first)
-        for (int j = 1; j < s.q - 1; ++j) k = join(k, keys_of_row(a, s, prefix, j));
-      const int2 t = tiles_of(k);
-      mine += (int64_t)a.kvh * (((int64_t)s.q * a.G + 15) / 16) * (t.y - t.x + kBiCost);
-    }
-    pre[threadIdx.x + 1] = mine;
-  }
-  if (blockIdx.x == 0) check_biased_batch(a);
-  __syncthreads();
-  if (warp == 0) {  // sums, five threads' costs a lane
-    int64_t v[kBiThreads / 32], sum = 0;
-#pragma unroll
-    for (int i = 0; i < kBiThreads / 32; ++i) sum += pre[lane * (kBiThreads / 32) + i + 1], v[i] = sum;
-    int64_t x = sum;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
-      if (lane >= d) x += y;
-    }
-#pragma unroll
-    for (int i = 0; i < kBiThreads / 32; ++i) pre[lane * (kBiThreads / 32) + i + 1] = x - sum + v[i];
-    if (lane == 0) pre[0] = 0;
-  }
-  __syncthreads();
-  const int64_t W = pre[kBiThreads];
-  const int C = (int)min((int64_t)gridDim.x, max(W / (kBiCost + 1), (int64_t)1));
-  const int c = blockIdx.x;
+  // (all earlier work is done: the tile kernel starts beside this one on what it leaves free, 24 rows beside 8
+  // chunks of 512 350 us instead of 356; the merge waits for both. With this kernel on few SMs for as long as the
+  // tile kernel takes it is no faster: a CTA's chain gives it at most 27 GB/s.)
+  pdl_launch_dependents();
+  const int c = blockIdx.x, rank = blockIdx.z;
   BiWalk walk;
-  walk.pos = c < C ? W * c / C : W;
-  walk.end = c < C ? W * (c + 1) / C : W;
-  walk.loaded = false;
-  {  // the thread whose sequences hold the share's beginning
-    int k = 0;
+  if (c == 0 && rank == 0) check_biased_batch(a);
+  if constexpr (CLUSTER) {
+    __syncthreads();  // the barriers are there
+    walk.b = c / a.kvh;
+    walk.load(a, lane);
+    if (walk.units == 0) return;  // (all CTAs of a cluster agree)
+  } else {
+    // the costs of all sequences, each thread those of a run of them
+    const int run = (a.B + kBiThreads - 1) / kBiThreads;
+    {
+      int64_t mine = 0;
+      for (int i = 0; i < run; ++i) {
+        const int b = threadIdx.x * run + i;
+        if (b >= a.B) break;
+        const Seq s = seq_at(a, b);
+        if (!short_rows(a, s)) continue;
+        const int prefix = a.prefix ? a.prefix[b] : 0;
+        Keys k = join(keys_of_row(a, s, prefix, 0), keys_of_row(a, s, prefix, s.q - 1));
+        if (a.first)
+          for (int j = 1; j < s.q - 1; ++j) k = join(k, keys_of_row(a, s, prefix, j));
+        const int2 t = tiles_of(k);
+        mine += (int64_t)a.kvh * (((int64_t)s.q * a.G + 15) / 16) * (t.y - t.x + kBiCost);
+      }
+      pre[threadIdx.x + 1] = mine;
+    }
+    __syncthreads();
+    if (warp == 0) {  // sums, five threads' costs a lane
+      int64_t v[kBiThreads / 32], sum = 0;
 #pragma unroll
-    for (int i = 0; i < kBiThreads / 32; ++i) k += __popc(__ballot_sync(0xffffffffu, pre[i * 32 + lane + 1] <= walk.pos));
-    k = min(k, kBiThreads - 1);
-    walk.b = k * run;
-    walk.base = pre[k];
-  }
-  if (walk.pos >= walk.end) {
-    if (threadIdx.x == 0) a.records[2 * c] = make_int4(0, 0, 0, 0), a.records[2 * c + 1] = make_int4(0, 0, 0, 0);
-    return;
+      for (int i = 0; i < kBiThreads / 32; ++i) sum += pre[lane * (kBiThreads / 32) + i + 1], v[i] = sum;
+      int64_t x = sum;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+      }
+#pragma unroll
+      for (int i = 0; i < kBiThreads / 32; ++i) pre[lane * (kBiThreads / 32) + i + 1] = x - sum + v[i];
+      if (lane == 0) pre[0] = 0;
+    }
+    __syncthreads();
+    const int64_t W = pre[kBiThreads];
+    const int C = (int)min((int64_t)gridDim.x, max(W / (kBiCost + 1), (int64_t)1));
+    walk.pos = c < C ? W * c / C : W;
+    walk.end = c < C ? W * (c + 1) / C : W;
+    walk.loaded = false;
+    {  // the thread whose sequences hold the share's beginning
+      int k = 0;
+#pragma unroll
+      for (int i = 0; i < kBiThreads / 32; ++i) k += __popc(__ballot_sync(0xffffffffu, pre[i * 32 + lane + 1] <= walk.pos));
+      k = min(k, kBiThreads - 1);
+      walk.b = k * run;
+      walk.base = pre[k];
+    }
+    if (walk.pos >= walk.end) {
+      if (threadIdx.x == 0) a.records[2 * c] = make_int4(0, 0, 0, 0), a.records[2 * c + 1] = make_int4(0, 0, 0, 0);
+      return;
+    }
   }
   BiItem it;
   int n = 0;  // tiles so far
@@ -273,7 +303,7 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
     const int nseg = kBiTile / seg_rows, oob = a.num_blocks * a.bs;
     int4 head = make_int4(0, 0, 0, 0);
     int cont = 0;
-    while (walk.next(a, lane, it)) {
+    while (CLUSTER ? walk.only(a, c % a.kvh, rank, gridDim.z, it) : walk.next(a, lane, it)) {
       if (it.first && !it.last) head = make_int4(it.n_rows, it.c0, it.r_first, it.g);
       if (!it.first) cont = it.last ? 2 : 1;
       const int* table = a.table + (int64_t)it.b * a.max_blocks;
@@ -307,12 +337,12 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
         z = z_next;
       }
     }
-    if (lane == 0) a.records[2 * c] = head, a.records[2 * c + 1] = make_int4(cont, 0, 0, 0);
+    if (!CLUSTER && lane == 0) a.records[2 * c] = head, a.records[2 * c + 1] = make_int4(cont, 0, 0, 0);
   } else {
     // ---- consumers: warp w has keys 16w .. 16w + 15 of every tile ----
     const int w = warp, tq = lane & 3, gq = lane >> 2;
     const int mi = lane >> 3, rr = lane & 7;
-    while (walk.next(a, lane, it)) {
+    while (CLUSTER ? walk.only(a, c % a.kvh, rank, gridDim.z, it) : walk.next(a, lane, it)) {
       Seq sq;
       sq.c0 = it.c0, sq.q = it.q, sq.past = it.past;
       uint32_t qa[NKS][4];  // Q as the A operand: rows gq and gq + 8
@@ -525,7 +555,10 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
         float S = 0.f;
         for (int v = 0; v < 4; ++v)
           if (ml[v * 16 + r] != -INFINITY) S += ml[64 + v * 16 + r] * fast_exp2(ml[v * 16 + r] - M);
-        if (whole) {
+        if constexpr (CLUSTER) {
+          *reinterpret_cast<float4*>(comb + r * L::kStride + cc) = x;
+          if (cc == 0) cl[r] = M, cl[16 + r] = S;
+        } else if (whole) {
           const int rs = it.r_first + r;
           const int64_t at = (int64_t)(it.c0 + rs / a.G) * a.nh + it.g * a.G + rs % a.G;
           const float inv = M == -INFINITY ? 0.f : 1.f / S;
@@ -540,6 +573,31 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
       }
       named_bar_sync(1, 128);  // the combining buffers are free again
     }
+  }
+  if constexpr (CLUSTER) {
+    const int C = gridDim.z;
+    cluster_sync();  // all results of the cluster
+    const int c0 = HS / 4 * rank / C, nc = HS / 4 * (rank + 1) / C - c0;  // this CTA's share of the columns, in quads
+    for (int i = threadIdx.x; i < it.n_rows * nc; i += kBiThreads) {
+      const int r = i / nc, cc = (c0 + i % nc) * 4;
+      float M = -INFINITY, S = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int k = 0; k < C; ++k) M = fmaxf(M, ld_cluster(cluster_addr(cl + r, k)));
+      for (int k = 0; k < C; ++k) {
+        const float m = ld_cluster(cluster_addr(cl + r, k));
+        if (m == -INFINITY) continue;
+        const float f = fast_exp2(m - M);
+        S += f * ld_cluster(cluster_addr(cl + 16 + r, k));
+        const float4 y = ld_cluster4(cluster_addr(comb + r * L::kStride + cc, k));
+        x[0] += f * y.x, x[1] += f * y.y, x[2] += f * y.z, x[3] += f * y.w;
+      }
+      const int64_t at = (int64_t)(it.c0 + r / a.G) * a.nh + it.g * a.G + r % a.G;
+      const float inv = M == -INFINITY ? 0.f : 1.f / S;
+      uint2 out = make_uint2(pack2<BF16>(x[0] * inv, x[1] * inv), pack2<BF16>(x[2] * inv, x[3] * inv));
+      if (M == -INFINITY) out = make_uint2(0, 0);
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.output) + at * HS + cc) = out;
+      if (a.lse && cc == 0) a.lse[at] = M == -INFINITY ? -INFINITY : (M + fast_log2(S)) * 0.69314718055994531f;
+    }
+    cluster_sync();  // no CTA leaves while another reads its shared memory
   }
   __syncthreads();
   if (threadIdx.x == 0 && *err && a.error) atomicOr(a.error, *err);
@@ -606,12 +664,23 @@ __global__ void __launch_bounds__(kMergeThreads) biased_merge_kernel(const Biase
   }
 }
 
+// most keys that `rows` rows of a sequence see, by the table's width or the window
+static int64_t keys_in_reach(const BiasedArgs& a, int rows) {
+  const int64_t keys = (int64_t)a.max_blocks * a.bs, reach = (int64_t)a.window + rows;
+  return a.window && !a.prefix && reach < keys ? reach : keys;
+}
+
 #include "biased_tile.cuh"
 
 // ---- host ----------------------------------------------------------------------------------
 int biased_ctas(int hs, int sms) {
   const int n = sms * (hs == 256 ? 1 : 2);
   return n < PA_BIASED_CTAS ? n : PA_BIASED_CTAS;
+}
+
+template <int HS, bool BF16>
+static cudaError_t launch_biased_merge(const BiasedArgs& a, int ctas, cudaStream_t s) {
+  return launch_pdl(biased_merge_kernel<HS, BF16>, dim3(ctas, 4), dim3(kMergeThreads), 0, s, a, ctas);
 }
 
 static int divisor(int a, int b) {
@@ -625,17 +694,33 @@ static int divisor(int a, int b) {
 
 template <int HS, bool BF16>
 static cudaError_t launch_biased_rows(const BiasedArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int seg,
-                                      int sms, cudaStream_t s) {
+                                      int sms, cudaStream_t s, int* kernels, int* merge) {
   const int ctas = biased_ctas(HS, sms);
   constexpr int smem = BiRows<HS>::kBytes;
-  if (cudaError_t e = cudaFuncSetAttribute(biased_rows_kernel<HS, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))
+  // Clusters where two to eight CTAs for each unit run at once and none has many tiles, by the table's
+  // width or the window: up to 8, or 16 where they are over half of what runs at once; else equal shares,
+  // which do not mind how lengths differ. Random lengths up to l, clusters against equal shares: 1 x 200
+  // keys 5.9 us and 9.9, 1 x 4000 12.9 and 13.7, 1 x 8000 16.7 and 14.5, 4 x 8000 22.9 and 26.1, 8 x 4000
+  // 23.6 and 27.1, 1 x 60000 73 and 37.
+  const int64_t units = (int64_t)a.B * a.kvh, tiles = ceil_div(keys_in_reach(a, 16), kBiTile) + 1;
+  const int cl = cluster_size(units, ctas, tiles, 1, 8);
+  if (a.G <= 16 && cl > 1 && tiles <= (int64_t)cl * (2 * units * cl > ctas ? 16 : 8)) {
+    *kernels += 1;
+    return launch_clusters(biased_rows_kernel<HS, BF16, true>, dim3((unsigned)units, 1, cl), kBiThreads, smem, smem, s, a, tk,
+                           tv, seg);
+  }
+  *kernels += 1;
+  if (cudaError_t e = cudaFuncSetAttribute(biased_rows_kernel<HS, BF16, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))
     return e;
-  if (cudaError_t e = launch_pdl(biased_rows_kernel<HS, BF16>, dim3(ctas), dim3(kBiThreads), smem, s, a, tk, tv, seg)) return e;
-  return launch_pdl(biased_merge_kernel<HS, BF16>, dim3(ctas, 4), dim3(kMergeThreads), 0, s, a,
-                    ctas);
+  if (cudaError_t e = launch_pdl(biased_rows_kernel<HS, BF16, false>, dim3(ctas), dim3(kBiThreads), smem, s, a, tk, tv, seg))
+    return e;
+  *merge = ctas;
+  return cudaSuccess;
 }
 
-cudaError_t launch_biased(const BiasedArgs& a, bool bf16, int sms, cudaStream_t s) {
+cudaError_t launch_biased(const BiasedArgs& args, bool bf16, int sms, cudaStream_t s, int* kernels) {
+  BiasedArgs a = args;
+  *kernels = 0;
   const int seg = divisor(a.bs, kBiTile);
   const int64_t slots = (int64_t)a.num_blocks * a.bs;
   CUtensorMap tk, tv, tq;
@@ -643,20 +728,26 @@ cudaError_t launch_biased(const BiasedArgs& a, bool bf16, int sms, cudaStream_t 
       !cache_map_16(&tv, a.value_cache, bf16, a.hs, a.kvh, slots, seg))
     return cudaErrorInvalidValue;
   // Sequences of up to 16 rows per KV head are the rows kernel's, longer ones the tile kernel's (groups
-  // of over 128 heads, more than a tile's rows, are all the rows kernel's); a kernel that can have none is not launched.
+  // of over 128 heads, more than a tile's rows, are all the rows kernel's); a kernel that can have none is
+  // not launched. The merge comes last: it needs the rows kernel's results, the tile kernel does not.
+  int merge = 0;
+#define PA_TYPES(F, HS, ...) (bf16 ? F<HS, true>(__VA_ARGS__) : F<HS, false>(__VA_ARGS__))
+#define PA_SIZES(F, ...) (a.hs == 64 ? PA_TYPES(F, 64, __VA_ARGS__) : a.hs == 128 ? PA_TYPES(F, 128, __VA_ARGS__) : PA_TYPES(F, 256, __VA_ARGS__))
   if (a.G <= 16 || a.G > 128) {
-#define PA_ROWS(HS) (bf16 ? launch_biased_rows<HS, true>(a, tk, tv, seg, sms, s) : launch_biased_rows<HS, false>(a, tk, tv, seg, sms, s))
-    if (cudaError_t e = a.hs == 64 ? PA_ROWS(64) : a.hs == 128 ? PA_ROWS(128) : PA_ROWS(256)) return e;
-#undef PA_ROWS
+    if (cudaError_t e = PA_SIZES(launch_biased_rows, a, tk, tv, seg, sms, s, kernels, &merge)) return e;
+    a.after_rows = 1;
   }
-  if (a.G > 128 || (a.max_rows > 0 && (int64_t)a.max_rows * a.G <= 16)) return cudaSuccess;
-  const int rows = 128 / a.G;
-  if (!query_block_map(&tq, a.query, bf16, a.hs, a.nh, a.N, a.q_stride, a.G, rows)) return cudaErrorInvalidValue;
-#define PA_TILE(HS)                                                       \
-  (bf16 ? launch_biased_tile<HS, true>(a, tq, tk, tv, seg, rows, sms, s)  \
-        : launch_biased_tile<HS, false>(a, tq, tk, tv, seg, rows, sms, s))
-  return a.hs == 64 ? PA_TILE(64) : a.hs == 128 ? PA_TILE(128) : PA_TILE(256);
-#undef PA_TILE
+  if (a.G <= 128 && (a.max_rows == 0 || (int64_t)a.max_rows * a.G > 16)) {
+    const int rows = 128 / a.G;
+    if (!query_block_map(&tq, a.query, bf16, a.hs, a.nh, a.N, a.q_stride, a.G, rows)) return cudaErrorInvalidValue;
+    *kernels += 1;
+    if (cudaError_t e = PA_SIZES(launch_biased_tile, a, tq, tk, tv, seg, rows, sms, s)) return e;
+  }
+  if (merge == 0) return cudaSuccess;
+  *kernels += 1;
+  return PA_SIZES(launch_biased_merge, a, merge, s);
+#undef PA_SIZES
+#undef PA_TYPES
 }
 
 }  // namespace pa

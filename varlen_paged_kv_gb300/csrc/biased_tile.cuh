@@ -249,7 +249,11 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
     *err = 0;
     fence_mbar_init();
   }
-  pdl_wait();
+  // Beside the rows kernel, which let this one start once everything before it was done, there is nothing to
+  // wait for but at the end, by one CTA for all: this kernel must not be over before that one, since what
+  // comes next waits for this one only.
+  if (!a.after_rows) pdl_wait();
+  const bool waits = a.after_rows && blockIdx.x == gridDim.x - 1 && blockIdx.y == 0 && blockIdx.z == 0;
   if (warp == 0) {
     const TileItem it = tile_item(a, u, sub_rows, lane);
     if (lane == 0) *item_s = it;
@@ -257,7 +261,10 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
   if (blockIdx.x == 0 && g == 0 && rank == 0) check_biased_batch(a);
   __syncthreads();
   const TileItem it = *item_s;
-  if (it.rows <= 0) return;  // (all CTAs of a cluster agree)
+  if (it.rows <= 0) {  // (all CTAs of a cluster agree)
+    if (waits) pdl_wait();
+    return;
+  }
   if (warp == 1) {
     tmem_alloc(tmem_slot, L::kTmem);
     tmem_relinquish();
@@ -614,14 +621,14 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
     tc_fence_after();
     tmem_dealloc(tmem, L::kTmem);
   }
+  if (waits) pdl_wait();
 }
 
 // The CTAs of a cluster share an item's tiles, as many as run at once.
 template <int HS, bool BF16>
 static cudaError_t launch_biased_tile(const BiasedArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
                                       const CUtensorMap& tv, int seg, int sub_rows, int sms, cudaStream_t s) {
-  int64_t keys = (int64_t)a.max_blocks * a.bs;
-  if (a.window && !a.prefix && (int64_t)a.window + sub_rows < keys) keys = (int64_t)a.window + sub_rows;
+  const int64_t keys = keys_in_reach(a, sub_rows);
   const int64_t items = items_of_batch(a.N, a.B, sub_rows, 1, 1) * a.kvh;
   const int c = cluster_size(items, (int64_t)sms * (HS == 256 ? 1 : 2), ceil_div(keys, kBiTile), 4, 8);
   const dim3 grid((unsigned)(a.N / sub_rows + a.B), (unsigned)a.kvh, (unsigned)c);

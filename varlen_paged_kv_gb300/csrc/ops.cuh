@@ -211,6 +211,7 @@ struct BiasedArgs {
   int64_t q_stride;
   int32_t N, B, nh, kvh, G, hs, num_blocks, bs, max_blocks;
   int32_t window, max_rows;  // 0: none
+  int32_t after_rows;        // the tile kernel runs beside the rows kernel: it starts without waiting for it
   // s log2(e) of a score q.k is q.k * scale_log2, or with a cap cap_log2 * tanh(q.k * scale_cap)
   float scale_log2, scale_cap, cap_log2;
   // split pieces of the rows kernel: two slots per CTA, and what they hold
@@ -222,7 +223,7 @@ cudaError_t launch_fork(const PoolArgs& a, int sms, cudaStream_t s, int* kernels
 cudaError_t launch_compact(const PoolArgs& a, int sms, cudaStream_t s, int* kernels);
 cudaError_t launch_copy_pages(CopyArgs& a, int sms, cudaStream_t s);
 int biased_ctas(int hs, int sms);  // CTAs of the rows kernel
-cudaError_t launch_biased(const BiasedArgs& a, bool bf16, int sms, cudaStream_t s);
+cudaError_t launch_biased(const BiasedArgs& a, bool bf16, int sms, cudaStream_t s, int* kernels);
 cudaError_t launch_tables(const TableArgs& a, int sms, cudaStream_t s);
 cudaError_t launch_rotate(const RotateArgs& a, bool bf16, int hs, int sms, cudaStream_t s);
 cudaError_t launch_bounds(const PageArgs& a, bool bf16, cudaStream_t s);

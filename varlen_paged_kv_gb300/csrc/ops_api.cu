@@ -448,8 +448,9 @@ pa_status pa_biased_paged_attention(const void* query, const void* key_cache, co
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = a.part_o + slots * 16 * (size_t)dims->head_size;
   a.records = reinterpret_cast<int4*>(a.part_ml + slots * 16 * 2);
-  return launched(pa::launch_biased(a, dims->dtype == PA_BFLOAT16, sms, static_cast<cudaStream_t>(stream)),
-                  "biased attention launch");
+  int kernels = 0;
+  const cudaError_t e = pa::launch_biased(a, dims->dtype == PA_BFLOAT16, sms, static_cast<cudaStream_t>(stream), &kernels);
+  return launched(e, "biased attention launch", kernels);
 }
 
 }  // extern "C"
