@@ -278,3 +278,38 @@ def test_captured_calls_on_two_streams_at_once():
         torch.cuda.synchronize()
         for t, (_, _, want) in zip(outs, made):
             assert torch.equal(t["output"], want[0]) and torch.equal(t["lse"], want[1])
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("fill", [float("nan"), float("inf")])
+@pytest.mark.parametrize("past,q,kw,longest", [
+    ([60], [3], dict(), 4),                             # a cluster's item
+    ([60, 900, 0], [3, 4, 2], dict(softcap=20.0), 0),   # whole items and pieces that are merged
+    ([9000] * 3, [4, 4, 1], dict(bias=True), 4),
+    ([60, 5], [70, 200], dict(softcap=9.0), 0),         # tiles
+    ([2000], [12], dict(prefix=30), 0),                 # a cluster's tile
+    ([100, 30], [90, 64], dict(documents=25), 0)])
+def test_values_that_are_not_finite_reach_the_rows_that_see_them_only(past, q, kw, longest, fill, dtype):
+    nh, kvh, hs = 8, 2, 128
+    b = Batch(41, dtype, nh, kvh, hs, 16, past, q)
+    rules = Rules(b, seed=5, bound=longest or None, **kw)
+    for s in range(len(past)):  # a key among the new rows, seen by the later ones of its block alone
+        t = past[s] + q[s] // 2
+        b.value_cache[b.table[s, t // 16], t % 16, 1] = fill
+    out, lse = rules.call(b)
+    assert int(b.error) == 0
+    sc = hs ** -0.5
+    with np.errstate(invalid="ignore"):
+        o, z, _, _, _ = ref.biased_attention(f64(b.query).reshape(b.N, nh, hs), f64(b.key_cache), f64(b.value_cache), b.cum,
+                                             b.past, b.table, sc, rules.softcap, rules.slopes, rules.window, rules.first,
+                                             rules.prefix)
+    got = f64(out).reshape(o.shape)
+    clean = np.isfinite(o).all((1, 2))
+    assert clean.any() and not clean.all()
+    with np.errstate(invalid="ignore"):
+        rules.check(b, out, lse, rows=np.flatnonzero(clean))
+    # a weight may be 0 in 32 bits where it is not in 64, and 0 times infinity is NaN
+    far = ~clean
+    assert np.array_equal(np.isfinite(got[far]), np.isfinite(o[far]))
+    assert (np.isposinf(got[far]) | np.isnan(got[far]) | np.isfinite(got[far])).all()
+    assert (np.abs(f64(lse)[~np.isneginf(z)] - z[~np.isneginf(z)]) < 1e-3).all()

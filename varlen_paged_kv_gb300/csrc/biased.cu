@@ -80,6 +80,47 @@ __device__ __forceinline__ void check_biased_batch(const BiasedArgs& a) {
   if (bad) atomicOr(a.error, PA_DEVERR_BAD_BATCH);
 }
 
+// ---- rows whose result is not finite ---------------------------------------------------------
+// The products P V run over all keys that some row of an item sees, with weights of 0 where a row does
+// not, and 0 times a value that is not finite is NaN. So a row whose result is not finite is computed
+// again, here, over its own keys alone, by one warp in fp32 (channels from .. to_channel - 1 of it): what is
+// left is what those keys make of it.
+// (Slow, 0.1 ms for 5000 keys, but bounded; finite values never come here.)
+template <int HS, bool BF16>
+__device__ __noinline__ void redo_row(const BiasedArgs& a, int b, int c0, int q_len, int past, int j, int h, int lane,
+                                      int from, int to_channel) {
+  constexpr int E = HS / 32;  // channels of a lane
+  Seq s;
+  s.b = b, s.c0 = c0, s.q = q_len, s.past = past, s.ok = true;
+  const Keys k = keys_of_row(a, s, a.prefix ? a.prefix[b] : 0, j);
+  const int64_t row = c0 + j;
+  auto value = [](uint16_t x) { return BF16 ? __uint_as_float((uint32_t)x << 16) : __half2float(__ushort_as_half(x)); };
+  float q[E], o[E], m = -INFINITY, l = 0.f;
+  for (int e = 0; e < E; ++e) q[e] = value(a.query[row * a.q_stride + (int64_t)h * HS + lane * E + e]), o[e] = 0.f;
+  for (int t = k.lo; t < k.hi; ++t) {
+    const int phys = a.table[(int64_t)b * a.max_blocks + t / a.bs];
+    const bool there = phys >= 0 && phys < a.num_blocks;  // (a page outside the pool reads as zeros)
+    const int64_t at = (((int64_t)phys * a.bs + t % a.bs) * a.kvh + h / a.G) * HS + lane * E;
+    float x = 0.f;
+    for (int e = 0; e < E; ++e) x += q[e] * (there ? value(a.key_cache[at + e]) : 0.f);
+    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    x = a.cap_log2 != 0.f ? a.cap_log2 * tanh_of(x * a.scale_cap) : x * a.scale_log2;
+    if (a.slopes) x -= a.slopes[h] * 1.4426950408889634f * (float)abs(past + j - t);
+    const float to = fmaxf(m, x), f = to == -INFINITY ? 1.f : fast_exp2(m - to), w = to == -INFINITY ? 0.f : fast_exp2(x - to);
+    m = to;
+    l = l * f + w;
+    for (int e = 0; e < E; ++e) o[e] = (f == 1.f ? o[e] : o[e] * f) + w * (there ? value(a.value_cache[at + e]) : 0.f);
+  }
+  uint16_t* out = static_cast<uint16_t*>(a.output) + (row * a.nh + h) * HS + lane * E;
+  for (int e = 0; e < E; e += 2)
+    if (lane * E + e >= from && lane * E + e < to_channel) *reinterpret_cast<uint32_t*>(out + e) = pack2<BF16>(o[e] / l, o[e + 1] / l);
+}
+
+__device__ __forceinline__ bool finite4(float x, float y, float z, float w) {
+  // (a sum of magnitudes is finite where all are, but for an overflow, which only costs a second look)
+  return fabsf(x) + fabsf(y) + fabsf(z) + fabsf(w) < INFINITY;
+}
+
 // ---- few rows: equal shares of all tiles ----------------------------------------------------
 // All (sequence, KV head, 16 rows) units stand in a row, each as long as its 64-key tiles and
 // kBiCost; CTA c of C takes the c-th C-th of that. What a CTA has of a unit is an item: its
@@ -100,7 +141,7 @@ struct BiRows {
   static constexpr int kCl = kMl + 2 * 4 * 16 * 4;            // float [2][16]: m and l of the CTA
   static constexpr int kPre = kCl + 2 * 16 * 4;               // int64 [kBiThreads + 1]: costs before each thread's sequences
   static constexpr int kBars = kPre + (kBiThreads + 2) * 8;
-  static constexpr int kAbort = kBars + 2 * kStages * 8;      // abort flag, error word
+  static constexpr int kAbort = kBars + 2 * kStages * 8;      // abort flag, error word, rows to redo
   static constexpr int kBytes = kAbort + 16 + 1024;
 };
 static_assert(2 * (BiRows<128>::kBytes + 1024) <= 233472 && BiRows<256>::kBytes <= 232448, "rows kernel's shared memory");
@@ -204,7 +245,7 @@ struct BiWalk {
 // take 12.6; but a cluster's CTAs are at most eight, and a unit is not cut between clusters.
 template <int HS, bool BF16, bool CLUSTER>
 __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
-    biased_rows_kernel(const BiasedArgs a, const __grid_constant__ CUtensorMap tmK,
+    biased_rows_kernel(const __grid_constant__ BiasedArgs a, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const int seg_rows) {
   using L = BiRows<HS>;
   constexpr int NKS = HS / 16, ND = HS / 8;
@@ -219,6 +260,7 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
   uint64_t* empty = full + L::kStages;
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kAbort);
   uint32_t* err = reinterpret_cast<uint32_t*>(smem + L::kAbort + 4);
+  uint32_t* redo = reinterpret_cast<uint32_t*>(smem + L::kAbort + 8);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kStages; ++s) {
@@ -227,6 +269,7 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
     }
     *abort = 0;
     *err = 0;
+    *redo = 0;
     fence_mbar_init();
   }
   pdl_wait();
@@ -302,9 +345,9 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
     // ---- producer ----
     const int nseg = kBiTile / seg_rows, oob = a.num_blocks * a.bs;
     int4 head = make_int4(0, 0, 0, 0);
-    int cont = 0;
+    int cont = 0, head_b = 0;
     while (CLUSTER ? walk.only(a, c % a.kvh, rank, gridDim.z, it) : walk.next(a, lane, it)) {
-      if (it.first && !it.last) head = make_int4(it.n_rows, it.c0, it.r_first, it.g);
+      if (it.first && !it.last) head = make_int4(it.n_rows, it.c0, it.r_first, it.g), head_b = it.b;
       if (!it.first) cont = it.last ? 2 : 1;
       const int* table = a.table + (int64_t)it.b * a.max_blocks;
       auto slot = [&](int t) {  // this lane's segment of tile t: its first cache row
@@ -337,7 +380,7 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
         z = z_next;
       }
     }
-    if (!CLUSTER && lane == 0) a.records[2 * c] = head, a.records[2 * c + 1] = make_int4(cont, 0, 0, 0);
+    if (!CLUSTER && lane == 0) a.records[2 * c] = head, a.records[2 * c + 1] = make_int4(cont, head_b, 0, 0);
   } else {
     // ---- consumers: warp w has keys 16w .. 16w + 15 of every tile ----
     const int w = warp, tq = lane & 3, gq = lane >> 2;
@@ -564,6 +607,7 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
           const float inv = M == -INFINITY ? 0.f : 1.f / S;
           uint2 out = make_uint2(pack2<BF16>(x.x * inv, x.y * inv), pack2<BF16>(x.z * inv, x.w * inv));
           if (M == -INFINITY) out = make_uint2(0, 0);
+          else if (!finite4(x.x * inv, x.y * inv, x.z * inv, x.w * inv)) atomicOr(redo, 1u << r);
           *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.output) + at * HS + cc) = out;
           if (a.lse && cc == 0) a.lse[at] = M == -INFINITY ? -INFINITY : (M + fast_log2(S)) * 0.69314718055994531f;
         } else {
@@ -572,6 +616,16 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
         }
       }
       named_bar_sync(1, 128);  // the combining buffers are free again
+      if (!CLUSTER && *redo) {
+        const uint32_t rows = *redo;
+        named_bar_sync(1, 128);
+        if (threadIdx.x == 0) *redo = 0;
+        for (int r = w; r < it.n_rows; r += 4)
+          if (rows >> r & 1)
+            redo_row<HS, BF16>(a, it.b, it.c0, it.q, it.past, (it.r_first + r) / a.G, it.g * a.G + (it.r_first + r) % a.G,
+                               lane, 0, HS);
+        named_bar_sync(1, 128);
+      }
     }
   }
   if constexpr (CLUSTER) {
@@ -594,10 +648,14 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
       const float inv = M == -INFINITY ? 0.f : 1.f / S;
       uint2 out = make_uint2(pack2<BF16>(x[0] * inv, x[1] * inv), pack2<BF16>(x[2] * inv, x[3] * inv));
       if (M == -INFINITY) out = make_uint2(0, 0);
+      else if (!finite4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv)) atomicOr(redo, 1u << r);
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.output) + at * HS + cc) = out;
       if (a.lse && cc == 0) a.lse[at] = M == -INFINITY ? -INFINITY : (M + fast_log2(S)) * 0.69314718055994531f;
     }
     cluster_sync();  // no CTA leaves while another reads its shared memory
+    for (int r = warp; *redo && r < it.n_rows; r += kBiThreads / 32)  // (this CTA's columns)
+      if (*redo >> r & 1)
+        redo_row<HS, BF16>(a, it.b, it.c0, it.q, it.past, r / a.G, it.g * a.G + r % a.G, lane, c0 * 4, (c0 + nc) * 4);
   }
   __syncthreads();
   if (threadIdx.x == 0 && *err && a.error) atomicOr(a.error, *err);
@@ -605,10 +663,10 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
 
 // The pieces of the units that the cuts between CTAs went through, in order: CTA c of the rows
 // kernel began such a unit (record 2c), its next ones went on with it (record 2k + 1: 1, and 2 for
-// the last). A lane has four columns of a row, eight warps share the pieces: what bounds it is the
+// the last; its second number is the sequence of the unit that record 2k begins). A lane has four columns of a row, eight warps share the pieces: what bounds it is the
 // latency of three loads, one after the other (a record, the next ones, the pieces).
 template <int HS, bool BF16>
-__global__ void __launch_bounds__(kMergeThreads) biased_merge_kernel(const BiasedArgs a, const int ctas) {
+__global__ void __launch_bounds__(kMergeThreads) biased_merge_kernel(const __grid_constant__ BiasedArgs a, const int ctas) {
   constexpr int WARPS = kMergeThreads / 32;
   __shared__ float part[WARPS][6][32];
   pdl_wait();
@@ -649,7 +707,7 @@ __global__ void __launch_bounds__(kMergeThreads) biased_merge_kernel(const Biase
 #pragma unroll
     for (int e = 0; e < 4; ++e) part[warp][2 + e][lane] = x[e];
     __syncthreads();
-    if (warp != 0 || i >= head.x * (HS / 4)) continue;
+    if (warp != 0) continue;
 #pragma unroll
     for (int w = 1; w < WARPS; ++w)
       add(part[w][0][lane], part[w][1][lane],
@@ -659,8 +717,21 @@ __global__ void __launch_bounds__(kMergeThreads) biased_merge_kernel(const Biase
     const float inv = M == -INFINITY ? 0.f : 1.f / S;
     uint2 out = make_uint2(pack2<BF16>(x[0] * inv, x[1] * inv), pack2<BF16>(x[2] * inv, x[3] * inv));
     if (M == -INFINITY) out = make_uint2(0, 0);
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.output) + at * HS + cc) = out;
-    if (a.lse && cc == 0) a.lse[at] = M == -INFINITY ? -INFINITY : (M + fast_log2(S)) * 0.69314718055994531f;
+    const bool there = i < head.x * (HS / 4);
+    if (there) {
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.output) + at * HS + cc) = out;
+      if (a.lse && cc == 0) a.lse[at] = M == -INFINITY ? -INFINITY : (M + fast_log2(S)) * 0.69314718055994531f;
+    }
+    unsigned bad = __ballot_sync(0xffffffffu, there && M != -INFINITY && !finite4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv));
+    while (bad) {  // (these 32 lanes' columns of the row)
+      const int first = __ffs(bad) - 1, row = __shfl_sync(0xffffffffu, r, first), rr = head.z + row;
+      const unsigned same = __ballot_sync(0xffffffffu, r == row && there);
+      const int from = __shfl_sync(0xffffffffu, cc, __ffs(same) - 1), b = a.records[2 * c + 1].y;
+      __syncwarp();
+      redo_row<HS, BF16>(a, b, head.y, a.cum[b + 1] - head.y, a.past[b], rr / a.G, head.w * a.G + rr % a.G, lane, from,
+                         from + 4 * __popc(same));
+      bad &= ~same;
+    }
   }
 }
 

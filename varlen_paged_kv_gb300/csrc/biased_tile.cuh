@@ -23,11 +23,12 @@ struct BiTile {
   static constexpr int kItem = (kAbort + 12 + 15) / 16 * 16;
   static constexpr int kMl = kItem + 64;                            // float [2][128]: m and l of the rows
   static constexpr int kX = kMl + 2 * 128 * 4;                      // float [2][128][2]: maxima and sums of half rows
+  static constexpr int kRedo = kX + 2 * 128 * 2 * 4;                // uint32 [4]: rows whose result is not finite
   static constexpr uint32_t kTmem = HS == 256 ? 512 : 256;          // S, S, O at columns 0, 64, 128
   static_assert(128 * HS * 4 <= 2 * kStages * kTileBytes, "the cluster's partial result lies over the ring");
   // At least a third of an SM's shared memory, so that no more CTAs share an SM than find TMEM
   // there: a CTA that waited for TMEM while its cluster waits for it could wait for ever.
-  static constexpr int kNeed = kX + 2 * 128 * 2 * 4 + 1024;
+  static constexpr int kNeed = kRedo + 16 + 1024;
   static constexpr int kBytes = kNeed < 80 * 1024 ? 80 * 1024 : kNeed;
 };
 // (where the compiler lays the rarer path out of line: the softmax's code is long, and what it jumps
@@ -201,7 +202,7 @@ __device__ __forceinline__ Keys keys_of_item_row(const BiasedArgs& a, const Tile
 
 template <int HS, bool BF16>
 __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
-    biased_tile_kernel(const BiasedArgs a, const __grid_constant__ CUtensorMap tmQ,
+    biased_tile_kernel(const __grid_constant__ BiasedArgs a, const __grid_constant__ CUtensorMap tmQ,
                        const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const int seg_rows, const int sub_rows) {
   using L = BiTile<HS>;
@@ -228,6 +229,7 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
   TileItem* item_s = reinterpret_cast<TileItem*>(smem + L::kItem);
   float* ml = reinterpret_cast<float*>(smem + L::kMl);
   float2* half = reinterpret_cast<float2*>(smem + L::kX);  // [2][128]
+  uint32_t* redo = reinterpret_cast<uint32_t*>(smem + L::kRedo);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // later rows see more keys, so their items start first
   const int g = blockIdx.y, u = gridDim.x - 1 - blockIdx.x;
@@ -247,6 +249,7 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
     }
     *abort = 0;
     *err = 0;
+    for (int i = 0; i < 4; ++i) redo[i] = 0;
     fence_mbar_init();
   }
   // Beside the rows kernel, which let this one start once everything before it was done, there is nothing to
@@ -557,6 +560,12 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
         }
         if (live) {
           const bool some = m_used != -INFINITY;
+          bool fine = true;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            fine = fine && finite4(__uint_as_float(ov[e]) * inv, __uint_as_float(ov[e + 1]) * inv,
+                                   __uint_as_float(ov[e + 2]) * inv, __uint_as_float(ov[e + 3]) * inv);
+          if (some && !fine) atomicOr(&redo[row >> 5], 1u << (row & 31));
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
             uint32_t w[4];
@@ -611,12 +620,17 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
       }
       const int64_t at = (int64_t)(it.row0 + r / a.G) * a.nh + g * a.G + r % a.G;
       *reinterpret_cast<uint2*>(out + at * HS + quad * 4) = make_uint2(pack2<BF16>(x.x, x.y), pack2<BF16>(x.z, x.w));
+      if (!finite4(x.x, x.y, x.z, x.w)) atomicOr(&redo[r >> 5], 1u << (r & 31));
     }
     cluster_sync();  // no CTA leaves while another reads its shared memory
   }
   tc_fence_before();
   __syncthreads();  // (no warp waits any more: whichever gave up has said so)
   if (threadIdx.x == 0 && *err && a.error) atomicOr(a.error, *err);
+  if (redo[0] | redo[1] | redo[2] | redo[3])
+    for (int r = warp; r < it.rows * a.G; r += THREADS / 32)
+      if (redo[r >> 5] >> (r & 31) & 1)  // (the item's rows counted from 0)
+        redo_row<HS, BF16>(a, it.b, it.row0, it.total - it.pos0, it.pos0, r / a.G, g * a.G + r % a.G, lane, 0, HS);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, L::kTmem);
