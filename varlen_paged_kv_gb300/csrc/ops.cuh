@@ -158,10 +158,11 @@ struct PoolArgs {
   int32_t* keeper;             // per page (fork)
   uint4* words;
   int2* chunks;
-  int32_t* first_child;        // per old row (fork, else null)
+  int32_t *first_child, *last;  // per old row (fork, else null): its lowest new row, its partly filled page
   uint32_t* row_bits;          // 32 new rows each (fork)
   int32_t* holes;              // per page (compact)
   int32_t B, Bn, max_blocks, bs, num_blocks, num_chunks, cap, max_moves;
+  int32_t row_blocks;  // blocks of the last kernel that write rows, the others pages
 };
 // bytes of the workspace of num_blocks pages; fills in its pointers where `a` is given
 inline size_t pool_workspace(int32_t num_blocks, bool fork, PoolArgs* a, uint8_t* base) {
@@ -173,7 +174,7 @@ inline size_t pool_workspace(int32_t num_blocks, bool fork, PoolArgs* a, uint8_t
     return at;
   };
   const size_t marks = take(pages), old_marks = take(fork ? pages : 0), keeper = take(fork ? 4 * pages : 0), cleared = off;
-  const size_t words = take(pages / 2), totals = take(8 * chunks), child = take(fork ? 4 * rows : 0),
+  const size_t words = take(pages / 2), totals = take(8 * chunks), child = take(fork ? 4 * rows : 0), last = take(fork ? 4 * rows : 0),
                row_bits = take(fork ? rows / 8 : 0), holes = take(fork ? 0 : 4 * pages);
   if (a) {
     a->clear = reinterpret_cast<uint4*>(base);
@@ -185,6 +186,7 @@ inline size_t pool_workspace(int32_t num_blocks, bool fork, PoolArgs* a, uint8_t
     a->words = reinterpret_cast<uint4*>(base + words);
     a->chunks = reinterpret_cast<int2*>(base + totals);
     a->first_child = fork ? reinterpret_cast<int32_t*>(base + child) : nullptr;
+    a->last = fork ? reinterpret_cast<int32_t*>(base + last) : nullptr;
     a->row_bits = reinterpret_cast<uint32_t*>(base + row_bits);
     a->holes = reinterpret_cast<int32_t*>(base + holes);
     a->num_chunks = (int32_t)chunks;

@@ -35,7 +35,7 @@ constexpr int kChunk = 1024;      // pages
 template <int ROWS_, int K_>
 struct Walk {
   static constexpr int ROWS = ROWS_, K = K_, COLUMNS = 32 * K_;
-  __device__ __forceinline__ static int parts(int columns) { return (columns + COLUMNS - 1) / COLUMNS; }
+  __host__ __device__ __forceinline__ static int parts(int columns) { return (columns + COLUMNS - 1) / COLUMNS; }
   // row and first column of item i
   __device__ __forceinline__ static int2 item(int i, int parts) {
     return parts == 1 ? make_int2(i, 0) : make_int2(i / parts, i % parts * COLUMNS);
@@ -145,7 +145,12 @@ __global__ void __launch_bounds__(kPoolThreads) pool_clear_kernel(const PoolArgs
   for (int64_t i = blockIdx.x * (int64_t)kPoolThreads + threadIdx.x; i < a.clear_words; i += (int64_t)gridDim.x * kPoolThreads)
     a.clear[i] = make_uint4(0, 0, 0, 0);
   if (a.pages_end && blockIdx.x == 0 && threadIdx.x == 0) *a.pages_end = 0;  // (the finish takes a maximum)
-  if (a.first_child && blockIdx.x == gridDim.x - 1) find_children(a, a.first_child);
+  if (a.first_child && blockIdx.x == gridDim.x - 1) {
+    extern __shared__ int children[];  // [B]
+    find_children(a, children);
+    __syncthreads();
+    for (int p = threadIdx.x; p < a.B; p += kPoolThreads) a.first_child[p] = children[p];
+  }
 }
 
 template <bool FORK>
@@ -156,22 +161,13 @@ __global__ void __launch_bounds__(kPoolThreads) pool_mark_kernel(const PoolArgs 
   if (FORK && blockIdx.x == 0)
     for (int b = threadIdx.x; b < a.Bn; b += kPoolThreads)
       if (a.parents[b] < -1 || a.parents[b] >= a.B) err = PA_DEVERR_BAD_BATCH;
-  err |= mark_pages<FORK, BigWalk>(a, a.past, a.held, a.first_child, ByteMarks{a.marks, a.old_marks, a.keeper}, nullptr,
+  err |= mark_pages<FORK, BigWalk>(a, a.past, a.held, a.first_child, ByteMarks{a.marks, a.old_marks, a.keeper}, a.last,
                                    blockIdx.x * (kPoolThreads / 32) + (threadIdx.x >> 5),
                                    gridDim.x * (kPoolThreads / 32), threadIdx.x & 31);
   if (err) atomicOr(a.ws_error, err);
 }
 
 // ---- words ---------------------------------------------------------------------------------
-// whether new row b takes a page of its own for the last, partly filled one of its parent
-template <typename Held>
-__device__ __forceinline__ bool row_copies(const PoolArgs& a, int b, Held held_elsewhere) {
-  const int p = a.parents[b], past = p < 0 ? 0 : a.past[p];
-  if (past % a.bs == 0) return false;
-  const int x = a.table[(int64_t)p * a.max_blocks + past / a.bs];
-  return held_elsewhere(x) || (a.pinned && a.pinned[x]);
-}
-
 // word i: {bits of the first kind, of the second, the counts of both before it in its chunk}.
 // fork: the first kind are the pages to give back; compact: the holes, and the movers. Blocks behind
 // the chunks': the fork's rows that copy.
@@ -182,10 +178,15 @@ __global__ void __launch_bounds__(kPoolThreads) pool_words_kernel(const PoolArgs
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (FORK && (int)blockIdx.x >= a.num_chunks) {
+    // whether a new row takes a page of its own for the last, partly filled one of its parent (a refused
+    // fork's parents and pages may be anything)
     const int b = (blockIdx.x - a.num_chunks) * kPoolThreads + threadIdx.x;
-    // (a refused fork's parents and pages may be anything)
-    const bool copy = b < a.Bn && *a.ws_error == 0 &&
-                      row_copies(a, b, [&](int x) { return a.keeper[x] != a.Bn - b || a.marks[x]; });
+    const int p = b < a.Bn ? a.parents[b] : -1, fine = *a.ws_error == 0;
+    bool copy = false;
+    if (fine && p >= 0) {
+      const int past = a.past[p], x = a.last[p];
+      if (past % a.bs) copy = a.keeper[x] != a.Bn - b || a.marks[x] || (a.pinned && a.pinned[x]);
+    }
     const uint32_t m = __ballot_sync(0xffffffffu, copy);
     if (lane == 0) a.row_bits[(blockIdx.x - a.num_chunks) * (kPoolThreads / 32) + warp] = m;
     return;
@@ -284,10 +285,9 @@ struct SmallRows {
 // ---- finish: fork --------------------------------------------------------------------------
 // The outputs, spread over the threads from `i0` on in steps of `step`. A refused fork (err) describes an
 // empty batch and changes nothing that it was given. `parents` and `pasts` are the call's, or their copies.
-template <typename W, typename Words, typename Rows>
-__device__ __forceinline__ void fork_outputs(const PoolArgs& a, uint32_t err, int head, int count, int copies, int freed,
-                                             const Words& pages, const Rows& rows, const int* parents, const int* pasts,
-                                             int i0, int step) {
+template <typename W, typename Rows>
+__device__ __forceinline__ void fork_rows(const PoolArgs& a, uint32_t err, int head, int count, int copies, int freed,
+                                          const Rows& rows, const int* parents, const int* pasts, int i0, int step) {
   auto rank_of = [&](int b) {  // which copy row b makes, -1 for none
     if (err) return -1;
     const int2 w = rows.at(b >> 5);
@@ -298,17 +298,19 @@ __device__ __forceinline__ void fork_outputs(const PoolArgs& a, uint32_t err, in
     a.state_out[0] = err ? head : ring_index(a, head, copies);
     a.state_out[1] = err ? count : count - copies + freed;
   }
-  for (int b = i0; b < a.Bn; b += step) {
-    const int p = err ? -1 : parents[b], past = p < 0 ? 0 : pasts[p], rank = rank_of(b);
-    a.past_out[b] = past;
-    a.held_out[b] = past / a.bs + (past % a.bs != 0);
-    if (err || b >= copies) a.copies[b] = make_int2(-1, -1);
-    if (rank >= 0)
-      a.copies[rank] = make_int2(a.table[(int64_t)p * a.max_blocks + past / a.bs], a.ring[ring_index(a, head, rank)]);
-  }
   const int parts = W::parts(a.max_blocks), items = a.Bn * parts, lane = threadIdx.x & 31, warps = step / 32;
   for (int j0 = i0 / 32; j0 < items; j0 += W::ROWS * warps) {
     int x[W::ROWS][W::K];
+#pragma unroll
+    for (int n = 0; n < W::ROWS; ++n) {  // (the parent's entries, whichever of them are its pages)
+      const int2 it = W::item(j0 + n * warps, parts);
+      const int p = err || j0 + n * warps >= items ? -1 : parents[it.x];
+#pragma unroll
+      for (int k = 0; k < W::K; ++k) {
+        const int c = it.y + k * 32 + lane;
+        x[n][k] = p >= 0 && c < a.max_blocks ? __ldg(a.table + (int64_t)p * a.max_blocks + c) : -1;
+      }
+    }
 #pragma unroll
     for (int n = 0; n < W::ROWS; ++n) {
       if (j0 + n * warps >= items) break;
@@ -318,24 +320,29 @@ __device__ __forceinline__ void fork_outputs(const PoolArgs& a, uint32_t err, in
 #pragma unroll
       for (int k = 0; k < W::K; ++k) {
         const int c = it.y + k * 32 + lane;
-        x[n][k] = c >= need ? -1 : rank >= 0 && c == whole ? a.ring[ring_index(a, head, rank)]
-                                                           : a.table[(int64_t)p * a.max_blocks + c];
+        if (c >= a.max_blocks) break;
+        int page = c < need ? x[n][k] : -1;
+        if (rank >= 0 && c == whole) {
+          const int fresh = a.ring[ring_index(a, head, rank)];
+          a.copies[rank] = make_int2(page, fresh);
+          page = fresh;
+        }
+        a.table_out[(int64_t)b * a.max_blocks + c] = page;
       }
-    }
-#pragma unroll
-    for (int n = 0; n < W::ROWS; ++n) {
-      if (j0 + n * warps >= items) break;
-      const int2 it = W::item(j0 + n * warps, parts);
-#pragma unroll
-      for (int k = 0; k < W::K; ++k) {
-        const int c = it.y + k * 32 + lane;
-        if (c < a.max_blocks) a.table_out[(int64_t)it.x * a.max_blocks + c] = x[n][k];
+      if (it.y == 0 && lane == 0) {
+        a.past_out[b] = past;
+        a.held_out[b] = need;
+        if (err || b >= copies) a.copies[b] = make_int2(-1, -1);
       }
     }
   }
-  if (err) return;
+}
+
+// the pages given back, behind the last free one
+template <typename Words>
+__device__ __forceinline__ void fork_pages(const PoolArgs& a, int head, int count, const Words& pages, int i0, int step) {
 #pragma unroll 4
-  for (int x = i0; x < a.num_blocks; x += step) {  // the pages given back, behind the last free one
+  for (int x = i0; x < a.num_blocks; x += step) {
     const uint4 w = pages.at(x >> 5);
     if (w.x >> (x & 31) & 1) {
       const int r = (int)w.z + __popc(w.x & ((1u << (x & 31)) - 1));
@@ -362,8 +369,14 @@ __global__ void __launch_bounds__(kPoolThreads) fork_finish_kernel(const PoolArg
   scan_pairs(row_words, before, [&](int i) { return make_int2(__popc(a.row_bits[i]), 0); });
   const int freed = sums[a.num_chunks].x, copies = before[row_words].x;
   const uint32_t err = fork_refusal(a, *a.ws_error, head, count, copies, freed);
-  fork_outputs<BigWalk>(a, err, head, count, copies, freed, BigWords{a.words, sums}, BigRows{a.row_bits, before}, a.parents, a.past,
-               blockIdx.x * kPoolThreads + threadIdx.x, gridDim.x * kPoolThreads);
+  // (rows by the first blocks, pages by the others, side by side)
+  const int i = blockIdx.x * kPoolThreads + threadIdx.x;
+  if ((int)blockIdx.x < a.row_blocks)
+    fork_rows<BigWalk>(a, err, head, count, copies, freed, BigRows{a.row_bits, before}, a.parents, a.past, i,
+                       a.row_blocks * kPoolThreads);
+  else if (!err)
+    fork_pages(a, head, count, BigWords{a.words, sums}, i - a.row_blocks * kPoolThreads,
+               ((int)gridDim.x - a.row_blocks) * kPoolThreads);
 }
 
 // Everything in one CTA: lengths, parents and pins are loaded at once, the table's entries after them,
@@ -423,8 +436,8 @@ __global__ void __launch_bounds__(kSmallThreads) fork_small_kernel(const PoolArg
   });
   const int freed = sums[n_sums].x, copies = sums[n_sums].y;
   err = fork_refusal(a, err, head, count, copies, freed);
-  fork_outputs<SmallWalk>(a, err, head, count, copies, freed, SmallWords{old, nullptr, sums}, SmallRows{rows, sums}, parent, past,
-               threadIdx.x, threads);
+  fork_rows<SmallWalk>(a, err, head, count, copies, freed, SmallRows{rows, sums}, parent, past, threadIdx.x, threads);
+  if (!err) fork_pages(a, head, count, SmallWords{old, nullptr, sums}, threadIdx.x, threads);
 }
 
 // ---- finish: compact -----------------------------------------------------------------------
@@ -464,9 +477,10 @@ __device__ __forceinline__ int count_moves(const PoolArgs& a, const BigWords& pa
 }
 
 // The outputs, spread over the threads from `i0` on in steps of `step`; hole(r) is the r-th hole.
-template <typename W, typename Words, typename Hole>
-__device__ __forceinline__ int compact_outputs(const PoolArgs& a, uint32_t err, int holes, int movers, int moves,
-                                               const Words& pages, Hole hole, int i0, int step) {
+// Ring and copies, page by page; one more than the highest page in use that the thread saw.
+template <typename Words, typename Hole>
+__device__ __forceinline__ int compact_pages(const PoolArgs& a, uint32_t err, int holes, int movers, int moves,
+                                             const Words& pages, Hole hole, int i0, int step) {
   if (i0 == 0) {
     a.error[0] = err;
     a.state_out[0] = 0;
@@ -474,26 +488,33 @@ __device__ __forceinline__ int compact_outputs(const PoolArgs& a, uint32_t err, 
   }
   for (int r = moves + i0; r < a.max_moves; r += step) a.copies[r] = make_int2(-1, -1);
   int end = 0;
-  if (!err)
+  if (err) return end;
 #pragma unroll 4
-    for (int x = i0; x < a.num_blocks; x += step) {
-      const uint4 w = pages.at(x >> 5);
-      const uint32_t bit = 1u << (x & 31);
-      const int h = (int)w.z + __popc(w.x & (bit - 1)), m = (int)w.w + __popc(w.y & (bit - 1));
-      bool free = false;
-      if (w.x & bit) {
-        free = h >= moves;
-      } else if (w.y & bit) {
-        const int above = movers - 1 - m;
-        if (above < moves) {
-          a.copies[above] = make_int2(x, hole(above));
-          free = true;
-        }
+  for (int x = i0; x < a.num_blocks; x += step) {
+    const uint4 w = pages.at(x >> 5);
+    const uint32_t bit = 1u << (x & 31);
+    const int h = (int)w.z + __popc(w.x & (bit - 1)), m = (int)w.w + __popc(w.y & (bit - 1));
+    bool free = false;
+    if (w.x & bit) {
+      free = h >= moves;
+    } else if (w.y & bit) {
+      const int above = movers - 1 - m;
+      if (above < moves) {
+        a.copies[above] = make_int2(x, hole(above));
+        free = true;
       }
-      // free pages below x: the holes that nothing moves into, and the pages moved away
-      if (free) a.ring[max(0, h - moves) + max(0, m - (movers - moves))] = x;
-      else end = max(end, x + 1);
     }
+    // free pages below x: the holes that nothing moves into, and the pages moved away
+    if (free) a.ring[max(0, h - moves) + max(0, m - (movers - moves))] = x;
+    else end = max(end, x + 1);
+  }
+  return end;
+}
+
+// the table, entry by entry
+template <typename W, typename Words, typename Hole>
+__device__ __forceinline__ void compact_table(const PoolArgs& a, uint32_t err, int movers, int moves, const Words& pages,
+                                              Hole hole, int i0, int step) {
   const int parts = W::parts(a.max_blocks), items = a.B * parts, lane = threadIdx.x & 31, warps = step / 32;
   for (int j0 = i0 / 32; j0 < items; j0 += W::ROWS * warps) {
     int x[W::ROWS][W::K], held[W::ROWS];
@@ -532,7 +553,6 @@ __device__ __forceinline__ int compact_outputs(const PoolArgs& a, uint32_t err, 
       }
     }
   }
-  return end;
 }
 
 // the holes in order
@@ -559,8 +579,15 @@ __global__ void __launch_bounds__(kPoolThreads) compact_finish_kernel(const Pool
   if (!err && holes > a.cap) err = PA_DEVERR_BAD_BATCH;
   const BigWords pages{a.words, smem2};
   const int moves = err ? 0 : count_moves(a, pages);
-  int end = compact_outputs<BigWalk>(a, err, holes, movers, moves, pages, [&](int r) { return __ldg(a.holes + r); },
-                            blockIdx.x * kPoolThreads + threadIdx.x, gridDim.x * kPoolThreads);
+  auto hole = [&](int r) { return __ldg(a.holes + r); };
+  // (rows by the first blocks, pages by the others, side by side)
+  const int i = blockIdx.x * kPoolThreads + threadIdx.x;
+  if ((int)blockIdx.x < a.row_blocks) {
+    compact_table<BigWalk>(a, err, movers, moves, pages, hole, i, a.row_blocks * kPoolThreads);
+    return;
+  }
+  int end = compact_pages(a, err, holes, movers, moves, pages, hole, i - a.row_blocks * kPoolThreads,
+                          ((int)gridDim.x - a.row_blocks) * kPoolThreads);
   end = __reduce_max_sync(0xffffffffu, end);
   if ((threadIdx.x & 31) == 0 && end) atomicMax(a.pages_end, end);
 }
@@ -608,7 +635,9 @@ __global__ void __launch_bounds__(kSmallThreads) compact_small_kernel(const Pool
   if (n) atomicAdd(&total[0], n);
   __syncthreads();
   const int moves = err ? 0 : min(total[0], a.max_moves);
-  const int end = compact_outputs<SmallWalk>(a, err, H, M, moves, pages, [&](int r) { return list[r]; }, threadIdx.x, threads);
+  auto hole = [&](int r) { return list[r]; };
+  const int end = compact_pages(a, err, H, M, moves, pages, hole, threadIdx.x, threads);
+  compact_table<SmallWalk>(a, err, M, moves, pages, hole, threadIdx.x, threads);
   if (end) atomicMax(&total[1], end);
   __syncthreads();
   if (threadIdx.x == 0) *a.pages_end = total[1];
@@ -712,17 +741,20 @@ static cudaError_t launch_pool(const PoolArgs& a, int sms, cudaStream_t s, int* 
   const dim3 block(kPoolThreads);
   const size_t sums = 8 * ((size_t)a.num_chunks + 1), rows_smem = FORK ? 8 * ((size_t)ceil_div(a.Bn, 32) + 1) : 0;
   *kernels = FORK ? 4 : 5;
-  if (cudaError_t e = launch_pdl(pool_clear_kernel, dim3(grid_of(a.clear_words, sms, 4)), block, 0, s, a)) return e;
-  const int64_t parts = ceil_div(a.max_blocks, BigWalk::COLUMNS) * 32;
+  if (cudaError_t e = launch_pdl(pool_clear_kernel, dim3(grid_of(a.clear_words, sms, 4)), block, FORK ? (size_t)a.B * 4 : 0, s, a))
+    return e;
+  const int64_t parts = BigWalk::parts(a.max_blocks) * 32;
   if (cudaError_t e = launch_pdl(pool_mark_kernel<FORK>, dim3(grid_of(a.B * parts, sms, 8)), block, 0, s, a)) return e;
-  const int64_t row_blocks = FORK ? ceil_div(a.Bn, kPoolThreads) : 0;
-  if (cudaError_t e = launch_pdl(pool_words_kernel<FORK>, dim3((unsigned)(a.num_chunks + row_blocks)), block, 0, s, a)) return e;
-  const int64_t rows = FORK ? a.Bn : a.B, work = rows * parts > a.num_blocks ? rows * parts : a.num_blocks;
+  const int64_t more = FORK ? ceil_div(a.Bn, kPoolThreads) : 0;
+  if (cudaError_t e = launch_pdl(pool_words_kernel<FORK>, dim3((unsigned)(a.num_chunks + more)), block, 0, s, a)) return e;
+  PoolArgs b = a;
+  b.row_blocks = grid_of((FORK ? a.Bn : a.B) * parts, sms, 4);
+  const dim3 grid(b.row_blocks + grid_of(ceil_div(a.num_blocks, 2), sms, 4));
   if constexpr (FORK) {
-    return launch_pdl(fork_finish_kernel, dim3(grid_of(work, sms, 4)), block, sums + rows_smem, s, a);
+    return launch_pdl(fork_finish_kernel, grid, block, sums + rows_smem, s, b);
   } else {
     if (cudaError_t e = launch_pdl(compact_lists_kernel, dim3(grid_of(a.num_blocks, sms, 4)), block, sums, s, a)) return e;
-    return launch_pdl(compact_finish_kernel, dim3(grid_of(work, sms, 4)), block, sums, s, a);
+    return launch_pdl(compact_finish_kernel, grid, block, sums, s, b);
   }
 }
 cudaError_t launch_fork(const PoolArgs& a, int sms, cudaStream_t s, int* kernels) { return launch_pool<true>(a, sms, s, kernels); }
