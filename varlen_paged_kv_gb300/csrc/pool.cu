@@ -3,8 +3,8 @@
 // fork_block_tables makes the rows of a new batch from rows of the old one; compact_block_tables
 // moves the highest pages in use into the lowest free ones. Both ask of every page of the pool
 // what the tables hold it for. Small batches over small pools do all of it in one CTA, with
-// the pages' marks as bits in shared memory (one launch: a fork of 64 rows SMALLFORK us instead of 9.4 of
-// the kernels below, a compaction SMALLCOMPACT instead of 10.0). Others take a few short kernels over a workspace:
+// the pages' marks as bits in shared memory (one launch: a fork of 64 rows 7.6 us instead of 9.4 with
+// the kernels below, a compaction 8.0 instead of 10.0). Others take a few short kernels over a workspace:
 //   clear   the marks; the fork's first new row of each old one
 //   mark    every held table entry stores a byte at its page (the same byte from whoever
 //           stores it, so without atomics); a row that would write into its last page next
@@ -17,8 +17,8 @@
 //           ring and copies are written from that, each entry by itself.
 // Every order (of pages given out, given back and moved) is one of page or row numbers, so results
 // do not depend on the order in which CTAs run. What bounds them is latency, a few dependent
-// loads from L2 per kernel: 1024 requests with 470000 held pages fork in BIGFORK us and are compacted
-// in BIGCOMPACT.
+// loads from L2 per kernel: 1024 requests with 470000 held pages fork in 23 us and are compacted
+// in 26.
 //
 // copy_pages moves the pages' data: one launch over the tensors of all layers, each CTA taking
 // pieces of 16 KB.
@@ -646,59 +646,68 @@ __global__ void __launch_bounds__(kSmallThreads) compact_small_kernel(const Pool
 // ---- copies --------------------------------------------------------------------------------
 constexpr int kCopyThreads = 256;
 constexpr int kPiece = 16384;   // bytes
-constexpr int kCopyRound = 1024;  // entries of the list looked at together
+constexpr int kCopyRound = 1024;  // entries of the list that a CTA takes
 
 __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_constant__ CopyArgs a) {
   __shared__ int2 list[kCopyRound];
-  __shared__ int part[kCopyThreads / 32];
+  __shared__ int part[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
-  for (int e0 = 0; e0 < a.n; e0 += kCopyRound) {
-    int kept = 0;
-    for (int i0 = 0; i0 < kCopyRound; i0 += kCopyThreads) {
-      const int i = e0 + i0 + threadIdx.x;
-      const int2 e = i < a.n && i < e0 + kCopyRound ? a.copies[i] : make_int2(-1, -1);
-      const bool none = e.x == -1 && e.y == -1;
-      const bool good = e.x >= 0 && e.x < a.num_blocks && e.y >= 0 && e.y < a.num_blocks;
-      if (!none && !good && blockIdx.x == 0 && a.error) atomicOr(a.error, PA_DEVERR_BAD_BLOCK);
-      const bool use = good && e.x != e.y;
-      const unsigned m = __ballot_sync(0xffffffffu, use);
-      if (lane == 0) part[warp] = __popc(m);
-      __syncthreads();
-      int before = kept;
-      for (int w = 0; w < kCopyThreads / 32; ++w) {
-        if (w < warp) before += part[w];
-        kept += part[w];
-      }
-      if (use) list[before + __popc(m & ((1u << lane) - 1))] = e;
-      __syncthreads();
-    }
-    const int64_t units = (int64_t)kept * a.num_tensors * a.pieces;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-      const int piece = (int)(u % a.pieces);
-      const int64_t v = u / a.pieces;
-      const int t = (int)(v % a.num_tensors);
-      const int2 e = list[v / a.num_tensors];
-      const int64_t bytes = a.bytes[t];
-      const int64_t off = (int64_t)piece * kPiece;
-      const uint8_t* src = a.data[t] + e.x * bytes + off;
-      uint8_t* dst = a.data[t] + e.y * bytes + off;
-      const int64_t left = bytes - off;
-      if (left >= kPiece) {
-        uint4 x[kPiece / 16 / kCopyThreads];
+  // this CTA's part of the list, entries that are none taken out
+  const int e0 = blockIdx.y * kCopyRound, entries = min(kCopyRound, a.n - e0);
+  constexpr int EACH = kCopyRound / kCopyThreads, WARPS = kCopyThreads / 32;
+  int2 e[EACH];
+  unsigned use[EACH];
 #pragma unroll
-        for (int k = 0; k < kPiece / 16 / kCopyThreads; ++k)
-          x[k] = __ldcs(reinterpret_cast<const uint4*>(src) + k * kCopyThreads + threadIdx.x);
+  for (int k = 0; k < EACH; ++k) {
+    const int i = k * kCopyThreads + threadIdx.x;
+    e[k] = i < entries ? a.copies[e0 + i] : make_int2(-1, -1);
+  }
 #pragma unroll
-        for (int k = 0; k < kPiece / 16 / kCopyThreads; ++k)
-          __stcs(reinterpret_cast<uint4*>(dst) + k * kCopyThreads + threadIdx.x, x[k]);
-      } else {
-        for (int64_t i = threadIdx.x * 16; i < left; i += kCopyThreads * 16)
-          *reinterpret_cast<uint4*>(dst + i) = *reinterpret_cast<const uint4*>(src + i);
-      }
+  for (int k = 0; k < EACH; ++k) {
+    use[k] = 0;
+    if (lane == 0) part[k * WARPS + warp] = 0;
+    if (k * kCopyThreads >= entries) continue;
+    const bool good = e[k].x >= 0 && e[k].x < a.num_blocks && e[k].y >= 0 && e[k].y < a.num_blocks;
+    if (!good && !(e[k].x == -1 && e[k].y == -1) && blockIdx.x == 0 && a.error) atomicOr(a.error, PA_DEVERR_BAD_BLOCK);
+    use[k] = __ballot_sync(0xffffffffu, good && e[k].x != e[k].y);
+    if (lane == 0) part[k * WARPS + warp] = __popc(use[k]);
+  }
+  __syncthreads();
+  // (counts of the warps' entries in the list's order, a lane each)
+  static_assert(EACH * WARPS == 32, "");
+  const int counts = part[lane], kept = __reduce_add_sync(0xffffffffu, counts);
+#pragma unroll
+  for (int k = 0; k < EACH; ++k) {
+    if (k * kCopyThreads >= entries) break;
+    const int before = __reduce_add_sync(0xffffffffu, lane < k * WARPS + warp ? counts : 0);
+    if (use[k] >> lane & 1) list[before + __popc(use[k] & ((1u << lane) - 1))] = e[k];
+  }
+  __syncthreads();
+  const int64_t units = (int64_t)kept * a.num_tensors * a.pieces;
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int piece = (int)(u % a.pieces);
+    const int64_t v = u / a.pieces;
+    const int t = (int)(v % a.num_tensors);
+    const int2 pair = list[v / a.num_tensors];
+    const int64_t bytes = a.bytes[t];
+    const int64_t off = (int64_t)piece * kPiece;
+    const uint8_t* src = a.data[t] + pair.x * bytes + off;
+    uint8_t* dst = a.data[t] + pair.y * bytes + off;
+    const int64_t left = bytes - off;
+    if (left >= kPiece) {
+      uint4 x[kPiece / 16 / kCopyThreads];
+#pragma unroll
+      for (int k = 0; k < kPiece / 16 / kCopyThreads; ++k)
+        x[k] = __ldcs(reinterpret_cast<const uint4*>(src) + k * kCopyThreads + threadIdx.x);
+#pragma unroll
+      for (int k = 0; k < kPiece / 16 / kCopyThreads; ++k)
+        __stcs(reinterpret_cast<uint4*>(dst) + k * kCopyThreads + threadIdx.x, x[k]);
+    } else {
+      for (int64_t i = threadIdx.x * 16; i < left; i += kCopyThreads * 16)
+        *reinterpret_cast<uint4*>(dst + i) = *reinterpret_cast<const uint4*>(src + i);
     }
-    __syncthreads();
   }
 }
 
@@ -764,9 +773,13 @@ cudaError_t launch_copy_pages(CopyArgs& a, int sms, cudaStream_t s) {
   int64_t most = 0;
   for (int t = 0; t < a.num_tensors; ++t) most = a.bytes[t] > most ? a.bytes[t] : most;
   a.pieces = (int)ceil_div(most, kPiece);
-  const int64_t units = (int64_t)a.n * a.num_tensors * a.pieces;
-  const int64_t g = units < (int64_t)sms * 8 ? units : (int64_t)sms * 8;
-  return launch_pdl(copy_pages_kernel, dim3((unsigned)g), dim3(kCopyThreads), 0, s, a);
+  const int64_t parts = ceil_div(a.n, kCopyRound), units = ceil_div(a.n, parts) * a.num_tensors * a.pieces;
+  // Up to 64 CTAs an SM: many of few pieces keep more loads in flight than a resident set that loops (160
+  // pages of 24 layers 293 us, with 16 an SM 302, with 8 319), but each looks through its part of the list first
+  // (400 pages among 5000 entries 24 us, with 16 an SM 16, with 400 62; among 200000 61, 191 and 89).
+  const int64_t ctas = ceil_div((int64_t)sms * 64, parts);
+  return launch_pdl(copy_pages_kernel, dim3((unsigned)(units < ctas ? units : ctas), (unsigned)parts), dim3(kCopyThreads), 0,
+                    s, a);
 }
 
 }  // namespace pa
