@@ -466,9 +466,10 @@ pa_status pa_sparse_paged_attention(const void* query, const void* key_cache, co
 
 /* ======================= pages that are shared, copied and moved ======================= */
 
-/* Most pages of a pool that the two entry points below take, and most tensors of one copy. */
+/* Most pages of a pool that the two entry points below take, and most tensors and entries of one copy. */
 #define PA_MAX_POOL_PAGES (1 << 20)
 #define PA_MAX_COPY_TENSORS 256
+#define PA_MAX_COPIES (1 << 25)
 
 /* Bytes of the device workspace (16-byte aligned) of pa_fork_block_tables and
  * pa_compact_block_tables for a pool of num_blocks pages; 0 for sizes they refuse. Calls that
@@ -563,7 +564,7 @@ pa_status pa_copy_pages(const pa_page_tensor* tensors, int32_t num_tensors, int3
 /* What pa_biased_paged_attention does to the scores, and which keys a row sees. All device
  * pointers may be NULL. */
 typedef struct pa_score_rules {
-  float softcap;               /* c > 0: a score s becomes c * tanh(s / c); 0: no cap */
+  float softcap;               /* c > 0: a score s becomes c * tanh(s / c); 0: no cap (1e-30 to 1e30) */
   int32_t window;              /* w > 0: a row at position p sees no key before p - w + 1; 0: no window */
   const float* slopes;         /* fp32 (num_heads): slopes[h] * |p - t| is taken off the score of key t */
   const int32_t* first_keys;   /* int32 (num_tokens): a row sees no key before its own first one (packed
@@ -608,10 +609,10 @@ size_t pa_biased_workspace_size(int32_t head_size);
  * query rows as in pa_sparse_paged_attention; the caches hold T and already hold this step's rows.
  *
  * Pages that no row of a sequence sees are not looked up (their table entries may be anything, as
- * those that a window has left behind), and what masked keys hold reaches no score. Rows of a
- * sequence are worked on in blocks of up to 128 / (num_heads / kv_num_heads): a value row that is
- * not finite and that one row of a block sees may reach the others of that block; value rows
- * that none of them sees, before the first or behind the last key, reach none.
+ * those that a window has left behind), and what the keys and values hold that a row does not see reaches
+ * neither its scores nor its output, whatever other rows see of them. (Rows are worked on in blocks, and one
+ * whose result is not finite is computed again over its own keys alone: values that are not finite
+ * cost time, 0.1 ms for every 5000 keys of a row.)
  * A page outside the pool reads as zeros, with PA_DEVERR_BAD_BLOCK in `error`; a pipeline wait that
  * runs out sets PA_DEVERR_TIMEOUT there and nowhere else.
  */

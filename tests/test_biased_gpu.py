@@ -114,7 +114,9 @@ def test_biased_attention(nh, kvh, hs, kind, dtype):
     (4, 2, 128, 16, [9000], [40], dict(softcap=20.0, prefix=9020)),        # few rows, many keys
     (1, 1, 128, 48, [0, 300], [257, 130], dict(documents=50, prefix=100)),
     (6, 2, 256, 16, [0, 77], [90, 300], dict(softcap=5.0, bias=True)),
-    (2, 2, 64, 16, [0], [600], dict(window=100, prefix=80))])
+    (2, 2, 64, 16, [0], [600], dict(window=100, prefix=80)),
+    (32, 8, 128, 64, [2500, 100], [600, 300], dict(softcap=30.0, bias=True, documents=900, prefix=200)),
+    (16, 4, 128, 256, [0] * 40, [70] * 40, dict(window=33, softcap=30.0))])
 def test_biased_attention_at_the_edges(nh, kvh, hs, bs, past, q, kw, dtype):
     b = Batch(nh + len(past), dtype, nh, kvh, hs, bs, past, q)
     rules = Rules(b, seed=3, **kw)

@@ -69,6 +69,7 @@ def test_copy_refusals(lib):
     assert copy(lib, [(FAKE, 0)]) == 1 and copy(lib, [(FAKE + 8, 64)]) == 1 and copy(lib, [(0, 64)]) == 1
     assert copy(lib, [(FAKE, 64)], copies=FAKE + 4) == 1 and copy(lib, [(FAKE, 64)], error=FAKE + 1) == 1
     assert copy(lib, [(FAKE, 72)]) == 2 and copy(lib, [(FAKE, 1 << 31)]) == 2 and copy(lib, [(FAKE, 64)] * 257) == 2
+    assert copy(lib, [(FAKE, 64)], n=(1 << 25) + 1) == 2
 
 
 def attend(lib, ptr=None, ws_bytes=BIG, scale=0.0, rules=None, **kw):
@@ -97,9 +98,10 @@ def test_biased_attention_refusals(lib):
         assert attend(lib, ptr={name: 0}) == 1
     for name in ("lse", "error"):
         assert attend(lib, ptr={name: FAKE + 2}) == 1
-    for rules in (dict(softcap=-1.0), dict(softcap=float("nan")), dict(softcap=float("inf")), dict(window=-1),
+    for rules in (dict(softcap=-1.0), dict(softcap=float("nan")), dict(softcap=float("inf")), dict(softcap=1e-35), dict(window=-1),
                   dict(slopes=FAKE + 2), dict(first_keys=FAKE + 1), dict(prefix_lens=FAKE + 2), dict(reserved=1)):
         assert attend(lib, rules=rules) == 1, rules
+    assert attend(lib, scale=3e38) == 1 and attend(lib, scale=1e30, rules=dict(softcap=1e-10)) == 1
     assert attend(lib, scale=float("inf")) == 1 and attend(lib, scale=float("nan")) == 1
     assert attend(lib, ws_bytes=lib.pa_biased_workspace_size(128) - 1) == 3
     assert lib.pa_biased_workspace_size(96) == 0

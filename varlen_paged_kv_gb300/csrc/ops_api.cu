@@ -361,7 +361,7 @@ pa_status pa_compact_block_tables(const int32_t* blocks_held, const int32_t* blo
 pa_status pa_copy_pages(const pa_page_tensor* tensors, int32_t num_tensors, int32_t num_blocks, const int32_t* copies,
                         int32_t num_copies, uint32_t* error, void* stream) {
   if (num_tensors < 0 || num_blocks < 0 || num_copies < 0) return PA_ERR_INVALID_ARGUMENT;
-  if (num_tensors > PA_MAX_COPY_TENSORS) return PA_ERR_UNSUPPORTED;
+  if (num_tensors > PA_MAX_COPY_TENSORS || num_copies > PA_MAX_COPIES) return PA_ERR_UNSUPPORTED;
   if (num_tensors == 0 || num_copies == 0) return PA_OK;
   if (!tensors || !aligned(copies, 8) || (error && !aligned(error, 4))) return PA_ERR_INVALID_ARGUMENT;
   pa::CopyArgs a{};
@@ -400,7 +400,10 @@ pa_status pa_biased_paged_attention(const void* query, const void* key_cache, co
                             1, 1, 0, 1, 0, dims->query_stride};
   if (pa_status st = check_batch_dims(&d)) return st;
   if (pa_status st = check_selection_dims(&d)) return st;
-  if (!(rules->softcap >= 0.f) || !(rules->softcap <= 1e30f) || rules->window < 0 || dims->max_query_len < 0 || !std::isfinite(scale))
+  const float sc = scale == 0.0f ? 1.0f / std::sqrt((float)dims->head_size) : scale;
+  if (!std::isfinite(sc * 1.4426950408889634f) || rules->window < 0 || dims->max_query_len < 0) return PA_ERR_INVALID_ARGUMENT;
+  // (a cap so small or large that a score in units of it, or it in powers of two, is none is no cap)
+  if (rules->softcap != 0.f && !(rules->softcap >= 1e-30f && rules->softcap <= 1e30f && std::isfinite(sc / rules->softcap)))
     return PA_ERR_INVALID_ARGUMENT;
   // (rows, heads and blocks of rows are numbered in 32 bits)
   if ((int64_t)dims->num_tokens * dims->num_heads > INT32_MAX) return PA_ERR_UNSUPPORTED;
@@ -438,7 +441,6 @@ pa_status pa_biased_paged_attention(const void* query, const void* key_cache, co
   a.max_blocks = dims->max_blocks_per_sequence;
   a.window = rules->window;
   a.max_rows = dims->max_query_len;
-  const float sc = scale == 0.0f ? 1.0f / std::sqrt((float)dims->head_size) : scale;
   a.scale_log2 = sc * 1.4426950408889634f;
   if (rules->softcap > 0.f) {
     a.scale_cap = sc / rules->softcap;
