@@ -116,7 +116,10 @@ def test_biased_attention(nh, kvh, hs, kind, dtype):
     (6, 2, 256, 16, [0, 77], [90, 300], dict(softcap=5.0, bias=True)),
     (2, 2, 64, 16, [0], [600], dict(window=100, prefix=80)),
     (32, 8, 128, 64, [2500, 100], [600, 300], dict(softcap=30.0, bias=True, documents=900, prefix=200)),
-    (16, 4, 128, 256, [0] * 40, [70] * 40, dict(window=33, softcap=30.0))])
+    (16, 4, 128, 256, [0] * 40, [70] * 40, dict(window=33, softcap=30.0)),
+    (16, 2, 256, 32, [900, 5, 300, 0], [5, 4, 8, 1], dict(softcap=30.0, window=400, bound=8)),  # 64 rows of a tile
+    (16, 2, 256, 16, [3000], [7], dict(bias=True, documents=500, bound=7)),
+    (3, 1, 256, 48, [700, 64], [21, 11], dict(prefix=800, bound=21))])
 def test_biased_attention_at_the_edges(nh, kvh, hs, bs, past, q, kw, dtype):
     b = Batch(nh + len(past), dtype, nh, kvh, hs, bs, past, q)
     rules = Rules(b, seed=3, **kw)

@@ -409,6 +409,7 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
     const int jc = min(j, it.rows - 1), h = g * a.G + min(row % a.G, a.G - 1);  // (rows past the item borrow the last row's keys)
     const Keys keys = keys_of_item_row(a, it, jc);
     const bool seeing = keys.hi > 0;  // (a row without keys is worked on as its neighbours, its result dropped)
+    const bool works = live && seeing;
     const int pos = it.pos0 + jc;
     const bool cap = a.cap_log2 != 0.f, bias = a.slopes != nullptr, bent = cap || bias;
     const float span = fabsf(a.scale_cap);
@@ -446,7 +447,10 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
         float top = u;
         int level = 0;
         if (cap) {
-          level = __all_sync(0xffffffffu, u <= kTanhNear) ? near : __all_sync(0xffffffffu, u <= kTanhReach) ? 2 : 3;
+          // (rows past the item may hold anything)
+          level = __all_sync(0xffffffffu, u <= kTanhNear || !works)    ? near
+                  : __all_sync(0xffffffffu, u <= kTanhReach || !works) ? 2
+                                                                       : 3;
           top = a.cap_log2 * fminf(u, 1.f);
         }
         const bool after = v0 + COLS > it.pos0 && it.prefix > it.pos0;
@@ -454,7 +458,7 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
           // (the bias of the nearest or farthest key, whichever is more; a key behind the row may be as near as 0)
           const float far = after ? fmaxf(fabsf(away), fabsf(away - (COLS - 1))) : away;
           top += fmaxf(slope * far, slope * (after ? 0.f : fmaxf(away - (COLS - 1), 0.f)));
-          find_max = __any_sync(0xffffffffu, live && seeing && !(top <= m_used + kLag));
+          find_max = __any_sync(0xffffffffu, works && !(top <= m_used + kLag));
         }
         const float shift = find_max || m_used == -INFINITY ? 0.f : kLift - m_used;
         if (!bias) bend_scores<false, COLS>(a, r, level, 0.f, 0.f, false, shift);
@@ -499,7 +503,7 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
           const float2 both = *hx;
           m_new = fmaxf(m_used, fmaxf(both.x, both.y));
         }
-        grow = __any_sync(0xffffffffu, live && seeing && m_new > m_used + kLag);
+        grow = __any_sync(0xffffffffu, works && m_new > m_used + kLag);
         if (unlikely(grow)) {
           // (fp16: a whole number, which kLift is taken off exactly)
           const float to = BF16 ? m_new : ceilf(m_new);
