@@ -318,3 +318,38 @@ def test_values_that_are_not_finite_reach_the_rows_that_see_them_only(past, q, k
     assert np.array_equal(np.isfinite(got[far]), np.isfinite(o[far]))
     assert (np.isposinf(got[far]) | np.isnan(got[far]) | np.isfinite(got[far])).all()
     assert (np.abs(f64(lse)[~np.isneginf(z)] - z[~np.isneginf(z)]) < 1e-3).all()
+
+
+LONG = [(8, 2, 128, 64, [100, 700, 0], [600, 3, 520], dict(softcap=20.0, bias=True, documents=300, prefix=50)),
+        (16, 16, 64, 16, [0], [2100], dict(window=200)),                 # one head a group
+        (16, 2, 256, 32, [300, 2000], [256, 300], dict(prefix=5000)),
+        (8, 2, 128, 48, [30], [515], dict(documents=60))]
+
+
+@pytest.mark.parametrize("values", ["plain", "large", "tiny", "inf", "small heads"])
+@pytest.mark.parametrize("nh,kvh,hs,bs,past,q,kw", LONG)
+def test_long_sequences_of_all_sorts_of_values(nh, kvh, hs, bs, past, q, kw, values):
+    """Values far apart, large and tiny ones, one that is not finite."""
+    b = Batch(61, "bf16", nh, kvh, hs, bs, past, q)
+    if values == "large":  # one that is larger than all others
+        b.value_cache[b.table[0, 1], 2, 0, 3] = 300.0
+    elif values == "tiny":
+        b.value_cache.mul_(1e-7)
+    elif values == "inf":
+        b.value_cache[b.table[0, (past[0] + q[0] - 1) // bs], 0, 0] = float("inf")
+    elif values == "small heads":  # the heads far apart
+        b.value_cache[:, :, 0] *= 2.0 ** -10
+        b.value_cache[:, :, -1] *= 60.0 if kvh > 1 else 1.0
+    rules = Rules(b, seed=7, **kw)
+    out, lse = rules.call(b)
+    assert int(b.error) == 0
+    if values == "inf":
+        o = f64(out).reshape(b.N, nh, hs)
+        first = past[0] + q[0] - 1
+        first -= first % bs  # the key that is not finite; the rows before it do not see it unless their prefix does
+        if "prefix" not in kw:
+            before = np.arange(max(0, first - past[0] - 1))
+            rules.check(b, out, lse, rows=before)
+        assert not np.isfinite(o).all()
+    else:
+        rules.check(b, out, lse)
