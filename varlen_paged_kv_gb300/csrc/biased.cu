@@ -12,114 +12,13 @@
 //                       bytes of K and V; the work is cut into equal shares whatever the lengths,
 //                       and biased_merge_kernel joins what a cut went through;
 //   biased_tile_kernel  longer ones (prompts, wide groups): tcgen05, 128 rows against tiles of 64 keys.
-#include "ops.cuh"
+#include "biased.cuh"
 
 namespace pa {
 
-constexpr int kBiTile = 64;          // keys per tile
 constexpr int kBiThreads = 160;      // rows kernel: four consumer warps and a producer
 constexpr int kBiCost = 3;           // what an item costs beside its tiles, in tiles
 constexpr int kMergeThreads = 256;
-
-// ---- scores --------------------------------------------------------------------------------
-// tanh as u times a polynomial in u^2 (minimax by weighted least squares on 4000 Chebyshev points),
-// of three terms up to |u| = 0.25 (4.9e-8 off at most) and of six up to 0.75 (9.5e-9), beyond that from
-// the exponential; the instruction tanh.approx is 5e-4 off, which a cap of 50 would turn into scores
-// 0.02 off. Scores are mostly well inside their cap, so a warp whose scores all are takes the short one.
-constexpr float kTanhNear = 0.25f, kTanhReach = 0.75f;
-__device__ constexpr float kTanh3[3] = {0.99999863f, -0.33315702f, 0.12762232f};
-__device__ constexpr float kTanh[6] = {0.99999983f, -0.33332471f, 0.1332058f, -0.05314926f, 0.01923724f, -0.00449346f};
-
-__device__ __forceinline__ float rcp_approx(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float tanh_far(float u) {  // 1 - 2 / (1 + e^2|u|), with u's sign
-  return copysignf(1.f - 2.f * rcp_approx(1.f + fast_exp2(fabsf(u) * 2.8853900818f)), u);
-}
-__device__ __forceinline__ float tanh_mid(float u) {
-  const float z = u * u;
-  float y = kTanh[5];
-#pragma unroll
-  for (int i = 4; i >= 0; --i) y = fmaf(y, z, kTanh[i]);
-  return u * y;
-}
-__device__ __forceinline__ float tanh_of(float u) { return fabsf(u) <= kTanhReach ? tanh_mid(u) : tanh_far(u); }
-
-// ---- ranges --------------------------------------------------------------------------------
-struct Keys {
-  int lo, hi;  // (lo >= hi: none, then lo = INT32_MAX and hi = 0)
-};
-__device__ __forceinline__ Keys keys_of_row(const BiasedArgs& a, const Seq& s, int prefix, int j) {
-  const int p = s.past + j;
-  Keys k;
-  k.lo = a.first ? max(a.first[s.c0 + j], 0) : 0;
-  if (a.window) k.lo = max(k.lo, p - a.window + 1);
-  k.hi = min(max(p + 1, prefix), s.past + s.q);
-  if (k.lo >= k.hi) k.lo = INT32_MAX, k.hi = 0;
-  return k;
-}
-__device__ __forceinline__ Keys join(Keys x, Keys y) { return {min(x.lo, y.lo), max(x.hi, y.hi)}; }
-
-__device__ __forceinline__ Seq seq_at(const BiasedArgs& a, int b) {
-  Seq s = make_seq(b, a.cum[b], a.cum[b + 1], a.past[b], a.N, a.max_blocks, a.bs);
-  s.ok = s.ok && (a.max_rows == 0 || s.q <= a.max_rows);
-  return s;
-}
-// whether a sequence is the rows kernel's
-__device__ __forceinline__ bool short_rows(const BiasedArgs& a, const Seq& s) {
-  return s.ok && s.q > 0 && (a.G > 128 || (int64_t)s.q * a.G <= 16);
-}
-
-// the checks of the whole batch, by one CTA
-__device__ __forceinline__ void check_biased_batch(const BiasedArgs& a) {
-  if (!a.error) return;
-  bool bad = threadIdx.x == 0 && a.cum[0] != 0;
-  for (int b = threadIdx.x; b < a.B; b += blockDim.x) bad |= !seq_at(a, b).ok;
-  if (bad) atomicOr(a.error, PA_DEVERR_BAD_BATCH);
-}
-
-// ---- rows whose result is not finite ---------------------------------------------------------
-// The products P V run over all keys that some row of an item sees, with weights of 0 where a row does
-// not, and 0 times a value that is not finite is NaN. So a row whose result is not finite is computed
-// again, here, over its own keys alone, by one warp in fp32 (channels from .. to_channel - 1 of it): what is
-// left is what those keys make of it.
-// (Slow, 0.1 ms for 5000 keys, but bounded; finite values never come here.)
-template <int HS, bool BF16>
-__device__ __noinline__ void redo_row(const BiasedArgs& a, int b, int c0, int q_len, int past, int j, int h, int lane,
-                                      int from, int to_channel) {
-  constexpr int E = HS / 32;  // channels of a lane
-  Seq s;
-  s.b = b, s.c0 = c0, s.q = q_len, s.past = past, s.ok = true;
-  const Keys k = keys_of_row(a, s, a.prefix ? a.prefix[b] : 0, j);
-  const int64_t row = c0 + j;
-  auto value = [](uint16_t x) { return BF16 ? __uint_as_float((uint32_t)x << 16) : __half2float(__ushort_as_half(x)); };
-  float q[E], o[E], m = -INFINITY, l = 0.f;
-  for (int e = 0; e < E; ++e) q[e] = value(a.query[row * a.q_stride + (int64_t)h * HS + lane * E + e]), o[e] = 0.f;
-  for (int t = k.lo; t < k.hi; ++t) {
-    const int phys = a.table[(int64_t)b * a.max_blocks + t / a.bs];
-    const bool there = phys >= 0 && phys < a.num_blocks;  // (a page outside the pool reads as zeros)
-    const int64_t at = (((int64_t)phys * a.bs + t % a.bs) * a.kvh + h / a.G) * HS + lane * E;
-    float x = 0.f;
-    for (int e = 0; e < E; ++e) x += q[e] * (there ? value(a.key_cache[at + e]) : 0.f);
-    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    x = a.cap_log2 != 0.f ? a.cap_log2 * tanh_of(x * a.scale_cap) : x * a.scale_log2;
-    if (a.slopes) x -= a.slopes[h] * 1.4426950408889634f * (float)abs(past + j - t);
-    const float to = fmaxf(m, x), f = to == -INFINITY ? 1.f : fast_exp2(m - to), w = to == -INFINITY ? 0.f : fast_exp2(x - to);
-    m = to;
-    l = l * f + w;
-    for (int e = 0; e < E; ++e) o[e] = (f == 1.f ? o[e] : o[e] * f) + w * (there ? value(a.value_cache[at + e]) : 0.f);
-  }
-  uint16_t* out = static_cast<uint16_t*>(a.output) + (row * a.nh + h) * HS + lane * E;
-  for (int e = 0; e < E; e += 2)
-    if (lane * E + e >= from && lane * E + e < to_channel) *reinterpret_cast<uint32_t*>(out + e) = pack2<BF16>(o[e] / l, o[e + 1] / l);
-}
-
-__device__ __forceinline__ bool finite4(float x, float y, float z, float w) {
-  // (a sum of magnitudes is finite where all are, but for an overflow, which only costs a second look)
-  return fabsf(x) + fabsf(y) + fabsf(z) + fabsf(w) < INFINITY;
-}
 
 // ---- few rows: equal shares of all tiles ----------------------------------------------------
 // All (sequence, KV head, 16 rows) units stand in a row, each as long as its 64-key tiles and
@@ -153,11 +52,6 @@ struct BiItem {
   Keys keys;               // of all rows of the sequence
   bool first, last;        // the unit's first, last tiles
 };
-
-// the tiles of a sequence's rows
-__device__ __forceinline__ int2 tiles_of(Keys k) {
-  return k.hi > 0 ? make_int2(k.lo / kBiTile, (k.hi + kBiTile - 1) / kBiTile) : make_int2(0, 0);
-}
 
 struct BiWalk {
   int64_t pos, end, base;  // the CTA's share; where sequence b begins
@@ -735,13 +629,6 @@ __global__ void __launch_bounds__(kMergeThreads) biased_merge_kernel(const __gri
   }
 }
 
-// most keys that `rows` rows of a sequence see, by the table's width or the window
-static int64_t keys_in_reach(const BiasedArgs& a, int rows) {
-  const int64_t keys = (int64_t)a.max_blocks * a.bs, reach = (int64_t)a.window + rows;
-  return a.window && !a.prefix && reach < keys ? reach : keys;
-}
-
-#include "biased_tile.cuh"
 
 // ---- host ----------------------------------------------------------------------------------
 int biased_ctas(int hs, int sms) {
@@ -812,7 +699,9 @@ cudaError_t launch_biased(const BiasedArgs& args, bool bf16, int sms, cudaStream
     const int rows = 128 / a.G;
     if (!query_block_map(&tq, a.query, bf16, a.hs, a.nh, a.N, a.q_stride, a.G, rows)) return cudaErrorInvalidValue;
     *kernels += 1;
-    if (cudaError_t e = PA_SIZES(launch_biased_tile, a, tq, tk, tv, seg, rows, sms, s)) return e;
+    if (cudaError_t e = bf16 ? launch_biased_tile_bf16(a, tq, tk, tv, seg, rows, sms, s)
+                             : launch_biased_tile_f16(a, tq, tk, tv, seg, rows, sms, s))
+      return e;
   }
   if (merge == 0) return cudaSuccess;
   *kernels += 1;

@@ -1,4 +1,4 @@
-// biased_tile_kernel: sequences of more than 16 rows per KV head (included by biased.cu, in its namespace).
+// biased_tile_kernel: the biased attention of sequences of more than 16 rows per KV head.
 //
 // The up to 128 rows r = j * G + head of 128 / G consecutive rows of a sequence are one M = 128
 // tile (TMA lays them out so from a (channel, head, row) view of the query; rows past the item are
@@ -11,6 +11,15 @@
 // during the softmax; two CTAs share an SM (one with 256-wide heads) and fill each other's gaps.
 // Where a batch has few tiles of rows, the CTAs of a cluster share an item's keys and add their
 // results through each other's shared memory.
+//
+// RULES (1: a cap, 2: a bias) are the call's: the softmax's code is long, and what it jumps over for other
+// calls' rules costs fetches (chunks with a cap and a window 340 us instead of 352 with all of it in one kernel).
+#pragma once
+
+#include "biased.cuh"
+
+namespace pa {
+
 template <int HS>
 struct BiTile {
   static constexpr int kStages = 2;
@@ -74,12 +83,12 @@ __device__ __forceinline__ TileItem tile_item(const BiasedArgs& a, int u, int su
   return it;
 }
 
-// N products q.k of a row as scores in powers of two, consecutive keys from v0 on: capped (`level`: not
-// at all, by tanh's short form, by its longer one, or wherever they are), less their distance's share
+// N products q.k of a row as scores in powers of two, consecutive keys from v0 on: capped (`level`: by
+// tanh's short form, by its longer one, or wherever they are), less their distance's share
 // (`slope` is minus the slope, `away` the distance of the first key; with `after` some keys may lie behind
 // the row), plus `shift`. On packed pairs: a score takes 2.5 instruction slots at level 1, 3 with a
 // bias, where one score at a time with a six-term tanh took 13.
-template <bool BIAS, int N>
+template <bool CAP, bool BIAS, int N>
 __device__ __forceinline__ void bend_scores(const BiasedArgs& a, uint32_t* r, int level, float slope, float away, bool after,
                                             float shift) {
   auto pair = [&](int e) { return f2_make(__uint_as_float(r[e]), __uint_as_float(r[e + 1])); };
@@ -88,12 +97,12 @@ __device__ __forceinline__ void bend_scores(const BiasedArgs& a, uint32_t* r, in
     f2_split(v, x, y);
     r[e] = __float_as_uint(x), r[e + 1] = __float_as_uint(y);
   };
-  const float scale = level == 0 ? a.scale_log2 : a.scale_cap, cl = a.cap_log2;
+  const float scale = CAP ? a.scale_cap : a.scale_log2, cl = a.cap_log2;
   if (BIAS && unlikely(after)) {
 #pragma unroll
     for (int e = 0; e < N; ++e) {
       const float x = __uint_as_float(r[e]) * scale;
-      r[e] = __float_as_uint(fmaf(slope, fabsf(away - (float)e), level == 0 ? x : cl * tanh_of(x)) + shift);
+      r[e] = __float_as_uint(fmaf(slope, fabsf(away - (float)e), CAP ? cl * tanh_of(x) : x) + shift);
     }
     return;
   }
@@ -116,7 +125,10 @@ __device__ __forceinline__ void bend_scores(const BiasedArgs& a, uint32_t* r, in
     return f2_add(eight[e % 8 / 2], from);
   };
   const uint64_t sc = f2_make(scale, scale);
-  if (likely(level == 1)) {
+  if constexpr (!CAP) {
+#pragma unroll
+    for (int e = 0; e < N; e += 2) put(e, f2_fma(pair(e), sc, bias_of(e)));
+  } else if (likely(level == 1)) {
     // cap * tanh(u) with u = scale * r as r times a polynomial in r^2 (level 1 is for scales whose fifth
     // power is a normal number)
     const float s1 = cl * scale, s2 = scale * scale, s3 = s1 * s2, s5 = s3 * s2;
@@ -127,9 +139,6 @@ __device__ __forceinline__ void bend_scores(const BiasedArgs& a, uint32_t* r, in
       const uint64_t x = pair(e), z = f2_mul(x, x);
       put(e, f2_fma(f2_fma(f2_fma(c2, z, c1), z, c0), x, bias_of(e)));
     }
-  } else if (level == 0) {
-#pragma unroll
-    for (int e = 0; e < N; e += 2) put(e, f2_fma(pair(e), sc, bias_of(e)));
   } else if (likely(level == 2)) {
     uint64_t c[6];
 #pragma unroll
@@ -200,7 +209,7 @@ __device__ __forceinline__ Keys keys_of_item_row(const BiasedArgs& a, const Tile
   return keys_of_row(a, s, it.prefix, j);
 }
 
-template <int HS, bool BF16>
+template <int HS, bool BF16, int RULES>
 __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
     biased_tile_kernel(const __grid_constant__ BiasedArgs a, const __grid_constant__ CUtensorMap tmQ,
                        const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -411,7 +420,7 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
     const bool seeing = keys.hi > 0;  // (a row without keys is worked on as its neighbours, its result dropped)
     const bool works = live && seeing;
     const int pos = it.pos0 + jc;
-    const bool cap = a.cap_log2 != 0.f, bias = a.slopes != nullptr, bent = cap || bias;
+    constexpr bool cap = RULES & 1, bias = RULES & 2, bent = cap || bias;
     const float span = fabsf(a.scale_cap);
     const int near = span > 1e-6f && span < 1e6f && a.cap_log2 < 1e6f ? 1 : 2;  // (the short tanh's coefficients hold)
     const float slope = bias ? -a.slopes[h] * 1.4426950408889634f : 0.f;
@@ -436,7 +445,7 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
       // the bound is over what the row's reference may lag behind; else the reference goes into the
       // bend (where two threads share a row they would have to agree: there it is always looked for).
       bool find_max = true;
-      if (bent) {
+      if constexpr (bent) {
         float most[2] = {0.f, 0.f};
 #pragma unroll
         for (int e = 0; e < COLS; e += 4)
@@ -461,8 +470,7 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
           find_max = __any_sync(0xffffffffu, works && !(top <= m_used + kLag));
         }
         const float shift = find_max || m_used == -INFINITY ? 0.f : kLift - m_used;
-        if (!bias) bend_scores<false, COLS>(a, r, level, 0.f, 0.f, false, shift);
-        else bend_scores<true, COLS>(a, r, level, slope, away, after, shift);
+        bend_scores<cap, bias, COLS>(a, r, level, slope, away, after, shift);
       }
       // (v0 and the bounds of all rows are the warp's: most tiles need neither side, few need both)
       if (unlikely(v0 < it.all_lo)) {
@@ -643,13 +651,26 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
 }
 
 // The CTAs of a cluster share an item's tiles, as many as run at once.
-template <int HS, bool BF16>
-static cudaError_t launch_biased_tile(const BiasedArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
-                                      const CUtensorMap& tv, int seg, int sub_rows, int sms, cudaStream_t s) {
+template <int HS, bool BF16, int RULES>
+static cudaError_t launch_biased_tile_of(const BiasedArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
+                                         const CUtensorMap& tv, int seg, int sub_rows, int sms, cudaStream_t s) {
   const int64_t keys = keys_in_reach(a, sub_rows);
   const int64_t items = items_of_batch(a.N, a.B, sub_rows, 1, 1) * a.kvh;
   const int c = cluster_size(items, (int64_t)sms * (HS == 256 ? 1 : 2), ceil_div(keys, kBiTile), 4, 8);
   const dim3 grid((unsigned)(a.N / sub_rows + a.B), (unsigned)a.kvh, (unsigned)c);
-  return launch_clusters(biased_tile_kernel<HS, BF16>, grid, bi_threads(HS), BiTile<HS>::kBytes, BiTile<HS>::kBytes, s, a,
-                         tq, tk, tv, seg, sub_rows);
+  return launch_clusters(biased_tile_kernel<HS, BF16, RULES>, grid, bi_threads(HS), BiTile<HS>::kBytes, BiTile<HS>::kBytes, s,
+                         a, tq, tk, tv, seg, sub_rows);
 }
+
+template <bool BF16>
+static cudaError_t launch_biased_tile(const BiasedArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
+                                      const CUtensorMap& tv, int seg, int sub_rows, int sms, cudaStream_t s) {
+  const int rules = (a.cap_log2 != 0.f ? 1 : 0) + (a.slopes ? 2 : 0);
+#define PA_TILE(HS, R) launch_biased_tile_of<HS, BF16, R>(a, tq, tk, tv, seg, sub_rows, sms, s)
+#define PA_RULES(HS) (rules == 0 ? PA_TILE(HS, 0) : rules == 1 ? PA_TILE(HS, 1) : rules == 2 ? PA_TILE(HS, 2) : PA_TILE(HS, 3))
+  return a.hs == 64 ? PA_RULES(64) : a.hs == 128 ? PA_RULES(128) : PA_RULES(256);
+#undef PA_RULES
+#undef PA_TILE
+}
+
+}  // namespace pa
