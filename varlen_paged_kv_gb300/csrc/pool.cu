@@ -18,7 +18,7 @@
 // Every order (of pages given out, given back and moved) is one of page or row numbers, so results
 // do not depend on the order in which CTAs run. What bounds them is latency, a few dependent
 // loads from L2 per kernel: 1024 requests with 470000 held pages fork in 23 us and are compacted
-// in 26.
+// in 24.
 //
 // copy_pages moves the pages' data: one launch over the tensors of all layers, each CTA taking
 // pieces of 16 KB.
@@ -758,7 +758,7 @@ static cudaError_t launch_pool(const PoolArgs& a, int sms, cudaStream_t s, int* 
   if (cudaError_t e = launch_pdl(pool_words_kernel<FORK>, dim3((unsigned)(a.num_chunks + more)), block, 0, s, a)) return e;
   PoolArgs b = a;
   b.row_blocks = grid_of((FORK ? a.Bn : a.B) * parts, sms, 4);
-  const dim3 grid(b.row_blocks + grid_of(ceil_div(a.num_blocks, 2), sms, 4));
+  const dim3 grid(b.row_blocks + grid_of(ceil_div(a.num_blocks, 2), sms, 2));
   if constexpr (FORK) {
     return launch_pdl(fork_finish_kernel, grid, block, sums + rows_smem, s, b);
   } else {
