@@ -353,3 +353,24 @@ def test_long_sequences_of_all_sorts_of_values(nh, kvh, hs, bs, past, q, kw, val
         assert not np.isfinite(o).all()
     else:
         rules.check(b, out, lse)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("past,q,kw", [([700, 3, 90], [1, 4, 2], dict()), ([300, 0], [120, 200], dict(softcap=20.0)),
+                                       ([200], [150], dict(prefix=260)), ([2000], [30], dict())])
+def test_slopes_of_either_sign(past, q, kw, dtype):
+    """A negative slope favours the farthest keys."""
+    b = Batch(51, dtype, 8, 2, 128, 32, past, q)
+    rules = Rules(b, seed=7, bias=True, **kw)
+    rules.slopes[::2] *= -1
+    rules.slopes[3] = 0
+    out, lse = rules.call(b)
+    assert int(b.error) == 0
+    rules.check(b, out, lse)
+
+
+@pytest.mark.parametrize("fill", [float("nan"), float("inf")])
+def test_values_that_are_not_finite_in_many_short_sequences(fill):
+    """Several whole sequences for each block, with rows to compute again in all of them."""
+    test_values_that_are_not_finite_reach_the_rows_that_see_them_only([30] * 300, [3] * 300, dict(softcap=20.0), 4, fill,
+                                                                      "fp16")

@@ -61,6 +61,20 @@ struct BiWalk {
   Keys keys;
   int prefix, units, chunks, t0, nt;
 
+  // by a whole warp: CTA c's share of all costs, `pre` the costs before each thread's run of sequences
+  __device__ __forceinline__ void begin(const int64_t* pre, int run, int c, int ctas, int lane) {
+    const int64_t W = pre[kBiThreads];
+    const int C = (int)min((int64_t)ctas, max(W / (kBiCost + 1), (int64_t)1));
+    pos = c < C ? W * c / C : W;
+    end = c < C ? W * (c + 1) / C : W;
+    loaded = false;
+    int k = 0;  // the thread whose sequences hold the share's beginning
+#pragma unroll
+    for (int i = 0; i < kBiThreads / 32; ++i) k += __popc(__ballot_sync(0xffffffffu, pre[i * 32 + lane + 1] <= pos));
+    k = min(k, kBiThreads - 1);
+    b = k * run;
+    base = pre[k];
+  }
   // by a whole warp: the sequence's lengths and keys
   __device__ __forceinline__ void load(const BiasedArgs& a, int lane) {
     s = seq_at(a, b);
@@ -214,19 +228,7 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
       if (lane == 0) pre[0] = 0;
     }
     __syncthreads();
-    const int64_t W = pre[kBiThreads];
-    const int C = (int)min((int64_t)gridDim.x, max(W / (kBiCost + 1), (int64_t)1));
-    walk.pos = c < C ? W * c / C : W;
-    walk.end = c < C ? W * (c + 1) / C : W;
-    walk.loaded = false;
-    {  // the thread whose sequences hold the share's beginning
-      int k = 0;
-#pragma unroll
-      for (int i = 0; i < kBiThreads / 32; ++i) k += __popc(__ballot_sync(0xffffffffu, pre[i * 32 + lane + 1] <= walk.pos));
-      k = min(k, kBiThreads - 1);
-      walk.b = k * run;
-      walk.base = pre[k];
-    }
+    walk.begin(pre, run, c, gridDim.x, lane);
     if (walk.pos >= walk.end) {
       if (threadIdx.x == 0) a.records[2 * c] = make_int4(0, 0, 0, 0), a.records[2 * c + 1] = make_int4(0, 0, 0, 0);
       return;
@@ -501,7 +503,7 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
           const float inv = M == -INFINITY ? 0.f : 1.f / S;
           uint2 out = make_uint2(pack2<BF16>(x.x * inv, x.y * inv), pack2<BF16>(x.z * inv, x.w * inv));
           if (M == -INFINITY) out = make_uint2(0, 0);
-          else if (!finite4(x.x * inv, x.y * inv, x.z * inv, x.w * inv)) atomicOr(redo, 1u << r);
+          else if (!finite4(x.x * inv, x.y * inv, x.z * inv, x.w * inv)) *redo = 1;
           *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.output) + at * HS + cc) = out;
           if (a.lse && cc == 0) a.lse[at] = M == -INFINITY ? -INFINITY : (M + fast_log2(S)) * 0.69314718055994531f;
         } else {
@@ -510,16 +512,6 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
         }
       }
       named_bar_sync(1, 128);  // the combining buffers are free again
-      if (!CLUSTER && *redo) {
-        const uint32_t rows = *redo;
-        named_bar_sync(1, 128);
-        if (threadIdx.x == 0) *redo = 0;
-        for (int r = w; r < it.n_rows; r += 4)
-          if (rows >> r & 1)
-            redo_row<HS, BF16>(a, it.b, it.c0, it.q, it.past, (it.r_first + r) / a.G, it.g * a.G + (it.r_first + r) % a.G,
-                               lane, 0, HS);
-        named_bar_sync(1, 128);
-      }
     }
   }
   if constexpr (CLUSTER) {
@@ -553,6 +545,25 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
   }
   __syncthreads();
   if (threadIdx.x == 0 && *err && a.error) atomicOr(a.error, *err);
+  if constexpr (!CLUSTER) {
+    // Rows of whole units that are not finite, as they stand in the output: after the last item, when no
+    // warp waits for another any more, since a row of many keys may take longer than a wait's limit.
+    if (*redo) {
+      walk.begin(pre, (a.B + kBiThreads - 1) / kBiThreads, c, gridDim.x, lane);
+      while (walk.next(a, lane, it)) {
+        if (!it.first || !it.last) continue;
+        for (int r = it.r_first + warp; r < it.r_first + it.n_rows; r += kBiThreads / 32) {
+          const int j = r / a.G, h = it.g * a.G + r % a.G;
+          const uint16_t* out = static_cast<const uint16_t*>(a.output) + ((int64_t)(it.c0 + j) * a.nh + h) * HS;
+          constexpr uint32_t top = BF16 ? 0x7F80u : 0x7C00u;
+          bool fine = true;
+          for (int e = lane; e < HS; e += 32) fine = fine && (out[e] & top) != top;
+          if (!__all_sync(0xffffffffu, fine))
+            redo_row<HS, BF16>(a, it.b, it.c0, it.q, it.past, j, h, lane, 0, HS);
+        }
+      }
+    }
+  }
 }
 
 // The pieces of the units that the cuts between CTAs went through, in order: CTA c of the rows
