@@ -606,7 +606,8 @@ size_t pa_biased_workspace_size(int32_t head_size);
  * (of the terms that are given) with scores scale * q.k, capped, then biased, as pa_score_rules says. Softmax and accumulation are
  * fp32, the output is rounded once to T; lse (fp32 (N, num_heads) or NULL) is the natural-log
  * log-sum-exp of those scores. A row that sees no key gives zeros and an lse of -inf. scale and
- * query rows as in pa_sparse_paged_attention; the caches hold T and already hold this step's rows.
+ * query rows as in pa_sparse_paged_attention; the caches hold T and already hold this step's rows. output
+ * and query do not overlap.
  *
  * Pages that no row of a sequence sees are not looked up (their table entries may be anything, as
  * those that a window has left behind), and what the keys and values hold that a row does not see reaches

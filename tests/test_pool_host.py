@@ -121,3 +121,17 @@ def test_python_calls_refuse_host_tensors(lib):
         pa.biased_paged_attention(q, q, q, i, i, t, num_heads=2, kv_num_heads=2)
     assert pa.copy_pages([], None) is None
     assert ctypes.sizeof(ctypes.c_void_p) == 8
+
+
+def test_biased_attention_refuses_an_output_over_the_query(lib):
+    out = FAKE + 4096 * 64
+    rows, row = 4, 1024 * 2  # bytes of a row, 8 heads of 128
+
+    def at(query, stride=1024):
+        return attend(lib, ptr={"query": query, "out": out}, num_tokens=rows, query_stride=stride, num_heads=8,
+                      kv_num_heads=2, head_size=128, ws_bytes=0)
+    for query in (out, out + 16, out - 16, out + rows * row - 16, out - rows * row + 16):
+        assert at(query) == 1
+    assert at(out - 3 * 4 * row, stride=4096) == 1          # its last row is the output's first
+    for query in (out + rows * row, out - rows * row):
+        assert at(query) == 3                               # the workspace is what is refused

@@ -413,6 +413,11 @@ pa_status pa_biased_paged_attention(const void* query, const void* key_cache, co
       (error && !aligned(error, 4)) || (rules->slopes && !aligned(rules->slopes, 4)) ||
       (rules->first_keys && !aligned(rules->first_keys, 4)) || (rules->prefix_lens && !aligned(rules->prefix_lens, 4)))
     return PA_ERR_INVALID_ARGUMENT;
+  // (rows are read again after others have been written)
+  const int64_t row = (int64_t)dims->num_heads * dims->head_size;
+  const uintptr_t q0 = (uintptr_t)query, q1 = q0 + 2 * ((dims->num_tokens - 1) * dims->query_stride + row);
+  const uintptr_t o0 = (uintptr_t)output, o1 = o0 + 2 * dims->num_tokens * row;
+  if (o0 < q1 && q0 < o1) return PA_ERR_INVALID_ARGUMENT;
   if (workspace_bytes < pa_biased_workspace_size(dims->head_size)) return PA_ERR_WORKSPACE_TOO_SMALL;
   int sms = 0;
   if (!pa::device_sms(&sms)) return pa::cuda_fail(cudaGetLastError(), "device query");
