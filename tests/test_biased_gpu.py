@@ -374,3 +374,25 @@ def test_values_that_are_not_finite_in_many_short_sequences(fill):
     """Several whole sequences for each block, with rows to compute again in all of them."""
     test_values_that_are_not_finite_reach_the_rows_that_see_them_only([30] * 300, [3] * 300, dict(softcap=20.0), 4, fill,
                                                                       "fp16")
+
+
+@pytest.mark.parametrize("where", ["first", "middle", "last"])
+@pytest.mark.parametrize("past,q,longest", [([90], [2], 2), ([90, 9000, 5], [2, 1, 1], 2), ([40], [60], 0)])
+def test_one_key_of_nan_makes_the_rows_nan_that_see_it(past, q, longest, where):
+    """A cluster's item, whole items and merged pieces, a tile's."""
+    b = Batch(61, "fp16", 8, 2, 128, 16, past, q)
+    rules = Rules(b, seed=2, bound=longest or None, softcap=20.0, window=80 if where == "first" else 0)
+    t = {"first": 20, "middle": 37, "last": past[0]}[where]  # (in a window of 80 the first rows' first key is 11 or more)
+    if where == "first" and past[0] == 90:
+        t = 11  # the first key of row 0, not seen by row 1
+    b.key_cache[b.table[0, t // 16], t % 16, 1] = float("nan")
+    out, lse = rules.call(b)
+    assert int(b.error) == 0
+    got, z = f64(out).reshape(b.N, 8, 128), f64(lse)
+    for j in range(b.N):
+        mine = j < q[0]
+        pos = past[0] + j
+        sees = mine and t <= pos and (not rules.window or t > pos - rules.window)
+        assert np.isnan(got[j, 4:]).all() if sees else np.isfinite(got[j]).all(), j
+        assert np.isnan(z[j, 4:]).all() if sees else np.isfinite(z[j]).all(), j
+        assert np.isfinite(got[j, :4]).all() and np.isfinite(z[j, :4]).all()

@@ -72,7 +72,8 @@ __device__ __forceinline__ void check_biased_batch(const BiasedArgs& a) {
 // not, and 0 times a value that is not finite is NaN. So a row whose result is not finite is computed
 // again, here, over its own keys alone, by one warp in fp32 (channels from .. to_channel - 1 of it): what is
 // left is what those keys make of it.
-// (Slow, 0.1 ms for 5000 keys, but bounded; finite values never come here.)
+// (Slow, 0.1 ms for 5000 keys, but bounded, and over at the first key whose score or values are NaN throughout;
+// finite values never come here.)
 template <int HS, bool BF16>
 __device__ __noinline__ void redo_row(const BiasedArgs& a, int b, int c0, int q_len, int past, int j, int h, int lane,
                                       int from, int to_channel) {
@@ -93,10 +94,16 @@ __device__ __noinline__ void redo_row(const BiasedArgs& a, int b, int c0, int q_
     for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
     x = a.cap_log2 != 0.f ? a.cap_log2 * tanh_of(x * a.scale_cap) : x * a.scale_log2;
     if (a.slopes) x -= a.slopes[h] * 1.4426950408889634f * (float)abs(past + j - t);
-    const float to = fmaxf(m, x), f = to == -INFINITY ? 1.f : fast_exp2(m - to), w = to == -INFINITY ? 0.f : fast_exp2(x - to);
+    const float to = fmaxf(m, x), f = to == -INFINITY ? 1.f : fast_exp2(m - to);
+    const float w = x == -INFINITY ? 0.f : fast_exp2(x - to);  // (NaN for a score of NaN, on the first key too)
     m = to;
     l = l * f + w;
-    for (int e = 0; e < E; ++e) o[e] = (f == 1.f ? o[e] : o[e] * f) + w * (there ? value(a.value_cache[at + e]) : 0.f);
+    bool lost = true;
+    for (int e = 0; e < E; ++e) {
+      o[e] = (f == 1.f ? o[e] : o[e] * f) + w * (there ? value(a.value_cache[at + e]) : 0.f);
+      lost = lost && o[e] != o[e];
+    }
+    if (__all_sync(0xffffffffu, lost)) break;  // NaN throughout: no key changes that
   }
   uint16_t* out = static_cast<uint16_t*>(a.output) + (row * a.nh + h) * HS + lane * E;
   for (int e = 0; e < E; e += 2)
