@@ -10,9 +10,10 @@
 // scores each and exchange their maxima through shared memory; with narrower ones two CTAs share an
 // SM and fill each other's gaps (there two threads a row were slower, 4 prompts of 2048 872 us
 // instead of 746). S_{t+1} is issued before P_t is waited for, so the tensor core works during the
-// softmax. What bounds it is that softmax: 4 prompts of 2048 with a cap and a bias take 740 us in bf16, 874 TFLOP/s
-// (P V counted once), 621 in fp16, and 505 in fp16 without cap and bias, 1289 TFLOP/s; issue slots 53% busy, the
-// tensor cores 61%.
+// softmax. What bounds it is that softmax: 4 prompts of 2048 with a cap and a bias take 667 us in bf16, 974 TFLOP/s
+// (P V counted once), 580 in fp16, and 490 in fp16 without cap and bias, 1328 TFLOP/s.
+// The load of S brings the row's largest magnitude (or score) with it; finding it score by score took
+// 738 us instead of 723 (before the steps below), and 344 instead of 329 for chunks with a cap and a window.
 // Where a batch has few tiles of rows, the CTAs of a cluster share an item's keys and add their
 // results through each other's shared memory.
 //
@@ -48,6 +49,43 @@ struct BiTile {
 // over costs fetches)
 __device__ __forceinline__ bool likely(bool x) { return __builtin_expect(x, 1); }
 __device__ __forceinline__ bool unlikely(bool x) { return __builtin_expect(x, 0); }
+
+// tcgen05.ld 32x32b of COLS consecutive columns of this thread's TMEM lane, with the largest of them, or of their
+// magnitudes, on the way (NaN passed over, as fmaxf does)
+template <int COLS, bool ABS>
+__device__ __forceinline__ float tmem_ld_max(uint32_t taddr, uint32_t* r) {
+  float m;
+  if constexpr (COLS == 64 && ABS) {
+    asm volatile(
+        "tcgen05.ld.red.sync.aligned.32x32b.x64.max.abs.f32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, %64, [%65];\n"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]), "=f"(m)
+        : "r"(taddr)
+        : "memory");
+  } else if constexpr (COLS == 64) {
+    asm volatile(
+        "tcgen05.ld.red.sync.aligned.32x32b.x64.max.f32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, %64, [%65];\n"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]), "=f"(m)
+        : "r"(taddr)
+        : "memory");
+  } else if constexpr (ABS) {
+    asm volatile(
+        "tcgen05.ld.red.sync.aligned.32x32b.x32.max.abs.f32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, %32, [%33];\n"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=f"(m)
+        : "r"(taddr)
+        : "memory");
+  } else {
+    asm volatile(
+        "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, %32, [%33];\n"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=f"(m)
+        : "r"(taddr)
+        : "memory");
+  }
+  return m;
+}
 
 // softmax threads that share a row, and the threads of a CTA
 __host__ __device__ constexpr int bi_sides(int hs) { return hs == 256 ? 2 : 1; }
@@ -169,11 +207,12 @@ __device__ __forceinline__ void bend_scores(const BiasedArgs& a, uint32_t* r, in
 __device__ __forceinline__ void cut_bf16x2(uint64_t p, uint32_t& hi, uint32_t& lo) {
   float p0, p1;
   f2_split(p, p0, p1);
-  const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
-  hi = prmt(u0, u1, 0x7632u);
-  float r0, r1;  // (weights are not negative: the sign bit set is minus the upper part)
-  f2_split(f2_add(p, f2_make(__uint_as_float((u0 & 0xFFFF0000u) | 0x80000000u), __uint_as_float((u1 & 0xFFFF0000u) | 0x80000000u))), r0, r1);
-  lo = pack2<true>(r0, r1);
+  hi = prmt(__float_as_uint(p0), __float_as_uint(p1), 0x7632u);
+  float r0, r1;  // (minus the rest: 4 prompts of 2048 26 us faster than with the upper part masked out and added)
+  asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; sub.rn.f32.bf16 %0, l, %3; sub.rn.f32.bf16 %1, h, %4;}"
+      : "=f"(r0), "=f"(r1)
+      : "r"(hi), "f"(p0), "f"(p1));
+  lo = pack2<true>(r0, r1) ^ 0x80008000u;
 }
 
 // The weights 2^(r c + shift) (c is 1 where SCALED is not set, and the shift 0) of COLS scores, written to
@@ -441,8 +480,7 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
       tc_fence_after();
       const uint32_t st = tmem + lane_off + (t & 1) * kBiTile;
       uint32_t r[COLS];
-      if constexpr (SIDES == 2) tmem_ld_x32(st + side * COLS, r);
-      else tmem_ld_x64(st, r);
+      const float most = tmem_ld_max<COLS, bent>(st + side * COLS, r);
       const int v0 = (last - t) * kBiTile + side * COLS;
       // With a cap or a bias the scores are bent first. The largest |q.k| of the row's keys tells how far
       // the cap bends them and bounds the scores from above, so that a maximum is only looked for where
@@ -450,13 +488,7 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
       // bend (where two threads share a row they would have to agree: there it is always looked for).
       bool find_max = true;
       if constexpr (bent) {
-        float most[2] = {0.f, 0.f};
-#pragma unroll
-        for (int e = 0; e < COLS; e += 4)
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            most[k] = fmax3(most[k], fabsf(__uint_as_float(r[e + 2 * k])), fabsf(__uint_as_float(r[e + 2 * k + 1])));
-        const float u = fmaxf(most[0], most[1]) * fabsf(cap ? a.scale_cap : a.scale_log2), away = (float)(pos - v0);
+        const float u = most * fabsf(cap ? a.scale_cap : a.scale_log2), away = (float)(pos - v0);
         float top = u;
         int level = 0;
         if (cap) {
@@ -474,6 +506,21 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
           find_max = __any_sync(0xffffffffu, works && !(top <= m_used + kLag));
         }
         const float shift = find_max || m_used == -INFINITY ? 0.f : kLift - m_used;
+        if (SIDES == 1 && !find_max && !after && level <= 1 && v0 >= it.all_lo && v0 + COLS <= it.all_hi) {
+          // The common case by itself, and in halves, the second loaded again when the first is done: with half
+          // of the registers the compiler finds a better order (4 prompts of 2048 667 us instead of 698).
+#pragma unroll
+          for (int k = 0; k < COLS / 32; ++k) {
+            uint32_t* x = r + 32 * k;
+            if (k) tmem_ld_x32(st + 32 * k, x);
+            bend_scores<cap, bias, 32>(a, x, 1, slope, away - (float)(32 * k), false, shift);
+            l += weigh<32, BF16, false>(x, 1.f, 0.f, st, 2 * k);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&p_full[t & 1]);
+          continue;
+        }
         bend_scores<cap, bias, COLS>(a, r, level, slope, away, after, shift);
       }
       // (v0 and the bounds of all rows are the warp's: most tiles need neither side, few need both)
@@ -493,7 +540,9 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
       float alpha = 1.f;
       if (find_max) {
         float mc[4] = {none, none, none, none};
-        if (c > 0.f) {
+        if (!bent && c > 0.f && v0 >= it.all_lo && v0 + COLS <= it.all_hi) {  // (the tile's keys are all rows')
+          mc[0] = most;
+        } else if (c > 0.f) {
 #pragma unroll
           for (int e = 0; e < COLS; e += 8)
 #pragma unroll
