@@ -180,19 +180,23 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
     *redo = 0;
     fence_mbar_init();
   }
-  pdl_wait();
-  // (all earlier work is done: the tile kernel starts beside this one on what it leaves free, 24 rows beside 8
-  // chunks of 512 350 us instead of 356; the merge waits for both. With this kernel on few SMs for as long as the
-  // tile kernel takes it is no faster: a CTA's chain gives it at most 27 GB/s.)
+  // Beside the tile kernel, whose every CTA has waited for what came before and let this one start, there is
+  // nothing to wait for but at the end, by one CTA for all: this kernel must not be over before that one, since
+  // what comes next waits for this one only.
+  if (!a.after_tiles) pdl_wait();
   pdl_launch_dependents();
   const int c = blockIdx.x, rank = blockIdx.z;
+  const bool waits = a.after_tiles && c == 0 && rank == 0;
   BiWalk walk;
   if (c == 0 && rank == 0) check_biased_batch(a);
   if constexpr (CLUSTER) {
     __syncthreads();  // the barriers are there
     walk.b = c / a.kvh;
     walk.load(a, lane);
-    if (walk.units == 0) return;  // (all CTAs of a cluster agree)
+    if (walk.units == 0) {  // (all CTAs of a cluster agree)
+      if (waits) pdl_wait();
+      return;
+    }
   } else {
     // the costs of all sequences, each thread those of a run of them
     const int run = (a.B + kBiThreads - 1) / kBiThreads;
@@ -231,6 +235,7 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
     walk.begin(pre, run, c, gridDim.x, lane);
     if (walk.pos >= walk.end) {
       if (threadIdx.x == 0) a.records[2 * c] = make_int4(0, 0, 0, 0), a.records[2 * c + 1] = make_int4(0, 0, 0, 0);
+      if (waits) pdl_wait();
       return;
     }
   }
@@ -564,6 +569,7 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
       }
     }
   }
+  if (waits) pdl_wait();
 }
 
 // The pieces of the units that the cuts between CTAs went through, in order: CTA c of the rows
@@ -698,14 +704,12 @@ cudaError_t launch_biased(const BiasedArgs& args, bool bf16, int sms, cudaStream
     return cudaErrorInvalidValue;
   // Sequences of up to 16 rows per KV head are the rows kernel's, longer ones the tile kernel's (groups
   // of over 128 heads, more than a tile's rows, are all the rows kernel's); a kernel that can have none is
-  // not launched. The merge comes last: it needs the rows kernel's results, the tile kernel does not.
+  // not launched. The tile kernel comes first, so that the rows' bytes fill what its last CTAs leave free (8 chunks
+  // of 512 and 24 decode rows 321 us, in the other order 331, with the rows on 120 CTAs through all of the tiles' time
+  // 325; the chunks alone 261: a rows CTA takes the place of a tile's), and the merge of the rows kernel's results last.
   int merge = 0;
 #define PA_TYPES(F, HS, ...) (bf16 ? F<HS, true>(__VA_ARGS__) : F<HS, false>(__VA_ARGS__))
 #define PA_SIZES(F, ...) (a.hs == 64 ? PA_TYPES(F, 64, __VA_ARGS__) : a.hs == 128 ? PA_TYPES(F, 128, __VA_ARGS__) : PA_TYPES(F, 256, __VA_ARGS__))
-  if (a.G <= 16 || a.G > 128) {
-    if (cudaError_t e = PA_SIZES(launch_biased_rows, a, tk, tv, seg, sms, s, kernels, &merge)) return e;
-    a.after_rows = 1;
-  }
   if (a.G <= 128 && (a.max_rows == 0 || (int64_t)a.max_rows * a.G > 16)) {
     const int rows = 128 / a.G;
     if (!query_block_map(&tq, a.query, bf16, a.hs, a.nh, a.N, a.q_stride, a.G, rows)) return cudaErrorInvalidValue;
@@ -713,7 +717,10 @@ cudaError_t launch_biased(const BiasedArgs& args, bool bf16, int sms, cudaStream
     if (cudaError_t e = bf16 ? launch_biased_tile_bf16(a, tq, tk, tv, seg, rows, sms, s)
                              : launch_biased_tile_f16(a, tq, tk, tv, seg, rows, sms, s))
       return e;
+    a.after_tiles = 1;
   }
+  if (a.G <= 16 || a.G > 128)
+    if (cudaError_t e = PA_SIZES(launch_biased_rows, a, tk, tv, seg, sms, s, kernels, &merge)) return e;
   if (merge == 0) return cudaSuccess;
   *kernels += 1;
   return PA_SIZES(launch_biased_merge, a, merge, s);

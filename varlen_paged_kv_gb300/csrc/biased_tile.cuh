@@ -304,11 +304,8 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
     for (int i = 0; i < 4; ++i) redo[i] = 0;
     fence_mbar_init();
   }
-  // Beside the rows kernel, which let this one start once everything before it was done, there is nothing to
-  // wait for but at the end, by one CTA for all: this kernel must not be over before that one, since what
-  // comes next waits for this one only.
-  if (!a.after_rows) pdl_wait();
-  const bool waits = a.after_rows && blockIdx.x == gridDim.x - 1 && blockIdx.y == 0 && blockIdx.z == 0;
+  pdl_wait();
+  pdl_launch_dependents();  // (the rows kernel starts when the last CTA has: beside the tiles that are left)
   if (warp == 0) {
     const TileItem it = tile_item(a, u, sub_rows, lane);
     if (lane == 0) *item_s = it;
@@ -316,10 +313,7 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
   if (blockIdx.x == 0 && g == 0 && rank == 0) check_biased_batch(a);
   __syncthreads();
   const TileItem it = *item_s;
-  if (it.rows <= 0) {  // (all CTAs of a cluster agree)
-    if (waits) pdl_wait();
-    return;
-  }
+  if (it.rows <= 0) return;  // (all CTAs of a cluster agree)
   if (warp == 1) {
     tmem_alloc(tmem_slot, L::kTmem);
     tmem_relinquish();
@@ -700,7 +694,6 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
     tc_fence_after();
     tmem_dealloc(tmem, L::kTmem);
   }
-  if (waits) pdl_wait();
 }
 
 // The CTAs of a cluster share an item's tiles, as many as run at once.

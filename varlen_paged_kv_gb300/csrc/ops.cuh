@@ -213,7 +213,7 @@ struct BiasedArgs {
   int64_t q_stride;
   int32_t N, B, nh, kvh, G, hs, num_blocks, bs, max_blocks;
   int32_t window, max_rows;  // 0: none
-  int32_t after_rows;        // the tile kernel runs beside the rows kernel: it starts without waiting for it
+  int32_t after_tiles;       // the rows kernel runs beside the tile kernel: it starts without waiting for it
   // s log2(e) of a score q.k is q.k * scale_log2, or with a cap cap_log2 * tanh(q.k * scale_cap)
   float scale_log2, scale_cap, cap_log2;
   // split pieces of the rows kernel: two slots per CTA, and what they hold
