@@ -476,10 +476,11 @@ PyObject* biased_paged_attention(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const float scale = real(v[8]);
     const size_t bytes = biased_workspace_size_fn(d.head_size);
     need(bytes > 0);
-    const at::Tensor out = call.empty({N, d.num_heads * k.size(3)}, type), ws = call.empty({(int64_t)bytes}, at::kByte);
+    const at::Tensor out = call.empty({N, d.num_heads * k.size(3)}, type);
+    const c10::DataPtr ws = c10::GetAllocator(c10::DeviceType::CUDA)->allocate(bytes);  // (no tensor: 0.5 us less)
     need(unlocked(biased_paged_attention_fn, query.data_ptr(), k.data_ptr(), value.data_ptr(), b.cum, b.past, b.table,
                   scale, (const pa_score_rules*)&rules, out.data_ptr(), lse, (const pa_biased_dims*)&d, error,
-                  ws.data_ptr(), bytes, call.stream()) == PA_OK);
+                  ws.get(), bytes, call.stream()) == PA_OK);
     return THPVariable_Wrap(out);
   });
 }
