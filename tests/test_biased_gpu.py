@@ -396,3 +396,19 @@ def test_one_key_of_nan_makes_the_rows_nan_that_see_it(past, q, longest, where):
         assert np.isnan(got[j, 4:]).all() if sees else np.isfinite(got[j]).all(), j
         assert np.isnan(z[j, 4:]).all() if sees else np.isfinite(z[j]).all(), j
         assert np.isfinite(got[j, :4]).all() and np.isfinite(z[j, :4]).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("softcap,size", [(50.0, 1.0), (50.0, 2.5), (50.0, 5.0), (50.0, 40.0), (160.0, 30.0), (400.0, 2.0), (400.0, 60.0),
+                                          (3000.0, 200.0), (1e30, 1.0)])
+def test_caps_small_and_large_against_their_scores(softcap, size, dtype):
+    """Every form of the cap: all scores near zero, some way up, most of them at the cap, caps that are none."""
+    for hs, past, q, bound in ((128, [70, 0, 300], [1, 200, 150], 0), (256, [130, 20], [60, 1], 0), (64, [400], [2], 2)):
+        b = Batch(71, dtype, 8, 2, hs, 32, past, q)
+        b.query[::2] *= size
+        b.query[1::4] *= -size
+        for kw in (dict(), dict(bias=True, prefix=150)):
+            rules = Rules(b, seed=9, softcap=softcap, bound=bound or None, **kw)
+            out, lse = rules.call(b)
+            assert int(b.error) == 0
+            rules.check(b, out, lse)

@@ -9,30 +9,24 @@ namespace pa {
 constexpr int kBiTile = 64;          // keys per tile
 
 // ---- scores --------------------------------------------------------------------------------
-// tanh as u times a polynomial in u^2 (minimax by weighted least squares on 4000 Chebyshev points),
-// of three terms up to |u| = 0.25 (4.9e-8 off at most) and of six up to 0.75 (9.5e-9), beyond that from
-// the exponential; the instruction tanh.approx is 5e-4 off, which a cap of 50 would turn into scores
-// 0.02 off. Scores are mostly well inside their cap, so a warp whose scores all are takes the short one.
-constexpr float kTanhNear = 0.25f, kTanhReach = 0.75f;
+// tanh as u times a polynomial in u^2 (minimax by weighted least squares on 4000 Chebyshev points) up
+// to |u| = 0.25, 4.9e-8 off at most (with six terms up to 0.75, 9.5e-9), beyond that from the exponential, 1 - 2 / (1 + e^2u), 2^-21 off at most (an
+// exponential, a sum, a reciprocal, a rounding); the instruction tanh.approx is 5e-4 off, which a cap of 50
+// would turn into scores 0.02 off.
+constexpr float kTanhNear = 0.25f, kTanhMid = 0.75f;
 __device__ constexpr float kTanh3[3] = {0.99999863f, -0.33315702f, 0.12762232f};
-__device__ constexpr float kTanh[6] = {0.99999983f, -0.33332471f, 0.1332058f, -0.05314926f, 0.01923724f, -0.00449346f};
+__device__ constexpr float kTanh6[6] = {0.99999983f, -0.33332471f, 0.1332058f, -0.05314926f, 0.01923724f, -0.00449346f};
 
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float tanh_far(float u) {  // 1 - 2 / (1 + e^2|u|), with u's sign
-  return copysignf(1.f - 2.f * rcp_approx(1.f + fast_exp2(fabsf(u) * 2.8853900818f)), u);
+__device__ __forceinline__ float tanh_of(float u) {
+  const float z = u * u, near = u * fmaf(fmaf(kTanh3[2], z, kTanh3[1]), z, kTanh3[0]);
+  const float far = copysignf(1.f - 2.f * rcp_approx(1.f + fast_exp2(fabsf(u) * 2.8853900818f)), u);
+  return fabsf(u) <= kTanhNear ? near : far;
 }
-__device__ __forceinline__ float tanh_mid(float u) {
-  const float z = u * u;
-  float y = kTanh[5];
-#pragma unroll
-  for (int i = 4; i >= 0; --i) y = fmaf(y, z, kTanh[i]);
-  return u * y;
-}
-__device__ __forceinline__ float tanh_of(float u) { return fabsf(u) <= kTanhReach ? tanh_mid(u) : tanh_far(u); }
 
 // ---- ranges --------------------------------------------------------------------------------
 struct Keys {

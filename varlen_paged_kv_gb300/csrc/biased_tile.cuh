@@ -125,11 +125,14 @@ __device__ __forceinline__ TileItem tile_item(const BiasedArgs& a, int u, int su
   return it;
 }
 
-// N products q.k of a row as scores in powers of two, consecutive keys from v0 on: capped (`level`: by
-// tanh's short form, by its longer one, or wherever they are), less their distance's share
-// (`slope` is minus the slope, `away` the distance of the first key; with `after` some keys may lie behind
-// the row), plus `shift`. On packed pairs: a score takes 2.5 instruction slots at level 1, 3 with a
-// bias, where one score at a time with a six-term tanh took 13.
+// N products q.k of a row as scores in powers of two, consecutive keys from v0 on: capped, less their
+// distance's share (`slope` is minus the slope, `away` the distance of the first key; with `after` some keys may lie
+// behind the row), plus `shift`. `level` says how the cap is taken: kNear and kMid, by polynomials in whose reach all
+// scores are; kFar, by the exponential, 2^-21 of the cap off wherever a score is; kAny, each score by what suits it,
+// for caps so large that this matters. 4 prompts of 2048 whose scores reach 0.1, 0.25, 0.4 and all of their cap take
+// 664, 764, 800 and 985 us (848, 1204 and 3757 the last three where each score past 0.75 chose its form). On packed pairs: a score takes 2, 4 and 3 instruction slots and none, none and
+// two more of the special function unit's, half a slot with a bias, where one score at a time took 13.
+constexpr int kNear = 1, kMid = 2, kFar = 3, kAny = 4;
 template <bool CAP, bool BIAS, int N>
 __device__ __forceinline__ void bend_scores(const BiasedArgs& a, uint32_t* r, int level, float slope, float away, bool after,
                                             float shift) {
@@ -170,9 +173,9 @@ __device__ __forceinline__ void bend_scores(const BiasedArgs& a, uint32_t* r, in
   if constexpr (!CAP) {
 #pragma unroll
     for (int e = 0; e < N; e += 2) put(e, f2_fma(pair(e), sc, bias_of(e)));
-  } else if (likely(level == 1)) {
-    // cap * tanh(u) with u = scale * r as r times a polynomial in r^2 (level 1 is for scales whose fifth
-    // power is a normal number)
+  } else if (likely(level == kNear)) {
+    // cap * tanh(u) with u = scale * r as r times a polynomial in r^2 (for scales whose fifth power is
+    // a normal number)
     const float s1 = cl * scale, s2 = scale * scale, s3 = s1 * s2, s5 = s3 * s2;
     const uint64_t c0 = f2_make(kTanh3[0] * s1, kTanh3[0] * s1), c1 = f2_make(kTanh3[1] * s3, kTanh3[1] * s3),
                    c2 = f2_make(kTanh3[2] * s5, kTanh3[2] * s5);
@@ -181,17 +184,27 @@ __device__ __forceinline__ void bend_scores(const BiasedArgs& a, uint32_t* r, in
       const uint64_t x = pair(e), z = f2_mul(x, x);
       put(e, f2_fma(f2_fma(f2_fma(c2, z, c1), z, c0), x, bias_of(e)));
     }
-  } else if (likely(level == 2)) {
-    uint64_t c[6];
+  } else if (level == kMid) {
+    uint64_t k[6];
 #pragma unroll
-    for (int k = 0; k < 6; ++k) c[k] = f2_make(kTanh[k] * cl, kTanh[k] * cl);
+    for (int i = 0; i < 6; ++i) k[i] = f2_make(kTanh6[i] * cl, kTanh6[i] * cl);
 #pragma unroll
     for (int e = 0; e < N; e += 2) {
       const uint64_t x = f2_mul(pair(e), sc), z = f2_mul(x, x);
-      uint64_t y = c[5];
+      uint64_t y = k[5];
 #pragma unroll
-      for (int k = 4; k >= 0; --k) y = f2_fma(y, z, c[k]);
+      for (int i = 4; i >= 0; --i) y = f2_fma(y, z, k[i]);
       put(e, f2_fma(y, x, bias_of(e)));
+    }
+  } else if (level == kFar) {
+    const uint64_t twice = f2_make(scale * 2.8853900818f, scale * 2.8853900818f), one = f2_make(1.f, 1.f);
+    const uint64_t less = f2_make(-2.f * cl, -2.f * cl), more = f2_make(cl, cl);
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+      float x, y;
+      f2_split(f2_mul(pair(e), twice), x, y);
+      f2_split(f2_add(f2_make(fast_exp2(x), fast_exp2(y)), one), x, y);
+      put(e, f2_fma(f2_make(rcp_approx(x), rcp_approx(y)), less, f2_add(bias_of(e), more)));
     }
   } else {
 #pragma unroll
@@ -459,7 +472,8 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
     const int pos = it.pos0 + jc;
     constexpr bool cap = RULES & 1, bias = RULES & 2, bent = cap || bias;
     const float span = fabsf(a.scale_cap);
-    const int near = span > 1e-6f && span < 1e6f && a.cap_log2 < 1e6f ? 1 : 2;  // (the short tanh's coefficients hold)
+    // the polynomial's coefficients hold; and kFar's error, 2^-21 of the cap, is 2^-13 of a power of two at most
+    const bool short_form = span > 1e-6f && span < 1e6f && a.cap_log2 < 1e6f, far_form = a.cap_log2 <= 256.f;
     const float slope = bias ? -a.slopes[h] * 1.4426950408889634f : 0.f;
     const float c = bent ? 1.f : a.scale_log2;  // what the scores below are still multiplied by
     const float none = c > 0.f ? -INFINITY : INFINITY;  // a score whose product with c is -inf
@@ -487,9 +501,11 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
         int level = 0;
         if (cap) {
           // (rows past the item may hold anything)
-          level = __all_sync(0xffffffffu, u <= kTanhNear || !works)    ? near
-                  : __all_sync(0xffffffffu, u <= kTanhReach || !works) ? 2
-                                                                       : 3;
+          const bool near = __all_sync(0xffffffffu, u <= kTanhNear || !works);
+          level = near && short_form                                      ? kNear
+                  : __all_sync(0xffffffffu, u <= kTanhMid || !works) ? kMid
+                  : far_form                                         ? kFar
+                                                                     : kAny;
           top = a.cap_log2 * fminf(u, 1.f);
         }
         const bool after = v0 + COLS > it.pos0 && it.prefix > it.pos0;
@@ -500,20 +516,30 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
           find_max = __any_sync(0xffffffffu, works && !(top <= m_used + kLag));
         }
         const float shift = find_max || m_used == -INFINITY ? 0.f : kLift - m_used;
-        if (SIDES == 1 && !find_max && !after && level <= 1 && v0 >= it.all_lo && v0 + COLS <= it.all_hi) {
-          // The common case by itself, and in halves, the second loaded again when the first is done: with half
-          // of the registers the compiler finds a better order (4 prompts of 2048 667 us instead of 698).
+        // The common cases by themselves, and in halves, the second loaded again when the first is done: with half
+        // of the registers the compiler finds a better order (4 prompts of 2048 667 us instead of 698; kMid 764 instead of 863; kFar too: 920 instead
+        // of 985, but 20 us more for the others).
+        auto by_halves = [&](int lv) {
 #pragma unroll
           for (int k = 0; k < COLS / 32; ++k) {
             uint32_t* x = r + 32 * k;
             if (k) tmem_ld_x32(st + 32 * k, x);
-            bend_scores<cap, bias, 32>(a, x, 1, slope, away - (float)(32 * k), false, shift);
+            bend_scores<cap, bias, 32>(a, x, lv, slope, away - (float)(32 * k), false, shift);
             l += weigh<32, BF16, false>(x, 1.f, 0.f, st, 2 * k);
           }
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(&p_full[t & 1]);
-          continue;
+        };
+        if (SIDES == 1 && !find_max && !after && level < kAny && v0 >= it.all_lo && v0 + COLS <= it.all_hi) {
+          if (!cap || level == kNear) {
+            by_halves(kNear);
+            continue;
+          }
+          if (level == kMid) {
+            by_halves(kMid);
+            continue;
+          }
         }
         bend_scores<cap, bias, COLS>(a, r, level, slope, away, after, shift);
       }
