@@ -135,3 +135,7 @@ def test_biased_attention_refuses_an_output_over_the_query(lib):
     assert at(out - 3 * 4 * row, stride=4096) == 1          # its last row is the output's first
     for query in (out + rows * row, out - rows * row):
         assert at(query) == 3                               # the workspace is what is refused
+
+
+def test_biased_attention_refuses_more_blocks_than_a_grid_has(lib):
+    assert attend(lib, batch_size=1 << 28, num_tokens=8) == 2

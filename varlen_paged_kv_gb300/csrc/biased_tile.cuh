@@ -10,8 +10,8 @@
 // scores each and exchange their maxima through shared memory; with narrower ones two CTAs share an
 // SM and fill each other's gaps (there two threads a row were slower, 4 prompts of 2048 872 us
 // instead of 746). S_{t+1} is issued before P_t is waited for, so the tensor core works during the
-// softmax. What bounds it is that softmax: 4 prompts of 2048 with a cap and a bias take 667 us in bf16, 974 TFLOP/s
-// (P V counted once), 580 in fp16, and 490 in fp16 without cap and bias, 1328 TFLOP/s.
+// softmax. What bounds it is that softmax: 4 prompts of 2048 with a cap and a bias take 637 us in bf16, 1020 TFLOP/s
+// (P V counted once), 540 in fp16, and 470 in fp16 without cap and bias, 1383 TFLOP/s.
 // The load of S brings the row's largest magnitude (or score) with it; finding it score by score took
 // 738 us instead of 723 (before the steps below), and 344 instead of 329 for chunks with a cap and a window.
 // Where a batch has few tiles of rows, the CTAs of a cluster share an item's keys and add their
@@ -130,7 +130,7 @@ __device__ __forceinline__ TileItem tile_item(const BiasedArgs& a, int u, int su
 // behind the row), plus `shift`. `level` says how the cap is taken: kNear and kMid, by polynomials in whose reach all
 // scores are; kFar, by the exponential, 2^-21 of the cap off wherever a score is; kAny, each score by what suits it,
 // for caps so large that this matters. 4 prompts of 2048 whose scores reach 0.1, 0.25, 0.4 and all of their cap take
-// 664, 764, 800 and 985 us (848, 1204 and 3757 the last three where each score past 0.75 chose its form). On packed pairs: a score takes 2, 4 and 3 instruction slots and none, none and
+// 637, 743, 800 and 950 us (848, 1204 and 3757 the last three where each score past 0.75 chose its form). On packed pairs: a score takes 2, 4 and 3 instruction slots and none, none and
 // two more of the special function unit's, half a slot with a bias, where one score at a time took 13.
 constexpr int kNear = 1, kMid = 2, kFar = 3, kAny = 4;
 template <bool CAP, bool BIAS, int N>
@@ -296,8 +296,10 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
   float2* half = reinterpret_cast<float2*>(smem + L::kX);  // [2][128]
   uint32_t* redo = reinterpret_cast<uint32_t*>(smem + L::kRedo);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // later rows see more keys, so their items start first
-  const int g = blockIdx.y, u = gridDim.x - 1 - blockIdx.x;
+  // Later rows see more keys, so their items start first, those of all heads: 4 prompts of 2048 634 us instead of 670
+  // with one head after the other, whose last CTAs leave SMs idle. (Sequences by length, too, make that 624, but 8
+  // chunks and 24 decode rows 323 instead of 321 and one chunk and 7 decode rows 69 instead of 65.)
+  const int i = gridDim.x - 1 - blockIdx.x, g = i % a.kvh, u = i / a.kvh;
   const int rank = blockIdx.z, C = gridDim.z;  // the cluster is a column of the grid
   if (threadIdx.x == 32) {
     mbar_init(q_full, 1);
@@ -323,7 +325,7 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
     const TileItem it = tile_item(a, u, sub_rows, lane);
     if (lane == 0) *item_s = it;
   }
-  if (blockIdx.x == 0 && g == 0 && rank == 0) check_biased_batch(a);
+  if (i == 0 && rank == 0) check_biased_batch(a);
   __syncthreads();
   const TileItem it = *item_s;
   if (it.rows <= 0) return;  // (all CTAs of a cluster agree)
@@ -729,7 +731,7 @@ static cudaError_t launch_biased_tile_of(const BiasedArgs& a, const CUtensorMap&
   const int64_t keys = keys_in_reach(a, sub_rows);
   const int64_t items = items_of_batch(a.N, a.B, sub_rows, 1, 1) * a.kvh;
   const int c = cluster_size(items, (int64_t)sms * (HS == 256 ? 1 : 2), ceil_div(keys, kBiTile), 4, 8);
-  const dim3 grid((unsigned)(a.N / sub_rows + a.B), (unsigned)a.kvh, (unsigned)c);
+  const dim3 grid((unsigned)((a.N / sub_rows + a.B) * a.kvh), 1, (unsigned)c);
   return launch_clusters(biased_tile_kernel<HS, BF16, RULES>, grid, bi_threads(HS), BiTile<HS>::kBytes, BiTile<HS>::kBytes, s,
                          a, tq, tk, tv, seg, sub_rows);
 }

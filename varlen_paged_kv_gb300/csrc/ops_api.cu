@@ -406,7 +406,7 @@ pa_status pa_biased_paged_attention(const void* query, const void* key_cache, co
   if (rules->softcap != 0.f && !(rules->softcap >= 1e-30f && rules->softcap <= 1e30f && std::isfinite(sc / rules->softcap)))
     return PA_ERR_INVALID_ARGUMENT;
   // (rows, heads and blocks of rows are numbered in 32 bits)
-  if ((int64_t)dims->num_tokens * dims->num_heads > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  if (((int64_t)dims->num_tokens + dims->batch_size) * dims->num_heads > INT32_MAX) return PA_ERR_UNSUPPORTED;
   if (dims->num_tokens == 0) return PA_OK;
   if (!all_aligned(16, {query, key_cache, value_cache, output, workspace}) ||
       !all_aligned(4, {cumulative_sequence_length, past_seqlens, block_table}) || (lse && !aligned(lse, 4)) ||
