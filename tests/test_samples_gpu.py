@@ -268,3 +268,83 @@ def test_a_padded_step_is_captured_and_replayed():
         assert torch.equal(out, o) and torch.equal(lse, z)
         assert (out[n:] == 5).all() and (lse[n:] == 5).all()
         assert n == 0 or not (lse[:n] == 5).any()
+
+
+@pytest.mark.parametrize("fast", [True, False])
+def test_calls_with_nothing_to_do(fast, monkeypatch):
+    """No rows, no new requests, no moves, no copies."""
+    from varlen_paged_kv_gb300 import step
+    if not fast:
+        monkeypatch.setattr(step, "_fast", _NoFast())
+    i = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    table, ring, state = i(0, 1, 2, 3).view(2, 2), i(4, 5, 6, 7, 0, 0, 0, 0), i(0, 4)
+    past, held = i(20, 32), i(2, 2)
+    f = pa.fork_block_tables(i(), past, held, table, ring, state, block_size=16, num_blocks=8)
+    assert f.block_table.shape == (0, 2) and f.copies.shape == (0, 2) and f.error.tolist() == [0]
+    assert f.free_state.tolist() == [0, 8] and ring.tolist() == [4, 5, 6, 7, 0, 1, 2, 3]  # all pages back
+    c = pa.compact_block_tables(held, table, ring, num_blocks=8, max_moves=0)
+    assert c.copies.shape == (0, 2) and c.free_state.tolist() == [0, 4] and ring[:4].tolist() == [4, 5, 6, 7]
+    assert c.pages_end.tolist() == [4] and torch.equal(c.block_table, table)
+    cache = torch.randn(8, 16, 1, 64, device="cuda").half()
+    was = cache.clone()
+    pa.copy_pages([cache], torch.empty(0, 2, dtype=torch.int32, device="cuda"))
+    pa.copy_pages([cache], torch.full((3, 2), -1, dtype=torch.int32, device="cuda"))
+    assert torch.equal(cache, was)
+    out = pa.biased_paged_attention(torch.empty(0, 128, device="cuda").half(), cache, cache, i(0, 0, 0), past, table, num_heads=2,
+                                    kv_num_heads=1)
+    assert out.shape == (0, 128)
+    lse = torch.full((2, 2), 3.0, device="cuda")
+    out = pa.biased_paged_attention(torch.zeros(2, 128, device="cuda").half(), cache, cache, i(0, 0, 0), past, table, num_heads=2,
+                                    kv_num_heads=1, output=torch.full((2, 128), 4.0, device="cuda").half(), lse=lse)
+    assert (out == 4).all() and (lse == 3).all()  # rows of no sequence
+
+
+def test_host_threads_on_streams_of_their_own():
+    """Eight threads call all four operators at once, each for a batch of its own: small kernels and large ones."""
+    import threading
+    wrong = []
+
+    def work(k):
+        try:
+            r = np.random.default_rng(k)
+            B, bs, blocks, cols = [6, 300][k % 2], 16, [200, 9000][k % 2], 24
+            past = r.integers(1, bs * cols - 40, B)
+            need = -(-past // bs)
+            order = r.permutation(blocks)
+            table, at = np.full((B, cols), -1), 0
+            for b in range(B):
+                table[b, :need[b]] = order[at: at + need[b]]
+                at += need[b]
+            free = order[at:]
+            parents = r.integers(-1, B, B)
+            q_len = [1, 3, 20, 1][k % 4]
+            cum = np.arange(0, (4 + 1) * q_len, q_len)
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                t = [i32(x) for x in (parents, past, need, table, np.concatenate([free, np.zeros(at, int)]), [0, len(free)])]
+                key = torch.randn(blocks, bs, 2, 64, device="cuda").half()
+                value = torch.randn(blocks, bs, 2, 64, device="cuda").half()
+                query = torch.randn(4 * q_len, 512, device="cuda").half()
+                first = None
+                for _ in range(20):
+                    ring, k2, v2 = t[4].clone(), key.clone(), value.clone()
+                    f = pa.fork_block_tables(*t[:4], ring, t[5], block_size=bs, num_blocks=blocks)
+                    pa.copy_pages([k2, v2], f.copies)
+                    out = pa.biased_paged_attention(query, k2, v2, i32(cum), f.past_seqlens[:4] - f.past_seqlens[:4].clamp(max=q_len),
+                                                    f.block_table[:4].contiguous(), num_heads=8, kv_num_heads=2, softcap=20.0,
+                                                    window=100)
+                    c = pa.compact_block_tables(f.blocks_held, f.block_table, ring, num_blocks=blocks, max_moves=64)
+                    pa.copy_pages([k2, v2], c.copies)
+                    got = [*f, *c, ring, k2, v2, out]
+                    stream.synchronize()
+                    first = first or [x.clone() for x in got]
+                    assert int(f.error) == 0 and int(c.error) == 0
+                    assert all(torch.equal(x, y) for x, y in zip(got, first))
+        except Exception as e:  # noqa: BLE001 (an assertion of a thread is the test's)
+            wrong.append((k, repr(e)))
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(8)]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    assert not wrong, wrong
