@@ -9,10 +9,10 @@ namespace pa {
 constexpr int kBiTile = 64;          // keys per tile
 
 // ---- scores --------------------------------------------------------------------------------
-// tanh as u times a polynomial in u^2 (minimax by weighted least squares on 4000 Chebyshev points) up
-// to |u| = 0.25, 4.9e-8 off at most (with six terms up to 0.75, 9.5e-9), beyond that from the exponential, 1 - 2 / (1 + e^2u), 2^-21 off at most (an
-// exponential, a sum, a reciprocal, a rounding); the instruction tanh.approx is 5e-4 off, which a cap of 50
-// would turn into scores 0.02 off.
+// tanh as u times a polynomial in u^2 (minimax by weighted least squares on 4000 Chebyshev points) up to
+// |u| = 0.25, 4.9e-8 off at most (with six terms up to 0.75, 9.5e-9), beyond that from the exponential,
+// 1 - 2 / (1 + e^2u), 2^-21 off at most (an exponential, a sum, a reciprocal, a rounding); the instruction
+// tanh.approx is 5e-4 off, which a cap of 50 would turn into scores 0.02 off.
 constexpr float kTanhNear = 0.25f, kTanhMid = 0.75f;
 __device__ constexpr float kTanh3[3] = {0.99999863f, -0.33315702f, 0.12762232f};
 __device__ constexpr float kTanh6[6] = {0.99999983f, -0.33332471f, 0.1332058f, -0.05314926f, 0.01923724f, -0.00449346f};

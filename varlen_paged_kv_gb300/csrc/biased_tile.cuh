@@ -519,8 +519,8 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
         }
         const float shift = find_max || m_used == -INFINITY ? 0.f : kLift - m_used;
         // The common cases by themselves, and in halves, the second loaded again when the first is done: with half
-        // of the registers the compiler finds a better order (4 prompts of 2048 667 us instead of 698; kMid 764 instead of 863; kFar too: 920 instead
-        // of 985, but 20 us more for the others).
+        // of the registers the compiler finds a better order (4 prompts of 2048 667 us instead of 698; kMid 764
+        // instead of 863; kFar too: 920 instead of 985, but 20 us more for the others).
         auto by_halves = [&](int lv) {
 #pragma unroll
           for (int k = 0; k < COLS / 32; ++k) {
