@@ -1,0 +1,67 @@
+"""Calls of the biased attention that the documentation allows and that once went wrong, or that no other test makes,
+against the plain statement in 64 bits (pool_reference)."""
+import numpy as np
+import pytest
+import torch
+
+import pool_reference as ref
+import varlen_paged_kv_gb300 as pa
+from test_biased_gpu import Rules
+from test_step_gpu import DT, Batch, _NoFast, f64, i32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.fail("CUDA is required for the gpu tests")
+    from varlen_paged_kv_gb300 import build
+    build.build()
+
+
+# ---- pages that no row sees, between pages that some rows of a block see -----------------------
+
+
+def _between_documents(nh, kvh, hs, past, q, pad, dtype="bf16"):
+    """One sequence of a document, `pad` rows that see nothing, and another document; the pages wholly inside the padding."""
+    b = Batch(81, dtype, nh, kvh, hs, 16, [past], [q])
+    rules = Rules(b)
+    at = (q - pad) // 2
+    rules.first = np.concatenate([np.zeros(at), np.full(pad, past + q), np.full(q - at - pad, past + at + pad)]).astype(int)
+    unseen = np.arange(-(-(past + at) // 16), (past + at + pad) // 16)
+    assert len(unseen)
+    return b, rules, unseen
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("nh,kvh,hs,past,q,pad", [
+    (2, 2, 64, 0, 120, 60), (2, 2, 128, 30, 126, 70), (2, 2, 256, 0, 128, 50),  # one block of 128 rows of a head
+    (2, 2, 128, 500, 100, 40), (4, 2, 64, 3000, 60, 45),                        # few blocks: clusters over the keys
+    (130, 1, 64, 20, 100, 60)])                                                 # a group of more than a tile's rows
+def test_pages_between_documents_may_be_anything(nh, kvh, hs, past, q, pad, dtype):
+    b, rules, unseen = _between_documents(nh, kvh, hs, past, q, pad, dtype)
+    want = rules.call(b)
+    rules.check(b, *want)
+    for fill in (-1, 1 << 30, b.blocks, -(1 << 31)):
+        table = b.table.copy()
+        table[0, unseen] = fill
+        b.meta = (*b.meta[:2], i32(table))
+        got = rules.call(b)
+        assert int(b.error) == 0
+        assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
+@pytest.mark.parametrize("nh,kvh,hs,past,q,pad", [(2, 2, 128, 30, 126, 70), (130, 1, 64, 20, 100, 60)])
+def test_a_bad_page_that_one_row_sees_is_reported(nh, kvh, hs, past, q, pad):
+    b, rules, unseen = _between_documents(nh, kvh, hs, past, q, pad)
+    page = unseen[1]
+    table = b.table.copy()
+    table[0, page] = b.blocks
+    b.meta = (*b.meta[:2], i32(table))
+    rules.call(b)
+    assert int(b.error) == 0
+    j = (page + 1) * 16 - 1 - past  # the row of the page's last key sees that key alone
+    rules.first[j] = past + j
+    rules.call(b)
+    assert int(b.error) == pa.DEVERR_BAD_BLOCK

@@ -80,8 +80,8 @@ def biased_paged_attention(query: torch.Tensor, key_cache: torch.Tensor, value_c
     (num_heads,)) times the distance of the positions. A row at position p sees keys up to p, or
     up to ``prefix_lens`` (int32 (batch,)) where that is more (never past the sequence's end), from
     the latest of 0, ``p - window + 1`` (``window`` > 0) and ``first_keys`` (int32 (N,): the start
-    of the row's document). A row that sees none gives zeros and an lse of -inf. Pages that no row
-    of a sequence sees are not looked up. ``max_query_len`` (optional) is the host's bound on new
+    of the row's document). A row that sees none gives zeros and an lse of -inf. The table's
+    entries of pages that no row of a sequence sees may be anything. ``max_query_len`` (optional) is the host's bound on new
     rows per sequence. ``query`` may be a view of packed rows; ``lse`` (float32 (N, num_heads))
     receives the log-sum-exp; rows behind the last sequence are left as they were. ``workspace``
     (``biased_workspace_size(head_size)`` bytes): else the call allocates its own. A pipeline wait

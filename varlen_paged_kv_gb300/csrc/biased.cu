@@ -4,8 +4,9 @@
 // Row j of a sequence is at position p = past + j and sees the keys [lo, hi): lo the largest of 0,
 // first_keys[row] and p - window + 1, hi the smaller of past + q and max(p + 1, prefix). Its score
 // of key t for head h is s = scale q.k, then cap * tanh(s / cap), then - slope_h |p - t|; softmax
-// and P V in fp32, rounded once to T. A row without keys gives zeros and an lse of -inf. Keys that
-// no row of an item sees are not read, so their pages need not be there (a window's old pages).
+// and P V in fp32, rounded once to T. A row without keys gives zeros and an lse of -inf. Keys
+// before the first and behind the last that a row of an item sees are not read, and pages between that no row sees (rows
+// without keys among packed documents) are not reported, so neither need be there (a window's old pages).
 //
 // Two kernels, by the rows that share a KV head's keys:
 //   biased_rows_kernel  sequences of up to 16 such rows (decode steps, short drafts): bound by the
@@ -256,7 +257,8 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
         if (lane >= nseg || t >= it.te || v >= it.keys.hi || v + seg_rows <= it.keys.lo) return oob;
         const int page = v / a.bs, phys = table[page];
         if (phys < 0 || phys >= a.num_blocks) {
-          atomicOr(err, PA_DEVERR_BAD_BLOCK);
+          const int j0 = it.r_first / a.G, j1 = (it.r_first + it.n_rows - 1) / a.G;
+          if (some_row_sees(a, it.c0, it.q, it.past, it.prefix, j0, j1 - j0 + 1, v, seg_rows)) atomicOr(err, PA_DEVERR_BAD_BLOCK);
           return oob;
         }
         return phys * a.bs + (v - page * a.bs);

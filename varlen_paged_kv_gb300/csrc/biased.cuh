@@ -41,6 +41,19 @@ __device__ __forceinline__ Keys keys_of_row(const BiasedArgs& a, const Seq& s, i
   if (k.lo >= k.hi) k.lo = INT32_MAX, k.hi = 0;
   return k;
 }
+// Whether some row of a sequence's `rows` from j0 on sees one of the keys [v, v + n). (Where rows that see nothing
+// lie between documents, the keys of a block of rows have gaps, and a page in one is no row's: what stands in the
+// table for it must not be reported. Asked of pages outside the pool only; later rows mostly see more.)
+static __device__ __noinline__ bool some_row_sees(const BiasedArgs& a, int c0, int q_len, int past, int prefix, int j0, int rows,
+                                                  int v, int n) {
+  Seq s;
+  s.c0 = c0, s.q = q_len, s.past = past;
+  for (int j = j0 + rows - 1; j >= j0; --j) {
+    const Keys k = keys_of_row(a, s, prefix, j);
+    if (k.lo < v + n && k.hi > v) return true;
+  }
+  return false;
+}
 __device__ __forceinline__ Keys join(Keys x, Keys y) { return {min(x.lo, y.lo), max(x.hi, y.hi)}; }
 
 __device__ __forceinline__ Seq seq_at(const BiasedArgs& a, int b) {

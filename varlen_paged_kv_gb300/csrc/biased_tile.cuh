@@ -369,7 +369,8 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
         if (lane >= nseg || t >= n || v >= it.hi || v + seg_rows <= it.lo) return oob;
         const int page = v / a.bs, phys = table[page];
         if (phys < 0 || phys >= a.num_blocks) {
-          atomicOr(err, PA_DEVERR_BAD_BLOCK);
+          if (some_row_sees(a, it.row0, it.total - it.pos0, it.pos0, it.prefix, 0, it.rows, v, seg_rows))
+            atomicOr(err, PA_DEVERR_BAD_BLOCK);
           return oob;
         }
         return phys * a.bs + (v - page * a.bs);
