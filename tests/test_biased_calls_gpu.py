@@ -65,3 +65,28 @@ def test_a_bad_page_that_one_row_sees_is_reported(nh, kvh, hs, past, q, pad):
     rules.first[j] = past + j
     rules.call(b)
     assert int(b.error) == pa.DEVERR_BAD_BLOCK
+
+
+# ---- values at the type's end ------------------------------------------------------------------
+
+
+SATURATED = [([0], [40], {}, 0), ([300, 5], [70, 200], dict(softcap=20.0), 0),  # tiles
+             ([3000], [12], {}, 0),                                             # a cluster's tile
+             ([60], [3], {}, 4), ([60, 900, 0], [3, 4, 2], dict(bias=True), 0),  # rows: a cluster's, whole items, merged pieces
+             ([9000] * 3, [4, 4, 1], {}, 4)]
+
+
+@pytest.mark.parametrize("hs", [64, 128, 256])
+@pytest.mark.parametrize("past,q,kw,longest", SATURATED)
+def test_fp16_values_at_the_types_end_stay_finite(past, q, kw, longest, hs):
+    """A mean of values of 65504 is 65504, however the weights are rounded on their way."""
+    for seed in range(3):
+        b = Batch(90 + seed, "fp16", 8, 2, hs, 16, past, q)
+        for channel, value in ((3, 65504.0), (hs - 1, -65504.0)):
+            v = b.value_cache[..., channel]
+            v.copy_(torch.where(v.isnan(), v, torch.full_like(v, value)))
+        rules = Rules(b, seed=3, bound=longest or None, **kw)
+        out, lse = rules.call(b)
+        assert int(b.error) == 0
+        assert torch.isfinite(out).all()
+        rules.check(b, out, lse)

@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
           const int rs = it.r_first + r;
           const int64_t at = (int64_t)(it.c0 + rs / a.G) * a.nh + it.g * a.G + rs % a.G;
           const float inv = M == -INFINITY ? 0.f : 1.f / S;
-          uint2 out = make_uint2(pack2<BF16>(x.x * inv, x.y * inv), pack2<BF16>(x.z * inv, x.w * inv));
+          uint2 out = make_uint2(pack_out<BF16>(x.x * inv, x.y * inv), pack_out<BF16>(x.z * inv, x.w * inv));
           if (M == -INFINITY) out = make_uint2(0, 0);
           else if (!finite4(x.x * inv, x.y * inv, x.z * inv, x.w * inv)) *redo = 1;
           *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.output) + at * HS + cc) = out;
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
       }
       const int64_t at = (int64_t)(it.c0 + r / a.G) * a.nh + it.g * a.G + r % a.G;
       const float inv = M == -INFINITY ? 0.f : 1.f / S;
-      uint2 out = make_uint2(pack2<BF16>(x[0] * inv, x[1] * inv), pack2<BF16>(x[2] * inv, x[3] * inv));
+      uint2 out = make_uint2(pack_out<BF16>(x[0] * inv, x[1] * inv), pack_out<BF16>(x[2] * inv, x[3] * inv));
       if (M == -INFINITY) out = make_uint2(0, 0);
       else if (!finite4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv)) atomicOr(redo, 1u << r);
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.output) + at * HS + cc) = out;
@@ -630,7 +630,7 @@ __global__ void __launch_bounds__(kMergeThreads) biased_merge_kernel(const __gri
     const int rs = head.z + r;
     const int64_t at = (int64_t)(head.y + rs / a.G) * a.nh + head.w * a.G + rs % a.G;
     const float inv = M == -INFINITY ? 0.f : 1.f / S;
-    uint2 out = make_uint2(pack2<BF16>(x[0] * inv, x[1] * inv), pack2<BF16>(x[2] * inv, x[3] * inv));
+    uint2 out = make_uint2(pack_out<BF16>(x[0] * inv, x[1] * inv), pack_out<BF16>(x[2] * inv, x[3] * inv));
     if (M == -INFINITY) out = make_uint2(0, 0);
     const bool there = i < head.x * (HS / 4);
     if (there) {

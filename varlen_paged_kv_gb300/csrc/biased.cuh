@@ -74,6 +74,19 @@ __device__ __forceinline__ void check_biased_batch(const BiasedArgs& a) {
   if (bad) atomicOr(a.error, PA_DEVERR_BAD_BATCH);
 }
 
+// ---- results ---------------------------------------------------------------------------------
+// Two results as T. The fp16 weights were rounded on their way into P V and their sum was not, so a mean of values near
+// 65504 may come out up to 2^-11 above it, where fp16 rounds to infinity: what is finite stays so.
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack_out(float x, float y) {
+  if constexpr (!BF16) {
+    constexpr float top = 65504.f;
+    if (fabsf(x) < INFINITY) x = fminf(fmaxf(x, -top), top);
+    if (fabsf(y) < INFINITY) y = fminf(fmaxf(y, -top), top);
+  }
+  return pack2<BF16>(x, y);
+}
+
 // ---- rows whose result is not finite ---------------------------------------------------------
 // The products P V run over all keys that some row of an item sees, with weights of 0 where a row does
 // not, and 0 times a value that is not finite is NaN. So a row whose result is not finite is computed
@@ -114,7 +127,7 @@ __device__ __noinline__ void redo_row(const BiasedArgs& a, int b, int c0, int q_
   }
   uint16_t* out = static_cast<uint16_t*>(a.output) + (row * a.nh + h) * HS + lane * E;
   for (int e = 0; e < E; e += 2)
-    if (lane * E + e >= from && lane * E + e < to_channel) *reinterpret_cast<uint32_t*>(out + e) = pack2<BF16>(o[e] / l, o[e + 1] / l);
+    if (lane * E + e >= from && lane * E + e < to_channel) *reinterpret_cast<uint32_t*>(out + e) = pack_out<BF16>(o[e] / l, o[e + 1] / l);
 }
 
 __device__ __forceinline__ bool finite4(float x, float y, float z, float w) {
