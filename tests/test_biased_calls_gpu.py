@@ -90,3 +90,19 @@ def test_fp16_values_at_the_types_end_stay_finite(past, q, kw, longest, hs):
         assert int(b.error) == 0
         assert torch.isfinite(out).all()
         rules.check(b, out, lse)
+
+
+@pytest.mark.parametrize("hs", [64, 128, 256])
+@pytest.mark.parametrize("past,q,kw,longest", SATURATED)
+def test_bf16_values_whose_sum_is_past_32_bits_keep_their_mean(past, q, kw, longest, hs):
+    b = Batch(95, "bf16", 8, 2, hs, 16, past, q)
+    v = b.value_cache[..., 5]
+    top = torch.finfo(torch.bfloat16).max
+    v.copy_(torch.where(v.isnan(), v, torch.full_like(v, top)))
+    v = b.value_cache[..., 7]
+    v.copy_(torch.where(v.isnan(), v, v.sign() * 2.0 ** 127))  # of both signs
+    rules = Rules(b, seed=3, bound=longest or None, **kw)
+    out, lse = rules.call(b)
+    assert int(b.error) == 0
+    assert torch.isfinite(out).all()
+    rules.check(b, out, lse)

@@ -91,9 +91,9 @@ __device__ __forceinline__ uint32_t pack_out(float x, float y) {
 // The products P V run over all keys that some row of an item sees, with weights of 0 where a row does
 // not, and 0 times a value that is not finite is NaN. So a row whose result is not finite is computed
 // again, here, over its own keys alone, by one warp in fp32 (channels from .. to_channel - 1 of it): what is
-// left is what those keys make of it.
-// (Slow, 0.1 ms for 5000 keys, but bounded, and over at the first key whose score or values are NaN throughout;
-// finite values never come here.)
+// left is what those keys make of it. bf16 values as large as 32 bits hold come here too, where their sum by
+// weights not yet divided by the weights' own sum overflowed; here it is their mean that is carried from key to key.
+// (Slow, 0.1 ms for 5000 keys, but bounded, and over at the first key whose score or values are NaN throughout.)
 template <int HS, bool BF16>
 __device__ __noinline__ void redo_row(const BiasedArgs& a, int b, int c0, int q_len, int past, int j, int h, int lane,
                                       int from, int to_channel) {
@@ -117,17 +117,19 @@ __device__ __noinline__ void redo_row(const BiasedArgs& a, int b, int c0, int q_
     const float to = fmaxf(m, x), f = to == -INFINITY ? 1.f : fast_exp2(m - to);
     const float w = x == -INFINITY ? 0.f : fast_exp2(x - to);  // (NaN for a score of NaN, on the first key too)
     m = to;
-    l = l * f + w;
+    const float sum = l * f + w;
+    const float old = sum == 0.f ? 1.f : l * f / sum, add = sum == 0.f ? 0.f : w / sum;  // (no weight yet: 0)
+    l = sum;
     bool lost = true;
-    for (int e = 0; e < E; ++e) {
-      o[e] = (f == 1.f ? o[e] : o[e] * f) + w * (there ? value(a.value_cache[at + e]) : 0.f);
+    for (int e = 0; e < E; ++e) {  // (the mean so far: no larger than its values)
+      o[e] = o[e] * old + add * (there ? value(a.value_cache[at + e]) : 0.f);
       lost = lost && o[e] != o[e];
     }
     if (__all_sync(0xffffffffu, lost)) break;  // NaN throughout: no key changes that
   }
   uint16_t* out = static_cast<uint16_t*>(a.output) + (row * a.nh + h) * HS + lane * E;
   for (int e = 0; e < E; e += 2)
-    if (lane * E + e >= from && lane * E + e < to_channel) *reinterpret_cast<uint32_t*>(out + e) = pack_out<BF16>(o[e] / l, o[e + 1] / l);
+    if (lane * E + e >= from && lane * E + e < to_channel) *reinterpret_cast<uint32_t*>(out + e) = pack_out<BF16>(o[e], o[e + 1]);
 }
 
 __device__ __forceinline__ bool finite4(float x, float y, float z, float w) {
