@@ -106,3 +106,56 @@ def test_bf16_values_whose_sum_is_past_32_bits_keep_their_mean(past, q, kw, long
     assert int(b.error) == 0
     assert torch.isfinite(out).all()
     rules.check(b, out, lse)
+
+
+# ---- inputs rewritten right before the call ----------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("nh,kvh,hs", [(8, 2, 128), (16, 2, 256), (32, 8, 64)])
+def test_inputs_rewritten_right_before_a_mixed_call(nh, kvh, hs, dtype):
+    """Prompts and decode rows in one call, whose kernels run side by side: each sees what the kernels right before the
+    call have written to the query, the lengths, the table and the rules, and none of what stood there in the call before."""
+    total = np.array([200, 300, 150, 400, 90, 700, 30, 600])
+    qs = [[1, 40, 1, 90, 1, 2, 1, 1], [40, 1, 90, 1, 1, 1, 1, 2], [1, 1, 1, 1, 2, 60, 2, 69]]
+    sets, want = [], []
+    for seed, q in enumerate(qs):
+        b = Batch(100 + seed, dtype, nh, kvh, hs, 16, total - q, q)
+        rules = Rules(b, documents=200, prefix=40, bias=True, seed=seed)
+        want.append(rules.call(b))
+        assert int(b.error) == 0
+        rules.check(b, *want[-1])
+        sets.append([b.query.contiguous(), *b.meta, b.key_cache, b.value_cache, i32(rules.first), i32(rules.prefix),
+                     torch.from_numpy(rules.slopes).cuda() * (1 + 0 * seed)])
+    assert all(x.shape == y.shape for s in sets for x, y in zip(s, sets[0]))
+    now = [t.clone() for t in sets[0]]
+
+    def call(k):
+        for t, x in zip(now, k):
+            t.copy_(x)
+        query, cum, past, table, kc, vc, first, prefix, slopes = now
+        lse = torch.empty(query.shape[0], nh, device="cuda")
+        out = pa.biased_paged_attention(query, kc, vc, cum, past, table, num_heads=nh, kv_num_heads=kvh, slopes=slopes,
+                                        first_keys=first, prefix_lens=prefix, lse=lse)
+        return out, lse
+
+    for _ in range(4):
+        got = [call(s) for s in sets]  # one after the other, nothing waited for
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+    turn = [[t.clone() for t in s] for s in sets[:2]]  # what the graph's two calls are given
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=stream):
+        got = [call(s) for s in turn]
+    for k in range(6):
+        for i, s in enumerate(turn):
+            for t, x in zip(s, sets[(k + i) % 3]):
+                t.copy_(x)
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, g in enumerate(got):
+            w = want[(k + i) % 3]
+            assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])

@@ -183,8 +183,11 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
   }
   // Beside the tile kernel, whose every CTA has waited for what came before and let this one start, there is
   // nothing to wait for but at the end, by one CTA for all: this kernel must not be over before that one, since
-  // what comes next waits for this one only.
-  if (!a.after_tiles) pdl_wait();
+  // what comes next waits for this one only. What came before is complete then and has left its writes in L2; that
+  // they are what the loads below see, which the wait says elsewhere, a fence says here (and the loads are plain
+  // ones: none may take its value from a cache that is not coherent).
+  if (a.after_tiles) acquire_earlier_kernels();
+  else pdl_wait();
   pdl_launch_dependents();
   const int c = blockIdx.x, rank = blockIdx.z;
   const bool waits = a.after_tiles && c == 0 && rank == 0;
@@ -302,8 +305,8 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
         const uint32_t* p = reinterpret_cast<const uint32_t*>(a.query + (int64_t)(it.c0 + j) * a.q_stride + (int64_t)h * HS + tq * 2);
 #pragma unroll
         for (int ks = 0; ks < NKS; ++ks) {
-          qa[ks][i] = rc == r ? __ldg(p + ks * 8) : 0u;
-          qa[ks][i + 2] = rc == r ? __ldg(p + ks * 8 + 4) : 0u;
+          qa[ks][i] = rc == r ? p[ks * 8] : 0u;
+          qa[ks][i + 2] = rc == r ? p[ks * 8 + 4] : 0u;
         }
         k[i] = keys_of_row(a, sq, it.prefix, j);
         pos[i] = it.past + j;

@@ -318,9 +318,19 @@ struct PreSmem {
 // completed and its writes are visible, and since the predecessor waited for its own
 // predecessor, completion is transitive along the stream. pdl_launch_dependents() lets the
 // next kernel launch (its CTAs then sit in their own pdl_wait until this grid completes).
+// One kernel does not wait at its start: biased_rows_kernel beside the biased tile kernel, whose
+// CTAs have all waited before they let it launch. What earlier kernels wrote is complete then;
+// acquire_earlier_kernels() takes the place of the wait before the first loads, and one of its
+// CTAs waits before it ends, so that completion stays transitive.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// by every thread: its plain loads behind this, and TMA loads, see what kernels that are complete have written
+__device__ __forceinline__ void acquire_earlier_kernels() {
+  asm volatile("fence.acq_rel.gpu;" ::: "memory");
+  asm volatile("fence.proxy.async.global;" ::: "memory");
 }
 
 // A launch that may start before the previous kernel of the stream finishes (programmatic
