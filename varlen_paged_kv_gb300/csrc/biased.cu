@@ -259,9 +259,16 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
         const int v = t * kBiTile + lane * seg_rows;
         if (lane >= nseg || t >= it.te || v >= it.keys.hi || v + seg_rows <= it.keys.lo) return oob;
         const int page = v / a.bs, phys = table[page];
-        if (phys < 0 || phys >= a.num_blocks) {
-          const int j0 = it.r_first / a.G, j1 = (it.r_first + it.n_rows - 1) / a.G;
-          if (some_row_sees(a, it.c0, it.q, it.past, it.prefix, j0, j1 - j0 + 1, v, seg_rows)) atomicOr(err, PA_DEVERR_BAD_BLOCK);
+        if (unlikely(phys < 0 || phys >= a.num_blocks)) {
+          // (reported if a row of the item sees one of these keys: with up to 16 rows in all, the gaps between their
+          // ranges are shorter than 16 keys, and of a wider group an item has two rows at most)
+          Seq sq;
+          sq.c0 = it.c0, sq.q = it.q, sq.past = it.past;
+          auto sees = [&](int r) {
+            const Keys k = keys_of_row(a, sq, it.prefix, r / a.G);
+            return k.lo < v + seg_rows && k.hi > v;
+          };
+          if (CLUSTER || a.G <= 16 || sees(it.r_first) || sees(it.r_first + it.n_rows - 1)) atomicOr(err, PA_DEVERR_BAD_BLOCK);
           return oob;
         }
         return phys * a.bs + (v - page * a.bs);

@@ -8,6 +8,11 @@ namespace pa {
 
 constexpr int kBiTile = 64;          // keys per tile
 
+// (where the compiler lays the rarer path out of line: the softmax's code is long, and what it jumps
+// over costs fetches)
+__device__ __forceinline__ bool likely(bool x) { return __builtin_expect(x, 1); }
+__device__ __forceinline__ bool unlikely(bool x) { return __builtin_expect(x, 0); }
+
 // ---- scores --------------------------------------------------------------------------------
 // tanh as u times a polynomial in u^2 (minimax by weighted least squares on 4000 Chebyshev points) up to
 // |u| = 0.25, 4.9e-8 off at most (with six terms up to 0.75, 9.5e-9), beyond that from the exponential,
@@ -40,19 +45,6 @@ __device__ __forceinline__ Keys keys_of_row(const BiasedArgs& a, const Seq& s, i
   k.hi = min(max(p + 1, prefix), s.past + s.q);
   if (k.lo >= k.hi) k.lo = INT32_MAX, k.hi = 0;
   return k;
-}
-// Whether some row of a sequence's `rows` from j0 on sees one of the keys [v, v + n). (Where rows that see nothing
-// lie between documents, the keys of a block of rows have gaps, and a page in one is no row's: what stands in the
-// table for it must not be reported. Asked of pages outside the pool only; later rows mostly see more.)
-static __device__ __noinline__ bool some_row_sees(const BiasedArgs& a, int c0, int q_len, int past, int prefix, int j0, int rows,
-                                                  int v, int n) {
-  Seq s;
-  s.c0 = c0, s.q = q_len, s.past = past;
-  for (int j = j0 + rows - 1; j >= j0; --j) {
-    const Keys k = keys_of_row(a, s, prefix, j);
-    if (k.lo < v + n && k.hi > v) return true;
-  }
-  return false;
 }
 __device__ __forceinline__ Keys join(Keys x, Keys y) { return {min(x.lo, y.lo), max(x.hi, y.hi)}; }
 

@@ -37,18 +37,14 @@ struct BiTile {
   static constexpr int kItem = (kAbort + 12 + 15) / 16 * 16;
   static constexpr int kMl = kItem + 64;                            // float [2][128]: m and l of the rows
   static constexpr int kX = kMl + 2 * 128 * 4;                      // float [2][128][2]: maxima and sums of half rows
-  static constexpr int kRedo = kX + 2 * 128 * 2 * 4;                // uint32 [4]: rows whose result is not finite
+  static constexpr int kRedo = kX + 2 * 128 * 2 * 4;                // uint32 [5]: rows whose result is not finite, pages to report
   static constexpr uint32_t kTmem = HS == 256 ? 512 : 256;          // S, S, O at columns 0, 64, 128
   static_assert(128 * HS * 4 <= 2 * kStages * kTileBytes, "the cluster's partial result lies over the ring");
   // At least a third of an SM's shared memory, so that no more CTAs share an SM than find TMEM
   // there: a CTA that waited for TMEM while its cluster waits for it could wait for ever.
-  static constexpr int kNeed = kRedo + 16 + 1024;
+  static constexpr int kNeed = kRedo + 32 + 1024;
   static constexpr int kBytes = kNeed < 80 * 1024 ? 80 * 1024 : kNeed;
 };
-// (where the compiler lays the rarer path out of line: the softmax's code is long, and what it jumps
-// over costs fetches)
-__device__ __forceinline__ bool likely(bool x) { return __builtin_expect(x, 1); }
-__device__ __forceinline__ bool unlikely(bool x) { return __builtin_expect(x, 0); }
 
 // tcgen05.ld 32x32b of COLS consecutive columns of this thread's TMEM lane, with the largest of them, or of their
 // magnitudes, on the way (NaN passed over, as fmaxf does)
@@ -123,6 +119,26 @@ __device__ __forceinline__ TileItem tile_item(const BiasedArgs& a, int u, int su
   it.all_lo = __reduce_max_sync(0xffffffffu, all.lo);
   it.all_hi = __reduce_min_sync(0xffffffffu, all.hi);
   return it;
+}
+
+// Reports the pages outside the pool among those of the keys [from, to), unless none of the sequence's `rows` rows from
+// j0 on sees a key of such a page: where rows that see nothing lie between documents, the keys of a block of rows have
+// gaps, and what stands in the table for a page in one must not be reported. By the whole block, at its end, and only
+// where a producer met such a page (asked there, it cost 4 of 321 us of chunks whose tables are good).
+static __device__ __noinline__ void report_pages(const BiasedArgs& a, int b, int c0, int q_len, int past, int prefix, int j0,
+                                                 int rows, int from, int to) {
+  Seq s;
+  s.c0 = c0, s.q = q_len, s.past = past;
+  for (int page = from / a.bs + (int)threadIdx.x; (int64_t)page * a.bs < to; page += (int)blockDim.x) {
+    const int phys = a.table[(int64_t)b * a.max_blocks + page], v = page * a.bs;
+    if (phys >= 0 && phys < a.num_blocks) continue;
+    for (int j = j0 + rows - 1; j >= j0; --j) {  // (later rows mostly see more)
+      const Keys k = keys_of_row(a, s, prefix, j);
+      if (k.lo >= min(v + a.bs, to) || k.hi <= max(v, from)) continue;
+      atomicOr(a.error, PA_DEVERR_BAD_BLOCK);
+      break;
+    }
+  }
 }
 
 // N products q.k of a row as scores in powers of two, consecutive keys from v0 on: capped, less their
@@ -316,7 +332,7 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
     }
     *abort = 0;
     *err = 0;
-    for (int i = 0; i < 4; ++i) redo[i] = 0;
+    for (int i = 0; i < 5; ++i) redo[i] = 0;
     fence_mbar_init();
   }
   pdl_wait();
@@ -368,9 +384,8 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
         const int v = (last - t) * kBiTile + lane * seg_rows;
         if (lane >= nseg || t >= n || v >= it.hi || v + seg_rows <= it.lo) return oob;
         const int page = v / a.bs, phys = table[page];
-        if (phys < 0 || phys >= a.num_blocks) {
-          if (some_row_sees(a, it.row0, it.total - it.pos0, it.pos0, it.prefix, 0, it.rows, v, seg_rows))
-            atomicOr(err, PA_DEVERR_BAD_BLOCK);
+        if (unlikely(phys < 0 || phys >= a.num_blocks)) {
+          redo[4] = 1;
           return oob;
         }
         return phys * a.bs + (v - page * a.bs);
@@ -715,6 +730,9 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
   tc_fence_before();
   __syncthreads();  // (no warp waits any more: whichever gave up has said so)
   if (threadIdx.x == 0 && *err && a.error) atomicOr(a.error, *err);
+  if (redo[4] && a.error)
+    report_pages(a, it.b, it.row0, it.total - it.pos0, it.pos0, it.prefix, 0, it.rows, max(t0 * kBiTile, it.lo),
+                 min((t0 + n) * kBiTile, it.hi));
   if (redo[0] | redo[1] | redo[2] | redo[3])
     for (int r = warp; r < it.rows * a.G; r += THREADS / 32)
       if (redo[r >> 5] >> (r & 31) & 1)  // (the item's rows counted from 0)
