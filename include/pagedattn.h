@@ -501,7 +501,7 @@ size_t pa_pool_workspace_size(int32_t num_blocks);
  * last free page in ascending order; none of them is given out by the same call.
  *
  * free_blocks is updated in place, free_state_out (2) is the state for the next step; the other
- * outputs are in memory of their own. error (1), not accumulated: 0, or why the fork was refused:
+ * outputs are in memory of their own (PA_ERR_INVALID_ARGUMENT where any of it overlaps). error (1), not accumulated: 0, or why the fork was refused:
  * PA_DEVERR_NO_BLOCKS (fewer free pages than copies), PA_DEVERR_BAD_BLOCK (a held entry outside
  * the pool) or PA_DEVERR_BAD_BATCH (a parent, length or count out of range, a parent that holds
  * less than its past, a free_state that does not fit the ring). A refused fork changes neither
@@ -528,7 +528,8 @@ pa_status pa_fork_block_tables(const int32_t* parents, const int32_t* past_seqle
  * (-1, -1): pa_copy_pages makes them before the new table is used. free_blocks (a ring of
  * free_capacity entries) receives all pages that are free after the moves in ascending order,
  * with free_state_out = {0, their count}; its other entries stay. pages_end (1): one more than the
- * highest page still in use.
+ * highest page still in use. Outputs that overlap each other or an input are refused
+ * (PA_ERR_INVALID_ARGUMENT), but for block_table_out that is block_table.
  *
  * error (1), not accumulated: 0, or why nothing was moved: PA_DEVERR_BAD_BLOCK (a held entry
  * outside the pool) or PA_DEVERR_BAD_BATCH (blocks_held out of range, more free pages than

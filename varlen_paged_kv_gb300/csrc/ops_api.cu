@@ -15,6 +15,25 @@ bool all_aligned(uintptr_t a, std::initializer_list<const void*> ps) {
   return true;
 }
 
+// memory that a call reads or writes
+struct Range {
+  uintptr_t from, to;
+  Range(const void* p, int64_t bytes)
+      : from(reinterpret_cast<uintptr_t>(p)), to(p && bytes > 0 ? from + (uintptr_t)bytes : from) {}
+  bool meets(const Range& r) const { return from < r.to && r.from < to; }
+};
+
+// whether each of `written` is apart from the others and from all of `read`
+bool all_apart(std::initializer_list<Range> written, std::initializer_list<Range> read) {
+  for (const Range* w = written.begin(); w != written.end(); ++w) {
+    for (const Range* o = written.begin(); o != w; ++o)
+      if (w->meets(*o)) return false;
+    for (const Range& r : read)
+      if (w->meets(r)) return false;
+  }
+  return true;
+}
+
 pa_status launched(cudaError_t e, const char* what, int kernels = 1) {
   if (e) return pa::cuda_fail(e, what);
   while (kernels-- > 0) pa::count_launch();
@@ -286,9 +305,12 @@ pa_status pa_fork_block_tables(const int32_t* parents, const int32_t* past_seqle
       (!all_aligned(4, {parents, past_seqlens_out, blocks_held_out, block_table_out}) || !aligned(copies, 8)))
     return PA_ERR_INVALID_ARGUMENT;
   // rows are read while others are written
-  if (free_state_out == free_state ||
-      (batch_size > 0 && new_batch_size > 0 &&
-       (past_seqlens_out == past_seqlens || blocks_held_out == blocks_held || block_table_out == block_table)))
+  const int64_t B = batch_size, n = new_batch_size, width = max_blocks_per_sequence;
+  if (!all_apart({{past_seqlens_out, 4 * n}, {blocks_held_out, 4 * n}, {block_table_out, 4 * n * width}, {copies, 8 * n},
+                  {free_state_out, 8}, {error, 4}, {free_blocks, 4 * (int64_t)free_capacity},
+                  {workspace, (int64_t)pa::pool_workspace(num_blocks, true, nullptr, nullptr)}},
+                 {{parents, 4 * n}, {past_seqlens, 4 * B}, {blocks_held, 4 * B}, {block_table, 4 * B * width},
+                  {free_state, 8}, {pinned, num_blocks}}))
     return PA_ERR_INVALID_ARGUMENT;
   if (workspace_bytes < pa::pool_workspace(num_blocks, true, nullptr, nullptr)) return PA_ERR_WORKSPACE_TOO_SMALL;
   int sms = 0;
@@ -334,6 +356,13 @@ pa_status pa_compact_block_tables(const int32_t* blocks_held, const int32_t* blo
     return PA_ERR_INVALID_ARGUMENT;
   if (batch_size > 0 && !all_aligned(4, {blocks_held, block_table, block_table_out})) return PA_ERR_INVALID_ARGUMENT;
   if (max_moves > 0 && !aligned(copies, 8)) return PA_ERR_INVALID_ARGUMENT;
+  // (a table that is renamed in place is one: each entry is read and written by one thread)
+  const int64_t B = batch_size, entries = B * max_blocks_per_sequence;
+  if (!all_apart({{block_table_out, 4 * entries}, {copies, 8 * (int64_t)max_moves}, {free_state_out, 8}, {pages_end, 4},
+                  {error, 4}, {free_blocks, 4 * (int64_t)free_capacity},
+                  {workspace, (int64_t)pa::pool_workspace(num_blocks, false, nullptr, nullptr)}},
+                 {{blocks_held, 4 * B}, {block_table, block_table_out == block_table ? 0 : 4 * entries}, {pinned, num_blocks}}))
+    return PA_ERR_INVALID_ARGUMENT;
   if (workspace_bytes < pa::pool_workspace(num_blocks, false, nullptr, nullptr)) return PA_ERR_WORKSPACE_TOO_SMALL;
   int sms = 0;
   if (!pa::device_sms(&sms)) return pa::cuda_fail(cudaGetLastError(), "device query");
