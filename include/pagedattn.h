@@ -466,7 +466,8 @@ pa_status pa_sparse_paged_attention(const void* query, const void* key_cache, co
 
 /* ======================= pages that are shared, copied and moved ======================= */
 
-/* Most pages of a pool that the two entry points below take, and most tensors and entries of one copy. */
+/* Most pages of a pool that the two entry points below take (of tables of up to 2^31 - 1025 columns), and most
+ * tensors and entries of one copy. */
 #define PA_MAX_POOL_PAGES (1 << 20)
 #define PA_MAX_COPY_TENSORS 256
 #define PA_MAX_COPIES (1 << 25)

@@ -1,4 +1,5 @@
-"""Outputs of the page operators that overlap an input, the ring or each other: refused on the host before any launch."""
+"""Sizes and memory that the page operators refuse on the host, before any launch: outputs that overlap an input, the ring
+or each other, and tables too wide to be counted."""
 import pytest
 
 from test_pool_host import FAKE, compact, fork, lib  # noqa: F401
@@ -58,3 +59,14 @@ def test_the_workspace_is_the_calls_alone(lib):  # noqa: F811
         for name in outs:
             assert call(lib, ws_bytes=16, **{"ws": FAKE + 4096 * 40, name: FAKE + 4096 * 40 + 64}) == 1, name
     assert fork(lib, ws_bytes=16, ws=FAKE + 4096 * 40, error=FAKE + 4096 * 40 + need) == 3
+
+
+@pytest.mark.parametrize("columns", [(1 << 31) - 1, (1 << 31) - 256, (1 << 31) - 1024])
+def test_rows_whose_columns_do_not_fit_32_bits_with_a_part_behind_them(lib, columns):  # noqa: F811
+    """Columns are counted in parts of up to 256: those behind the last must have numbers too."""
+    assert fork(lib, B=1, n=1, cols=columns, bs=1, ws_bytes=16) == 2
+    assert fork(lib, B=0, n=1, cols=columns, bs=1, ws_bytes=16) == 2
+    assert compact(lib, B=1, cols=columns, ws_bytes=16) == 2
+    most = (1 << 31) - 1025
+    assert fork(lib, B=0, n=0, cols=most, bs=1, ws_bytes=16) == 3
+    assert compact(lib, B=0, cols=most, ws_bytes=16) == 3

@@ -15,6 +15,9 @@ bool all_aligned(uintptr_t a, std::initializer_list<const void*> ps) {
   return true;
 }
 
+// (the page operators go over a row's columns in parts, and count past the last one in 32 bits)
+constexpr int32_t kMostColumns = INT32_MAX - 1024;
+
 // memory that a call reads or writes
 struct Range {
   uintptr_t from, to;
@@ -294,6 +297,7 @@ pa_status pa_fork_block_tables(const int32_t* parents, const int32_t* past_seqle
       free_capacity <= 0)
     return PA_ERR_INVALID_ARGUMENT;
   if (batch_size > PA_MAX_TABLE_REQUESTS || new_batch_size > PA_MAX_TABLE_REQUESTS || num_blocks > PA_MAX_POOL_PAGES ||
+      max_blocks_per_sequence > kMostColumns ||
       (int64_t)max_blocks_per_sequence * block_size > INT32_MAX ||
       (int64_t)batch_size * max_blocks_per_sequence > INT32_MAX ||
       (int64_t)new_batch_size * max_blocks_per_sequence > INT32_MAX || free_capacity > (1 << 30))
@@ -350,6 +354,7 @@ pa_status pa_compact_block_tables(const int32_t* blocks_held, const int32_t* blo
   if (batch_size < 0 || max_blocks_per_sequence <= 0 || num_blocks <= 0 || free_capacity <= 0 || max_moves < 0)
     return PA_ERR_INVALID_ARGUMENT;
   if (batch_size > PA_MAX_TABLE_REQUESTS || num_blocks > PA_MAX_POOL_PAGES || max_moves > PA_MAX_POOL_PAGES ||
+      max_blocks_per_sequence > kMostColumns ||
       (int64_t)batch_size * max_blocks_per_sequence > INT32_MAX || free_capacity > (1 << 30))
     return PA_ERR_UNSUPPORTED;
   if (!all_aligned(4, {free_blocks, free_state_out, pages_end, error}) || !aligned(workspace, 16))
