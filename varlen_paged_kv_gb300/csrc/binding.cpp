@@ -325,20 +325,6 @@ PyObject* sparse_paged_attention(PyObject*, PyObject* const* v, Py_ssize_t n) {
   });
 }
 
-// The outputs (`ints` int32 values) and the workspace of a page operator: one allocation where the workspace is
-// small, so that the outputs, which live longer, do not hold much of it.
-struct PoolMemory {
-  at::Tensor all, own;
-  void* workspace;
-  PoolMemory(const Call& call, int64_t ints, size_t bytes) {
-    const bool together = bytes <= 65536;
-    const int64_t at = (ints + 3) / 4 * 4;
-    all = call.empty({together ? at + (int64_t)(bytes / 4) : ints}, at::kInt);
-    if (!together) own = call.empty({(int64_t)bytes}, at::kByte);
-    workspace = together ? (void*)((int32_t*)all.data_ptr() + at) : own.data_ptr();
-  }
-};
-
 const uint8_t* pinned_of(const Call& call, PyObject* o, int64_t blocks) {
   if (is_none(o)) return nullptr;
   const at::Tensor& t = tensor(o);
@@ -368,14 +354,13 @@ PyObject* fork_block_tables(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const uint8_t* pins = pinned_of(call, v[6], blocks);
     const size_t bytes = pool_workspace_size_fn(i32(blocks));
     need(bytes > 0);
-    const PoolMemory m(call, N * (cols + 4) + 3, bytes);
-    const at::Tensor& all = m.all;
+    const at::Tensor all = call.empty({N * (cols + 4) + 3}, at::kInt), ws = call.empty({(int64_t)bytes}, at::kByte);
     int32_t* p = (int32_t*)all.data_ptr();  // copies, table, past, held, state, error
     const int64_t t = 2 * N, q = t + N * cols, h = q + N, s = h + N;
     need(unlocked(fork_block_tables_fn, (const int32_t*)parents.data_ptr(), past, held, (const int32_t*)table.data_ptr(),
                   (int32_t*)ring.data_ptr(), state, pins, i32(B), i32(N), i32(cols), (int32_t)integer(v[7]),
                   i32(blocks), i32(ring.size(0)), p + q, p + h, p + t, p, p + s, (uint32_t*)(p + s + 2),
-                  m.workspace, bytes, call.stream()) == PA_OK);
+                  ws.data_ptr(), bytes, call.stream()) == PA_OK);
     return tuple_of({piece_of(all, q, {N}), piece_of(all, h, {N}), piece_of(all, t, {N, cols}), piece_of(all, 0, {N, 2}),
                      piece_of(all, s, {2}), piece_of(all, s + 2, {1})});
   });
@@ -394,13 +379,12 @@ PyObject* compact_block_tables(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const uint8_t* pins = pinned_of(call, v[3], blocks);
     const size_t bytes = pool_workspace_size_fn(i32(blocks));
     need(bytes > 0);
-    const PoolMemory m(call, 2 * moves + B * cols + 4, bytes);
-    const at::Tensor& all = m.all;
+    const at::Tensor all = call.empty({2 * moves + B * cols + 4}, at::kInt), ws = call.empty({(int64_t)bytes}, at::kByte);
     int32_t* p = (int32_t*)all.data_ptr();  // copies, table, state, end, error
     const int64_t t = 2 * moves, s = t + B * cols;
     need(unlocked(compact_block_tables_fn, held, (const int32_t*)table.data_ptr(), (int32_t*)ring.data_ptr(), pins,
                   i32(B), i32(cols), i32(blocks), i32(ring.size(0)), i32(moves), p + t, p, p + s, p + s + 2,
-                  (uint32_t*)(p + s + 3), m.workspace, bytes, call.stream()) == PA_OK);
+                  (uint32_t*)(p + s + 3), ws.data_ptr(), bytes, call.stream()) == PA_OK);
     return tuple_of({piece_of(all, t, {B, cols}), piece_of(all, 0, {moves, 2}), piece_of(all, s, {2}),
                      piece_of(all, s + 2, {1}), piece_of(all, s + 3, {1})});
   });
