@@ -159,3 +159,18 @@ def test_inputs_rewritten_right_before_a_mixed_call(nh, kvh, hs, dtype):
         for i, g in enumerate(got):
             w = want[(k + i) % 3]
             assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+
+
+# ---- numbers that 32 bits cannot hold ------------------------------------------------------------
+
+
+@pytest.mark.parametrize("fast", [True, False])
+def test_a_cap_or_scale_that_32_bits_round_to_nothing_is_refused(fast, monkeypatch):
+    """None of them may be taken for the 0 that stands for no cap, or for the scale by the head size."""
+    if not fast:
+        monkeypatch.setattr(pa.step, "_fast", _NoFast())
+    b = Batch(110, "fp16", 8, 2, 64, 16, [40], [2])
+    for kw in (dict(softcap=1e-60), dict(softcap=-1e-60), dict(scale=1e-60), dict(scale=-1e-60)):
+        with pytest.raises(ValueError, match=next(iter(kw))):
+            pa.biased_paged_attention(b.query, b.key_cache, b.value_cache, *b.meta, num_heads=8, kv_num_heads=2, **kw)
+    pa.biased_paged_attention(b.query, b.key_cache, b.value_cache, *b.meta, num_heads=8, kv_num_heads=2, softcap=0, scale=0)

@@ -117,6 +117,9 @@ def biased_paged_attention(query: torch.Tensor, key_cache: torch.Tensor, value_c
                             not lse.is_contiguous()):
         raise ValueError("lse must be contiguous float32 (rows, num_heads)")
     _sizes(window=window)
+    for name, x in (("softcap", softcap), ("scale", scale)):  # (0 stands for no cap, and for the scale by the head size)
+        if x != 0 and _f32(x).value == 0:
+            raise ValueError(f"{name} is 0 in 32 bits")
     rules = PaScoreRules(softcap, window, _of_rows(slopes, "slopes", num_heads, torch.float32, index),
                          _of_rows(first_keys, "first_keys", N, torch.int32, index),
                          _of_rows(prefix_lens, "prefix_lens", B, torch.int32, index), 0)

@@ -60,6 +60,13 @@ float real(PyObject* o) {
   return (float)v;
 }
 
+// one that is not 0 in 32 bits unless it is 0
+float real_or_0(PyObject* o) {
+  const float v = real(o);
+  need(v != 0.f || PyFloat_AsDouble(o) == 0.);
+  return v;
+}
+
 // the device that the call's tensors are on, which must be the current one
 struct Call {
   c10::Device device;
@@ -441,7 +448,7 @@ PyObject* biased_paged_attention(PyObject*, PyObject* const* v, Py_ssize_t n) {
     d.max_blocks_per_sequence = b.columns;
     d.max_query_len = i32(integer(v[14]));
     pa_score_rules rules{};
-    rules.softcap = real(v[9]);
+    rules.softcap = real_or_0(v[9]);
     rules.window = i32(integer(v[11]));
     if (!is_none(v[10])) {
       const at::Tensor& s = call.whole(v[10], at::kFloat, 1);
@@ -457,7 +464,7 @@ PyObject* biased_paged_attention(PyObject*, PyObject* const* v, Py_ssize_t n) {
       lse = (float*)l.data_ptr();
     }
     uint32_t* error = call.error(v[16]);
-    const float scale = real(v[8]);
+    const float scale = real_or_0(v[8]);
     const size_t bytes = biased_workspace_size_fn(d.head_size);
     need(bytes > 0);
     const at::Tensor out = call.empty({N, d.num_heads * k.size(3)}, type);
