@@ -174,3 +174,32 @@ def test_a_cap_or_scale_that_32_bits_round_to_nothing_is_refused(fast, monkeypat
         with pytest.raises(ValueError, match=next(iter(kw))):
             pa.biased_paged_attention(b.query, b.key_cache, b.value_cache, *b.meta, num_heads=8, kv_num_heads=2, **kw)
     pa.biased_paged_attention(b.query, b.key_cache, b.value_cache, *b.meta, num_heads=8, kv_num_heads=2, softcap=0, scale=0)
+
+
+# ---- caps that are none ----------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("softcap", [1e8, 1e30])
+@pytest.mark.parametrize("hs,past,q,bound", [(128, [70, 0, 300], [1, 200, 150], 0), (256, [130, 20], [60, 1], 0), (64, [400], [2], 2),
+                                             (128, [9000, 3], [1, 2], 2)])
+def test_a_cap_far_above_all_scores_leaves_them(hs, past, q, bound, softcap, dtype):
+    """Against the statement without a cap."""
+    b = Batch(120, dtype, 8, 2, hs, 32, past, q)
+    b.query[::2] *= 4
+    for kw in (dict(), dict(bias=True, prefix=150)):
+        rules, plain = (Rules(b, seed=9, softcap=c, bound=bound or None, **kw) for c in (softcap, 0.0))
+        out, lse = rules.call(b)
+        assert int(b.error) == 0
+        o, z, size, mag, far = ref.biased_attention(
+            f64(b.query).reshape(b.N, b.nh, hs), f64(b.key_cache), f64(b.value_cache), b.cum, b.past, b.table, hs ** -0.5,
+            0.0, plain.slopes, 0, None, plain.prefix)
+        # as Rules.check, but what the cap costs is in proportion to the score: the polynomial of three terms is 2^-19.4
+        # off at a score of almost no size, the cap itself (s / c)^2 / 3, two products and the scale 2^-24 each
+        delta = mag * ((hs + 8) * 2.0 ** -23 + 2.0 ** -19 + 2.0 ** -22) + far * 2.0 ** -22 + 2.0 ** -21 * (1 + np.abs(z))
+        weight = 2.0 ** -11 if dtype == "fp16" else 2.0 ** -16
+        eps, tiny = torch.finfo(DT[dtype]).eps / 2, 2.0 ** -25 if dtype == "fp16" else 0.0
+        bound_o = eps * np.abs(o) * (1 + 2.0 ** -7) + size * (weight + 2 * delta[..., None] + 2.0 ** -17) + tiny
+        assert (np.abs(f64(out).reshape(o.shape) - o) <= bound_o).all()
+        assert (np.abs(f64(lse) - z) <= delta + 2.0 ** -17).all()
+        assert delta.max() < 0.05  # (so that a wrong score shows)
