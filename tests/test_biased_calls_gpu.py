@@ -203,3 +203,80 @@ def test_a_cap_far_above_all_scores_leaves_them(hs, past, q, bound, softcap, dty
         assert (np.abs(f64(out).reshape(o.shape) - o) <= bound_o).all()
         assert (np.abs(f64(lse) - z) <= delta + 2.0 ** -17).all()
         assert delta.max() < 0.05  # (so that a wrong score shows)
+
+
+# ---- infinities and NaN that a row sees --------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("hs", [64, 128, 256])
+@pytest.mark.parametrize("past,q,kw,longest", [
+    ([200], [60], dict(), 0), ([0, 700], [300, 40], dict(bias=True), 0), ([3000], [12], dict(), 0),    # tiles, a cluster's
+    ([0], [500], dict(documents=60, prefix=80), 0), ([100], [300], dict(window=90, softcap=20.0), 0),
+    ([150], [3], dict(), 4), ([150, 900, 0], [3, 4, 2], dict(bias=True), 0), ([9000] * 3, [4, 4, 1], dict(softcap=9.0), 4)])
+def test_values_that_a_row_sees_decide_its_channels_whatever_their_weights(past, q, kw, longest, hs, dtype):
+    """An infinity is one and NaN is NaN in the rows that see it, however small its weight; infinities of both signs are
+    NaN; all other rows and channels are as if it were not there."""
+    b = Batch(130, dtype, 8, 2, hs, 16, past, q)
+    rules = Rules(b, seed=4, bound=longest or None, **kw)
+    plain = b.value_cache.clone()
+    r = np.random.default_rng(5)
+    for s in range(len(past)):
+        total = past[s] + q[s]
+        for channel, fills in ((1, [np.inf]), (2, [-np.inf]), (5, [np.nan]), (hs - 2, [np.inf, -np.inf]), (hs - 1, [np.inf, np.inf])):
+            for fill in fills:
+                t = int(r.integers(0, total)) if channel != 1 else int(r.integers(0, min(total, 20)))
+                b.value_cache[b.table[s, t // 16], t % 16, 0, channel] = float(fill)
+    out, lse = rules.call(b)
+    assert int(b.error) == 0
+    # what each row sees in each channel, from its range of keys
+    want = np.zeros((b.N, 8, hs), int)  # 1: infinity, 2: minus infinity, 3: both, 4: NaN
+    held = f64(b.value_cache)
+    for s in range(len(past)):
+        for j in range(q[s]):
+            i = int(b.cum[s]) + j
+            lo, hi = ref.key_range(past[s], q[s], j, rules.window, None if rules.first is None else int(rules.first[i]),
+                                   None if rules.prefix is None else int(rules.prefix[s]))
+            t = np.arange(lo, hi)
+            v = held[b.table[s, t // 16], t % 16]  # (keys, kv heads, channels)
+            for g in range(2):
+                kind = np.isposinf(v[:, g]).any(0) * 1 | np.isneginf(v[:, g]).any(0) * 2 | np.isnan(v[:, g]).any(0) * 4
+                want[i, g * 4: (g + 1) * 4] = kind
+    got = f64(out).reshape(want.shape)
+    assert (want == 0).any() and (want == 1).any()
+    assert np.array_equal(np.isposinf(got), want == 1)
+    assert np.array_equal(np.isneginf(got), want == 2)
+    assert np.array_equal(np.isnan(got), want >= 3)
+    clean = torch.where(torch.from_numpy(want != 0).cuda().flatten(1), torch.zeros_like(out), out)
+    b.value_cache = plain
+    o, z, size, mag, far = ref.biased_attention(
+        f64(b.query).reshape(want.shape), f64(b.key_cache), f64(plain), b.cum, b.past, b.table, hs ** -0.5, rules.softcap,
+        rules.slopes, rules.window, rules.first, rules.prefix)
+    finite = np.where(np.isfinite(z), np.abs(z), 0)  # the bounds of Rules.check
+    delta = mag * (hs + 8) * 2.0 ** -23 + far * 2.0 ** -22 + 2.0 ** -21 * (1 + finite + 2 * rules.softcap)
+    weight = 2.0 ** -11 if dtype == "fp16" else 2.0 ** -16
+    eps, tiny = torch.finfo(DT[dtype]).eps / 2, 2.0 ** -25 if dtype == "fp16" else 0.0
+    bound = eps * np.abs(o) * (1 + 2.0 ** -7) + size * (weight + 2 * delta[..., None] + 2.0 ** -17) + tiny
+    assert (np.abs(f64(clean).reshape(want.shape) - o) <= bound)[want == 0].all()
+    none = np.isneginf(z)
+    assert np.array_equal(none, np.isneginf(f64(lse))) and (np.abs(f64(lse)[~none] - z[~none]) <= (delta + 2.0 ** -17)[~none]).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("past,q", [(50000, 1), (0, 4096)])
+def test_what_a_value_that_is_not_finite_costs(past, q, dtype):
+    """The header gives a row 0.05 ms for every 1000 keys; rows of a prompt share the chip's warps (over 900)."""
+    b = Batch(141, dtype, 8, 2, 128, 16, [past], [q])
+    rules = Rules(b, bound=q)
+    b.value_cache[b.table[0, 0], 0, 0, 3] = float("inf")
+    times = []
+    for _ in range(4):
+        start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        start.record()
+        out, _ = rules.call(b)
+        end.record()
+        torch.cuda.synchronize()
+        times.append(start.elapsed_time(end))
+    assert torch.isposinf(out.view(-1, 8, 128)[:, :4, 3]).all()
+    ms = 0.05 * (past + q) / 1000 if q == 1 else 0.05 * q / 2 / 1000 * (4 * q / 900)
+    assert min(times) < 4 * ms + 1, (times, ms)

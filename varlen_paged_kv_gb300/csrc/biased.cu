@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
           const float inv = M == -INFINITY ? 0.f : 1.f / S;
           uint2 out = make_uint2(pack_out<BF16>(x.x * inv, x.y * inv), pack_out<BF16>(x.z * inv, x.w * inv));
           if (M == -INFINITY) out = make_uint2(0, 0);
-          else if (!finite4(x.x * inv, x.y * inv, x.z * inv, x.w * inv)) *redo = 1;
+          else if (S == S && !finite4(x.x * inv, x.y * inv, x.z * inv, x.w * inv)) *redo = 1;
           *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.output) + at * HS + cc) = out;
           if (a.lse && cc == 0) a.lse[at] = M == -INFINITY ? -INFINITY : (M + fast_log2(S)) * 0.69314718055994531f;
         } else {
@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
       const float inv = M == -INFINITY ? 0.f : 1.f / S;
       uint2 out = make_uint2(pack_out<BF16>(x[0] * inv, x[1] * inv), pack_out<BF16>(x[2] * inv, x[3] * inv));
       if (M == -INFINITY) out = make_uint2(0, 0);
-      else if (!finite4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv)) atomicOr(redo, 1u << r);
+      else if (S == S && !finite4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv)) atomicOr(redo, 1u << r);
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.output) + at * HS + cc) = out;
       if (a.lse && cc == 0) a.lse[at] = M == -INFINITY ? -INFINITY : (M + fast_log2(S)) * 0.69314718055994531f;
     }
@@ -589,8 +589,9 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
 // the last; its second number is the sequence of the unit that record 2k begins). A lane has four columns of a row,
 // eight warps share the pieces: what bounds it is latency, of its launch and of two loads, one after the other (the
 // records, the pieces): 2.6 us behind one row of 200 keys, 3.7 behind 8 of 8000.
+// (Four CTAs to an SM: with the registers that redo_row would take, two, 64 decode rows 120.5 us instead of 117.5.)
 template <int HS, bool BF16>
-__global__ void __launch_bounds__(kMergeThreads) biased_merge_kernel(const __grid_constant__ BiasedArgs a, const int ctas) {
+__global__ void __launch_bounds__(kMergeThreads, 4) biased_merge_kernel(const __grid_constant__ BiasedArgs a, const int ctas) {
   constexpr int WARPS = kMergeThreads / 32;
   __shared__ float part[WARPS][6][32];
   pdl_wait();
@@ -610,6 +611,7 @@ __global__ void __launch_bounds__(kMergeThreads) biased_merge_kernel(const __gri
       break;
     }
   }
+  unsigned again = 0;  // a bit for each row
   for (int i = blockIdx.y * 32 + lane; i - lane < head.x * (HS / 4); i += gridDim.y * 32) {
     const int r = min(i / (HS / 4), head.x - 1), cc = i % (HS / 4) * 4;
     float M = -INFINITY, S = 0.f;
@@ -647,16 +649,18 @@ __global__ void __launch_bounds__(kMergeThreads) biased_merge_kernel(const __gri
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.output) + at * HS + cc) = out;
       if (a.lse && cc == 0) a.lse[at] = M == -INFINITY ? -INFINITY : (M + fast_log2(S)) * 0.69314718055994531f;
     }
-    unsigned bad = __ballot_sync(0xffffffffu, there && M != -INFINITY && !finite4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv));
-    while (bad) {  // (these 32 lanes' columns of the row)
-      const int first = __ffs(bad) - 1, row = __shfl_sync(0xffffffffu, r, first), rr = head.z + row;
-      const unsigned same = __ballot_sync(0xffffffffu, r == row && there);
-      const int from = __shfl_sync(0xffffffffu, cc, __ffs(same) - 1), b = a.records[2 * c + 1].y;
-      __syncwarp();
-      redo_row<HS, BF16>(a, b, head.y, a.cum[b + 1] - head.y, a.past[b], rr / a.G, head.w * a.G + rr % a.G, lane, from,
-                         from + 4 * __popc(same));
-      bad &= ~same;
-    }
+    if (there && M != -INFINITY && S == S && !finite4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv)) again |= 1u << r;
+  }
+  // rows to look at again, this block's columns of them (here, where little else is alive: called in the loop above, it
+  // cost 2 of 117 us of 64 decode rows)
+  if (warp != 0) return;
+  __syncwarp();
+  again = __reduce_or_sync(0xffffffffu, again);
+  const int from = (blockIdx.y * 32) % (HS / 4) * 4;
+  for (; again; again &= again - 1) {
+    const int row = __ffs(again) - 1, rr = head.z + row, b = a.records[2 * c + 1].y;
+    redo_row<HS, BF16>(a, b, head.y, a.cum[b + 1] - head.y, a.past[b], rr / a.G, head.w * a.G + rr % a.G, lane, from,
+                       min(from + 128, HS));
   }
 }
 

@@ -668,7 +668,7 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
           for (int e = 0; e < 32; e += 4)
             fine = fine && finite4(__uint_as_float(ov[e]) * inv, __uint_as_float(ov[e + 1]) * inv,
                                    __uint_as_float(ov[e + 2]) * inv, __uint_as_float(ov[e + 3]) * inv);
-          if (some && !fine) atomicOr(&redo[row >> 5], 1u << (row & 31));
+          if (some && !fine && l == l) atomicOr(&redo[row >> 5], 1u << (row & 31));
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
             uint32_t w[4];
@@ -723,7 +723,14 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
       }
       const int64_t at = (int64_t)(it.row0 + r / a.G) * a.nh + g * a.G + r % a.G;
       *reinterpret_cast<uint2*>(out + at * HS + quad * 4) = make_uint2(pack_sat<BF16>(x.x, x.y), pack_sat<BF16>(x.z, x.w));
-      if (!finite4(x.x, x.y, x.z, x.w)) atomicOr(&redo[r >> 5], 1u << (r & 31));
+      if (!finite4(x.x, x.y, x.z, x.w)) {
+        bool lost = false;  // (a sum of weights that is NaN makes the row so)
+        for (int k = 0; k < C; ++k) {
+          const float sum = ld_cluster(cluster_addr(ml + 128 + r, k));
+          lost = lost || sum != sum;
+        }
+        if (!lost) atomicOr(&redo[r >> 5], 1u << (r & 31));
+      }
     }
     cluster_sync();  // no CTA leaves while another reads its shared memory
   }
