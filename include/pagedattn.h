@@ -614,7 +614,7 @@ size_t pa_biased_workspace_size(int32_t head_size);
  * The table entries of pages that no row of a sequence sees may be anything (those that a window has left
  * behind, those of padding between documents), and what the keys and values hold that a row does not see reaches
  * neither its scores nor its output, whatever other rows see of them. An infinite value that a row does see makes that
- * channel of its output infinite; NaN, or infinities of both signs, make it NaN. (Rows are
+ * channel of its output infinite, however small its weight; NaN, or infinities of both signs, make it NaN. (Rows are
  * worked on in blocks, and one whose result is not finite is looked at again over its own keys alone, which costs time:
  * 0.05 ms for every 1000 keys of a row where its own values are what is not finite, about 0.2 ms where other rows'
  * are or where a sum of bf16 values is past 32 bits; 256-wide heads take 0.15 and 0.8.)

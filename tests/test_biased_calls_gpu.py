@@ -262,6 +262,21 @@ def test_values_that_a_row_sees_decide_its_channels_whatever_their_weights(past,
     assert np.array_equal(none, np.isneginf(f64(lse))) and (np.abs(f64(lse)[~none] - z[~none]) <= (delta + 2.0 ** -17)[~none]).all()
 
 
+@pytest.mark.parametrize("past,q,longest", [([30], [3], 4), ([40, 900], [2, 2], 2), ([20], [60], 0)])
+def test_an_infinite_value_of_no_weight_in_32_bits_is_infinite(past, q, longest):
+    """A slope of 300 takes each key's weight to e^-300 of the next one's."""
+    b = Batch(140, "bf16", 8, 2, 64, 16, past, q)
+    rules = Rules(b, bias=True, bound=longest or None)
+    rules.slopes[:] = 300.0
+    for channel, fill in ((1, float("inf")), (40, float("-inf"))):
+        b.value_cache[b.table[0, 0], 7, 1, channel] = fill
+    out, lse = rules.call(b)
+    got = f64(out).reshape(b.N, 8, 64)
+    assert np.isposinf(got[: q[0], 4:, 1]).all() and np.isneginf(got[: q[0], 4:, 40]).all()
+    got[: q[0], 4:, [1, 40]] = 0
+    assert np.isfinite(got).all() and torch.isfinite(lse).all()
+
+
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("past,q", [(50000, 1), (0, 4096)])
 def test_what_a_value_that_is_not_finite_costs(past, q, dtype):

@@ -468,12 +468,14 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
       }
       named_bar_sync(1, 128);
       float f[2];
+      bool none[2];  // no keys (O may be anything); a factor that is 0 in 32 bits makes NaN of an infinity, which redo_row settles
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = gq + 8 * i;
         const float M = fmaxf(fmaxf(ml[r], ml[16 + r]), fmaxf(ml[32 + r], ml[48 + r]));
         const float m = i ? m1 : m0;
-        f[i] = m == -INFINITY ? 0.f : fast_exp2(m - M) * (1.f / kLift);
+        none[i] = m == -INFINITY;
+        f[i] = none[i] ? 0.f : fast_exp2(m - M) * (1.f / kLift);
       }
       // up to four rows: the warps' side by side; more: the warps in turn add into the same rows
       const bool side = it.n_rows <= 4;
@@ -486,7 +488,7 @@ __global__ void __launch_bounds__(kBiThreads, HS == 256 ? 1 : 2)
             float* dst = comb + (side ? w * 4 + r : r) * L::kStride + tq * 2;
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
-              float2 y = f[i] != 0.f ? make_float2(o[d][2 * i] * f[i], o[d][2 * i + 1] * f[i]) : make_float2(0.f, 0.f);
+              float2 y = none[i] ? make_float2(0.f, 0.f) : make_float2(o[d][2 * i] * f[i], o[d][2 * i + 1] * f[i]);
               if (!side && turn > 0) {
                 const float2 old = *reinterpret_cast<float2*>(dst + d * 8);
                 y.x += old.x, y.y += old.y;

@@ -703,7 +703,7 @@ __global__ void __launch_bounds__(bi_threads(HS), HS == 256 ? 1 : 2)
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
           float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (n > 0 && f != 0.f)
+          if (n > 0 && m_used != -INFINITY)  // (a factor that is 0 in 32 bits makes NaN of an infinity: redo_row's)
             x = make_float4(__uint_as_float(ov[e]) * f, __uint_as_float(ov[e + 1]) * f, __uint_as_float(ov[e + 2]) * f,
                             __uint_as_float(ov[e + 3]) * f);
           const int quad = ((cc + e) / 4 + row) % (HS / 4);
