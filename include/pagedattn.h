@@ -566,7 +566,9 @@ pa_status pa_copy_pages(const pa_page_tensor* tensors, int32_t num_tensors, int3
 /* What pa_biased_paged_attention does to the scores, and which keys a row sees. All device
  * pointers may be NULL. */
 typedef struct pa_score_rules {
-  float softcap;               /* c > 0: a score s becomes c * tanh(s / c); 0: no cap (1e-30 to 1e30) */
+  float softcap;               /* c > 0: a score s becomes c * tanh(s / c); 0: no cap (1e-30 to 1e30). The form of the
+                                  tanh, and with it the time, is chosen by the scores: prompts take up to 1.55 times as
+                                  long where scores reach their cap, and with caps above 177 up to 2.4 times */
   int32_t window;              /* w > 0: a row at position p sees no key before p - w + 1; 0: no window */
   const float* slopes;         /* fp32 (num_heads): slopes[h] * |p - t| is taken off the score of key t */
   const int32_t* first_keys;   /* int32 (num_tokens): a row sees no key before its own first one (packed

@@ -15,7 +15,7 @@ __device__ __forceinline__ bool unlikely(bool x) { return __builtin_expect(x, 0)
 
 // ---- scores --------------------------------------------------------------------------------
 // tanh as u times a polynomial in u^2 (minimax by weighted least squares on 4000 Chebyshev points) up to
-// |u| = 0.25, 4.9e-8 off at most (with six terms up to 0.75, 9.5e-9), beyond that from the exponential,
+// |u| = 0.25, 4.9e-8 off at most (with six terms up to 0.75, 1.4e-8), beyond that from the exponential,
 // 1 - 2 / (1 + e^2u), 2^-21 off at most (an exponential, a sum, a reciprocal, a rounding); the instruction
 // tanh.approx is 5e-4 off, which a cap of 50 would turn into scores 0.02 off.
 constexpr float kTanhNear = 0.25f, kTanhMid = 0.75f;

@@ -10,7 +10,7 @@
 // scores each and exchange their maxima through shared memory; with narrower ones two CTAs share an
 // SM and fill each other's gaps (there two threads a row were slower, 4 prompts of 2048 872 us
 // instead of 746). S_{t+1} is issued before P_t is waited for, so the tensor core works during the
-// softmax. What bounds it is that softmax: 4 prompts of 2048 with a cap and a bias take 637 us in bf16, 1020 TFLOP/s
+// softmax. What bounds it is that softmax: 4 prompts of 2048 with a cap and a bias take 638 us in bf16, 1020 TFLOP/s
 // (P V counted once), 540 in fp16, and 470 in fp16 without cap and bias, 1383 TFLOP/s.
 // The load of S brings the row's largest magnitude (or score) with it; finding it score by score took
 // 738 us instead of 723 (before the steps below), and 344 instead of 329 for chunks with a cap and a window.
@@ -146,8 +146,10 @@ static __device__ __noinline__ void report_pages(const BiasedArgs& a, int b, int
 // behind the row), plus `shift`. `level` says how the cap is taken: kNear and kMid, by polynomials in whose reach all
 // scores are; kFar, by the exponential, 2^-21 of the cap off wherever a score is; kAny, each score by what suits it,
 // for caps so large that this matters. 4 prompts of 2048 whose scores reach 0.1, 0.25, 0.4 and all of their cap take
-// 637, 743, 800 and 950 us (848, 1204 and 3757 the last three where each score past 0.75 chose its form). On packed pairs: a score takes 2, 4 and 3 instruction slots and none, none and
-// two more of the special function unit's, half a slot with a bias, where one score at a time took 13.
+// 638, 750, 784 and 920 us (848, 1204 and 3757 the last three where each score past 0.75 chose its form by a branch), 980 up to
+// a cap of 170, and with kAny, at one of 200, 1500.
+// On packed pairs: a score takes 2, 4 and 3 instruction slots and none, none and two more of the special function unit's,
+// half a slot with a bias, where one score at a time took 13.
 constexpr int kNear = 1, kMid = 2, kFar = 3, kAny = 4;
 template <bool CAP, bool BIAS, int N>
 __device__ __forceinline__ void bend_scores(const BiasedArgs& a, uint32_t* r, int level, float slope, float away, bool after,
