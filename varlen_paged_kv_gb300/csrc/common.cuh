@@ -318,7 +318,7 @@ struct PreSmem {
 // completed and its writes are visible, and since the predecessor waited for its own
 // predecessor, completion is transitive along the stream. pdl_launch_dependents() lets the
 // next kernel launch (its CTAs then sit in their own pdl_wait until this grid completes).
-// One kernel does not wait at its start: biased_rows_kernel beside the biased tile kernel, whose
+// biased_rows_kernel beside the biased tile kernel does not wait at its start: that kernel's
 // CTAs have all waited before they let it launch. What earlier kernels wrote is complete then;
 // acquire_earlier_kernels() takes the place of the wait before the first loads, and one of its
 // CTAs waits before it ends, so that completion stays transitive.
