@@ -608,7 +608,8 @@ size_t pa_biased_workspace_size(int32_t head_size);
  *   lo = max(0, first_keys[row], p - window + 1),
  *   hi = min(past_seqlens[b] + q_len, max(p + 1, prefix_lens[b])),
  * (of the terms that are given) with scores scale * q.k, capped, then biased, as pa_score_rules says. Softmax and accumulation are
- * fp32, the output is rounded once to T; lse (fp32 (N, num_heads) or NULL) is the natural-log
+ * fp32, the output is rounded once to T; on their way into the product with the values the weights are rounded to fp16
+ * (2^-11 of each; of bf16 caches to two bf16 terms, 2^-16), which their sum and the lse are not; lse (fp32 (N, num_heads) or NULL) is the natural-log
  * log-sum-exp of those scores. A row that sees no key gives zeros and an lse of -inf. scale and
  * query rows as in pa_sparse_paged_attention; the caches hold T and already hold this step's rows. output
  * and query do not overlap.
